@@ -421,6 +421,157 @@ qsa_status qsa_qk_proj(const uint16_t *x, int64_t x_stride, const uint16_t *w, i
                        int32_t hidden, int32_t out_cols, uint16_t *y, int64_t y_stride,
                        int32_t *dev_status, void *stream);
 
+/*
+ * Attention of each sequence's drafted rows over every token of its paged
+ * cache: the context and, behind it, a tree (or chain) of drafted tokens.  It is
+ * the attention of rows under the inert bound (metrale layers/qsa.rs
+ * decode_select: up to budget/ratio complete blocks the step attends densely),
+ * of one decode row (row_start 0, 1, 2, ...; tree_mask NULL), of a chunk of a
+ * prompt (tree_mask NULL), and of the verification of drafted tokens.
+ *  q        DEVICE bf16, row i at q + i*q_stride: nq heads of head_dim values
+ *           (already rotated), 16-byte aligned, q_stride a multiple of 8 and
+ *           >= nq*head_dim.  Query head h reads KV head h / (nq / nkv).
+ *  k_pool, v_pool  DEVICE bf16 [pool_pages * page_size, nkv, head_dim],
+ *           16-byte aligned; head_dim is 128 or 256; pool_pages * page_size *
+ *           nkv < 2^31.
+ *  table, table_len, table_cols, page_size: as in qsa_gather_kv, a sequence's
+ *           page table at table + s*table_cols.
+ *  ctx_len  DEVICE int32 [n_seqs]: the sequence's context tokens.
+ *  row_start  DEVICE int32 [n_seqs + 1], ascending: sequence s owns rows
+ *           [row_start[s], row_start[s+1]) of q and out; its j-th row is
+ *           drafted token j, whose K and V are token ctx_len[s] + j of the cache.
+ *           Rows of q and out outside every sequence are neither read nor written.
+ *  n_rows   rows of q and out; row_start's entries are <= n_rows.
+ *  tree_mask  DEVICE uint32 [n_rows, mask_words] or NULL: row j of a sequence
+ *           attends drafted token k iff bit k % 32 of word k / 32 of its mask row
+ *           is set (bits past the sequence's own drafted tokens are ignored; its
+ *           own bit is not implied).  NULL: k <= j.  Every row attends every
+ *           context token.  A sequence has at most 32 * mask_words drafted tokens.
+ *  scale    multiplies every logit q_h . k (finite; typically 1/sqrt(head_dim)).
+ *  out      DEVICE bf16, row i at out + i*out_stride (nq*head_dim values),
+ *           16-byte aligned, out_stride a multiple of 8 and >= nq*head_dim.
+ *  lse      DEVICE f32 [n_rows, nq] or NULL: ln of the row's and head's sum of
+ *           exp(logit), which qsa_attn_mass takes.
+ *  A row that attends no token gets zeros, and lse -inf.  What a row's mask
+ *  leaves out does not reach its output, NaN or infinity though it be; nor does
+ *  what the cache holds past a sequence's tokens.
+ *  Logits, softmax and sums run in f32; the weights are rounded to bf16 for the
+ *  weighted sum of V alone (the normaliser and lse use them unrounded).
+ *  workspace  DEVICE scratch of at least qsa_tree_workspace_bytes(...) bytes,
+ *           16-byte aligned; its contents on entry do not matter.  Calls that
+ *           share one must be stream-ordered.
+ *  Device errors: a sequence whose rows, context or drafted count contradict
+ *  n_rows, the table or the mask is QSA_ERR_ROW_RANGE (with the sequence's
+ *  index) and its rows are left alone; a table entry outside the pool is
+ *  QSA_ERR_TOKEN_RANGE (the sequence's index) and its sequence's output is
+ *  unspecified.  Refused: pool_pages * page_size * nkv or table_len * page_size
+ *  past 31 bits, n_seqs > 65535, a small or unaligned workspace.
+ */
+qsa_status qsa_tree_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
+                         int32_t head_dim, const uint16_t *k_pool, const uint16_t *v_pool,
+                         int32_t pool_pages, int32_t page_size, const int32_t *table,
+                         int32_t table_len, int64_t table_cols, const int32_t *ctx_len,
+                         const int32_t *row_start, int32_t n_seqs, int32_t n_rows,
+                         const uint32_t *tree_mask, int32_t mask_words, float scale, uint16_t *out,
+                         int64_t out_stride, float *lse, int32_t *dev_status, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/* Bytes of the workspace qsa_tree_attn needs; -1 for arguments it refuses. */
+int64_t qsa_tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int32_t nkv,
+                                 int32_t head_dim);
+
+/*
+ * The attention weight that a cache's tokens gather, summed over drafted rows
+ * and over the query heads of each KV head:
+ *   mass[s, g, t] = (t < ctx_len[s] ? carry * mass[s, g, t] : 0)
+ *                 + sum_j row_weight[j] * sum_{h in group g} exp(scale q_jh . k_tg - lse[j, h])
+ * over the rows j of sequence s that attend token t.  Drafted tokens start at
+ * zero, so a cache that grows needs no clearing.  What qsa_evict_select reads.
+ *  q ... scale  as in qsa_tree_attn (the same rows, cache and masks).
+ *  lse      DEVICE f32 [n_rows, nq], as qsa_tree_attn wrote it; a head with lse
+ *           -inf adds nothing.
+ *  row_weight  DEVICE f32 [n_rows] or NULL (= 1): a row of weight 0 (a
+ *           rejected draft) adds nothing, whatever its logits are.
+ *  carry    finite, >= 0: the share of the mass that stays; 0 does not read it.
+ *  mass     DEVICE f32 [n_seqs, nkv, mass_cols], 16-byte aligned, mass_cols a
+ *           multiple of 4.  Entries from ctx_len + drafted on are left alone, and
+ *           so is a sequence without rows.
+ *  The sums run in f32 in an order that the arguments alone decide.
+ *  Device errors as in qsa_tree_attn; more cached tokens than mass_cols is
+ *  QSA_ERR_ROW_RANGE.  A sequence that reports QSA_ERR_TOKEN_RANGE has
+ *  unspecified mass.
+ */
+qsa_status qsa_attn_mass(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
+                         int32_t head_dim, const uint16_t *k_pool, int32_t pool_pages,
+                         int32_t page_size, const int32_t *table, int32_t table_len,
+                         int64_t table_cols, const int32_t *ctx_len, const int32_t *row_start,
+                         int32_t n_seqs, int32_t n_rows, const uint32_t *tree_mask,
+                         int32_t mask_words, float scale, const float *lse, const float *row_weight,
+                         float carry, float *mass, int64_t mass_cols, int32_t *dev_status,
+                         void *stream);
+
+/*
+ * The tokens that a cache cut back to its heaviest ones keeps, ascending.
+ *  mass     DEVICE f32 [n_seqs, nkv, mass_cols], as in qsa_attn_mass (mass_cols
+ *           >= tokens).
+ *  length   DEVICE int32 [n_seqs]: a sequence's cached tokens, <= tokens.
+ *  unit     1, or 4 to keep or drop whole 4-token blocks (whose pooled keys then
+ *           stay valid): unit u is tokens [unit*u, unit*u + unit).  The length %
+ *           unit tokens past the last whole unit always stay.
+ *  keep     tokens to keep in whole units, a positive multiple of unit.
+ *  n_first, n_last  multiples of unit, n_first + n_last <= keep: that many
+ *           tokens at the front, and in the last whole units, always stay.
+ *  sel      DEVICE int32, row s at sel + s*sel_cols, sel_cols >= min(tokens,
+ *           keep + unit - 1); the rest of a row is left alone.
+ *  n_sel    DEVICE int32 [n_seqs]: length if length / unit <= keep / unit (all
+ *           stay), else keep + length % unit.
+ *  A token's mass is the f32 sum over its KV heads in head order, a unit's the
+ *  f32 sum over its tokens in token order.  The units kept are the largest under
+ *  (mass descending, index ascending, -0.0 == +0.0), as in qsa_select_mask.
+ *  Device errors: a length outside [0, tokens] is QSA_ERR_ROW_RANGE, a
+ *  non-finite unit mass of a sequence that is cut QSA_ERR_NONFINITE (both with
+ *  the sequence's index); its row of sel and its n_sel are left alone.
+ */
+qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
+                            const int32_t *length, int32_t n_seqs, int32_t tokens, int32_t keep,
+                            int32_t n_first, int32_t n_last, int32_t unit, int32_t *sel,
+                            int64_t sel_cols, int32_t *n_sel, int32_t *dev_status, void *stream);
+
+/*
+ * Move a list's tokens together inside a paged cache, in place: token keep[j]
+ * of a sequence becomes token first + j (K and V rows, and with them mass and
+ * pooled block keys).  With first = 0 and qsa_evict_select's list it shortens a
+ * cache; with first = ctx_len and the accepted drafted tokens it joins a
+ * verified path to its context.
+ *  k_pool, v_pool, width, pool_pages, table, table_len, table_cols, page_size:
+ *           as in qsa_gather_kv.  No page may be in two sequences' tables among
+ *           the tokens that are read or written here (table_cols = 0 is refused
+ *           for n_seqs > 1).
+ *  keep     DEVICE int32, row s at keep + s*keep_cols, its first n_keep[s] <=
+ *           max_keep entries; keep[j] >= first + j (tokens only move towards the
+ *           front; an ascending list of tokens from first on always does).
+ *  first    DEVICE int32 [n_seqs] or NULL (= 0).
+ *  mass     DEVICE f32 [n_seqs, nkv, mass_cols] or NULL.
+ *  block_keys  DEVICE bf16 pooled keys or NULL: block b of sequence s at
+ *           block_keys + (key_base[s] + b)*128, 16-byte aligned.  The list's
+ *           first 4 * (n_keep / 4) entries must then be whole blocks (4b, 4b+1,
+ *           4b+2, 4b+3) and first a multiple of 4.
+ *  key_base  DEVICE int64 [n_seqs], or NULL (= 0) for one sequence.
+ *  What lies past the moved tokens is left as it is.
+ *  Device errors: n_keep or first out of range (also past mass_cols), a first
+ *  that is no multiple of 4 or a negative key_base with block_keys:
+ *  QSA_ERR_ROW_RANGE, the sequence (or its block keys) left alone; an entry
+ *  below first + j or past the table (or mass_cols), an entry of the page table
+ *  outside the pool, or a broken block: QSA_ERR_TOKEN_RANGE, that entry not moved.
+ */
+qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, int32_t pool_pages,
+                             const int32_t *table, int32_t table_len, int64_t table_cols,
+                             int32_t page_size, const int32_t *keep, int64_t keep_cols,
+                             const int32_t *n_keep, int32_t n_seqs, int32_t max_keep,
+                             const int32_t *first, float *mass, int64_t mass_cols, int32_t nkv,
+                             uint16_t *block_keys, const int64_t *key_base, int32_t *dev_status,
+                             void *stream);
+
 /* Zero a DEVICE status word (stream-ordered). */
 qsa_status qsa_reset_status(int32_t *dev_status, void *stream);
 

@@ -38,7 +38,9 @@ EXPORTED = ("qsa_version", "qsa_status_string", "qsa_rope_tables", "qsa_pool_blo
             "qsa_score_rows", "qsa_score_rows_with", "qsa_score_workspace_bytes",
             "qsa_score_rows_noalloc", "qsa_select_mask", "qsa_index_select",
             "qsa_decode_workspace_bytes", "qsa_decode_index_select", "qsa_mask_tokens",
-            "qsa_gather_kv", "qsa_sparse_attn", "qsa_qk_proj", "qsa_reset_status",
+            "qsa_gather_kv", "qsa_sparse_attn", "qsa_qk_proj", "qsa_tree_attn",
+            "qsa_tree_workspace_bytes", "qsa_attn_mass", "qsa_evict_select", "qsa_cache_compact",
+            "qsa_reset_status",
             "qsa_read_status", "qsa_set_wait_limit_cycles", "qsa_wait_limit_cycles")
 
 
@@ -78,6 +80,14 @@ def _load() -> ctypes.CDLL:
         "qsa_sparse_attn": ([P, i64, i32, i32, i32, P, P, i32, i32, P, i32, i64, P, i64, P, i32,
                              i32, f32, P, i64, P, P], i32),
         "qsa_qk_proj": ([P, i64, P, i32, i32, i32, P, i64, P, P], i32),
+        "qsa_tree_attn": ([P, i64, i32, i32, i32, P, P, i32, i32, P, i32, i64, P, P, i32, i32, P,
+                           i32, f32, P, i64, P, P, P, i64, P], i32),
+        "qsa_tree_workspace_bytes": ([i32, i32, i32, i32, i32], i64),
+        "qsa_attn_mass": ([P, i64, i32, i32, i32, P, i32, i32, P, i32, i64, P, P, i32, i32, P, i32,
+                           f32, P, P, f32, P, i64, P, P], i32),
+        "qsa_evict_select": ([P, i64, i32, P, i32, i32, i32, i32, i32, i32, P, i64, P, P, P], i32),
+        "qsa_cache_compact": ([P, P, i32, i32, P, i32, i64, i32, P, i64, P, i32, i32, P, P, i64,
+                               i32, P, P, P, P], i32),
         "qsa_reset_status": ([P, P], i32),
         "qsa_read_status": ([P, P, P, P], i32),
         "qsa_set_wait_limit_cycles": ([i64], i32),
@@ -312,6 +322,71 @@ def qsa_qk_proj(x, x_stride, w, n_rows, hidden, out_cols, y, y_stride, dev_statu
                             int(out_cols), _dev(y, "y"), int(y_stride),
                             _dev(dev_status, "dev_status"), _stream(stream)),
            "qsa_qk_proj")
+
+
+def qsa_tree_workspace_bytes(n_seqs: int, n_rows: int, nq: int, nkv: int, head_dim: int) -> int:
+    return int(_lib.qsa_tree_workspace_bytes(int(n_seqs), int(n_rows), int(nq), int(nkv),
+                                             int(head_dim)))
+
+
+def new_tree_workspace(n_seqs: int, n_rows: int, nq: int, nkv: int, head_dim: int,
+                       device="cuda") -> torch.Tensor:
+    """A workspace for qsa_tree_attn calls of at most these sizes."""
+    n = max(16, qsa_tree_workspace_bytes(n_seqs, n_rows, nq, nkv, head_dim))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def qsa_tree_attn(q, q_stride, nq, nkv, head_dim, k_pool, v_pool, pool_pages, page_size, table,
+                  table_len, table_cols, ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words,
+                  scale, out, out_stride, lse, dev_status, workspace, stream=None) -> None:
+    ws, wsb = _ws(workspace)
+    _check(_lib.qsa_tree_attn(_dev(q, "q"), int(q_stride), int(nq), int(nkv), int(head_dim),
+                              _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), int(pool_pages),
+                              int(page_size), _dev(table, "table"), int(table_len),
+                              int(table_cols), _dev(ctx_len, "ctx_len"),
+                              _dev(row_start, "row_start"), int(n_seqs), int(n_rows),
+                              _dev(tree_mask, "tree_mask"), int(mask_words), float(scale),
+                              _dev(out, "out"), int(out_stride), _dev(lse, "lse"),
+                              _dev(dev_status, "dev_status"), ws, int(wsb), _stream(stream)),
+           "qsa_tree_attn")
+
+
+def qsa_attn_mass(q, q_stride, nq, nkv, head_dim, k_pool, pool_pages, page_size, table, table_len,
+                  table_cols, ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words, scale,
+                  lse, row_weight, carry, mass, mass_cols, dev_status, stream=None) -> None:
+    _check(_lib.qsa_attn_mass(_dev(q, "q"), int(q_stride), int(nq), int(nkv), int(head_dim),
+                              _dev(k_pool, "k_pool"), int(pool_pages), int(page_size),
+                              _dev(table, "table"), int(table_len), int(table_cols),
+                              _dev(ctx_len, "ctx_len"), _dev(row_start, "row_start"), int(n_seqs),
+                              int(n_rows), _dev(tree_mask, "tree_mask"), int(mask_words),
+                              float(scale), _dev(lse, "lse"), _dev(row_weight, "row_weight"),
+                              float(carry), _dev(mass, "mass"), int(mass_cols),
+                              _dev(dev_status, "dev_status"), _stream(stream)),
+           "qsa_attn_mass")
+
+
+def qsa_evict_select(mass, mass_cols, nkv, length, n_seqs, tokens, keep, n_first, n_last, unit,
+                     sel, sel_cols, n_sel, dev_status, stream=None) -> None:
+    _check(_lib.qsa_evict_select(_dev(mass, "mass"), int(mass_cols), int(nkv),
+                                 _dev(length, "length"), int(n_seqs), int(tokens), int(keep),
+                                 int(n_first), int(n_last), int(unit), _dev(sel, "sel"),
+                                 int(sel_cols), _dev(n_sel, "n_sel"),
+                                 _dev(dev_status, "dev_status"), _stream(stream)),
+           "qsa_evict_select")
+
+
+def qsa_cache_compact(k_pool, v_pool, width, pool_pages, table, table_len, table_cols, page_size,
+                      keep, keep_cols, n_keep, n_seqs, max_keep, first, mass, mass_cols, nkv,
+                      block_keys, key_base, dev_status, stream=None) -> None:
+    _check(_lib.qsa_cache_compact(_dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), int(width),
+                                  int(pool_pages), _dev(table, "table"), int(table_len),
+                                  int(table_cols), int(page_size), _dev(keep, "keep"),
+                                  int(keep_cols), _dev(n_keep, "n_keep"), int(n_seqs),
+                                  int(max_keep), _dev(first, "first"), _dev(mass, "mass"),
+                                  int(mass_cols), int(nkv), _dev(block_keys, "block_keys"),
+                                  _dev(key_base, "key_base"), _dev(dev_status, "dev_status"),
+                                  _stream(stream)),
+           "qsa_cache_compact")
 
 
 def qsa_reset_status(dev_status, stream=None) -> None:

@@ -420,6 +420,162 @@ qsa_status qsa_qk_proj(const uint16_t *x, int64_t x_stride, const uint16_t *w, i
                                     dev_status, (cudaStream_t)stream));
 }
 
+namespace {
+
+constexpr int64_t kMostElems = (int64_t)1 << 46;  // products below this cannot overflow
+
+// The arguments that the cache's attention calls share.  *empty: nothing to do.
+qsa_status check_cached(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
+                        int32_t head_dim, const uint16_t *k_pool, int32_t pool_pages,
+                        int32_t page_size, const int32_t *table, int32_t table_len,
+                        int64_t table_cols, const int32_t *ctx_len, const int32_t *row_start,
+                        int32_t n_seqs, int32_t n_rows, const uint32_t *tree_mask,
+                        int32_t mask_words, float scale, const int32_t *dev_status, bool *empty) {
+  *empty = false;
+  if (n_seqs < 0 || n_rows < 0 || pool_pages < 0 || table_len < 0 || table_cols < 0 ||
+      q_stride < 0 || mask_words < 0)
+    return QSA_ERR_INVALID_VALUE;
+  if (n_seqs == 0 || n_rows == 0) {
+    *empty = true;
+    return QSA_OK;
+  }
+  if (nq <= 0 || nkv <= 0 || nq % nkv != 0 || (head_dim != 128 && head_dim != 256) ||
+      page_size <= 0 || pool_pages == 0 || table_len == 0 || !std::isfinite(scale))
+    return QSA_ERR_INVALID_VALUE;
+  if (table_cols != 0 && table_cols < table_len) return QSA_ERR_INVALID_VALUE;
+  if (q_stride < (int64_t)nq * head_dim || (q_stride & 7) != 0) return QSA_ERR_INVALID_VALUE;
+  if (tree_mask != nullptr && mask_words == 0) return QSA_ERR_INVALID_VALUE;
+  if (!q || !k_pool || !table || !ctx_len || !row_start || !dev_status) return QSA_ERR_INVALID_VALUE;
+  if (!aligned16(q) || !aligned16(k_pool)) return QSA_ERR_INVALID_VALUE;
+  // a pool row is one KV head of one token; TMA numbers them with 32 bits
+  if ((int64_t)pool_pages * page_size > INT32_MAX / nkv ||
+      (int64_t)table_len * page_size > INT32_MAX - 256 || (int64_t)n_rows * nq > INT32_MAX ||
+      (int64_t)n_rows * q_stride > kMostElems || n_seqs > 65535 || nkv > 65535 ||
+      (int64_t)n_rows * mask_words > kMostElems)
+    return QSA_ERR_INVALID_VALUE;
+  return QSA_OK;
+}
+
+}  // namespace
+
+int64_t qsa_tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int32_t nkv,
+                                 int32_t head_dim) {
+  if (n_seqs < 0 || n_rows < 0 || nq <= 0 || nkv <= 0 || nq % nkv != 0 ||
+      (head_dim != 128 && head_dim != 256))
+    return -1;
+  return qsa::tree_workspace_bytes(n_seqs, n_rows, nq / nkv, head_dim);
+}
+
+qsa_status qsa_tree_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
+                         int32_t head_dim, const uint16_t *k_pool, const uint16_t *v_pool,
+                         int32_t pool_pages, int32_t page_size, const int32_t *table,
+                         int32_t table_len, int64_t table_cols, const int32_t *ctx_len,
+                         const int32_t *row_start, int32_t n_seqs, int32_t n_rows,
+                         const uint32_t *tree_mask, int32_t mask_words, float scale, uint16_t *out,
+                         int64_t out_stride, float *lse, int32_t *dev_status, void *workspace,
+                         int64_t workspace_bytes, void *stream) {
+  bool empty;
+  const qsa_status st =
+      check_cached(q, q_stride, nq, nkv, head_dim, k_pool, pool_pages, page_size, table, table_len,
+                   table_cols, ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words, scale,
+                   dev_status, &empty);
+  if (st != QSA_OK) return st;
+  if (out_stride < 0 || workspace_bytes < 0) return QSA_ERR_INVALID_VALUE;
+  if (empty) return QSA_OK;
+  if (!v_pool || !out || !aligned16(v_pool) || !aligned16(out) ||
+      out_stride < (int64_t)nq * head_dim || (out_stride & 7) != 0 ||
+      (int64_t)n_rows * out_stride > kMostElems)
+    return QSA_ERR_INVALID_VALUE;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < qsa_tree_workspace_bytes(n_seqs, n_rows, nq, nkv, head_dim))
+    return QSA_ERR_INVALID_VALUE;
+  const qsa::TreeArgs a{{pool_pages, qsa::make_fast_div(page_size), table, table_len, table_cols,
+                         ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words},
+                        q, q_stride, nq, nkv, nq / nkv, k_pool, v_pool,
+                        scale * 1.4426950408889634f, out, out_stride, lse, dev_status, workspace,
+                        qsa::wait_limit_cycles()};
+  return from_cuda(qsa::launch_tree_attn(a, head_dim, (cudaStream_t)stream));
+}
+
+qsa_status qsa_attn_mass(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
+                         int32_t head_dim, const uint16_t *k_pool, int32_t pool_pages,
+                         int32_t page_size, const int32_t *table, int32_t table_len,
+                         int64_t table_cols, const int32_t *ctx_len, const int32_t *row_start,
+                         int32_t n_seqs, int32_t n_rows, const uint32_t *tree_mask,
+                         int32_t mask_words, float scale, const float *lse, const float *row_weight,
+                         float carry, float *mass, int64_t mass_cols, int32_t *dev_status,
+                         void *stream) {
+  bool empty;
+  const qsa_status st =
+      check_cached(q, q_stride, nq, nkv, head_dim, k_pool, pool_pages, page_size, table, table_len,
+                   table_cols, ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words, scale,
+                   dev_status, &empty);
+  if (st != QSA_OK) return st;
+  if (mass_cols < 0 || !(carry >= 0.0f) || std::isinf(carry)) return QSA_ERR_INVALID_VALUE;
+  if (empty) return QSA_OK;
+  if (!lse || !mass || !aligned16(mass) || (mass_cols & 3) != 0 ||
+      mass_cols > kMostElems / n_seqs / nkv)
+    return QSA_ERR_INVALID_VALUE;
+  const qsa::MassArgs a{{pool_pages, qsa::make_fast_div(page_size), table, table_len, table_cols,
+                         ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words},
+                        q, q_stride, nq, nkv, nq / nkv, k_pool, scale, lse, row_weight, carry, mass,
+                        mass_cols, dev_status, qsa::wait_limit_cycles()};
+  return from_cuda(qsa::launch_attn_mass(a, head_dim, (cudaStream_t)stream));
+}
+
+qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
+                            const int32_t *length, int32_t n_seqs, int32_t tokens, int32_t keep,
+                            int32_t n_first, int32_t n_last, int32_t unit, int32_t *sel,
+                            int64_t sel_cols, int32_t *n_sel, int32_t *dev_status, void *stream) {
+  if (n_seqs < 0 || tokens < 0 || mass_cols < 0 || sel_cols < 0 || n_first < 0 || n_last < 0)
+    return QSA_ERR_INVALID_VALUE;
+  if ((unit != 1 && unit != 4) || keep <= 0 || keep % unit != 0 || n_first % unit != 0 ||
+      n_last % unit != 0 || (int64_t)n_first + n_last > keep || nkv <= 0)
+    return QSA_ERR_INVALID_VALUE;
+  if (n_seqs == 0) return QSA_OK;
+  const int64_t most = (int64_t)keep + unit - 1 < tokens ? (int64_t)keep + unit - 1 : tokens;
+  if (!length || !n_sel || !dev_status || (tokens > 0 && (!mass || !sel))) return QSA_ERR_INVALID_VALUE;
+  if (mass_cols < tokens || (mass_cols & 3) != 0 || !aligned16(mass) || sel_cols < most)
+    return QSA_ERR_INVALID_VALUE;
+  if (tokens > INT32_MAX - 65536 || nkv > 65535 || n_seqs > (1 << 20) ||
+      mass_cols > kMostElems / n_seqs / nkv || sel_cols > kMostElems / n_seqs)
+    return QSA_ERR_INVALID_VALUE;
+  const qsa::EvictArgs a{mass, mass_cols, nkv, length, tokens, keep, n_first, n_last, unit,
+                         sel,  sel_cols,  n_sel, dev_status};
+  return from_cuda(qsa::launch_evict_select(a, n_seqs, (cudaStream_t)stream));
+}
+
+qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, int32_t pool_pages,
+                             const int32_t *table, int32_t table_len, int64_t table_cols,
+                             int32_t page_size, const int32_t *keep, int64_t keep_cols,
+                             const int32_t *n_keep, int32_t n_seqs, int32_t max_keep,
+                             const int32_t *first, float *mass, int64_t mass_cols, int32_t nkv,
+                             uint16_t *block_keys, const int64_t *key_base, int32_t *dev_status,
+                             void *stream) {
+  if (n_seqs < 0 || max_keep < 0 || width < 0 || pool_pages < 0 || table_len < 0 ||
+      table_cols < 0 || keep_cols < 0 || mass_cols < 0 || nkv < 0)
+    return QSA_ERR_INVALID_VALUE;
+  if (n_seqs == 0 || max_keep == 0) return QSA_OK;
+  if (width == 0 || width % 8 != 0 || page_size <= 0 || max_keep > keep_cols)
+    return QSA_ERR_INVALID_VALUE;
+  // a table shared by several sequences would have them overwrite each other
+  if (table_cols != 0 ? table_cols < table_len : n_seqs > 1) return QSA_ERR_INVALID_VALUE;
+  if (!k_pool || !v_pool || !table || !keep || !n_keep || !dev_status || !aligned16(k_pool) ||
+      !aligned16(v_pool))
+    return QSA_ERR_INVALID_VALUE;
+  if (mass && nkv == 0) return QSA_ERR_INVALID_VALUE;
+  if (block_keys && (!aligned16(block_keys) || (!key_base && n_seqs > 1))) return QSA_ERR_INVALID_VALUE;
+  if ((int64_t)pool_pages * page_size > kMostElems / width ||
+      (int64_t)table_len * page_size > INT32_MAX || keep_cols > kMostElems / n_seqs ||
+      (mass && mass_cols > kMostElems / n_seqs / nkv) || nkv > 65535 || width > (1 << 24) ||
+      n_seqs > 65535)
+    return QSA_ERR_INVALID_VALUE;
+  const qsa::CompactArgs a{k_pool, v_pool, width, pool_pages, qsa::make_fast_div(page_size), table,
+                           table_len, table_cols, keep, keep_cols, n_keep, max_keep, first, mass,
+                           mass_cols, mass ? nkv : 0, block_keys, key_base, dev_status};
+  return from_cuda(qsa::launch_cache_compact(a, n_seqs, (cudaStream_t)stream));
+}
+
 qsa_status qsa_reset_status(int32_t *dev_status, void *stream) {
   if (!dev_status) return QSA_ERR_INVALID_VALUE;
   return from_cuda(cudaMemsetAsync(dev_status, 0, 2 * sizeof(int32_t), (cudaStream_t)stream));

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "qsa_paged.cuh"
 #include "qsa_per_device.h"
 
 namespace qsa {
@@ -132,5 +133,77 @@ cudaError_t launch_sparse_attn(const uint16_t *q, int64_t q_stride, int32_t nq, 
 cudaError_t launch_proj(const uint16_t *x, int64_t x_stride, const uint16_t *w, int32_t n_rows,
                         int32_t hidden, int32_t out_cols, uint16_t *y, int64_t y_stride,
                         int32_t *status, cudaStream_t stream);
+
+// Attention of drafted rows over every cached token (qsa_tree.cu).
+struct TreeArgs {
+  CachedSeqs seqs;
+  const uint16_t *q;
+  int64_t q_stride;
+  int32_t nq, nkv, group;  // group = nq / nkv
+  const uint16_t *k_pool, *v_pool;
+  float scale_log2;  // scale * log2(e)
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;  // nullptr: not written
+  int32_t *status;
+  void *ws;
+  long long wait_limit;
+};
+int64_t tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t group, int32_t head_dim);
+cudaError_t launch_tree_attn(const TreeArgs &a, int32_t head_dim, cudaStream_t stream);
+
+// The attention weight that cached tokens gather (qsa_mass.cu).
+struct MassArgs {
+  CachedSeqs seqs;
+  const uint16_t *q;
+  int64_t q_stride;
+  int32_t nq, nkv, group;
+  const uint16_t *k_pool;
+  float scale;
+  const float *lse;
+  const float *weight;  // nullptr: every row counts once
+  float carry;
+  float *mass;
+  int64_t mass_cols;
+  int32_t *status;
+  long long wait_limit;
+};
+cudaError_t launch_attn_mass(const MassArgs &a, int32_t head_dim, cudaStream_t stream);
+
+// The tokens a shortened cache keeps (qsa_evict.cu).
+struct EvictArgs {
+  const float *mass;
+  int64_t mass_cols;
+  int32_t nkv;
+  const int32_t *length;
+  int32_t tokens, keep, n_first, n_last, unit;
+  int32_t *sel;
+  int64_t sel_cols;
+  int32_t *n_sel;
+  int32_t *status;
+};
+cudaError_t launch_evict_select(const EvictArgs &a, int32_t n_seqs, cudaStream_t stream);
+
+// Kept tokens moved to the front of a paged cache (qsa_compact.cu).
+struct CompactArgs {
+  uint16_t *k_pool, *v_pool;
+  int32_t width, pool_pages;
+  FastDiv page;
+  const int32_t *table;
+  int32_t table_len;
+  int64_t table_cols;
+  const int32_t *keep;
+  int64_t keep_cols;
+  const int32_t *n_keep;
+  int32_t max_keep;
+  const int32_t *first;  // nullptr: 0
+  float *mass;           // nullptr: none
+  int64_t mass_cols;
+  int32_t nkv;
+  uint16_t *block_keys;  // nullptr: none
+  const int64_t *key_base;
+  int32_t *status;
+};
+cudaError_t launch_cache_compact(const CompactArgs &a, int32_t n_seqs, cudaStream_t stream);
 
 }  // namespace qsa
