@@ -440,7 +440,8 @@ qsa_status check_cached(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t
     return QSA_OK;
   }
   if (nq <= 0 || nkv <= 0 || nq % nkv != 0 || (head_dim != 128 && head_dim != 256) ||
-      page_size <= 0 || pool_pages == 0 || table_len == 0 || !std::isfinite(scale))
+      page_size <= 0 || pool_pages == 0 || table_len == 0 ||
+      !std::isfinite(scale * 1.4426950408889634f))
     return QSA_ERR_INVALID_VALUE;
   if (table_cols != 0 && table_cols < table_len) return QSA_ERR_INVALID_VALUE;
   if (q_stride < (int64_t)nq * head_dim || (q_stride & 7) != 0) return QSA_ERR_INVALID_VALUE;

@@ -5,93 +5,720 @@
 // context token and the drafted tokens its mask names:
 //   s_t = scale q . k_t,  lse = ln sum_t exp(s_t),  out = sum_t exp(s_t - lse) v_t.
 //
-// One CTA of four warps per (row, query head).  A warp takes every fourth
-// token: a lane holds head_dim / 32 dims of q and of the running sum, the dot
-// is reduced by shuffles, and the running maximum and sum of the softmax are
-// updated per token; the warps' states are joined once at the end.
+// The rows of one sequence that read the same KV head (drafted row x query
+// head of the group) form the M dimension of two tcgen05 products per tile of
+// 128 tokens: S = Q K^T (operands in shared memory, accumulator in TMEM), and
+// O += P V (P as bf16 in TMEM over S's columns, V read MN-major).  A unit of work
+// is (sequence, KV head, 128 such rows); its tiles are a run of the launch's
+// linear list of tiles, of which every CTA (one per SM) takes an equal,
+// contiguous share, so ragged batches balance and one long context spreads over
+// the GPU.  A unit that lies in one CTA's share is written at once; the parts
+// of any other go to the workspace as (O, max, sum) and a second launch joins
+// them in a fixed order.
+//
+// Ten warps: warps 0-7 the softmax (a row per thread, warps w and w + 4 half of
+// a tile's tokens each, the row maximum exchanged through shared memory), warp
+// 8 fetches K and V rows by four-row TMA gathers into a ring of 32 KiB slots
+// (128 tokens x 128 dims, 128-byte swizzle), warp 9 issues the MMAs, S of the
+// next tile ahead of P V of this one.  The running maximum moves only when a
+// row's grows by more than 2^8, so O is rarely rescaled; what is left of the
+// softmax is one pass over registers.
+//
+// Decode (M = group rows of 128) is bound by HBM: the padded products take 2 x
+// 128 x 128 x head_dim x 2 flop a tile, under half the time its K and V take to
+// arrive.  Wide trees are bound by the products and the L2 reads of each
+// 128-row unit.
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
+#include "qsa_tc_cache.cuh"
+#include "qsa_tma.h"
 
 namespace qsa {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kTrWarps = 10, kTrThreads = 32 * kTrWarps;
+constexpr int kTrSoft = 8;     // softmax warps
+constexpr int kTrTile = 128;   // tokens per tile
+constexpr int kTrMaxCtas = 160;
+constexpr uint32_t kTrBox = kTrTile * 64 * 2;  // 64 dims of a tile: 16 KiB
+constexpr uint32_t kTrSlot = 2 * kTrBox;       // a ring slot: 128 dims
+constexpr float kTrSlack = 8.0f;               // log2 units a maximum may grow before O moves
+constexpr long long kTrSpinLimit = 4000000000LL;
 
 template <int HD>
-__global__ void __launch_bounds__(32 * kWarps) tree_attn_kernel(const TreeArgs a) {
-  constexpr int kE = HD / 32;
-  __shared__ float acc_s[kWarps][HD], m_s[kWarps], l_s[kWarps];
-  grid_dependency_sync();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t row = blockIdx.x / a.nq, h = blockIdx.x % a.nq;
-  const int32_t s = seq_of_row(a.seqs, row);
-  const SeqView v = view_seq(a.seqs, s);
-  if (!v.ok) {
-    if (threadIdx.x == 0) report_error(a.status, kErrRowRange, s);
-    return;
-  }
-  if (row < v.row0 || row >= v.row0 + v.rows) return;
-  const int32_t j = row - v.row0, kvh = h / a.group;
-  const uint32_t *mrow = a.seqs.mask ? a.seqs.mask + (int64_t)row * a.seqs.mask_words : nullptr;
-  float q[kE], acc[kE], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < kE; ++e) {
-    q[e] = bf16_to_f32(a.q[(int64_t)row * a.q_stride + (int64_t)h * HD + lane * kE + e]);
-    acc[e] = 0.f;
-  }
-  for (int32_t t = warp; t < v.ctx + v.rows; t += kWarps) {
-    if (t >= v.ctx && !sees_draft(mrow, j, t - v.ctx)) continue;
-    const int64_t slot = token_slot(a.seqs, s, t);
-    if (slot < 0) {
-      if (lane == 0) report_error(a.status, kErrTokenRange, s);
-      continue;
+struct TreeGeom {
+  static constexpr int kC = HD / 128;                   // ring slots per tile of K (or V)
+  static constexpr int kSlots = HD == 256 ? 5 : 6;
+  static constexpr uint32_t kQBytes = (HD / 64) * kTrBox;
+  static constexpr uint32_t kRingOff = kQBytes;
+  static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kTrSlot;
+  static constexpr uint32_t kSCol = HD;                 // O in columns 0..HD-1, then two S buffers
+};
+
+struct TreeCtrl {
+  float xch[2][2][kTrTile];  // [exchange parity][half][row]
+  uint64_t full[6], empty[6];
+  uint64_t s_full[2], p_ready[2];
+  uint64_t pv_done[2];       // by tile parity
+  uint64_t q_full, drain;
+  int64_t scan[kTrWarps], found_off;
+  int32_t found_seq, bad[2], abort, issued;
+  uint32_t tmem_base;
+};
+template <int HD>
+constexpr size_t tree_smem() { return TreeGeom<HD>::kCtrlOff + sizeof(TreeCtrl); }
+static_assert(tree_smem<256>() <= 232448 && tree_smem<128>() <= 232448, "227 KiB per CTA");
+
+// kind::f16, D f32, A and B bf16, M = 128, N = 128; K-major B (S), MN-major B (P V)
+constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescO = kIdescS | (1u << 16);
+
+// What the plan below needs of a sequence.
+struct SeqTiles {
+  SeqView v;
+  int32_t tiles, m_tiles;
+  int64_t count;  // tiles of all its units
+};
+
+__device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs &a, int32_t s) {
+  SeqTiles q;
+  q.v = view_seq(a.seqs, s);
+  q.tiles = q.v.rows > 0 ? (q.v.ctx + q.v.rows + kTrTile - 1) / kTrTile : 0;
+  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + kTrTile - 1) / kTrTile);
+  q.count = (int64_t)q.tiles * q.m_tiles * a.nkv;
+  return q;
+}
+
+// One CTA's part of one unit.
+struct TreeSeg {
+  int32_t s, kvh, mt;      // sequence, KV head, 128-row tile
+  int32_t t0, n;           // first tile, tiles to process
+  bool whole, head;        // the unit's every tile; the unit began in an earlier CTA
+  SeqView v;
+};
+
+// Walks a CTA's share of the tile list, unit by unit (each role its own walk).
+struct TreeWalk {
+  const TreeArgs &a;
+  int64_t left, off;
+  int32_t s;
+  SeqTiles q;
+  bool loaded;
+  __device__ TreeWalk(const TreeArgs &a_, int32_t s_, int64_t off_, int64_t left_)
+      : a(a_), left(left_), off(off_), s(s_), loaded(false) {}
+  __device__ bool next(TreeSeg &g) {
+    if (left <= 0) return false;
+    while (true) {
+      if (s >= a.seqs.n_seqs) return false;
+      if (!loaded) {
+        q = seq_tiles(a, s);
+        loaded = true;
+      }
+      if (off < q.count) break;
+      off -= q.count;
+      ++s;
+      loaded = false;
     }
-    const int64_t at = (slot * a.nkv + kvh) * HD + lane * kE;
-    float d = 0.f;
-    for (int e = 0; e < kE; ++e) d = fmaf(q[e], bf16_to_f32(a.k_pool[at + e]), d);
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    const float x = d * a.scale_log2;
-    const float m1 = fmaxf(m, x), use = m1 == -INFINITY ? 0.f : m1;
-    const float keep = exp2f(m - use), p = exp2f(x - use);
-    m = m1;
-    l = fmaf(l, keep, p);
-    for (int e = 0; e < kE; ++e) acc[e] = fmaf(acc[e], keep, p * bf16_to_f32(a.v_pool[at + e]));
+    const int64_t unit = off / q.tiles;
+    g.t0 = (int32_t)(off - unit * q.tiles);
+    const int32_t take = (int32_t)min((int64_t)(q.tiles - g.t0), left);
+    off += take;
+    left -= take;
+    g.s = s;
+    g.kvh = (int32_t)(unit / q.m_tiles);
+    g.mt = (int32_t)(unit - (int64_t)g.kvh * q.m_tiles);
+    g.v = q.v;
+    g.whole = take == q.tiles;
+    g.head = g.t0 > 0;
+    g.n = take;
+    if (a.seqs.mask == nullptr) {  // no row of this tile sees past its last row's own token
+      const int64_t m_end = min((int64_t)(g.mt + 1) * kTrTile, (int64_t)q.v.rows * a.group);
+      const int32_t end = (q.v.ctx + (int32_t)((m_end - 1) / a.group) + kTrTile) / kTrTile;
+      g.n = max(0, min(take, end - g.t0));
+    }
+    return true;
   }
-  for (int e = 0; e < kE; ++e) acc_s[warp][lane * kE + e] = acc[e];
-  if (lane == 0) {
-    m_s[warp] = m;
-    l_s[warp] = l;
+};
+
+// Ring position (in tiles of K or V) of tile j's K and V among a segment's n
+// tiles: K0, K1, V0, K2, V1, ..., V(n-1), the order the MMAs take them in.
+__device__ __forceinline__ int v_pos(int j, int n) { return j + 1 < n ? 2 + 2 * j : 2 * n - 1; }
+
+__device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+
+template <int HD>
+__global__ void __launch_bounds__(kTrThreads, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const TreeArgs a, const FastDiv group_div, int32_t part_rows, uint32_t q_and,
+                 uint32_t q_xor, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml,
+                 float *__restrict__ part_o) {
+  using G = TreeGeom<HD>;
+  extern __shared__ __align__(1024) uint8_t tr_smem[];
+  TreeCtrl &C = *reinterpret_cast<TreeCtrl *>(tr_smem + G::kCtrlOff);
+  const uint32_t sQ = sm32(tr_smem), sRing = sm32(tr_smem + G::kRingOff);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long lim = a.wait_limit > 0 ? a.wait_limit : kTrSpinLimit;
+  volatile int32_t *abort_flag = &C.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < G::kSlots; ++i) {
+      mbar_init(sm32(&C.full[i]), 1);
+      mbar_init(sm32(&C.empty[i]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(sm32(&C.s_full[b]), 1);
+      mbar_init(sm32(&C.p_ready[b]), kTrSoft);
+      mbar_init(sm32(&C.pv_done[b]), 1);
+      C.bad[b] = 0;
+    }
+    mbar_init(sm32(&C.q_full), kTrSoft);
+    mbar_init(sm32(&C.drain), 1);
+    C.abort = 0;
+    C.issued = 0;
+    C.found_seq = a.seqs.n_seqs;
+    C.found_off = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   __syncthreads();
-  float top = -INFINITY, total = 0.f, w[kWarps];
-  for (int i = 0; i < kWarps; ++i) top = fmaxf(top, m_s[i]);
-  for (int i = 0; i < kWarps; ++i) {
-    w[i] = exp2f(m_s[i] - (top == -INFINITY ? 0.f : top));
-    total = fmaf(l_s[i], w[i], total);
+  grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     sm32(&C.tmem_base)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  for (int d = threadIdx.x; d < HD; d += 32 * kWarps) {
-    float o = 0.f;
-    for (int i = 0; i < kWarps; ++i) o = fmaf(acc_s[i][d], w[i], o);
-    a.out[(int64_t)row * a.out_stride + (int64_t)h * HD + d] = (uint16_t)f32_to_bf16(o * inv);
+
+  // ---- the plan: every sequence's tiles summed, then the sequence this CTA's
+  // share starts in (CTA 0 also leaves the sums for the joining launch)
+  int64_t total = 0;
+  for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles(a, s).count;
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) C.scan[warp] = total;
+  __syncthreads();
+  total = 0;
+  for (int i = 0; i < kTrWarps; ++i) total += C.scan[i];
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t w0 = per * blockIdx.x, share = max((int64_t)0, min(per, total - w0));
+  int64_t before = 0;
+  for (int32_t s0 = 0; s0 < a.seqs.n_seqs && (blockIdx.x == 0 || (share > 0 && before <= w0)); s0 += kTrThreads) {
+    const int32_t s = s0 + tid;
+    int64_t count = 0;
+    if (s < a.seqs.n_seqs) {
+      const SeqTiles q = seq_tiles(a, s);
+      count = q.count;
+      if (blockIdx.x == 0 && !q.v.ok) report_error(a.status, kErrRowRange, s);
+    }
+    int64_t incl = count;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) C.scan[warp] = incl;
+    __syncthreads();
+    int64_t at = before + incl - count;
+    for (int i = 0; i < kTrWarps; ++i) {
+      at += i < warp ? C.scan[i] : 0;
+      before += C.scan[i];
+    }
+    if (s < a.seqs.n_seqs && blockIdx.x == 0) base_out[s] = at;
+    if (count > 0 && at <= w0 && w0 < at + count) {
+      C.found_seq = s;
+      C.found_off = w0 - at;
+    }
   }
-  if (threadIdx.x == 0 && a.lse)
-    a.lse[(int64_t)row * a.nq + h] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+  if (blockIdx.x == 0 && tid == 0) base_out[a.seqs.n_seqs] = total;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = C.tmem_base;
+  const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
+  TreeWalk walk(a, C.found_seq, C.found_off, laid_out ? share : 0);
+  TreeSeg g;
+
+  if (warp == 8) {
+    // ---- producer: lane l brings tokens 4l .. 4l+3 of each tile
+    uint32_t ns = 0;  // slots filled
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const int32_t kv = g.v.ctx + g.v.rows;
+      int32_t y[3][4];  // pool rows of tiles j, j + 1, j + 2
+      auto fetch = [&](int j, int32_t (&r)[4]) {
+        if (j >= g.n) return;
+        const int32_t t0 = (g.t0 + j) * kTrTile;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t t = t0 + 4 * lane + i;
+          r[i] = -1;  // outside the pool's rows: the copy fills in zeros
+          if (t < kv) {
+            const int64_t slot = token_slot(a.seqs, g.s, t);
+            if (slot >= 0) r[i] = (int32_t)(slot * a.nkv + g.kvh);
+            else bad = true;
+          }
+        }
+        if (bad) report_error(a.status, kErrTokenRange, g.s);
+      };
+      auto bring = [&](const CUtensorMap *map, const int32_t (&r)[4]) {
+#pragma unroll
+        for (int c = 0; c < G::kC; ++c) {
+          const uint32_t slot = ns % G::kSlots;
+          if (!tc_warp_wait(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
+            ok = false;
+            return;
+          }
+          const uint32_t fb = sm32(&C.full[slot]);
+          if (lane == 0) mbar_expect_tx(fb, kTrSlot);
+          __syncwarp();
+          const uint32_t dst = sRing + slot * kTrSlot + (uint32_t)lane * 512u;
+          tma_gather4(dst, map, c * 128, r[0], r[1], r[2], r[3], fb);
+          tma_gather4(dst + kTrBox, map, c * 128 + 64, r[0], r[1], r[2], r[3], fb);
+          ++ns;
+        }
+      };
+      if (g.n > 0) {
+        fetch(0, y[0]);
+        fetch(1, y[1]);
+        bring(&kmap, y[0]);
+        for (int j = 0; j < g.n && ok; ++j) {
+          fetch(j + 2, y[2]);
+          if (j + 1 < g.n) bring(&kmap, y[1]);
+          if (ok) bring(&vmap, y[0]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[0][i] = y[1][i];
+            y[1][i] = y[2][i];
+          }
+        }
+      }
+    }
+    if (lane == 0) C.issued = (int32_t)ns;
+  } else if (warp == 9) {
+    // ---- MMA issuer
+    if (lane == 0) {
+      uint32_t ns = 0, jg = 0, nq = 0;
+      bool ok = true;
+      auto take = [&]() -> uint32_t {  // the next slot's address, its copies landed
+        const uint32_t slot = ns % G::kSlots;
+        ok = ok && tc_wait(sm32(&C.full[slot]), (ns / G::kSlots) & 1u, lim, abort_flag);
+        return sRing + slot * kTrSlot;
+      };
+      auto release = [&]() {
+        mma_commit(sm32(&C.empty[ns % G::kSlots]));
+        ++ns;
+      };
+      auto scores = [&](uint32_t jj) {  // S of tile jj into its buffer
+        const uint32_t d = tmem + G::kSCol + (jj & 1u) * kTrTile;
+        for (int c = 0; c < G::kC && ok; ++c) {
+          const uint32_t kb = take();
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t in = (uint32_t)(kk >> 2) * kTrBox + (uint32_t)(kk & 3) * 32u;
+            mma_bf16(d, sw128_desc(sQ + (uint32_t)c * 2u * kTrBox + in), sw128_desc(kb + in), kIdescS,
+                     (c > 0 || kk > 0) ? 1u : 0u);
+          }
+          release();
+        }
+        mma_commit(sm32(&C.s_full[jj & 1u]));
+      };
+      while (ok && walk.next(g)) {
+        if (g.n == 0) continue;
+        ok = tc_wait(sm32(&C.q_full), nq & 1u, lim, abort_flag);
+        ++nq;
+        if (!ok) break;
+        tc_fence_after();
+        scores(jg);
+        for (int j = 0; j < g.n && ok; ++j, ++jg) {
+          if (j + 1 < g.n) scores(jg + 1);
+          if (!ok) break;
+          const uint32_t b = jg & 1u;
+          ok = tc_wait(sm32(&C.p_ready[b]), (jg >> 1) & 1u, lim, abort_flag);
+          if (!ok) break;
+          for (int c = 0; c < G::kC && ok; ++c) {
+            const uint32_t vb = take();
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
+              mma_bf16_ts(tmem + (uint32_t)c * 128u, tmem + G::kSCol + b * kTrTile + 8u * kk,
+                          sw128_mn_desc(vb + 2048u * kk, kTrBox), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+            release();
+          }
+          mma_commit(sm32(&C.pv_done[b]));
+        }
+      }
+      // every MMA this thread issued has finished before TMEM is freed
+      mma_commit(sm32(&C.drain));
+      tc_wait(sm32(&C.drain), 0u, kTrSpinLimit, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = TMEM lane (row) r, half h of the tile's tokens and
+    // of the output's dims.  After an abort every wait returns at once, and the
+    // loops and the pairs' barriers run on to the end.
+    const int h = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t xn = 0;
+    auto exchange = [&](float x) -> float {  // the other half's value of this row
+      float(&x2)[2][kTrTile] = C.xch[xn++ & 1u];
+      x2[h][r] = x;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+      return x2[h ^ 1][r];
+    };
+    // P V of tile i, the last or the last but one issued: the barrier of its
+    // parity cannot be further behind, for S of tile i + 1 (or i) being done tells
+    // that P V of tile i - 2 is.
+    auto wait_pv = [&](uint32_t i) {
+      tc_warp_wait(sm32(&C.pv_done[i & 1u]), (i >> 1) & 1u, lim, abort_flag);
+    };
+    auto load_q = [&](const TreeSeg &e) {
+      const int64_t m0 = (int64_t)e.mt * kTrTile;
+      const int rows = (int)min((int64_t)kTrTile, (int64_t)e.v.rows * a.group - m0);
+      constexpr int kCh = HD / 8;          // 16-byte chunks per row
+      constexpr int kPer = 32 / kCh;       // rows per warp load (2 at head_dim 128... 1)
+      constexpr int kStep = kPer * kTrSoft;
+      const int ch = lane % kCh, sub = lane / kCh;
+      for (int r0 = warp * kPer + sub; r0 < rows; r0 += 4 * kStep) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = r0 + i * kStep;
+          if (rr < rows) {
+            const int32_t m = (int32_t)(m0 + rr), j = fast_div(group_div, m);
+            const int32_t head = e.kvh * a.group + (m - j * a.group);
+            x[i] = ldg_nc_v4(a.q + (int64_t)(e.v.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = r0 + i * kStep;
+          if (rr < rows) {
+            uint4 v = x[i];
+            v.x = (v.x & q_and) ^ q_xor;
+            v.y = (v.y & q_and) ^ q_xor;
+            v.z = (v.z & q_and) ^ q_xor;
+            v.w = (v.w & q_and) ^ q_xor;
+            *reinterpret_cast<uint4 *>(tr_smem + (ch >> 3) * kTrBox + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm32(&C.q_full));
+    };
+    uint32_t jg = 0, ns = 0;
+    int32_t seg = 0;
+    bool more = walk.next(g);
+    if (more && g.n > 0) load_q(g);
+    while (more) {
+      ++seg;
+      const int64_t m = (int64_t)g.mt * kTrTile + r;
+      const bool valid = m < (int64_t)g.v.rows * a.group;
+      const bool live = __any_sync(0xffffffffu, valid);  // this warp (and its pair) has rows
+      const int32_t j_row = valid ? fast_div(group_div, (int32_t)m) : 0;
+      const int32_t row = g.v.row0 + j_row;
+      const int32_t head = g.kvh * a.group + (valid ? (int32_t)m - j_row * a.group : 0);
+      const uint32_t *mrow = a.seqs.mask ? a.seqs.mask + (int64_t)row * a.seqs.mask_words : nullptr;
+      // whether a row may be blind to a token that another one sees
+      const bool veiled = g.v.rows > 1 || a.seqs.mask != nullptr;
+      float top = -INFINITY, sum = 0.f;
+      for (int j = 0; j < g.n; ++j, ++jg) {
+        const uint32_t b = jg & 1u;
+        const int32_t t0 = (g.t0 + j) * kTrTile;
+        const bool masked = t0 + kTrTile > g.v.ctx;
+        tc_warp_wait(sm32(&C.s_full[b]), (jg >> 1) & 1u, lim, abort_flag);
+        tc_fence_after();
+        if (live) {
+          uint32_t sv[64];
+          const uint32_t sc = lane_base + G::kSCol + b * kTrTile;
+          tmem_ld32(sc + 64u * h, sv);
+          tmem_ld32(sc + 64u * h + 32u, sv + 32);
+          tmem_wait_ld32(sv);
+          tmem_wait_ld32(sv + 32);
+          if (masked) {
+            const uint64_t see = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 + 64 * h - g.v.ctx);
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (!((see >> i) & 1ull)) sv[i] = 0xFF800000u;  // -inf
+          }
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(sv[i]);
+#pragma unroll
+          for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sv[i]));
+          float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          mine = fmaxf(mine, exchange(mine));
+          const float want = mine == -INFINITY ? -INFINITY : mine * a.scale_log2;
+          const bool move = valid && (want > top + kTrSlack || (top == -INFINITY && want != -INFINITY));
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? (top == -INFINITY ? 0.f : ex2(top - want)) : 1.f;
+            if (move) top = want;
+            sum *= alpha;
+            if (j > 0) {  // O holds the earlier tiles of this part
+              wait_pv(jg - 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < HD / 64; ++c) {
+                uint32_t o[32];
+                const uint32_t oc = lane_base + (uint32_t)(h * (HD / 2) + c * 32);
+                tmem_ld32(oc, o);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st32(oc, o);
+              }
+            }
+          }
+          const float use = top == -INFINITY ? 0.f : top;
+          const uint64_t c2 = pair_f32(a.scale_log2, a.scale_log2), m2 = pair_f32(-use, -use);
+          uint64_t part[2] = {0ull, 0ull};
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float lo, hi;
+            unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, m2), lo, hi);
+            lo = ex2(lo);
+            hi = ex2(hi);
+            part[i & 1] = add2(part[i & 1], pair_f32(lo, hi));
+            p[i] = pack_f32_bf16(lo, hi);
+          }
+          float s0, s1;
+          unpair_f32(add2(part[0], part[1]), s0, s1);
+          sum += s0 + s1;
+          tmem_st32(sc + 32u * h, p);
+          tmem_wait_st();
+        }
+        if (masked && veiled) {
+          // A value that is not finite would reach, as 0 x inf, the rows that do
+          // not see its token: it is cleared here and given to the rows that do
+          // see it when the output is written.
+          // (P V of the tile before is done, so each of V's slots has had its
+          // earlier copy: a parity alone could not tell)
+          if (jg > 0) wait_pv(jg - 1);
+          const uint32_t at = ns + (uint32_t)(v_pos(j, g.n) * G::kC);
+          for (int c = 0; c < G::kC; ++c) {
+            const uint32_t slot = (at + c) % G::kSlots;
+            tc_warp_wait(sm32(&C.full[slot]), ((at + c) / G::kSlots) & 1u, lim, abort_flag);
+            __syncwarp();
+            uint8_t *vs = tr_smem + G::kRingOff + slot * kTrSlot;
+            for (int i = warp * 32 + lane; i < (int)(kTrSlot / 16); i += 32 * kTrSoft) {
+              uint4 *w = reinterpret_cast<uint4 *>(vs) + i;
+              const uint4 x = *w;
+              uint32_t e[4] = {x.x, x.y, x.z, x.w};
+              bool hit = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (nonfinite16(e[k])) { e[k] &= 0xFFFF0000u; hit = true; }
+                if (nonfinite16(e[k] >> 16)) { e[k] &= 0xFFFFu; hit = true; }
+              }
+              if (hit) {
+                *w = make_uint4(e[0], e[1], e[2], e[3]);
+                *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) = seg;
+              }
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm32(&C.p_ready[b]));
+      }
+      ns += (uint32_t)(2 * g.n * G::kC);
+      TreeSeg next;
+      more = walk.next(next);
+      if (more && next.n > 0) load_q(next);  // every S of this part is done
+      if (g.n > 0) {
+        wait_pv(jg - 1);
+        tc_fence_after();
+      }
+      if (live) {
+        const float all = sum + exchange(sum);
+        const float inv = all == 0.f ? 0.f : 1.f / all;
+        const bool fix = *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) == seg;
+        const int64_t part = (int64_t)blockIdx.x * 2 + (g.head ? 0 : 1);
+        if (valid && h == 0) {
+          if (!g.whole) part_ml[part * part_rows + r] = make_float2(top, all);
+          else if (a.lse) a.lse[(int64_t)row * a.nq + head] =
+              all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+        }
+#pragma unroll 1
+        for (int c = 0; c < HD / 64; ++c) {
+          const int d0 = h * (HD / 2) + c * 32;
+          uint32_t o[32];
+          if (g.n > 0) {
+            tmem_ld32(lane_base + (uint32_t)d0, o);
+            tmem_wait_ld32(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (!valid) continue;
+          if (fix) {
+            // every token of the tiles that were cleared
+            const int32_t t_lo = max(g.t0, g.v.ctx / kTrTile) * kTrTile;
+            const int32_t t_hi = min(g.v.ctx + g.v.rows, (g.t0 + g.n) * kTrTile);
+            for (int32_t t = t_lo; t < t_hi; ++t) {
+              if (t >= g.v.ctx && !sees_draft(mrow, j_row, t - g.v.ctx)) continue;
+              const int64_t slot = token_slot(a.seqs, g.s, t);
+              if (slot < 0) continue;
+              const uint16_t *v = a.v_pool + (slot * a.nkv + g.kvh) * HD + d0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (nonfinite16(v[i])) o[i] = __float_as_uint(__uint_as_float(o[i]) + bf16_to_f32(v[i]));
+            }
+          }
+          if (g.whole) {
+            uint16_t *dst = a.out + (int64_t)row * a.out_stride + (int64_t)head * HD + d0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_f32_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+              reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float *dst = part_o + (part * part_rows + r) * HD + d0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4 *>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        tc_fence_before();
+      }
+      g = next;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && (C.abort || !laid_out)) {
+    // the copies issued land before the CTA's shared memory is released
+    for (int k = max(0, C.issued - G::kSlots); k < C.issued; ++k)
+      tc_wait(sm32(&C.full[k % G::kSlots]), (uint32_t)(k / G::kSlots) & 1u, kTrSpinLimit, nullptr);
+    report_error(a.status, kErrTimeout, C.found_seq);
+  }
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// Joins the parts of the units that several CTAs share: one warp per (row, query
+// head), every part's maximum and sum first, then its share of O in CTA order.
+constexpr int kJoinWarps = 4;
+
+template <int HD>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+tree_join_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, int32_t ctas,
+                 const int64_t *__restrict__ base, const float2 *__restrict__ part_ml,
+                 const float *__restrict__ part_o) {
+  grid_dependency_sync();
+  const int lane = threadIdx.x & 31;
+  const int64_t at = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (at >= (int64_t)a.seqs.n_rows * a.nq) return;
+  const int32_t row = (int32_t)(at / a.nq), head = (int32_t)(at - (int64_t)row * a.nq);
+  const int32_t s = seq_of_row(a.seqs, row);
+  const SeqTiles q = seq_tiles(a, s);
+  if (row < q.v.row0 || row >= q.v.row0 + q.v.rows) return;
+  const int32_t kvh = fast_div(group_div, head);
+  const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
+  const int32_t mt = (int32_t)(m / kTrTile), r = (int32_t)(m % kTrTile);
+  const int64_t per = (base[a.seqs.n_seqs] + ctas - 1) / ctas;
+  const int64_t u0 = base[s] + ((int64_t)kvh * q.m_tiles + mt) * q.tiles;
+  const int32_t c0 = (int32_t)(u0 / per), c1 = (int32_t)((u0 + q.tiles - 1) / per);
+  if (c0 == c1) return;
+  auto slot = [&](int32_t c) { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_rows + r; };
+  float top = -INFINITY;
+  for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_ml[slot(c)].x);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float use = top == -INFINITY ? 0.f : top;
+  constexpr int kE = HD / 128;  // float4s per lane
+  float4 acc[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float all = 0.f;
+#pragma unroll 4
+  for (int32_t c = c0; c <= c1; ++c) {
+    const float2 ml = part_ml[slot(c)];
+    const float w = ex2(ml.x - use);
+    all = fmaf(ml.y, w, all);
+    const float4 *o = reinterpret_cast<const float4 *>(part_o + slot(c) * HD);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const float4 x = o[e * 32 + lane];
+      acc[e].x = fmaf(x.x, w, acc[e].x);
+      acc[e].y = fmaf(x.y, w, acc[e].y);
+      acc[e].z = fmaf(x.z, w, acc[e].z);
+      acc[e].w = fmaf(x.w, w, acc[e].w);
+    }
+  }
+  const float inv = all == 0.f ? 0.f : 1.f / all;
+  uint16_t *dst = a.out + (int64_t)row * a.out_stride + (int64_t)head * HD;
+#pragma unroll
+  for (int e = 0; e < kE; ++e)
+    reinterpret_cast<uint2 *>(dst)[e * 32 + lane] =
+        make_uint2(pack_f32_bf16(acc[e].x * inv, acc[e].y * inv), pack_f32_bf16(acc[e].z * inv, acc[e].w * inv));
+  if (lane == 0 && a.lse)
+    a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+}
+
+// The workspace: the sequences' first tiles, then the parts' (max, sum) and O.
+int32_t part_rows_of(int64_t n_rows, int32_t group) {
+  return (int32_t)(n_rows * group < kTrTile ? n_rows * group : kTrTile);
+}
+int64_t base_bytes(int32_t n_seqs) { return ((int64_t)(n_seqs + 1) * 8 + 255) / 256 * 256; }
+int64_t ml_bytes(int32_t part_rows) { return ((int64_t)kTrMaxCtas * 2 * part_rows * 8 + 255) / 256 * 256; }
+
+template <int HD>
+cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
+  static PerDevice smem_attr;
+  const cudaError_t e = set_smem_once(smem_attr, tree_attn_kernel<HD>, tree_smem<HD>());
+  if (e != cudaSuccess) return e;
+  TreeArgs a = args;
+  // the kernel takes scale > 0: a negative one turns q's signs, a zero one clears q
+  uint32_t q_and = 0xFFFFFFFFu, q_xor = 0u;
+  if (a.scale_log2 < 0.f) {
+    a.scale_log2 = -a.scale_log2;
+    q_xor = 0x80008000u;
+  } else if (a.scale_log2 == 0.f) {
+    a.scale_log2 = 1.f;
+    q_and = 0u;
+  }
+  CUtensorMap kmap, vmap;
+  const uint64_t rows = (uint64_t)a.seqs.pool_pages * a.seqs.page.d * a.nkv;
+  if (!encode_bf16_sw128(&kmap, a.k_pool, HD, rows, HD, 64, 1) || !encode_bf16_sw128(&vmap, a.v_pool, HD, rows, HD, 64, 1))
+    return cudaErrorInvalidValue;
+  const int32_t part_rows = part_rows_of(a.seqs.n_rows, a.group);
+  uint8_t *ws = static_cast<uint8_t *>(a.ws);
+  int64_t *base = reinterpret_cast<int64_t *>(ws);
+  float2 *ml = reinterpret_cast<float2 *>(ws + base_bytes(a.seqs.n_seqs));
+  float *o = reinterpret_cast<float *>(ws + base_bytes(a.seqs.n_seqs) + ml_bytes(part_rows));
+  const int ctas = device_sm_count() < kTrMaxCtas ? device_sm_count() : kTrMaxCtas;
+  const FastDiv group_div = make_fast_div(a.group);
+  cudaError_t r = launch_dependent(tree_attn_kernel<HD>, dim3((unsigned)ctas), dim3(kTrThreads), tree_smem<HD>(), stream, 1u,
+                                   kmap, vmap, a, group_div, part_rows, q_and, q_xor, base, ml, o);
+  // a table of one tile leaves no unit to share
+  if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kTrTile) return r;
+  const int64_t warps = (int64_t)a.seqs.n_rows * a.nq;
+  return launch_dependent(tree_join_kernel<HD>, dim3((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)),
+                          dim3(32 * kJoinWarps), 0, stream, 1u, a, group_div, part_rows, (int32_t)ctas, base, ml, o);
 }
 
 }  // namespace
 
 int64_t tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t group, int32_t head_dim) {
-  constexpr int64_t kCtas = 160;
-  const int64_t rows = (int64_t)n_rows * group < 128 ? (int64_t)n_rows * group : 128;
-  return ((int64_t)(n_seqs + 1) * 8 + 255) / 256 * 256 + kCtas * 2 * rows * (head_dim + 2) * 4;
+  const int32_t rows = part_rows_of(n_rows, group);
+  return base_bytes(n_seqs) + ml_bytes(rows) + (int64_t)kTrMaxCtas * 2 * rows * head_dim * 4;
 }
 
 cudaError_t launch_tree_attn(const TreeArgs &a, int32_t head_dim, cudaStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)a.seqs.n_rows * a.nq));
-  if (head_dim == 256)
-    return launch_dependent(tree_attn_kernel<256>, grid, dim3(32 * kWarps), 0, stream, 1u, a);
-  return launch_dependent(tree_attn_kernel<128>, grid, dim3(32 * kWarps), 0, stream, 1u, a);
+  return head_dim == 256 ? launch_hd<256>(a, stream) : launch_hd<128>(a, stream);
 }
 
 }  // namespace qsa
