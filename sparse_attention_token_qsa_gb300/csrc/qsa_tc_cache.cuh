@@ -1,22 +1,20 @@
 // Device helpers that the tcgen05 kernels over a paged cache share, beside
-// qsa_tc_device.cuh: the four-row TMA gather, wide TMEM loads and stores, the MMA
-// whose A operand lies in TMEM, the MN-major descriptor, and packed f32 pairs.
+// qsa_tc_device.cuh: the 16-byte copy, wide TMEM loads and stores, the MMA whose
+// A operand lies in TMEM, the MN-major descriptor, and packed f32 pairs.
 #pragma once
 
 #include "qsa_tc_device.cuh"
 
 namespace qsa {
 
-// Four rows (y) of 64 bf16 columns from x on, one below the other: 512 bytes.
-// The 128-byte swizzle follows the shared-memory address, so a destination may
-// be any 512-byte piece of a 1024-byte swizzle atom.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int x, int y0,
-                                            int y1, int y2, int y3, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(mbar)
-      : "memory");
+// 16 bytes from global to shared memory, asynchronously; bytes 0: zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Arrives on the barrier once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t mbar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
 // Shared-memory matrix descriptor of an MN-major operand in 128-byte swizzle:
@@ -69,16 +67,26 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t *v) {
   asm volatile("" : "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
+// ... 16 columns, completed.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[15])
       : "memory");
 }
 

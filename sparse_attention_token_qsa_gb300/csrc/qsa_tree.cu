@@ -16,11 +16,14 @@
 // of any other go to the workspace as (O, max, sum) and a second launch joins
 // them in a fixed order.
 //
-// Ten warps: warps 0-7 the softmax (a row per thread, warps w and w + 4 half of
-// a tile's tokens each, the row maximum exchanged through shared memory), warp
-// 8 fetches K and V rows by four-row TMA gathers into a ring of 32 KiB slots
-// (128 tokens x 128 dims, 128-byte swizzle), warp 9 issues the MMAs, S of the
-// next tile ahead of P V of this one.  The running maximum moves only when a
+// Thirteen warps: warps 0-7 the softmax (a row per thread, warps w and w + 4 half
+// of a tile's tokens each, the row maximum exchanged through shared memory),
+// warps 8-11 copy K and V rows into a ring of 32 KiB slots (128 tokens x 128
+// dims, 128-byte swizzle), warp 12 issues the MMAs, S of the next tile ahead of
+// P V of this one.  The copies are 16-byte cp.async, which take any page size
+// alike: streaming tiles of pages of 16 tokens and nothing else, they moved 9.7
+// TB/s out of L2 and 5.7 TB/s out of HBM, four-row TMA gathers 5.7 and 4.8, TMA
+// boxes of a page 5.5 and 4.6.  The running maximum moves only when a
 // row's grows by more than 2^8, so O is rarely rescaled; what is left of the
 // softmax is one pass over registers.
 //
@@ -31,14 +34,15 @@
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"
-#include "qsa_tma.h"
 
 namespace qsa {
 
 namespace {
 
-constexpr int kTrWarps = 10, kTrThreads = 32 * kTrWarps;
 constexpr int kTrSoft = 8;     // softmax warps
+constexpr int kTrProd = 4;     // producer warps
+constexpr int kTrMma = kTrSoft + kTrProd;  // the MMA warp
+constexpr int kTrWarps = kTrMma + 1, kTrThreads = 32 * kTrWarps;
 constexpr int kTrTile = 128;   // tokens per tile
 constexpr int kTrMaxCtas = 160;
 constexpr uint32_t kTrBox = kTrTile * 64 * 2;  // 64 dims of a tile: 16 KiB
@@ -63,7 +67,7 @@ struct TreeCtrl {
   uint64_t pv_done[2];       // by tile parity
   uint64_t q_full, drain;
   int64_t scan[kTrWarps], found_off;
-  int32_t found_seq, bad[2], abort, issued;
+  int32_t found_seq, bad[2], abort;
   uint32_t tmem_base;
 };
 template <int HD>
@@ -149,8 +153,7 @@ __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) =
 
 template <int HD>
 __global__ void __launch_bounds__(kTrThreads, 1)
-tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                 const TreeArgs a, const FastDiv group_div, int32_t part_rows, uint32_t q_and,
+tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, uint32_t q_and,
                  uint32_t q_xor, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml,
                  float *__restrict__ part_o) {
   using G = TreeGeom<HD>;
@@ -163,7 +166,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 
   if (tid == 0) {
     for (int i = 0; i < G::kSlots; ++i) {
-      mbar_init(sm32(&C.full[i]), 1);
+      mbar_init(sm32(&C.full[i]), 32 * kTrProd);
       mbar_init(sm32(&C.empty[i]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -175,16 +178,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     mbar_init(sm32(&C.q_full), kTrSoft);
     mbar_init(sm32(&C.drain), 1);
     C.abort = 0;
-    C.issued = 0;
     C.found_seq = a.seqs.n_seqs;
     C.found_off = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   __syncthreads();
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
-  if (warp == 9) {
+  if (warp == kTrMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      sm32(&C.tmem_base)),
                  "r"(512u)
@@ -240,30 +240,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   TreeWalk walk(a, C.found_seq, C.found_off, laid_out ? share : 0);
   TreeSeg g;
 
-  if (warp == 8) {
-    // ---- producer: lane l brings tokens 4l .. 4l+3 of each tile
-    uint32_t ns = 0;  // slots filled
+  if (warp >= kTrSoft && warp < kTrMma) {
+    // ---- producers: warp p brings tokens 32p .. 32p + 31 of each tile, two
+    // 256-byte rows an instruction; lane i looks up the pool row of token 32p + i.
+    // A slot's barrier takes each thread's arrival when its copies have landed, so
+    // the whole ring may be in flight.
+    const int p0 = (warp - kTrSoft) * 32, ch = lane & 15, hl = lane >> 4;
+    const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * kTrBox + (uint32_t)(p0 + hl) * 128u;
+    const uint32_t swz = (uint32_t)((ch & 7) ^ hl);
+    uint32_t ns = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
       const int32_t kv = g.v.ctx + g.v.rows;
-      int32_t y[3][4];  // pool rows of tiles j, j + 1, j + 2
-      auto fetch = [&](int j, int32_t (&r)[4]) {
-        if (j >= g.n) return;
-        const int32_t t0 = (g.t0 + j) * kTrTile;
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int32_t t = t0 + 4 * lane + i;
-          r[i] = -1;  // outside the pool's rows: the copy fills in zeros
-          if (t < kv) {
-            const int64_t slot = token_slot(a.seqs, g.s, t);
-            if (slot >= 0) r[i] = (int32_t)(slot * a.nkv + g.kvh);
-            else bad = true;
-          }
-        }
-        if (bad) report_error(a.status, kErrTokenRange, g.s);
+      auto fetch = [&](int j) -> int32_t {  // pool row of this lane's token of tile j, -1: zeros
+        const int32_t t = (g.t0 + j) * kTrTile + p0 + lane;
+        if (j >= g.n || t >= kv) return -1;
+        const int64_t slot = token_slot(a.seqs, g.s, t);
+        if (slot < 0) report_error(a.status, kErrTokenRange, g.s);
+        return slot < 0 ? -1 : (int32_t)(slot * a.nkv + g.kvh);
       };
-      auto bring = [&](const CUtensorMap *map, const int32_t (&r)[4]) {
+      auto bring = [&](const uint16_t *pool, int32_t y) {
 #pragma unroll
         for (int c = 0; c < G::kC; ++c) {
           const uint32_t slot = ns % G::kSlots;
@@ -271,33 +267,32 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             ok = false;
             return;
           }
-          const uint32_t fb = sm32(&C.full[slot]);
-          if (lane == 0) mbar_expect_tx(fb, kTrSlot);
-          __syncwarp();
-          const uint32_t dst = sRing + slot * kTrSlot + (uint32_t)lane * 512u;
-          tma_gather4(dst, map, c * 128, r[0], r[1], r[2], r[3], fb);
-          tma_gather4(dst + kTrBox, map, c * 128 + 64, r[0], r[1], r[2], r[3], fb);
+          const uint32_t dst = dst0 + slot * kTrSlot;
+          const uint16_t *src = pool + c * 128 + ch * 8;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {  // rows 2k, 2k + 1 of this warp's 32
+            const int32_t yr = __shfl_sync(0xffffffffu, y, 2 * k + hl);
+            cp_async16(dst + (uint32_t)k * 256u + ((swz ^ (uint32_t)(2 * (k & 3))) << 4),
+                       src + (int64_t)max(yr, 0) * HD, yr >= 0 ? 16u : 0u);
+          }
+          cp_async_arrive(sm32(&C.full[slot]));
           ++ns;
         }
       };
       if (g.n > 0) {
-        fetch(0, y[0]);
-        fetch(1, y[1]);
-        bring(&kmap, y[0]);
+        int32_t y0 = fetch(0), y1 = fetch(1);
+        bring(a.k_pool, y0);
         for (int j = 0; j < g.n && ok; ++j) {
-          fetch(j + 2, y[2]);
-          if (j + 1 < g.n) bring(&kmap, y[1]);
-          if (ok) bring(&vmap, y[0]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[0][i] = y[1][i];
-            y[1][i] = y[2][i];
-          }
+          const int32_t y2 = fetch(j + 2);
+          if (j + 1 < g.n) bring(a.k_pool, y1);
+          if (ok) bring(a.v_pool, y0);
+          y0 = y1;
+          y1 = y2;
         }
       }
     }
-    if (lane == 0) C.issued = (int32_t)ns;
-  } else if (warp == 9) {
+    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
+  } else if (warp == kTrMma) {
     // ---- MMA issuer
     if (lane == 0) {
       uint32_t ns = 0, jg = 0, nq = 0;
@@ -305,6 +300,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       auto take = [&]() -> uint32_t {  // the next slot's address, its copies landed
         const uint32_t slot = ns % G::kSlots;
         ok = ok && tc_wait(sm32(&C.full[slot]), (ns / G::kSlots) & 1u, lim, abort_flag);
+        // the copies wrote through the generic proxy; the MMAs read through the async one
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_after();
         return sRing + slot * kTrSlot;
       };
       auto release = [&]() {
@@ -316,7 +314,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         for (int c = 0; c < G::kC && ok; ++c) {
           const uint32_t kb = take();
           if (!ok) return;
-          tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t in = (uint32_t)(kk >> 2) * kTrBox + (uint32_t)(kk & 3) * 32u;
@@ -343,7 +340,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           for (int c = 0; c < G::kC && ok; ++c) {
             const uint32_t vb = take();
             if (!ok) break;
-            tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
               mma_bf16_ts(tmem + (uint32_t)c * 128u, tmem + G::kSCol + b * kTrTile + 8u * kk,
@@ -464,34 +460,37 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
               wait_pv(jg - 1);
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < HD / 64; ++c) {
-                uint32_t o[32];
-                const uint32_t oc = lane_base + (uint32_t)(h * (HD / 2) + c * 32);
-                tmem_ld32(oc, o);
-                tmem_wait_ld32(o);
+              for (int c = 0; c < HD / 32; ++c) {
+                uint32_t o[16];
+                const uint32_t oc = lane_base + (uint32_t)(h * (HD / 2) + c * 16);
+                tmem_ld16(oc, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st32(oc, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(oc, o);
               }
             }
           }
           const float use = top == -INFINITY ? 0.f : top;
           const uint64_t c2 = pair_f32(a.scale_log2, a.scale_log2), m2 = pair_f32(-use, -use);
           uint64_t part[2] = {0ull, 0ull};
-          uint32_t p[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float lo, hi;
-            unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, m2), lo, hi);
-            lo = ex2(lo);
-            hi = ex2(hi);
-            part[i & 1] = add2(part[i & 1], pair_f32(lo, hi));
-            p[i] = pack_f32_bf16(lo, hi);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float lo, hi;
+              unpair_f32(fma2(pair_f32(__uint_as_float(sv[32 * q + 2 * i]), __uint_as_float(sv[32 * q + 2 * i + 1])), c2, m2),
+                         lo, hi);
+              lo = ex2(lo);
+              hi = ex2(hi);
+              part[i & 1] = add2(part[i & 1], pair_f32(lo, hi));
+              p[i] = pack_f32_bf16(lo, hi);
+            }
+            tmem_st16(sc + 32u * h + 16u * q, p);
           }
           float s0, s1;
           unpair_f32(add2(part[0], part[1]), s0, s1);
           sum += s0 + s1;
-          tmem_st32(sc + 32u * h, p);
           tmem_wait_st();
         }
         if (masked && veiled) {
@@ -599,13 +598,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0 && (C.abort || !laid_out)) {
-    // the copies issued land before the CTA's shared memory is released
-    for (int k = max(0, C.issued - G::kSlots); k < C.issued; ++k)
-      tc_wait(sm32(&C.full[k % G::kSlots]), (uint32_t)(k / G::kSlots) & 1u, kTrSpinLimit, nullptr);
-    report_error(a.status, kErrTimeout, C.found_seq);
-  }
-  if (warp == 9)
+  if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, C.found_seq);
+  if (warp == kTrMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -690,10 +684,6 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
     a.scale_log2 = 1.f;
     q_and = 0u;
   }
-  CUtensorMap kmap, vmap;
-  const uint64_t rows = (uint64_t)a.seqs.pool_pages * a.seqs.page.d * a.nkv;
-  if (!encode_bf16_sw128(&kmap, a.k_pool, HD, rows, HD, 64, 1) || !encode_bf16_sw128(&vmap, a.v_pool, HD, rows, HD, 64, 1))
-    return cudaErrorInvalidValue;
   const int32_t part_rows = part_rows_of(a.seqs.n_rows, a.group);
   uint8_t *ws = static_cast<uint8_t *>(a.ws);
   int64_t *base = reinterpret_cast<int64_t *>(ws);
@@ -702,7 +692,7 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   const int ctas = device_sm_count() < kTrMaxCtas ? device_sm_count() : kTrMaxCtas;
   const FastDiv group_div = make_fast_div(a.group);
   cudaError_t r = launch_dependent(tree_attn_kernel<HD>, dim3((unsigned)ctas), dim3(kTrThreads), tree_smem<HD>(), stream, 1u,
-                                   kmap, vmap, a, group_div, part_rows, q_and, q_xor, base, ml, o);
+                                   a, group_div, part_rows, q_and, q_xor, base, ml, o);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kTrTile) return r;
   const int64_t warps = (int64_t)a.seqs.n_rows * a.nq;
