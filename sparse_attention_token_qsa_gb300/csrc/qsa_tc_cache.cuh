@@ -17,6 +17,29 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t mbar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t mb, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(mb), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// tc_wait and tc_warp_wait with the completed phase's case in line.
+__device__ __forceinline__ bool tc_wait_ready(uint32_t mb, uint32_t parity, long long limit,
+                                              volatile int32_t *abort_flag) {
+  return mbar_test(mb, parity) || tc_wait(mb, parity, limit, abort_flag);
+}
+__device__ __forceinline__ bool tc_warp_wait_ready(uint32_t mb, uint32_t parity, long long limit,
+                                                   volatile int32_t *abort_flag) {
+  return __all_sync(0xffffffffu, mbar_test(mb, parity)) || tc_warp_wait(mb, parity, limit, abort_flag);
+}
+
 // Shared-memory matrix descriptor of an MN-major operand in 128-byte swizzle:
 // 64 MN values a 128-byte row, K in groups of 8 rows 1024 bytes apart, the next
 // 64 MN values `mn_stride` bytes on.

@@ -16,11 +16,13 @@
 // of any other go to the workspace as (O, max, sum) and a second launch joins
 // them in a fixed order.
 //
-// Thirteen warps: warps 0-7 the softmax (a row per thread, warps w and w + 4 half
-// of a tile's tokens each, the row maximum exchanged through shared memory),
-// warps 8-11 copy K and V rows into a ring of 32 KiB slots (128 tokens x 128
-// dims, 128-byte swizzle), warp 12 issues the MMAs, S of the next tile ahead of
-// P V of this one.  The copies are 16-byte cp.async, which take any page size
+// Fourteen warps: two groups of four (warps 0-3 and 4-7) do the softmax, a row
+// per thread, tiles in turn; warps 8-11 copy K and V rows into a ring of 32 KiB
+// slots (128 tokens x 128 dims, 128-byte swizzle); warp 12 issues S, a tile
+// ahead, warp 13 P V, so that neither one's waits leave the tensor pipe idle.
+// The groups share a row's running maximum through shared memory: a group has
+// the other's before it takes its own exponentials, and its row sum relative to
+// the last maximum it used.  The copies are 16-byte cp.async, which take any page size
 // alike: streaming tiles of pages of 16 tokens and nothing else, they moved 9.7
 // TB/s out of L2 and 5.7 TB/s out of HBM, four-row TMA gathers 5.7 and 4.8, TMA
 // boxes of a page 5.5 and 4.6.  The running maximum moves only when a
@@ -41,12 +43,14 @@ namespace {
 
 constexpr int kTrSoft = 8;     // softmax warps
 constexpr int kTrProd = 4;     // producer warps
-constexpr int kTrMma = kTrSoft + kTrProd;  // the MMA warp
-constexpr int kTrWarps = kTrMma + 1, kTrThreads = 32 * kTrWarps;
+constexpr int kTrMmaS = kTrSoft + kTrProd;  // issues S = Q K^T
+constexpr int kTrMmaO = kTrMmaS + 1;        // issues O += P V
+constexpr int kTrWarps = kTrMmaO + 1, kTrThreads = 32 * kTrWarps;
 constexpr int kTrTile = 128;   // tokens per tile
 constexpr int kTrMaxCtas = 160;
 constexpr uint32_t kTrBox = kTrTile * 64 * 2;  // 64 dims of a tile: 16 KiB
 constexpr uint32_t kTrSlot = 2 * kTrBox;       // a ring slot: 128 dims
+constexpr uint32_t kPCol = 64;                 // P (64 columns) inside an S buffer
 constexpr float kTrSlack = 8.0f;               // log2 units a maximum may grow before O moves
 constexpr long long kTrSpinLimit = 4000000000LL;
 
@@ -61,11 +65,12 @@ struct TreeGeom {
 };
 
 struct TreeCtrl {
-  float xch[2][2][kTrTile];  // [exchange parity][half][row]
+  float top[2][kTrTile];     // [group that wrote it][row]: the running maximum, log2 units
+  float sums[2][kTrTile];    // [group][row]: its share of the row's sum
   uint64_t full[6], empty[6];
   uint64_t s_full[2], p_ready[2];
   uint64_t pv_done[2];       // by tile parity
-  uint64_t q_full, drain;
+  uint64_t q_full, o_free, drain[2];
   int64_t scan[kTrWarps], found_off;
   int32_t found_seq, bad[2], abort;
   uint32_t tmem_base;
@@ -147,6 +152,7 @@ struct TreeWalk {
 
 // Ring position (in tiles of K or V) of tile j's K and V among a segment's n
 // tiles: K0, K1, V0, K2, V1, ..., V(n-1), the order the MMAs take them in.
+__device__ __forceinline__ int k_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int v_pos(int j, int n) { return j + 1 < n ? 2 + 2 * j : 2 * n - 1; }
 
 __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
@@ -171,12 +177,13 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
-      mbar_init(sm32(&C.p_ready[b]), kTrSoft);
+      mbar_init(sm32(&C.p_ready[b]), kTrSoft / 2);
+      mbar_init(sm32(&C.drain[b]), 1);
       mbar_init(sm32(&C.pv_done[b]), 1);
       C.bad[b] = 0;
     }
     mbar_init(sm32(&C.q_full), kTrSoft);
-    mbar_init(sm32(&C.drain), 1);
+    mbar_init(sm32(&C.o_free), kTrSoft);
     C.abort = 0;
     C.found_seq = a.seqs.n_seqs;
     C.found_off = 0;
@@ -184,7 +191,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   }
   __syncthreads();
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
-  if (warp == kTrMma) {
+  if (warp == kTrMmaS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      sm32(&C.tmem_base)),
                  "r"(512u)
@@ -240,14 +247,16 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   TreeWalk walk(a, C.found_seq, C.found_off, laid_out ? share : 0);
   TreeSeg g;
 
-  if (warp >= kTrSoft && warp < kTrMma) {
+  if (warp >= kTrSoft && warp < kTrMmaS) {
     // ---- producers: warp p brings tokens 32p .. 32p + 31 of each tile, two
     // 256-byte rows an instruction; lane i looks up the pool row of token 32p + i.
     // A slot's barrier takes each thread's arrival when its copies have landed, so
     // the whole ring may be in flight.
     const int p0 = (warp - kTrSoft) * 32, ch = lane & 15, hl = lane >> 4;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * kTrBox + (uint32_t)(p0 + hl) * 128u;
-    const uint32_t swz = (uint32_t)((ch & 7) ^ hl);
+    uint32_t dsts[4];  // rows 2k + hl: the swizzle repeats every 8 rows
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dsts[k] = dst0 + (uint32_t)k * 256u + (uint32_t)(((ch & 7) ^ hl ^ (2 * k)) << 4);
     uint32_t ns = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
@@ -259,119 +268,134 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         if (slot < 0) report_error(a.status, kErrTokenRange, g.s);
         return slot < 0 ? -1 : (int32_t)(slot * a.nkv + g.kvh);
       };
-      auto bring = [&](const uint16_t *pool, int32_t y) {
+      // Pool rows of this thread's 16 copies of a slot, spread from the lanes that
+      // looked them up before the slot is waited for: a shuffle between the copies
+      // of a slot cost 90 cycles a copy.
+      auto spread = [&](int32_t y, int32_t (&r)[16]) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) r[k] = __shfl_sync(0xffffffffu, y, 2 * k + hl);
+      };
+      auto bring = [&](const uint16_t *pool, const int32_t (&r)[16]) {
 #pragma unroll
         for (int c = 0; c < G::kC; ++c) {
           const uint32_t slot = ns % G::kSlots;
-          if (!tc_warp_wait(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
+          if (!tc_warp_wait_ready(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
             ok = false;
             return;
           }
-          const uint32_t dst = dst0 + slot * kTrSlot;
           const uint16_t *src = pool + c * 128 + ch * 8;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {  // rows 2k, 2k + 1 of this warp's 32
-            const int32_t yr = __shfl_sync(0xffffffffu, y, 2 * k + hl);
-            cp_async16(dst + (uint32_t)k * 256u + ((swz ^ (uint32_t)(2 * (k & 3))) << 4),
-                       src + (int64_t)max(yr, 0) * HD, yr >= 0 ? 16u : 0u);
-          }
+          for (int k = 0; k < 16; ++k)
+            cp_async16(dsts[k & 3] + slot * kTrSlot + (uint32_t)(k >> 2) * 1024u, src + (int64_t)max(r[k], 0) * HD,
+                       r[k] >= 0 ? 16u : 0u);
           cp_async_arrive(sm32(&C.full[slot]));
           ++ns;
         }
       };
       if (g.n > 0) {
-        int32_t y0 = fetch(0), y1 = fetch(1);
-        bring(a.k_pool, y0);
+        int32_t rv[16], rk[16];
+        int32_t y = fetch(0);
+        spread(y, rv);
+        y = fetch(1);
+        bring(a.k_pool, rv);
         for (int j = 0; j < g.n && ok; ++j) {
-          const int32_t y2 = fetch(j + 2);
-          if (j + 1 < g.n) bring(a.k_pool, y1);
-          if (ok) bring(a.v_pool, y0);
-          y0 = y1;
-          y1 = y2;
+          spread(y, rk);
+          y = fetch(j + 2);
+          if (j + 1 < g.n) bring(a.k_pool, rk);
+          if (ok) bring(a.v_pool, rv);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) rv[k] = rk[k];
         }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
-  } else if (warp == kTrMma) {
-    // ---- MMA issuer
+  } else if (warp >= kTrMmaS) {
+    // ---- MMA issuers, one thread each
     if (lane == 0) {
-      uint32_t ns = 0, jg = 0, nq = 0;
+      const bool is_s = warp == kTrMmaS;
+      uint32_t ns = 0, jg = 0, segs = 0;  // slots, tiles and parts before this part
       bool ok = true;
-      auto take = [&]() -> uint32_t {  // the next slot's address, its copies landed
-        const uint32_t slot = ns % G::kSlots;
-        ok = ok && tc_wait(sm32(&C.full[slot]), (ns / G::kSlots) & 1u, lim, abort_flag);
+      auto wait = [&](uint64_t &bar, uint32_t parity) {
+        ok = ok && tc_wait_ready(sm32(&bar), parity, lim, abort_flag);
+        return ok;
+      };
+      auto landed = [&](uint32_t i) {  // slot number i of the ring holds its copy
+        if (!wait(C.full[i % G::kSlots], (i / G::kSlots) & 1u)) return false;
         // the copies wrote through the generic proxy; the MMAs read through the async one
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_after();
-        return sRing + slot * kTrSlot;
-      };
-      auto release = [&]() {
-        mma_commit(sm32(&C.empty[ns % G::kSlots]));
-        ++ns;
-      };
-      auto scores = [&](uint32_t jj) {  // S of tile jj into its buffer
-        const uint32_t d = tmem + G::kSCol + (jj & 1u) * kTrTile;
-        for (int c = 0; c < G::kC && ok; ++c) {
-          const uint32_t kb = take();
-          if (!ok) return;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t in = (uint32_t)(kk >> 2) * kTrBox + (uint32_t)(kk & 3) * 32u;
-            mma_bf16(d, sw128_desc(sQ + (uint32_t)c * 2u * kTrBox + in), sw128_desc(kb + in), kIdescS,
-                     (c > 0 || kk > 0) ? 1u : 0u);
-          }
-          release();
-        }
-        mma_commit(sm32(&C.s_full[jj & 1u]));
+        return true;
       };
       while (ok && walk.next(g)) {
         if (g.n == 0) continue;
-        ok = tc_wait(sm32(&C.q_full), nq & 1u, lim, abort_flag);
-        ++nq;
-        if (!ok) break;
-        tc_fence_after();
-        scores(jg);
-        for (int j = 0; j < g.n && ok; ++j, ++jg) {
-          if (j + 1 < g.n) scores(jg + 1);
-          if (!ok) break;
-          const uint32_t b = jg & 1u;
-          ok = tc_wait(sm32(&C.p_ready[b]), (jg >> 1) & 1u, lim, abort_flag);
-          if (!ok) break;
-          for (int c = 0; c < G::kC && ok; ++c) {
-            const uint32_t vb = take();
-            if (!ok) break;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
-              mma_bf16_ts(tmem + (uint32_t)c * 128u, tmem + G::kSCol + b * kTrTile + 8u * kk,
-                          sw128_mn_desc(vb + 2048u * kk, kTrBox), kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-            release();
-          }
-          mma_commit(sm32(&C.pv_done[b]));
+        if (is_s) {
+          if (!wait(C.q_full, segs & 1u)) break;
+        } else {  // the part before this one has left O
+          if (segs > 0 && !wait(C.o_free, (segs - 1) & 1u)) break;
         }
+        for (int j = 0; j < g.n && ok; ++j) {
+          const uint32_t b = (jg + j) & 1u, ph = ((jg + j) >> 1) & 1u;
+          const uint32_t s0 = tmem + G::kSCol + b * kTrTile;
+          if (is_s) {
+            // the buffer's last tile: its P has been multiplied
+            if (jg + j >= 2 && !wait(C.pv_done[b], ph ^ 1u)) break;
+            for (int c = 0; c < G::kC; ++c) {
+              const uint32_t i = ns + (uint32_t)(k_pos(j) * G::kC + c);
+              if (!landed(i)) break;
+              const uint32_t kb = sRing + (i % G::kSlots) * kTrSlot;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t in = (uint32_t)(kk >> 2) * kTrBox + (uint32_t)(kk & 3) * 32u;
+                mma_bf16(s0, sw128_desc(sQ + (uint32_t)c * 2u * kTrBox + in), sw128_desc(kb + in), kIdescS,
+                         (c > 0 || kk > 0) ? 1u : 0u);
+              }
+              mma_commit(sm32(&C.empty[i % G::kSlots]));
+            }
+            if (ok) mma_commit(sm32(&C.s_full[b]));
+          } else {
+            if (!wait(C.p_ready[b], ph)) break;
+            for (int c = 0; c < G::kC; ++c) {
+              const uint32_t i = ns + (uint32_t)(v_pos(j, g.n) * G::kC + c);
+              if (!landed(i)) break;
+              const uint32_t vb = sRing + (i % G::kSlots) * kTrSlot;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
+                mma_bf16_ts(tmem + (uint32_t)c * 128u, s0 + kPCol + 8u * kk, sw128_mn_desc(vb + 2048u * kk, kTrBox), kIdescO,
+                            (j > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(sm32(&C.empty[i % G::kSlots]));
+            }
+            if (ok) mma_commit(sm32(&C.pv_done[b]));
+          }
+        }
+        jg += (uint32_t)g.n;
+        ns += (uint32_t)(2 * g.n * G::kC);
+        ++segs;
       }
       // every MMA this thread issued has finished before TMEM is freed
-      mma_commit(sm32(&C.drain));
-      tc_wait(sm32(&C.drain), 0u, kTrSpinLimit, nullptr);
+      mma_commit(sm32(&C.drain[warp - kTrMmaS]));
+      tc_wait(sm32(&C.drain[warp - kTrMmaS]), 0u, kTrSpinLimit, nullptr);
     }
     __syncwarp();
   } else {
-    // ---- softmax: thread = TMEM lane (row) r, half h of the tile's tokens and
-    // of the output's dims.  After an abort every wait returns at once, and the
-    // loops and the pairs' barriers run on to the end.
-    const int h = warp >> 2, r = (warp & 3) * 32 + lane;
+    // ---- softmax: thread = TMEM lane (row) r of group w; the groups take the
+    // CTA's tiles in turn and half of the output's dims each.  After an abort every
+    // wait returns at once, and the loops and the pairs' barriers run on to the end.
+    const int w = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    uint32_t xn = 0;
-    auto exchange = [&](float x) -> float {  // the other half's value of this row
-      float(&x2)[2][kTrTile] = C.xch[xn++ & 1u];
-      x2[h][r] = x;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-      return x2[h ^ 1][r];
+    // a row's maximum from one group to the other: barrier 1 + warp (0..7) of the
+    // sender, which arrives, while the warp of the same rows waits
+    auto post = [&](float x) {
+      C.top[w][r] = x;
+      asm volatile("bar.arrive %0, 64;" ::"r"(1 + warp) : "memory");
     };
-    // P V of tile i, the last or the last but one issued: the barrier of its
-    // parity cannot be further behind, for S of tile i + 1 (or i) being done tells
-    // that P V of tile i - 2 is.
+    auto receive = [&]() -> float {
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp ^ 4)) : "memory");
+      return C.top[w ^ 1][r];
+    };
+    // P V of tile i, the last issued: the barrier of its parity cannot be further
+    // behind, for S of tile i (or a later one) waited for P V of tile i - 2.
     auto wait_pv = [&](uint32_t i) {
-      tc_warp_wait(sm32(&C.pv_done[i & 1u]), (i >> 1) & 1u, lim, abort_flag);
+      tc_warp_wait_ready(sm32(&C.pv_done[i & 1u]), (i >> 1) & 1u, lim, abort_flag);
     };
     auto load_q = [&](const TreeSeg &e) {
       const int64_t m0 = (int64_t)e.mt * kTrTile;
@@ -410,6 +434,8 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     };
     uint32_t jg = 0, ns = 0;
     int32_t seg = 0;
+    const uint64_t c2 = pair_f32(a.scale_log2, a.scale_log2);
+    const uint32_t sc = lane_base + G::kSCol + (uint32_t)w * kTrTile;  // this group's S and P
     bool more = walk.next(g);
     if (more && g.n > 0) load_q(g);
     while (more) {
@@ -423,70 +449,96 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       const uint32_t *mrow = a.seqs.mask ? a.seqs.mask + (int64_t)row * a.seqs.mask_words : nullptr;
       // whether a row may be blind to a token that another one sees
       const bool veiled = g.v.rows > 1 || a.seqs.mask != nullptr;
-      float top = -INFINITY, sum = 0.f;
+      float top = -INFINITY, sum = 0.f;  // sum is relative to top
+      auto rebase = [&](float t) {
+        if (t != top) {
+          sum = top == -INFINITY ? 0.f : sum * ex2(top - t);
+          top = t;
+        }
+      };
       for (int j = 0; j < g.n; ++j, ++jg) {
-        const uint32_t b = jg & 1u;
+        if ((int)(jg & 1u) != w) continue;
         const int32_t t0 = (g.t0 + j) * kTrTile;
         const bool masked = t0 + kTrTile > g.v.ctx;
-        tc_warp_wait(sm32(&C.s_full[b]), (jg >> 1) & 1u, lim, abort_flag);
+        tc_warp_wait_ready(sm32(&C.s_full[w]), (jg >> 1) & 1u, lim, abort_flag);
         tc_fence_after();
         if (live) {
-          uint32_t sv[64];
-          const uint32_t sc = lane_base + G::kSCol + b * kTrTile;
-          tmem_ld32(sc + 64u * h, sv);
-          tmem_ld32(sc + 64u * h + 32u, sv + 32);
-          tmem_wait_ld32(sv);
-          tmem_wait_ld32(sv + 32);
+          uint64_t see[2] = {~0ull, ~0ull};
           if (masked) {
-            const uint64_t see = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 + 64 * h - g.v.ctx);
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (!((see >> i) & 1ull)) sv[i] = 0xFF800000u;  // -inf
+            see[0] = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 - g.v.ctx);
+            see[1] = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 + 64 - g.v.ctx);
           }
-          float mx[4];
+          uint32_t sv[64];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(sv[i]);
+          for (int q = 0; q < 2; ++q) {
+            tmem_ld32(sc + 64u * q, sv);
+            tmem_ld32(sc + 64u * q + 32u, sv + 32);
+            tmem_wait_ld32(sv);
+            tmem_wait_ld32(sv + 32);
+            if (masked) {
 #pragma unroll
-          for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sv[i]));
-          float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          mine = fmaxf(mine, exchange(mine));
+              for (int i = 0; i < 64; ++i)
+                if (!((see[q] >> i) & 1ull)) sv[i] = 0xFF800000u;  // -inf
+            }
+#pragma unroll
+            for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sv[i]));
+          }
+          const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const float want = mine == -INFINITY ? -INFINITY : mine * a.scale_log2;
+          if (j > 0) rebase(receive());
           const bool move = valid && (want > top + kTrSlack || (top == -INFINITY && want != -INFINITY));
-          if (__any_sync(0xffffffffu, move)) {
-            const float alpha = move ? (top == -INFINITY ? 0.f : ex2(top - want)) : 1.f;
-            if (move) top = want;
+          const float alpha = move ? (top == -INFINITY ? 0.f : ex2(top - want)) : 1.f;
+          if (move) {
+            top = want;
             sum *= alpha;
-            if (j > 0) {  // O holds the earlier tiles of this part
-              wait_pv(jg - 1);
-              tc_fence_after();
+          }
+          post(top);
+          if (j > 0 && __any_sync(0xffffffffu, move)) {  // O holds the earlier tiles of this part
+            wait_pv(jg - 1);
+            tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < HD / 32; ++c) {
-                uint32_t o[16];
-                const uint32_t oc = lane_base + (uint32_t)(h * (HD / 2) + c * 16);
-                tmem_ld16(oc, o);
+            for (int c = 0; c < HD / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(lane_base + (uint32_t)(c * 16), o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st16(oc, o);
-              }
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(lane_base + (uint32_t)(c * 16), o);
             }
           }
           const float use = top == -INFINITY ? 0.f : top;
-          const uint64_t c2 = pair_f32(a.scale_log2, a.scale_log2), m2 = pair_f32(-use, -use);
+          const uint64_t m2 = pair_f32(-use, -use);
           uint64_t part[2] = {0ull, 0ull};
+          // The second half of S is still in registers, the first is read again; P
+          // lies over the second half.
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t p[16];
+          for (int q = 1; q >= 0; --q) {
+            if (q == 0) {
+              tmem_ld32(sc, sv);
+              tmem_ld32(sc + 32u, sv + 32);
+              tmem_wait_ld32(sv);
+              tmem_wait_ld32(sv + 32);
+              if (masked) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float lo, hi;
-              unpair_f32(fma2(pair_f32(__uint_as_float(sv[32 * q + 2 * i]), __uint_as_float(sv[32 * q + 2 * i + 1])), c2, m2),
-                         lo, hi);
-              lo = ex2(lo);
-              hi = ex2(hi);
-              part[i & 1] = add2(part[i & 1], pair_f32(lo, hi));
-              p[i] = pack_f32_bf16(lo, hi);
+                for (int i = 0; i < 64; ++i)
+                  if (!((see[0] >> i) & 1ull)) sv[i] = 0xFF800000u;
+              }
             }
-            tmem_st16(sc + 32u * h + 16u * q, p);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t p[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float lo, hi;
+                unpair_f32(fma2(pair_f32(__uint_as_float(sv[32 * e + 2 * i]), __uint_as_float(sv[32 * e + 2 * i + 1])), c2, m2),
+                           lo, hi);
+                lo = ex2(lo);
+                hi = ex2(hi);
+                part[i & 1] = add2(part[i & 1], pair_f32(lo, hi));
+                p[i] = pack_f32_bf16(lo, hi);
+              }
+              tmem_st16(sc + kPCol + 32u * q + 16u * e, p);
+            }
           }
           float s0, s1;
           unpair_f32(add2(part[0], part[1]), s0, s1);
@@ -496,19 +548,18 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         if (masked && veiled) {
           // A value that is not finite would reach, as 0 x inf, the rows that do
           // not see its token: it is cleared here and given to the rows that do
-          // see it when the output is written.
-          // (P V of the tile before is done, so each of V's slots has had its
-          // earlier copy: a parity alone could not tell)
+          // see it when the output is written.  (P V of the tile before is done, so
+          // each of V's slots has had its earlier copy: a parity alone could not tell.)
           if (jg > 0) wait_pv(jg - 1);
           const uint32_t at = ns + (uint32_t)(v_pos(j, g.n) * G::kC);
           for (int c = 0; c < G::kC; ++c) {
             const uint32_t slot = (at + c) % G::kSlots;
-            tc_warp_wait(sm32(&C.full[slot]), ((at + c) / G::kSlots) & 1u, lim, abort_flag);
+            tc_warp_wait_ready(sm32(&C.full[slot]), ((at + c) / G::kSlots) & 1u, lim, abort_flag);
             __syncwarp();
             uint8_t *vs = tr_smem + G::kRingOff + slot * kTrSlot;
-            for (int i = warp * 32 + lane; i < (int)(kTrSlot / 16); i += 32 * kTrSoft) {
-              uint4 *w = reinterpret_cast<uint4 *>(vs) + i;
-              const uint4 x = *w;
+            for (int i = (warp & 3) * 32 + lane; i < (int)(kTrSlot / 16); i += 128) {
+              uint4 *q = reinterpret_cast<uint4 *>(vs) + i;
+              const uint4 x = *q;
               uint32_t e[4] = {x.x, x.y, x.z, x.w};
               bool hit = false;
 #pragma unroll
@@ -517,7 +568,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
                 if (nonfinite16(e[k] >> 16)) { e[k] &= 0xFFFFu; hit = true; }
               }
               if (hit) {
-                *w = make_uint4(e[0], e[1], e[2], e[3]);
+                *q = make_uint4(e[0], e[1], e[2], e[3]);
                 *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) = seg;
               }
             }
@@ -526,29 +577,37 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm32(&C.p_ready[b]));
+        if (lane == 0) mbar_arrive(sm32(&C.p_ready[w]));
       }
       ns += (uint32_t)(2 * g.n * G::kC);
+      const uint32_t last = jg - 1;  // the part's last tile
+      if (g.n > 0) {  // its S is done, and with it every one of this part: Q may go
+        tc_warp_wait_ready(sm32(&C.s_full[last & 1u]), (last >> 1) & 1u, lim, abort_flag);
+        if (live && (int)(last & 1u) != w) rebase(receive());
+      }
       TreeSeg next;
       more = walk.next(next);
-      if (more && next.n > 0) load_q(next);  // every S of this part is done
+      if (more && next.n > 0) load_q(next);
       if (g.n > 0) {
-        wait_pv(jg - 1);
+        wait_pv(last);
         tc_fence_after();
       }
       if (live) {
-        const float all = sum + exchange(sum);
+        C.sums[w][r] = sum;
+        asm volatile("bar.sync %0, 64;" ::"r"(9 + (warp & 3)) : "memory");
+        const float all = C.sums[0][r] + C.sums[1][r];
+        asm volatile("bar.sync %0, 64;" ::"r"(9 + (warp & 3)) : "memory");  // read before the next part's
         const float inv = all == 0.f ? 0.f : 1.f / all;
         const bool fix = *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) == seg;
         const int64_t part = (int64_t)blockIdx.x * 2 + (g.head ? 0 : 1);
-        if (valid && h == 0) {
+        if (valid && w == 0) {
           if (!g.whole) part_ml[part * part_rows + r] = make_float2(top, all);
           else if (a.lse) a.lse[(int64_t)row * a.nq + head] =
               all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
         }
 #pragma unroll 1
         for (int c = 0; c < HD / 64; ++c) {
-          const int d0 = h * (HD / 2) + c * 32;
+          const int d0 = w * (HD / 2) + c * 32;
           uint32_t o[32];
           if (g.n > 0) {
             tmem_ld32(lane_base + (uint32_t)d0, o);
@@ -589,8 +648,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
               reinterpret_cast<uint4 *>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
-        tc_fence_before();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && g.n > 0) mbar_arrive(sm32(&C.o_free));
       g = next;
     }
   }
@@ -599,7 +660,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, C.found_seq);
-  if (warp == kTrMma)
+  if (warp == kTrMmaS)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
