@@ -50,19 +50,29 @@ struct SeqView {
   bool ok;
 };
 
-// Sequence s of the call: its rows and its context length, rows 0 (and ok
-// false) where they contradict the row count, the mask's width or the table.
-__device__ __forceinline__ SeqView view_seq(const CachedSeqs &c, int32_t s) {
+// What the arrays say of sequence s.
+struct SeqRaw {
+  int32_t r0, r1, ctx;
+};
+__device__ __forceinline__ SeqRaw read_seq(const CachedSeqs &c, int32_t s) {
+  return SeqRaw{c.row_start[s], c.row_start[s + 1], c.ctx_len[s]};
+}
+
+// Its rows and its context length, rows 0 (and ok false) where they contradict
+// the row count, the mask's width or the table.
+__device__ __forceinline__ SeqView view_seq(const CachedSeqs &c, const SeqRaw &raw) {
   SeqView v;
-  v.row0 = c.row_start[s];
-  const int32_t r1 = c.row_start[s + 1];
-  v.ctx = c.ctx_len[s];
-  const bool range = v.row0 >= 0 && r1 >= v.row0 && r1 <= c.n_rows && v.ctx >= 0;
-  v.rows = range ? r1 - v.row0 : 0;
+  v.row0 = raw.r0;
+  v.ctx = raw.ctx;
+  const bool range = raw.r0 >= 0 && raw.r1 >= raw.r0 && raw.r1 <= c.n_rows && raw.ctx >= 0;
+  v.rows = range ? raw.r1 - raw.r0 : 0;
   v.ok = range && (int64_t)v.ctx + v.rows <= (int64_t)c.table_len * c.page.d &&
          (c.mask == nullptr || v.rows <= (int64_t)32 * c.mask_words);
   if (!v.ok) v.rows = 0;
   return v;
+}
+__device__ __forceinline__ SeqView view_seq(const CachedSeqs &c, int32_t s) {
+  return view_seq(c, read_seq(c, s));
 }
 
 // Pool row (slot) of token t >= 0 of sequence s, or -1 where the table's entry

@@ -58,18 +58,18 @@ template <int HD>
 struct TreeGeom {
   static constexpr int kC = HD / 128;                   // ring slots per tile of K (or V)
   static constexpr int kSlots = HD == 256 ? 5 : 6;
+  static constexpr int kSBuf = HD == 256 ? 2 : 3;       // S buffers: what TMEM holds beside O
   static constexpr uint32_t kQBytes = (HD / 64) * kTrBox;
   static constexpr uint32_t kRingOff = kQBytes;
   static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kTrSlot;
-  static constexpr uint32_t kSCol = HD;                 // O in columns 0..HD-1, then two S buffers
+  static constexpr uint32_t kSCol = HD;                 // O in columns 0..HD-1, then the S buffers
 };
 
 struct TreeCtrl {
   float top[2][kTrTile];     // [group that wrote it][row]: the running maximum, log2 units
   float sums[2][kTrTile];    // [group][row]: its share of the row's sum
   uint64_t full[6], empty[6];
-  uint64_t s_full[2], p_ready[2];
-  uint64_t pv_done[2];       // by tile parity
+  uint64_t s_full[3], p_ready[3], pv_done[3];  // per S buffer
   uint64_t q_full, o_free, drain[2];
   int64_t scan[kTrWarps], found_off;
   int32_t found_seq, bad[2], abort;
@@ -90,9 +90,9 @@ struct SeqTiles {
   int64_t count;  // tiles of all its units
 };
 
-__device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs &a, int32_t s) {
+__device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs &a, const SeqRaw &raw) {
   SeqTiles q;
-  q.v = view_seq(a.seqs, s);
+  q.v = view_seq(a.seqs, raw);
   q.tiles = q.v.rows > 0 ? (q.v.ctx + q.v.rows + kTrTile - 1) / kTrTile : 0;
   q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + kTrTile - 1) / kTrTile);
   q.count = (int64_t)q.tiles * q.m_tiles * a.nkv;
@@ -108,35 +108,41 @@ struct TreeSeg {
 };
 
 // Walks a CTA's share of the tile list, unit by unit (each role its own walk).
+// A sequence's lengths are read one sequence ahead: under load a read takes
+// several thousand cycles.
 struct TreeWalk {
   const TreeArgs &a;
   int64_t left, off;
   int32_t s;
   SeqTiles q;
-  bool loaded;
+  SeqRaw ahead;
   __device__ TreeWalk(const TreeArgs &a_, int32_t s_, int64_t off_, int64_t left_)
-      : a(a_), left(left_), off(off_), s(s_), loaded(false) {}
+      : a(a_), left(left_), off(off_), s(s_) {
+    if (left <= 0) return;
+    q = seq_tiles(a, read_seq(a.seqs, s));
+    ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
+  }
   __device__ bool next(TreeSeg &g) {
     if (left <= 0) return false;
-    while (true) {
-      if (s >= a.seqs.n_seqs) return false;
-      if (!loaded) {
-        q = seq_tiles(a, s);
-        loaded = true;
-      }
-      if (off < q.count) break;
+    while (off >= q.count) {
       off -= q.count;
-      ++s;
-      loaded = false;
+      if (++s >= a.seqs.n_seqs) {
+        left = 0;
+        return false;
+      }
+      q = seq_tiles(a, ahead);
+      ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
     }
-    const int64_t unit = off / q.tiles;
-    g.t0 = (int32_t)(off - unit * q.tiles);
+    int32_t unit;  // (KV head, 128-row tile)
+    if ((off >> 31) == 0) unit = (int32_t)((uint32_t)off / (uint32_t)q.tiles);
+    else unit = (int32_t)(off / q.tiles);
+    g.t0 = (int32_t)(off - (int64_t)unit * q.tiles);
     const int32_t take = (int32_t)min((int64_t)(q.tiles - g.t0), left);
     off += take;
     left -= take;
     g.s = s;
-    g.kvh = (int32_t)(unit / q.m_tiles);
-    g.mt = (int32_t)(unit - (int64_t)g.kvh * q.m_tiles);
+    g.kvh = unit / q.m_tiles;
+    g.mt = unit - g.kvh * q.m_tiles;
     g.v = q.v;
     g.whole = take == q.tiles;
     g.head = g.t0 > 0;
@@ -175,14 +181,16 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       mbar_init(sm32(&C.full[i]), 32 * kTrProd);
       mbar_init(sm32(&C.empty[i]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < G::kSBuf; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
       mbar_init(sm32(&C.p_ready[b]), kTrSoft / 2);
-      mbar_init(sm32(&C.drain[b]), 1);
       mbar_init(sm32(&C.pv_done[b]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(sm32(&C.drain[b]), 1);
       C.bad[b] = 0;
     }
-    mbar_init(sm32(&C.q_full), kTrSoft);
+    mbar_init(sm32(&C.q_full), 32 * kTrSoft);
     mbar_init(sm32(&C.o_free), kTrSoft);
     C.abort = 0;
     C.found_seq = a.seqs.n_seqs;
@@ -200,22 +208,24 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   }
 
   // ---- the plan: every sequence's tiles summed, then the sequence this CTA's
-  // share starts in (CTA 0 also leaves the sums for the joining launch)
+  // share starts in (CTA 0 also leaves the sums for the joining launch); one
+  // thread a sequence, in chunks where there are more
+  const bool one_chunk = a.seqs.n_seqs <= kTrThreads;
   int64_t total = 0;
-  for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles(a, s).count;
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) C.scan[warp] = total;
-  __syncthreads();
-  total = 0;
-  for (int i = 0; i < kTrWarps; ++i) total += C.scan[i];
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t w0 = per * blockIdx.x, share = max((int64_t)0, min(per, total - w0));
-  int64_t before = 0;
-  for (int32_t s0 = 0; s0 < a.seqs.n_seqs && (blockIdx.x == 0 || (share > 0 && before <= w0)); s0 += kTrThreads) {
+  if (!one_chunk) {
+    for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles(a, read_seq(a.seqs, s)).count;
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) C.scan[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int i = 0; i < kTrWarps; ++i) total += C.scan[i];
+  }
+  int64_t before = 0, per = 0, w0 = 0, share = 0;
+  for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += kTrThreads) {
     const int32_t s = s0 + tid;
     int64_t count = 0;
     if (s < a.seqs.n_seqs) {
-      const SeqTiles q = seq_tiles(a, s);
+      const SeqTiles q = seq_tiles(a, read_seq(a.seqs, s));
       count = q.count;
       if (blockIdx.x == 0 && !q.v.ok) report_error(a.status, kErrRowRange, s);
     }
@@ -228,15 +238,21 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     if (lane == 31) C.scan[warp] = incl;
     __syncthreads();
     int64_t at = before + incl - count;
+#pragma unroll
     for (int i = 0; i < kTrWarps; ++i) {
       at += i < warp ? C.scan[i] : 0;
       before += C.scan[i];
     }
+    if (one_chunk) total = before;
+    per = (total >> 31) == 0 ? (int64_t)(((uint32_t)total + gridDim.x - 1u) / gridDim.x) : (total + gridDim.x - 1) / gridDim.x;
+    w0 = per * blockIdx.x;
+    share = max((int64_t)0, min(per, total - w0));
     if (s < a.seqs.n_seqs && blockIdx.x == 0) base_out[s] = at;
-    if (count > 0 && at <= w0 && w0 < at + count) {
+    if (share > 0 && count > 0 && at <= w0 && w0 < at + count) {
       C.found_seq = s;
       C.found_off = w0 - at;
     }
+    if (blockIdx.x != 0 && before > w0) break;
   }
   if (blockIdx.x == 0 && tid == 0) base_out[a.seqs.n_seqs] = total;
   tc_fence_before();
@@ -330,15 +346,16 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         if (g.n == 0) continue;
         if (is_s) {
           if (!wait(C.q_full, segs & 1u)) break;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         } else {  // the part before this one has left O
           if (segs > 0 && !wait(C.o_free, (segs - 1) & 1u)) break;
         }
         for (int j = 0; j < g.n && ok; ++j) {
-          const uint32_t b = (jg + j) & 1u, ph = ((jg + j) >> 1) & 1u;
+          const uint32_t b = (jg + j) % G::kSBuf, ph = ((jg + j) / G::kSBuf) & 1u;
           const uint32_t s0 = tmem + G::kSCol + b * kTrTile;
           if (is_s) {
             // the buffer's last tile: its P has been multiplied
-            if (jg + j >= 2 && !wait(C.pv_done[b], ph ^ 1u)) break;
+            if (jg + j >= G::kSBuf && !wait(C.pv_done[b], ph ^ 1u)) break;
             for (int c = 0; c < G::kC; ++c) {
               const uint32_t i = ns + (uint32_t)(k_pos(j) * G::kC + c);
               if (!landed(i)) break;
@@ -392,50 +409,42 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp ^ 4)) : "memory");
       return C.top[w ^ 1][r];
     };
-    // P V of tile i, the last issued: the barrier of its parity cannot be further
-    // behind, for S of tile i (or a later one) waited for P V of tile i - 2.
+    // P V of tile i, the last issued: its buffer's barrier cannot be further
+    // behind, for S of tile i (or a later one) waited for P V of tile i - kSBuf.
     auto wait_pv = [&](uint32_t i) {
-      tc_warp_wait_ready(sm32(&C.pv_done[i & 1u]), (i >> 1) & 1u, lim, abort_flag);
+      tc_warp_wait_ready(sm32(&C.pv_done[i % G::kSBuf]), (i / G::kSBuf) & 1u, lim, abort_flag);
     };
+    // This warp's rows of a part's Q into shared memory.  The copies arrive on
+    // q_full by themselves; a sign or a zero scale has to pass through registers.
     auto load_q = [&](const TreeSeg &e) {
       const int64_t m0 = (int64_t)e.mt * kTrTile;
       const int rows = (int)min((int64_t)kTrTile, (int64_t)e.v.rows * a.group - m0);
-      constexpr int kCh = HD / 8;          // 16-byte chunks per row
-      constexpr int kPer = 32 / kCh;       // rows per warp load (2 at head_dim 128... 1)
-      constexpr int kStep = kPer * kTrSoft;
+      constexpr int kCh = HD / 8;     // 16-byte chunks per row
+      constexpr int kPer = 32 / kCh;  // rows per warp copy
       const int ch = lane % kCh, sub = lane / kCh;
-      for (int r0 = warp * kPer + sub; r0 < rows; r0 += 4 * kStep) {
-        uint4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = r0 + i * kStep;
-          if (rr < rows) {
-            const int32_t m = (int32_t)(m0 + rr), j = fast_div(group_div, m);
-            const int32_t head = e.kvh * a.group + (m - j * a.group);
-            x[i] = ldg_nc_v4(a.q + (int64_t)(e.v.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = r0 + i * kStep;
-          if (rr < rows) {
-            uint4 v = x[i];
-            v.x = (v.x & q_and) ^ q_xor;
-            v.y = (v.y & q_and) ^ q_xor;
-            v.z = (v.z & q_and) ^ q_xor;
-            v.w = (v.w & q_and) ^ q_xor;
-            *reinterpret_cast<uint4 *>(tr_smem + (ch >> 3) * kTrBox + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
-          }
+      const bool plain = q_and == 0xFFFFFFFFu && q_xor == 0u;
+#pragma unroll 4
+      for (int rr = warp * kPer + sub; rr < rows; rr += kPer * kTrSoft) {
+        const int32_t m = (int32_t)(m0 + rr), j = fast_div(group_div, m);
+        const int32_t head = e.kvh * a.group + (m - j * a.group);
+        const uint16_t *src = a.q + (int64_t)(e.v.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch;
+        const uint32_t to = (uint32_t)(ch >> 3) * kTrBox + (uint32_t)rr * 128u + (uint32_t)(((ch & 7) ^ (rr & 7)) << 4);
+        if (plain) {
+          cp_async16(sQ + to, src, 16u);
+        } else {
+          uint4 v = ldg_nc_v4(src);
+          v.x = (v.x & q_and) ^ q_xor;
+          v.y = (v.y & q_and) ^ q_xor;
+          v.z = (v.z & q_and) ^ q_xor;
+          v.w = (v.w & q_and) ^ q_xor;
+          *reinterpret_cast<uint4 *>(tr_smem + to) = v;
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the MMAs
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm32(&C.q_full));
+      cp_async_arrive(sm32(&C.q_full));
     };
     uint32_t jg = 0, ns = 0;
     int32_t seg = 0;
     const uint64_t c2 = pair_f32(a.scale_log2, a.scale_log2);
-    const uint32_t sc = lane_base + G::kSCol + (uint32_t)w * kTrTile;  // this group's S and P
     bool more = walk.next(g);
     if (more && g.n > 0) load_q(g);
     while (more) {
@@ -458,9 +467,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       };
       for (int j = 0; j < g.n; ++j, ++jg) {
         if ((int)(jg & 1u) != w) continue;
+        const uint32_t b = jg % G::kSBuf, sc = lane_base + G::kSCol + b * kTrTile;  // S and P
         const int32_t t0 = (g.t0 + j) * kTrTile;
         const bool masked = t0 + kTrTile > g.v.ctx;
-        tc_warp_wait_ready(sm32(&C.s_full[w]), (jg >> 1) & 1u, lim, abort_flag);
+        tc_warp_wait_ready(sm32(&C.s_full[b]), (jg / G::kSBuf) & 1u, lim, abort_flag);
         tc_fence_after();
         if (live) {
           uint64_t see[2] = {~0ull, ~0ull};
@@ -577,12 +587,12 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm32(&C.p_ready[w]));
+        if (lane == 0) mbar_arrive(sm32(&C.p_ready[b]));
       }
       ns += (uint32_t)(2 * g.n * G::kC);
       const uint32_t last = jg - 1;  // the part's last tile
       if (g.n > 0) {  // its S is done, and with it every one of this part: Q may go
-        tc_warp_wait_ready(sm32(&C.s_full[last & 1u]), (last >> 1) & 1u, lim, abort_flag);
+        tc_warp_wait_ready(sm32(&C.s_full[last % G::kSBuf]), (last / G::kSBuf) & 1u, lim, abort_flag);
         if (live && (int)(last & 1u) != w) rebase(receive());
       }
       TreeSeg next;
@@ -642,10 +652,11 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
               reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            float *dst = part_o + (part * part_rows + r) * HD + d0;
+            // [dims / 4][row] quads: a warp's rows lie side by side
+            uint4 *dst = reinterpret_cast<uint4 *>(part_o) + (part * (HD / 4) + d0 / 4) * part_rows + r;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4 *>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              dst[i * part_rows] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
       }
@@ -654,6 +665,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       if (lane == 0 && g.n > 0) mbar_arrive(sm32(&C.o_free));
       g = next;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   tc_fence_before();
@@ -664,62 +676,92 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// Joins the parts of the units that several CTAs share: one warp per (row, query
-// head), every part's maximum and sum first, then its share of O in CTA order.
-constexpr int kJoinWarps = 4;
+// Joins the parts of the units that several CTAs share.  A warp takes 8 rows x 4
+// quads of dims (a part's rows lie side by side) and every kGroups-th part, with
+// the running maximum of those; the groups' results are then added in order.
+constexpr int kJoinWarps = 8;
 
-template <int HD>
+template <int HD, int kGroups>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 tree_join_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, int32_t ctas,
                  const int64_t *__restrict__ base, const float2 *__restrict__ part_ml,
-                 const float *__restrict__ part_o) {
+                 const float4 *__restrict__ part_o) {
+  __shared__ float4 acc_s[kGroups > 1 ? kJoinWarps : 1][32];
+  __shared__ float2 ml_s[kGroups > 1 ? kJoinWarps : 1][32];
   grid_dependency_sync();
-  const int lane = threadIdx.x & 31;
-  const int64_t at = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (at >= (int64_t)a.seqs.n_rows * a.nq) return;
-  const int32_t row = (int32_t)(at / a.nq), head = (int32_t)(at - (int64_t)row * a.nq);
-  const int32_t s = seq_of_row(a.seqs, row);
-  const SeqTiles q = seq_tiles(a, s);
-  if (row < q.v.row0 || row >= q.v.row0 + q.v.rows) return;
-  const int32_t kvh = fast_div(group_div, head);
-  const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
-  const int32_t mt = (int32_t)(m / kTrTile), r = (int32_t)(m % kTrTile);
-  const int64_t per = (base[a.seqs.n_seqs] + ctas - 1) / ctas;
-  const int64_t u0 = base[s] + ((int64_t)kvh * q.m_tiles + mt) * q.tiles;
-  const int32_t c0 = (int32_t)(u0 / per), c1 = (int32_t)((u0 + q.tiles - 1) / per);
-  if (c0 == c1) return;
-  auto slot = [&](int32_t c) { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_rows + r; };
-  float top = -INFINITY;
-  for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, part_ml[slot(c)].x);
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float use = top == -INFINITY ? 0.f : top;
-  constexpr int kE = HD / 128;  // float4s per lane
-  float4 acc[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float all = 0.f;
-#pragma unroll 4
-  for (int32_t c = c0; c <= c1; ++c) {
-    const float2 ml = part_ml[slot(c)];
-    const float w = ex2(ml.x - use);
-    all = fmaf(ml.y, w, all);
-    const float4 *o = reinterpret_cast<const float4 *>(part_o + slot(c) * HD);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const float4 x = o[e * 32 + lane];
-      acc[e].x = fmaf(x.x, w, acc[e].x);
-      acc[e].y = fmaf(x.y, w, acc[e].y);
-      acc[e].z = fmaf(x.z, w, acc[e].z);
-      acc[e].w = fmaf(x.w, w, acc[e].w);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp % kGroups;
+  const int64_t mg = ((int64_t)blockIdx.x * (kJoinWarps / kGroups) + warp / kGroups) * 8 + (lane & 7);
+  const int32_t quad = blockIdx.y * 4 + (lane >> 3), kvh = blockIdx.z;
+  const int32_t row = mg < (int64_t)a.seqs.n_rows * a.group ? fast_div(group_div, (int32_t)mg) : -1;
+  const int32_t head = kvh * a.group + (int32_t)(mg - (int64_t)row * a.group);
+  int32_t c0 = 0, c1 = 0, r = 0;
+  bool mine = false;
+  if (row >= 0) {
+    const int32_t s = seq_of_row(a.seqs, row);
+    const SeqTiles q = seq_tiles(a, read_seq(a.seqs, s));
+    if (row >= q.v.row0 && row < q.v.row0 + q.v.rows) {
+      const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
+      const int32_t mt = (int32_t)(m / kTrTile);
+      r = (int32_t)(m % kTrTile);
+      const int64_t per = (base[a.seqs.n_seqs] + ctas - 1) / ctas;
+      const int64_t u0 = base[s] + ((int64_t)kvh * q.m_tiles + mt) * q.tiles;
+      if (((u0 + q.tiles) >> 31) == 0) {
+        c0 = (int32_t)((uint32_t)u0 / (uint32_t)per);
+        c1 = (int32_t)((uint32_t)(u0 + q.tiles - 1) / (uint32_t)per);
+      } else {
+        c0 = (int32_t)(u0 / per);
+        c1 = (int32_t)((u0 + q.tiles - 1) / per);
+      }
+      mine = c0 != c1;
     }
   }
-  const float inv = all == 0.f ? 0.f : 1.f / all;
-  uint16_t *dst = a.out + (int64_t)row * a.out_stride + (int64_t)head * HD;
+  auto ml_at = [&](int32_t c) { return part_ml[((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_rows + r]; };
+  auto o_at = [&](int32_t c) {
+    return part_o[(((int64_t)c * 2 + (c == c0 ? 1 : 0)) * (HD / 4) + quad) * part_rows + r];
+  };
+  float top = -INFINITY, all = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mine) {
+    for (int32_t c = c0 + grp; c <= c1; c += kGroups) top = fmaxf(top, ml_at(c).x);
+    const float use = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+    for (int32_t c = c0 + grp; c <= c1; c += kGroups) {
+      const float2 ml = ml_at(c);
+      const float4 x = o_at(c);
+      const float w = ex2(ml.x - use);
+      all = fmaf(ml.y, w, all);
+      acc.x = fmaf(x.x, w, acc.x);
+      acc.y = fmaf(x.y, w, acc.y);
+      acc.z = fmaf(x.z, w, acc.z);
+      acc.w = fmaf(x.w, w, acc.w);
+    }
+  }
+  if constexpr (kGroups > 1) {
+    acc_s[warp][lane] = acc;
+    ml_s[warp][lane] = make_float2(top, all);
+    __syncthreads();
+    if (grp != 0) return;
+    for (int i = 0; i < kGroups; ++i) top = fmaxf(top, ml_s[warp + i][lane].x);
+    const float use = top == -INFINITY ? 0.f : top;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    all = 0.f;
 #pragma unroll
-  for (int e = 0; e < kE; ++e)
-    reinterpret_cast<uint2 *>(dst)[e * 32 + lane] =
-        make_uint2(pack_f32_bf16(acc[e].x * inv, acc[e].y * inv), pack_f32_bf16(acc[e].z * inv, acc[e].w * inv));
-  if (lane == 0 && a.lse)
+    for (int i = 0; i < kGroups; ++i) {
+      const float w = ex2(ml_s[warp + i][lane].x - use);
+      const float4 x = acc_s[warp + i][lane];
+      all = fmaf(ml_s[warp + i][lane].y, w, all);
+      acc.x = fmaf(x.x, w, acc.x);
+      acc.y = fmaf(x.y, w, acc.y);
+      acc.z = fmaf(x.z, w, acc.z);
+      acc.w = fmaf(x.w, w, acc.w);
+    }
+  }
+  if (!mine) return;
+  const float inv = all == 0.f ? 0.f : 1.f / all;
+  *reinterpret_cast<uint2 *>(a.out + (int64_t)row * a.out_stride + (int64_t)head * HD + 4 * quad) =
+      make_uint2(pack_f32_bf16(acc.x * inv, acc.y * inv), pack_f32_bf16(acc.z * inv, acc.w * inv));
+  if (quad == 0 && a.lse)
     a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
 }
 
@@ -756,9 +798,15 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
                                    a, group_div, part_rows, q_and, q_xor, base, ml, o);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kTrTile) return r;
-  const int64_t warps = (int64_t)a.seqs.n_rows * a.nq;
-  return launch_dependent(tree_join_kernel<HD>, dim3((unsigned)((warps + kJoinWarps - 1) / kJoinWarps)),
-                          dim3(32 * kJoinWarps), 0, stream, 1u, a, group_div, part_rows, (int32_t)ctas, base, ml, o);
+  // One group of parts per warp where units outnumber the CTAs (few parts each),
+  // eight where a unit spreads over many.
+  const int64_t rows8 = ((int64_t)a.seqs.n_rows * a.group + 7) / 8;
+  const int64_t units = (int64_t)a.nkv * (((int64_t)a.seqs.n_rows * a.group + kTrTile - 1) / kTrTile);
+  const bool many = ctas >= 8 * units;
+  const int64_t blocks = many ? rows8 : (rows8 + kJoinWarps - 1) / kJoinWarps;
+  return launch_dependent(many ? tree_join_kernel<HD, kJoinWarps> : tree_join_kernel<HD, 1>,
+                          dim3((unsigned)blocks, HD / 16, (unsigned)a.nkv), dim3(32 * kJoinWarps), 0, stream, 1u, a,
+                          group_div, part_rows, (int32_t)ctas, base, ml, reinterpret_cast<const float4 *>(o));
 }
 
 }  // namespace
