@@ -7,10 +7,10 @@
 //
 // The rows of one sequence that read the same KV head (drafted row x query
 // head of the group) form the M dimension of two tcgen05 products per tile of
-// 128 tokens: S = Q K^T (operands in shared memory, accumulator in TMEM), and
-// O += P V (P as bf16 in TMEM over S's columns, V read MN-major).  A unit of work
-// is (sequence, KV head, 128 such rows); its tiles are a run of the launch's
-// linear list of tiles, of which every CTA (one per SM) takes an equal,
+// 128 tokens (64 at head_dim 256): S = Q K^T (operands in shared memory,
+// accumulator in TMEM), and O += P V (P as bf16 in TMEM, V read MN-major).  A unit
+// of work is (sequence, KV head, 128 such rows); its tiles are a run of the
+// launch's linear list of tiles, of which every CTA (one per SM) takes an equal,
 // contiguous share, so ragged batches balance and one long context spreads over
 // the GPU.  A unit that lies in one CTA's share is written at once; the parts
 // of any other go to the workspace as (O, max, sum) and a second launch joins
@@ -18,21 +18,25 @@
 //
 // Fourteen warps: two groups of four (warps 0-3 and 4-7) do the softmax, a row
 // per thread, tiles in turn; warps 8-11 copy K and V rows into a ring of 32 KiB
-// slots (128 tokens x 128 dims, 128-byte swizzle); warp 12 issues S, a tile
-// ahead, warp 13 P V, so that neither one's waits leave the tensor pipe idle.
-// The groups share a row's running maximum through shared memory: a group has
-// the other's before it takes its own exponentials, and its row sum relative to
-// the last maximum it used.  The copies are 16-byte cp.async, which take any page size
-// alike: streaming tiles of pages of 16 tokens and nothing else, they moved 9.7
-// TB/s out of L2 and 5.7 TB/s out of HBM, four-row TMA gathers 5.7 and 4.8, TMA
-// boxes of a page 5.5 and 4.6.  The running maximum moves only when a
-// row's grows by more than 2^8, so O is rarely rescaled; what is left of the
-// softmax is one pass over registers.
+// slots (a tile of K or of V, 128-byte swizzle); warp 12 issues S, up to two
+// tiles ahead, warp 13 P V, so that neither one's waits leave the tensor pipe
+// idle.  The copies are 16-byte cp.async, which take any page size alike:
+// streaming tiles of pages of 16 tokens and nothing else, they moved 9.7 TB/s
+// out of L2 and 5.7 TB/s out of HBM, four-row TMA gathers 5.7 and 4.8, TMA boxes
+// of a page 5.5 and 4.6.
+//
+// The softmax is one pass over a tile's S: the exponentials are taken relative
+// to a reference that is a maximum of the row seen earlier, not its running
+// maximum.  f32 and bf16 keep their relative precision under any such reference,
+// so it only moves (O and the sums rescaled, the tile's pass taken again) when a
+// logit passes it by 2^16.  The groups tell each other a row's reference through
+// shared memory after each tile; a part's first tile is passed over twice, first
+// for its maximum.
 //
 // Decode (M = group rows of 128) is bound by HBM: the padded products take 2 x
-// 128 x 128 x head_dim x 2 flop a tile, under half the time its K and V take to
-// arrive.  Wide trees are bound by the products and the L2 reads of each
-// 128-row unit.
+// 128 x 128 x head_dim x 2 flop per 128 tokens, under half the time their K and V
+// take to arrive.  Wide trees are bound by the softmax (128 exponentials a row and
+// tile) and the products.
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"
@@ -46,30 +50,34 @@ constexpr int kTrProd = 4;     // producer warps
 constexpr int kTrMmaS = kTrSoft + kTrProd;  // issues S = Q K^T
 constexpr int kTrMmaO = kTrMmaS + 1;        // issues O += P V
 constexpr int kTrWarps = kTrMmaO + 1, kTrThreads = 32 * kTrWarps;
-constexpr int kTrTile = 128;   // tokens per tile
+constexpr int kTrRows = 128;   // rows of a unit: the MMA's M
 constexpr int kTrMaxCtas = 160;
-constexpr uint32_t kTrBox = kTrTile * 64 * 2;  // 64 dims of a tile: 16 KiB
-constexpr uint32_t kTrSlot = 2 * kTrBox;       // a ring slot: 128 dims
-constexpr uint32_t kPCol = 64;                 // P (64 columns) inside an S buffer
-constexpr float kTrSlack = 8.0f;               // log2 units a maximum may grow before O moves
+constexpr uint32_t kTrSlot = 32768;  // a ring slot: a tile of K or V
+constexpr float kTrSlack = 16.0f;    // log2 units a logit may pass the reference by
 constexpr long long kTrSpinLimit = 4000000000LL;
 
 template <int HD>
 struct TreeGeom {
-  static constexpr int kC = HD / 128;                   // ring slots per tile of K (or V)
+  static constexpr int kT = (int)kTrSlot / (2 * HD);        // tokens per tile
   static constexpr int kSlots = HD == 256 ? 5 : 6;
-  static constexpr int kSBuf = HD == 256 ? 2 : 3;       // S buffers: what TMEM holds beside O
-  static constexpr uint32_t kQBytes = (HD / 64) * kTrBox;
-  static constexpr uint32_t kRingOff = kQBytes;
+  static constexpr uint32_t kQBox = kTrRows * 128;          // 64 dims of Q
+  static constexpr uint32_t kBox = kT * 128;                // 64 dims of a tile
+  static constexpr uint32_t kRingOff = (HD / 64) * kQBox;
   static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kTrSlot;
-  static constexpr uint32_t kSCol = HD;                 // O in columns 0..HD-1, then the S buffers
+  // TMEM columns: O, then an S and a P buffer per softmax group
+  static constexpr uint32_t kSCol = HD, kPCol = HD + 2 * kT;
+  static_assert(kPCol + kT <= 512, "TMEM has 512 columns");
+  // kind::f16, D f32, A and B bf16, M = 128; S: N = tokens, K-major B; O: N = dims, MN-major B
+  static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+  static constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kT >> 3) << 17);
+  static constexpr uint32_t kIdescO = kIdesc | ((uint32_t)(HD >> 3) << 17) | (1u << 16);
 };
 
 struct TreeCtrl {
-  float top[2][kTrTile];     // [group that wrote it][row]: the running maximum, log2 units
-  float sums[2][kTrTile];    // [group][row]: its share of the row's sum
+  float top[2][kTrRows];   // [group that wrote it][row]: the reference, log2 units
+  float sums[2][kTrRows];  // [group][row]: its share of the row's sum
   uint64_t full[6], empty[6];
-  uint64_t s_full[3], p_ready[3], pv_done[3];  // per S buffer
+  uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];  // per softmax group
   uint64_t q_full, o_free, drain[2];
   int64_t scan[kTrWarps], found_off;
   int32_t found_seq, bad[2], abort;
@@ -79,10 +87,6 @@ template <int HD>
 constexpr size_t tree_smem() { return TreeGeom<HD>::kCtrlOff + sizeof(TreeCtrl); }
 static_assert(tree_smem<256>() <= 232448 && tree_smem<128>() <= 232448, "227 KiB per CTA");
 
-// kind::f16, D f32, A and B bf16, M = 128, N = 128; K-major B (S), MN-major B (P V)
-constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kIdescO = kIdescS | (1u << 16);
-
 // What the plan below needs of a sequence.
 struct SeqTiles {
   SeqView v;
@@ -90,11 +94,12 @@ struct SeqTiles {
   int64_t count;  // tiles of all its units
 };
 
+template <int T>
 __device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs &a, const SeqRaw &raw) {
   SeqTiles q;
   q.v = view_seq(a.seqs, raw);
-  q.tiles = q.v.rows > 0 ? (q.v.ctx + q.v.rows + kTrTile - 1) / kTrTile : 0;
-  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + kTrTile - 1) / kTrTile);
+  q.tiles = q.v.rows > 0 ? (q.v.ctx + q.v.rows + T - 1) / T : 0;
+  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + kTrRows - 1) / kTrRows);
   q.count = (int64_t)q.tiles * q.m_tiles * a.nkv;
   return q;
 }
@@ -110,6 +115,7 @@ struct TreeSeg {
 // Walks a CTA's share of the tile list, unit by unit (each role its own walk).
 // A sequence's lengths are read one sequence ahead: under load a read takes
 // several thousand cycles.
+template <int T>
 struct TreeWalk {
   const TreeArgs &a;
   int64_t left, off;
@@ -119,7 +125,7 @@ struct TreeWalk {
   __device__ TreeWalk(const TreeArgs &a_, int32_t s_, int64_t off_, int64_t left_)
       : a(a_), left(left_), off(off_), s(s_) {
     if (left <= 0) return;
-    q = seq_tiles(a, read_seq(a.seqs, s));
+    q = seq_tiles<T>(a, read_seq(a.seqs, s));
     ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
   }
   __device__ bool next(TreeSeg &g) {
@@ -130,7 +136,7 @@ struct TreeWalk {
         left = 0;
         return false;
       }
-      q = seq_tiles(a, ahead);
+      q = seq_tiles<T>(a, ahead);
       ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
     }
     int32_t unit;  // (KV head, 128-row tile)
@@ -148,16 +154,15 @@ struct TreeWalk {
     g.head = g.t0 > 0;
     g.n = take;
     if (a.seqs.mask == nullptr) {  // no row of this tile sees past its last row's own token
-      const int64_t m_end = min((int64_t)(g.mt + 1) * kTrTile, (int64_t)q.v.rows * a.group);
-      const int32_t end = (q.v.ctx + (int32_t)((m_end - 1) / a.group) + kTrTile) / kTrTile;
+      const int64_t m_end = min((int64_t)(g.mt + 1) * kTrRows, (int64_t)q.v.rows * a.group);
+      const int32_t end = (q.v.ctx + (int32_t)((m_end - 1) / a.group) + T) / T;
       g.n = max(0, min(take, end - g.t0));
     }
     return true;
   }
 };
 
-// Ring position (in tiles of K or V) of tile j's K and V among a segment's n
-// tiles: K0, K1, V0, K2, V1, ..., V(n-1), the order the MMAs take them in.
+// Ring position of tile j's K and V among a part's n tiles: K0, K1, V0, K2, V1, ..., V(n-1), the order the MMAs take them in.
 __device__ __forceinline__ int k_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int v_pos(int j, int n) { return j + 1 < n ? 2 + 2 * j : 2 * n - 1; }
 
@@ -181,12 +186,11 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       mbar_init(sm32(&C.full[i]), 32 * kTrProd);
       mbar_init(sm32(&C.empty[i]), 1);
     }
-    for (int b = 0; b < G::kSBuf; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
+      mbar_init(sm32(&C.s_free[b]), kTrSoft / 2);
       mbar_init(sm32(&C.p_ready[b]), kTrSoft / 2);
       mbar_init(sm32(&C.pv_done[b]), 1);
-    }
-    for (int b = 0; b < 2; ++b) {
       mbar_init(sm32(&C.drain[b]), 1);
       C.bad[b] = 0;
     }
@@ -213,7 +217,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   const bool one_chunk = a.seqs.n_seqs <= kTrThreads;
   int64_t total = 0;
   if (!one_chunk) {
-    for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles(a, read_seq(a.seqs, s)).count;
+    for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles<G::kT>(a, read_seq(a.seqs, s)).count;
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) C.scan[warp] = total;
     __syncthreads();
@@ -225,7 +229,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     const int32_t s = s0 + tid;
     int64_t count = 0;
     if (s < a.seqs.n_seqs) {
-      const SeqTiles q = seq_tiles(a, read_seq(a.seqs, s));
+      const SeqTiles q = seq_tiles<G::kT>(a, read_seq(a.seqs, s));
       count = q.count;
       if (blockIdx.x == 0 && !q.v.ok) report_error(a.status, kErrRowRange, s);
     }
@@ -260,26 +264,24 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   tc_fence_after();
   const uint32_t tmem = C.tmem_base;
   const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
-  TreeWalk walk(a, C.found_seq, C.found_off, laid_out ? share : 0);
+  TreeWalk<G::kT> walk(a, C.found_seq, C.found_off, laid_out ? share : 0);
   TreeSeg g;
 
   if (warp >= kTrSoft && warp < kTrMmaS) {
-    // ---- producers: warp p brings tokens 32p .. 32p + 31 of each tile, two
-    // 256-byte rows an instruction; lane i looks up the pool row of token 32p + i.
-    // A slot's barrier takes each thread's arrival when its copies have landed, so
-    // the whole ring may be in flight.
-    const int p0 = (warp - kTrSoft) * 32, ch = lane & 15, hl = lane >> 4;
-    const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * kTrBox + (uint32_t)(p0 + hl) * 128u;
-    uint32_t dsts[4];  // rows 2k + hl: the swizzle repeats every 8 rows
-#pragma unroll
-    for (int k = 0; k < 4; ++k) dsts[k] = dst0 + (uint32_t)k * 256u + (uint32_t)(((ch & 7) ^ hl ^ (2 * k)) << 4);
+    // ---- producers: warp p brings a quarter of each tile's tokens, 512 bytes an
+    // instruction (kRows rows); lane i looks up the pool row of its i-th token.  A
+    // slot's barrier takes each thread's arrival when its copies have landed, so the
+    // whole ring may be in flight.
+    constexpr int kCh = HD / 8, kRows = 32 / kCh, kTok = G::kT / kTrProd;
+    const int p0 = (warp - kTrSoft) * kTok, ch = lane % kCh, hl = lane / kCh;
+    const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * G::kBox + (uint32_t)(p0 + hl) * 128u;
     uint32_t ns = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
       const int32_t kv = g.v.ctx + g.v.rows;
       auto fetch = [&](int j) -> int32_t {  // pool row of this lane's token of tile j, -1: zeros
-        const int32_t t = (g.t0 + j) * kTrTile + p0 + lane;
-        if (j >= g.n || t >= kv) return -1;
+        const int32_t t = (g.t0 + j) * G::kT + p0 + lane;
+        if (j >= g.n || t >= kv || lane >= kTok) return -1;
         const int64_t slot = token_slot(a.seqs, g.s, t);
         if (slot < 0) report_error(a.status, kErrTokenRange, g.s);
         return slot < 0 ? -1 : (int32_t)(slot * a.nkv + g.kvh);
@@ -289,24 +291,22 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       // of a slot cost 90 cycles a copy.
       auto spread = [&](int32_t y, int32_t (&r)[16]) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) r[k] = __shfl_sync(0xffffffffu, y, 2 * k + hl);
+        for (int k = 0; k < 16; ++k) r[k] = __shfl_sync(0xffffffffu, y, kRows * k + hl);
       };
       auto bring = [&](const uint16_t *pool, const int32_t (&r)[16]) {
-#pragma unroll
-        for (int c = 0; c < G::kC; ++c) {
-          const uint32_t slot = ns % G::kSlots;
-          if (!tc_warp_wait_ready(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
-            ok = false;
-            return;
-          }
-          const uint16_t *src = pool + c * 128 + ch * 8;
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            cp_async16(dsts[k & 3] + slot * kTrSlot + (uint32_t)(k >> 2) * 1024u, src + (int64_t)max(r[k], 0) * HD,
-                       r[k] >= 0 ? 16u : 0u);
-          cp_async_arrive(sm32(&C.full[slot]));
-          ++ns;
+        const uint32_t slot = ns % G::kSlots;
+        if (!tc_warp_wait_ready(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
+          ok = false;
+          return;
         }
+        const uint16_t *src = pool + ch * 8;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)  // row p0 + kRows k + hl, its 16-byte chunks swizzled by row % 8
+          cp_async16(dst0 + slot * kTrSlot + (uint32_t)(k * kRows) * 128u +
+                         (uint32_t)(((ch & 7) ^ ((kRows * k + hl) & 7)) << 4),
+                     src + (int64_t)max(r[k], 0) * HD, r[k] >= 0 ? 16u : 0u);
+        cp_async_arrive(sm32(&C.full[slot]));
+        ++ns;
       };
       if (g.n > 0) {
         int32_t rv[16], rk[16];
@@ -335,7 +335,13 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         ok = ok && tc_wait_ready(sm32(&bar), parity, lim, abort_flag);
         return ok;
       };
-      auto landed = [&](uint32_t i) {  // slot number i of the ring holds its copy
+      // Slot number i of the ring holds its copy.  A parity tells two phases apart,
+      // so the slot's copy before this one has to be known to have landed.  S of
+      // tile j: that one is K, of a tile whose S this thread issued, or V of tile
+      // j - 4 at the latest, or the last V of a part that ended before tile j - 2;
+      // the group that freed the buffer of tile j - 2 had waited for its P V.  P V
+      // of tile j: it is V, or K of an earlier tile.
+      auto landed = [&](uint32_t i) {
         if (!wait(C.full[i % G::kSlots], (i / G::kSlots) & 1u)) return false;
         // the copies wrote through the generic proxy; the MMAs read through the async one
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -346,46 +352,36 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         if (g.n == 0) continue;
         if (is_s) {
           if (!wait(C.q_full, segs & 1u)) break;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         } else {  // the part before this one has left O
           if (segs > 0 && !wait(C.o_free, (segs - 1) & 1u)) break;
         }
         for (int j = 0; j < g.n && ok; ++j) {
-          const uint32_t b = (jg + j) % G::kSBuf, ph = ((jg + j) / G::kSBuf) & 1u;
-          const uint32_t s0 = tmem + G::kSCol + b * kTrTile;
+          const uint32_t jj = jg + j;
+          const uint32_t i = ns + (uint32_t)(is_s ? k_pos(j) : v_pos(j, g.n));
+          const uint32_t kv = sRing + (i % G::kSlots) * kTrSlot, b = jj & 1u;
           if (is_s) {
-            // the buffer's last tile: its P has been multiplied
-            if (jg + j >= G::kSBuf && !wait(C.pv_done[b], ph ^ 1u)) break;
-            for (int c = 0; c < G::kC; ++c) {
-              const uint32_t i = ns + (uint32_t)(k_pos(j) * G::kC + c);
-              if (!landed(i)) break;
-              const uint32_t kb = sRing + (i % G::kSlots) * kTrSlot;
+            if (jj >= 2 && !wait(C.s_free[b], ((jj >> 1) - 1u) & 1u)) break;  // tile j - 2 is read
+            if (!landed(i)) break;
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t in = (uint32_t)(kk >> 2) * kTrBox + (uint32_t)(kk & 3) * 32u;
-                mma_bf16(s0, sw128_desc(sQ + (uint32_t)c * 2u * kTrBox + in), sw128_desc(kb + in), kIdescS,
-                         (c > 0 || kk > 0) ? 1u : 0u);
-              }
-              mma_commit(sm32(&C.empty[i % G::kSlots]));
+            for (int kk = 0; kk < HD / 16; ++kk) {
+              const uint32_t in = (uint32_t)(kk & 3) * 32u;
+              mma_bf16(tmem + G::kSCol + b * G::kT, sw128_desc(sQ + (uint32_t)(kk >> 2) * G::kQBox + in),
+                       sw128_desc(kv + (uint32_t)(kk >> 2) * G::kBox + in), G::kIdescS, kk > 0 ? 1u : 0u);
             }
-            if (ok) mma_commit(sm32(&C.s_full[b]));
+            mma_commit(sm32(&C.empty[i % G::kSlots]));
+            mma_commit(sm32(&C.s_full[b]));
           } else {
-            if (!wait(C.p_ready[b], ph)) break;
-            for (int c = 0; c < G::kC; ++c) {
-              const uint32_t i = ns + (uint32_t)(v_pos(j, g.n) * G::kC + c);
-              if (!landed(i)) break;
-              const uint32_t vb = sRing + (i % G::kSlots) * kTrSlot;
+            if (!wait(C.p_ready[b], (jj >> 1) & 1u) || !landed(i)) break;
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
-                mma_bf16_ts(tmem + (uint32_t)c * 128u, s0 + kPCol + 8u * kk, sw128_mn_desc(vb + 2048u * kk, kTrBox), kIdescO,
-                            (j > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(sm32(&C.empty[i % G::kSlots]));
-            }
-            if (ok) mma_commit(sm32(&C.pv_done[b]));
+            for (int kk = 0; kk < G::kT / 16; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
+              mma_bf16_ts(tmem, tmem + G::kPCol + b * (G::kT / 2) + 8u * kk, sw128_mn_desc(kv + 2048u * kk, G::kBox),
+                          G::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(sm32(&C.empty[i % G::kSlots]));
+            mma_commit(sm32(&C.pv_done[b]));
           }
         }
         jg += (uint32_t)g.n;
-        ns += (uint32_t)(2 * g.n * G::kC);
+        ns += (uint32_t)(2 * g.n);
         ++segs;
       }
       // every MMA this thread issued has finished before TMEM is freed
@@ -409,16 +405,16 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp ^ 4)) : "memory");
       return C.top[w ^ 1][r];
     };
-    // P V of tile i, the last issued: its buffer's barrier cannot be further
-    // behind, for S of tile i (or a later one) waited for P V of tile i - kSBuf.
+    // P V of tile i.  A group waits for tile i - 2 before its tile i, so of either
+    // barrier no phase but the last two is ever in question.
     auto wait_pv = [&](uint32_t i) {
-      tc_warp_wait_ready(sm32(&C.pv_done[i % G::kSBuf]), (i / G::kSBuf) & 1u, lim, abort_flag);
+      tc_warp_wait_ready(sm32(&C.pv_done[i & 1u]), (i >> 1) & 1u, lim, abort_flag);
     };
     // This warp's rows of a part's Q into shared memory.  The copies arrive on
     // q_full by themselves; a sign or a zero scale has to pass through registers.
     auto load_q = [&](const TreeSeg &e) {
-      const int64_t m0 = (int64_t)e.mt * kTrTile;
-      const int rows = (int)min((int64_t)kTrTile, (int64_t)e.v.rows * a.group - m0);
+      const int64_t m0 = (int64_t)e.mt * kTrRows;
+      const int rows = (int)min((int64_t)kTrRows, (int64_t)e.v.rows * a.group - m0);
       constexpr int kCh = HD / 8;     // 16-byte chunks per row
       constexpr int kPer = 32 / kCh;  // rows per warp copy
       const int ch = lane % kCh, sub = lane / kCh;
@@ -428,7 +424,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         const int32_t m = (int32_t)(m0 + rr), j = fast_div(group_div, m);
         const int32_t head = e.kvh * a.group + (m - j * a.group);
         const uint16_t *src = a.q + (int64_t)(e.v.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch;
-        const uint32_t to = (uint32_t)(ch >> 3) * kTrBox + (uint32_t)rr * 128u + (uint32_t)(((ch & 7) ^ (rr & 7)) << 4);
+        const uint32_t to = (uint32_t)(ch >> 3) * G::kQBox + (uint32_t)rr * 128u + (uint32_t)(((ch & 7) ^ (rr & 7)) << 4);
         if (plain) {
           cp_async16(sQ + to, src, 16u);
         } else {
@@ -449,7 +445,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     if (more && g.n > 0) load_q(g);
     while (more) {
       ++seg;
-      const int64_t m = (int64_t)g.mt * kTrTile + r;
+      const int64_t m = (int64_t)g.mt * kTrRows + r;
       const bool valid = m < (int64_t)g.v.rows * a.group;
       const bool live = __any_sync(0xffffffffu, valid);  // this warp (and its pair) has rows
       const int32_t j_row = valid ? fast_div(group_div, (int32_t)m) : 0;
@@ -467,104 +463,94 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       };
       for (int j = 0; j < g.n; ++j, ++jg) {
         if ((int)(jg & 1u) != w) continue;
-        const uint32_t b = jg % G::kSBuf, sc = lane_base + G::kSCol + b * kTrTile;  // S and P
-        const int32_t t0 = (g.t0 + j) * kTrTile;
-        const bool masked = t0 + kTrTile > g.v.ctx;
-        tc_warp_wait_ready(sm32(&C.s_full[b]), (jg / G::kSBuf) & 1u, lim, abort_flag);
+        const uint32_t sc = lane_base + G::kSCol + (uint32_t)w * G::kT, pc = lane_base + G::kPCol + (uint32_t)w * (G::kT / 2);
+        const int32_t t0 = (g.t0 + j) * G::kT;
+        const bool masked = t0 + G::kT > g.v.ctx;
+        tc_warp_wait_ready(sm32(&C.s_full[w]), (jg >> 1) & 1u, lim, abort_flag);
+        if (jg >= 2) wait_pv(jg - 2);  // P's buffer is free
         tc_fence_after();
         if (live) {
-          uint64_t see[2] = {~0ull, ~0ull};
+          uint64_t see[G::kT / 64];
           if (masked) {
-            see[0] = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 - g.v.ctx);
-            see[1] = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 + 64 - g.v.ctx);
+#pragma unroll
+            for (int i = 0; i < G::kT / 64; ++i)
+              see[i] = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 + 64 * i - g.v.ctx);
           }
-          uint32_t sv[64];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          bool probe = j == 0, settled = false;  // probe: for the maximum alone
+          float part;
+          while (true) {
+            const float use = top == -INFINITY ? 0.f : top;
+            const uint64_t m2 = pair_f32(-use, -use);
+            uint64_t part2[2] = {0ull, 0ull};
+            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tmem_ld32(sc + 64u * q, sv);
-            tmem_ld32(sc + 64u * q + 32u, sv + 32);
-            tmem_wait_ld32(sv);
-            tmem_wait_ld32(sv + 32);
-            if (masked) {
+            for (int c = 0; c < G::kT / 32; ++c) {
+              uint32_t sv[32];
+              tmem_ld32(sc + 32u * c, sv);
+              tmem_wait_ld32(sv);
+              if (masked) {
+                const uint32_t bits = (uint32_t)(see[c >> 1] >> (32 * (c & 1)));
 #pragma unroll
-              for (int i = 0; i < 64; ++i)
-                if (!((see[q] >> i) & 1ull)) sv[i] = 0xFF800000u;  // -inf
+                for (int i = 0; i < 32; ++i)
+                  if (!((bits >> i) & 1u)) sv[i] = 0xFF800000u;  // -inf
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                mx[i & 1] = max3(mx[i & 1], __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
+              if (!probe) {
+                uint32_t p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float lo, hi;
+                  unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, m2), lo, hi);
+                  lo = ex2(lo);
+                  hi = ex2(hi);
+                  part2[i & 1] = add2(part2[i & 1], pair_f32(lo, hi));
+                  p[i] = pack_f32_bf16(lo, hi);
+                }
+                tmem_st16(pc + 16u * c, p);
+              }
             }
+            float s0, s1;
+            unpair_f32(add2(part2[0], part2[1]), s0, s1);
+            part = s0 + s1;
+            if (settled) break;
+            // what the other group's tile left, and whether this one passes it
+            const float t = j > 0 ? receive() : -INFINITY;
+            const float mine = fmaxf(mx[0], mx[1]);
+            const float want = mine == -INFINITY ? -INFINITY : mine * a.scale_log2;
+            const bool move = valid && (want > t + kTrSlack || (t == -INFINITY && want != -INFINITY));
+            const float now = move ? want : t;
+            if (!__any_sync(0xffffffffu, probe || now != top)) break;
+            if (j > 0 && __any_sync(0xffffffffu, move)) {  // O holds the earlier tiles of this part
+              const float alpha = move ? (t == -INFINITY ? 0.f : ex2(t - now)) : 1.f;
+              wait_pv(jg - 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < HD / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(lane_base + (uint32_t)(c * 16), o);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(sv[i]));
-          }
-          const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const float want = mine == -INFINITY ? -INFINITY : mine * a.scale_log2;
-          if (j > 0) rebase(receive());
-          const bool move = valid && (want > top + kTrSlack || (top == -INFINITY && want != -INFINITY));
-          const float alpha = move ? (top == -INFINITY ? 0.f : ex2(top - want)) : 1.f;
-          if (move) {
-            top = want;
-            sum *= alpha;
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(lane_base + (uint32_t)(c * 16), o);
+              }
+            }
+            rebase(now);
+            probe = false;
+            settled = true;
           }
           post(top);
-          if (j > 0 && __any_sync(0xffffffffu, move)) {  // O holds the earlier tiles of this part
-            wait_pv(jg - 1);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < HD / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(lane_base + (uint32_t)(c * 16), o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st16(lane_base + (uint32_t)(c * 16), o);
-            }
-          }
-          const float use = top == -INFINITY ? 0.f : top;
-          const uint64_t m2 = pair_f32(-use, -use);
-          uint64_t part[2] = {0ull, 0ull};
-          // The second half of S is still in registers, the first is read again; P
-          // lies over the second half.
-#pragma unroll
-          for (int q = 1; q >= 0; --q) {
-            if (q == 0) {
-              tmem_ld32(sc, sv);
-              tmem_ld32(sc + 32u, sv + 32);
-              tmem_wait_ld32(sv);
-              tmem_wait_ld32(sv + 32);
-              if (masked) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  if (!((see[0] >> i) & 1ull)) sv[i] = 0xFF800000u;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t p[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float lo, hi;
-                unpair_f32(fma2(pair_f32(__uint_as_float(sv[32 * e + 2 * i]), __uint_as_float(sv[32 * e + 2 * i + 1])), c2, m2),
-                           lo, hi);
-                lo = ex2(lo);
-                hi = ex2(hi);
-                part[i & 1] = add2(part[i & 1], pair_f32(lo, hi));
-                p[i] = pack_f32_bf16(lo, hi);
-              }
-              tmem_st16(sc + kPCol + 32u * q + 16u * e, p);
-            }
-          }
-          float s0, s1;
-          unpair_f32(add2(part[0], part[1]), s0, s1);
-          sum += s0 + s1;
+          sum += part;
           tmem_wait_st();
         }
         if (masked && veiled) {
           // A value that is not finite would reach, as 0 x inf, the rows that do
           // not see its token: it is cleared here and given to the rows that do
-          // see it when the output is written.  (P V of the tile before is done, so
-          // each of V's slots has had its earlier copy: a parity alone could not tell.)
-          if (jg > 0) wait_pv(jg - 1);
-          const uint32_t at = ns + (uint32_t)(v_pos(j, g.n) * G::kC);
-          for (int c = 0; c < G::kC; ++c) {
-            const uint32_t slot = (at + c) % G::kSlots;
-            tc_warp_wait_ready(sm32(&C.full[slot]), ((at + c) / G::kSlots) & 1u, lim, abort_flag);
+          // see it when the output is written.  (The slot's earlier copy is known to
+          // have landed, as for the P V issuer: P V of the tile before the last is done.)
+          {
+            const uint32_t at = ns + (uint32_t)v_pos(j, g.n), slot = at % G::kSlots;
+            tc_warp_wait_ready(sm32(&C.full[slot]), (at / G::kSlots) & 1u, lim, abort_flag);
             __syncwarp();
             uint8_t *vs = tr_smem + G::kRingOff + slot * kTrSlot;
             for (int i = (warp & 3) * 32 + lane; i < (int)(kTrSlot / 16); i += 128) {
@@ -587,18 +573,22 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sm32(&C.p_ready[b]));
+        if (lane == 0) {
+          mbar_arrive(sm32(&C.s_free[w]));
+          mbar_arrive(sm32(&C.p_ready[w]));
+        }
       }
-      ns += (uint32_t)(2 * g.n * G::kC);
+      ns += (uint32_t)(2 * g.n);
       const uint32_t last = jg - 1;  // the part's last tile
       if (g.n > 0) {  // its S is done, and with it every one of this part: Q may go
-        tc_warp_wait_ready(sm32(&C.s_full[last % G::kSBuf]), (last / G::kSBuf) & 1u, lim, abort_flag);
+        tc_warp_wait_ready(sm32(&C.s_full[last & 1u]), (last >> 1) & 1u, lim, abort_flag);
         if (live && (int)(last & 1u) != w) rebase(receive());
       }
       TreeSeg next;
       more = walk.next(next);
       if (more && next.n > 0) load_q(next);
       if (g.n > 0) {
+        if (last > 0 && (int)(last & 1u) != w) wait_pv(last - 1);
         wait_pv(last);
         tc_fence_after();
       }
@@ -629,8 +619,8 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
           if (!valid) continue;
           if (fix) {
             // every token of the tiles that were cleared
-            const int32_t t_lo = max(g.t0, g.v.ctx / kTrTile) * kTrTile;
-            const int32_t t_hi = min(g.v.ctx + g.v.rows, (g.t0 + g.n) * kTrTile);
+            const int32_t t_lo = max(g.t0, g.v.ctx / G::kT) * G::kT;
+            const int32_t t_hi = min(g.v.ctx + g.v.rows, (g.t0 + g.n) * G::kT);
             for (int32_t t = t_lo; t < t_hi; ++t) {
               if (t >= g.v.ctx && !sees_draft(mrow, j_row, t - g.v.ctx)) continue;
               const int64_t slot = token_slot(a.seqs, g.s, t);
@@ -699,11 +689,11 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, i
   bool mine = false;
   if (row >= 0) {
     const int32_t s = seq_of_row(a.seqs, row);
-    const SeqTiles q = seq_tiles(a, read_seq(a.seqs, s));
+    const SeqTiles q = seq_tiles<TreeGeom<HD>::kT>(a, read_seq(a.seqs, s));
     if (row >= q.v.row0 && row < q.v.row0 + q.v.rows) {
       const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
-      const int32_t mt = (int32_t)(m / kTrTile);
-      r = (int32_t)(m % kTrTile);
+      const int32_t mt = (int32_t)(m / kTrRows);
+      r = (int32_t)(m % kTrRows);
       const int64_t per = (base[a.seqs.n_seqs] + ctas - 1) / ctas;
       const int64_t u0 = base[s] + ((int64_t)kvh * q.m_tiles + mt) * q.tiles;
       if (((u0 + q.tiles) >> 31) == 0) {
@@ -767,7 +757,7 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, i
 
 // The workspace: the sequences' first tiles, then the parts' (max, sum) and O.
 int32_t part_rows_of(int64_t n_rows, int32_t group) {
-  return (int32_t)(n_rows * group < kTrTile ? n_rows * group : kTrTile);
+  return (int32_t)(n_rows * group < kTrRows ? n_rows * group : kTrRows);
 }
 int64_t base_bytes(int32_t n_seqs) { return ((int64_t)(n_seqs + 1) * 8 + 255) / 256 * 256; }
 int64_t ml_bytes(int32_t part_rows) { return ((int64_t)kTrMaxCtas * 2 * part_rows * 8 + 255) / 256 * 256; }
@@ -797,11 +787,11 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   cudaError_t r = launch_dependent(tree_attn_kernel<HD>, dim3((unsigned)ctas), dim3(kTrThreads), tree_smem<HD>(), stream, 1u,
                                    a, group_div, part_rows, q_and, q_xor, base, ml, o);
   // a table of one tile leaves no unit to share
-  if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kTrTile) return r;
+  if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= TreeGeom<HD>::kT) return r;
   // One group of parts per warp where units outnumber the CTAs (few parts each),
   // eight where a unit spreads over many.
   const int64_t rows8 = ((int64_t)a.seqs.n_rows * a.group + 7) / 8;
-  const int64_t units = (int64_t)a.nkv * (((int64_t)a.seqs.n_rows * a.group + kTrTile - 1) / kTrTile);
+  const int64_t units = (int64_t)a.nkv * (((int64_t)a.seqs.n_rows * a.group + kTrRows - 1) / kTrRows);
   const bool many = ctas >= 8 * units;
   const int64_t blocks = many ? rows8 : (rows8 + kJoinWarps - 1) / kJoinWarps;
   return launch_dependent(many ? tree_join_kernel<HD, kJoinWarps> : tree_join_kernel<HD, 1>,
