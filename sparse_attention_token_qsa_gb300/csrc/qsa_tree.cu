@@ -7,7 +7,7 @@
 //
 // The rows of one sequence that read the same KV head (drafted row x query
 // head of the group) form the M dimension of two tcgen05 products per tile of
-// 128 tokens (64 at head_dim 256): S = Q K^T (operands in shared memory,
+// 96 tokens (64 at head_dim 256): S = Q K^T (operands in shared memory,
 // accumulator in TMEM), and O += P V (P as bf16 in TMEM, V read MN-major).  A unit
 // of work is (sequence, KV head, 128 such rows); its tiles are a run of the
 // launch's linear list of tiles, of which every CTA (one per SM) takes an equal,
@@ -17,8 +17,8 @@
 // them in a fixed order.
 //
 // Fourteen warps: two groups of four (warps 0-3 and 4-7) do the softmax, a row
-// per thread, tiles in turn; warps 8-11 copy K and V rows into a ring of 32 KiB
-// slots (a tile of K or of V, 128-byte swizzle); warp 12 issues S, up to two
+// per thread, tiles in turn; warps 8-11 copy K and V rows into a ring of
+// slots (a tile of K or of V, 128-byte swizzle); warp 12 issues S, up to three
 // tiles ahead, warp 13 P V, so that neither one's waits leave the tensor pipe
 // idle.  The copies are 16-byte cp.async, which take any page size alike:
 // streaming tiles of pages of 16 tokens and nothing else, they moved 9.7 TB/s
@@ -52,20 +52,22 @@ constexpr int kTrMmaO = kTrMmaS + 1;        // issues O += P V
 constexpr int kTrWarps = kTrMmaO + 1, kTrThreads = 32 * kTrWarps;
 constexpr int kTrRows = 128;   // rows of a unit: the MMA's M
 constexpr int kTrMaxCtas = 160;
-constexpr uint32_t kTrSlot = 32768;  // a ring slot: a tile of K or V
-constexpr float kTrSlack = 16.0f;    // log2 units a logit may pass the reference by
+constexpr float kTrSlack = 16.0f;  // log2 units a logit may pass the reference by
 constexpr long long kTrSpinLimit = 4000000000LL;
 
 template <int HD>
 struct TreeGeom {
-  static constexpr int kT = (int)kTrSlot / (2 * HD);        // tokens per tile
-  static constexpr int kSlots = HD == 256 ? 5 : 6;
+  // Tokens per tile: as many as leave TMEM room for three S buffers beside O and P
+  // (with two, S of the tile after the next waited for this one's softmax).
+  static constexpr int kT = HD == 256 ? 64 : 96;
   static constexpr uint32_t kQBox = kTrRows * 128;          // 64 dims of Q
   static constexpr uint32_t kBox = kT * 128;                // 64 dims of a tile
+  static constexpr uint32_t kSlot = kT * HD * 2;            // a ring slot: a tile of K or V
+  static constexpr int kSlots = HD == 256 ? 5 : 8;
   static constexpr uint32_t kRingOff = (HD / 64) * kQBox;
-  static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kTrSlot;
-  // TMEM columns: O, then an S and a P buffer per softmax group
-  static constexpr uint32_t kSCol = HD, kPCol = HD + 2 * kT;
+  static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kSlot;
+  // TMEM columns: O, three S buffers, a P buffer per softmax group
+  static constexpr uint32_t kSCol = HD, kPCol = HD + 3 * kT;
   static_assert(kPCol + kT <= 512, "TMEM has 512 columns");
   // kind::f16, D f32, A and B bf16, M = 128; S: N = tokens, K-major B; O: N = dims, MN-major B
   static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
@@ -76,8 +78,10 @@ struct TreeGeom {
 struct TreeCtrl {
   float top[2][kTrRows];   // [group that wrote it][row]: the reference, log2 units
   float sums[2][kTrRows];  // [group][row]: its share of the row's sum
-  uint64_t full[6], empty[6];
-  uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];  // per softmax group
+  uint64_t full[8], empty[8];
+  uint64_t s_full[3], s_free[3];  // per S buffer: tile % 3
+  uint64_t p_ready[2];            // per softmax group
+  uint64_t pv_done[4];            // tile % 4
   uint64_t q_full, o_free, drain[2];
   int64_t scan[kTrWarps], found_off;
   int32_t found_seq, bad[2], abort;
@@ -186,14 +190,16 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       mbar_init(sm32(&C.full[i]), 32 * kTrProd);
       mbar_init(sm32(&C.empty[i]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 3; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
       mbar_init(sm32(&C.s_free[b]), kTrSoft / 2);
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(sm32(&C.p_ready[b]), kTrSoft / 2);
-      mbar_init(sm32(&C.pv_done[b]), 1);
       mbar_init(sm32(&C.drain[b]), 1);
       C.bad[b] = 0;
     }
+    for (int b = 0; b < 4; ++b) mbar_init(sm32(&C.pv_done[b]), 1);
     mbar_init(sm32(&C.q_full), 32 * kTrSoft);
     mbar_init(sm32(&C.o_free), kTrSoft);
     C.abort = 0;
@@ -272,7 +278,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     // instruction (kRows rows); lane i looks up the pool row of its i-th token.  A
     // slot's barrier takes each thread's arrival when its copies have landed, so the
     // whole ring may be in flight.
-    constexpr int kCh = HD / 8, kRows = 32 / kCh, kTok = G::kT / kTrProd;
+    constexpr int kCh = HD / 8, kRows = 32 / kCh, kTok = G::kT / kTrProd, kN = kTok / kRows;
     const int p0 = (warp - kTrSoft) * kTok, ch = lane % kCh, hl = lane / kCh;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * G::kBox + (uint32_t)(p0 + hl) * 128u;
     uint32_t ns = 0;
@@ -286,14 +292,14 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         if (slot < 0) report_error(a.status, kErrTokenRange, g.s);
         return slot < 0 ? -1 : (int32_t)(slot * a.nkv + g.kvh);
       };
-      // Pool rows of this thread's 16 copies of a slot, spread from the lanes that
+      // Pool rows of this thread's copies of a slot, spread from the lanes that
       // looked them up before the slot is waited for: a shuffle between the copies
       // of a slot cost 90 cycles a copy.
-      auto spread = [&](int32_t y, int32_t (&r)[16]) {
+      auto spread = [&](int32_t y, int32_t (&r)[kN]) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) r[k] = __shfl_sync(0xffffffffu, y, kRows * k + hl);
+        for (int k = 0; k < kN; ++k) r[k] = __shfl_sync(0xffffffffu, y, kRows * k + hl);
       };
-      auto bring = [&](const uint16_t *pool, const int32_t (&r)[16]) {
+      auto bring = [&](const uint16_t *pool, const int32_t (&r)[kN]) {
         const uint32_t slot = ns % G::kSlots;
         if (!tc_warp_wait_ready(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
           ok = false;
@@ -301,15 +307,15 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         }
         const uint16_t *src = pool + ch * 8;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)  // row p0 + kRows k + hl, its 16-byte chunks swizzled by row % 8
-          cp_async16(dst0 + slot * kTrSlot + (uint32_t)(k * kRows) * 128u +
+        for (int k = 0; k < kN; ++k)  // row p0 + kRows k + hl, its 16-byte chunks swizzled by row % 8
+          cp_async16(dst0 + slot * G::kSlot + (uint32_t)(k * kRows) * 128u +
                          (uint32_t)(((ch & 7) ^ ((kRows * k + hl) & 7)) << 4),
                      src + (int64_t)max(r[k], 0) * HD, r[k] >= 0 ? 16u : 0u);
         cp_async_arrive(sm32(&C.full[slot]));
         ++ns;
       };
       if (g.n > 0) {
-        int32_t rv[16], rk[16];
+        int32_t rv[kN], rk[kN];
         int32_t y = fetch(0);
         spread(y, rv);
         y = fetch(1);
@@ -320,7 +326,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
           if (j + 1 < g.n) bring(a.k_pool, rk);
           if (ok) bring(a.v_pool, rv);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) rv[k] = rk[k];
+          for (int k = 0; k < kN; ++k) rv[k] = rk[k];
         }
       }
     }
@@ -329,6 +335,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     // ---- MMA issuers, one thread each
     if (lane == 0) {
       const bool is_s = warp == kTrMmaS;
+      // A descriptor's address sits in its low word: the steps of a tile add to it
+      // (shared memory ends below 2^18, so no carry leaves the address's 14 bits).
+      const uint32_t q_lo = (uint32_t)sw128_desc(sQ);
+      const uint32_t kDescHi = (uint32_t)(sw128_desc(0) >> 32);
       uint32_t ns = 0, jg = 0, segs = 0;  // slots, tiles and parts before this part
       bool ok = true;
       auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -337,10 +347,11 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       };
       // Slot number i of the ring holds its copy.  A parity tells two phases apart,
       // so the slot's copy before this one has to be known to have landed.  S of
-      // tile j: that one is K, of a tile whose S this thread issued, or V of tile
-      // j - 4 at the latest, or the last V of a part that ended before tile j - 2;
-      // the group that freed the buffer of tile j - 2 had waited for its P V.  P V
-      // of tile j: it is V, or K of an earlier tile.
+      // tile j (five slots; more are easier): that one is K, of a tile whose S this
+      // thread issued, or V of tile j - 4 at the latest, whose P V was waited for, or,
+      // where j begins a part, the last V of a part before the last, whose output was
+      // written before this part's Q was fetched.  P V of tile j: it is V, or K of an
+      // earlier tile.
       auto landed = [&](uint32_t i) {
         if (!wait(C.full[i % G::kSlots], (i / G::kSlots) & 1u)) return false;
         // the copies wrote through the generic proxy; the MMAs read through the async one
@@ -358,26 +369,30 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         for (int j = 0; j < g.n && ok; ++j) {
           const uint32_t jj = jg + j;
           const uint32_t i = ns + (uint32_t)(is_s ? k_pos(j) : v_pos(j, g.n));
-          const uint32_t kv = sRing + (i % G::kSlots) * kTrSlot, b = jj & 1u;
+          const uint32_t kv = sRing + (i % G::kSlots) * G::kSlot;
           if (is_s) {
-            if (jj >= 2 && !wait(C.s_free[b], ((jj >> 1) - 1u) & 1u)) break;  // tile j - 2 is read
+            const uint32_t b = jj % 3u;
+            if (jj >= 3 && !wait(C.s_free[b], (jj / 3u - 1u) & 1u)) break;  // tile j - 3 is read
+            if (jj >= 4 && !wait(C.pv_done[jj & 3u], ((jj >> 2) - 1u) & 1u)) break;
             if (!landed(i)) break;
+            const uint32_t d = tmem + G::kSCol + b * G::kT, k_lo = (uint32_t)sw128_desc(kv);
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint32_t in = (uint32_t)(kk & 3) * 32u;
-              mma_bf16(tmem + G::kSCol + b * G::kT, sw128_desc(sQ + (uint32_t)(kk >> 2) * G::kQBox + in),
-                       sw128_desc(kv + (uint32_t)(kk >> 2) * G::kBox + in), G::kIdescS, kk > 0 ? 1u : 0u);
+              const uint32_t in = (uint32_t)(kk & 3) * 2u;  // 32 bytes
+              mma_bf16(d, desc_of(q_lo + (uint32_t)(kk >> 2) * (G::kQBox >> 4) + in, kDescHi),
+                       desc_of(k_lo + (uint32_t)(kk >> 2) * (G::kBox >> 4) + in, kDescHi), G::kIdescS, kk > 0 ? 1u : 0u);
             }
             mma_commit(sm32(&C.empty[i % G::kSlots]));
             mma_commit(sm32(&C.s_full[b]));
           } else {
+            const uint32_t b = jj & 1u;
             if (!wait(C.p_ready[b], (jj >> 1) & 1u) || !landed(i)) break;
+            const uint32_t p = tmem + G::kPCol + b * (G::kT / 2), v_lo = (uint32_t)sw128_mn_desc(kv, G::kBox);
 #pragma unroll
             for (int kk = 0; kk < G::kT / 16; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
-              mma_bf16_ts(tmem, tmem + G::kPCol + b * (G::kT / 2) + 8u * kk, sw128_mn_desc(kv + 2048u * kk, G::kBox),
-                          G::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+              mma_bf16_ts(tmem, p + 8u * kk, desc_of(v_lo + 128u * kk, kDescHi), G::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
             mma_commit(sm32(&C.empty[i % G::kSlots]));
-            mma_commit(sm32(&C.pv_done[b]));
+            mma_commit(sm32(&C.pv_done[jj & 3u]));
           }
         }
         jg += (uint32_t)g.n;
@@ -405,10 +420,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp ^ 4)) : "memory");
       return C.top[w ^ 1][r];
     };
-    // P V of tile i.  A group waits for tile i - 2 before its tile i, so of either
-    // barrier no phase but the last two is ever in question.
+    // P V of tile i.  A group has waited for tile i - 4 (or a later one) by then,
+    // so of a barrier no phase but the last two is ever in question.
     auto wait_pv = [&](uint32_t i) {
-      tc_warp_wait_ready(sm32(&C.pv_done[i & 1u]), (i >> 1) & 1u, lim, abort_flag);
+      tc_warp_wait_ready(sm32(&C.pv_done[i & 3u]), (i >> 2) & 1u, lim, abort_flag);
     };
     // This warp's rows of a part's Q into shared memory.  The copies arrive on
     // q_full by themselves; a sign or a zero scale has to pass through registers.
@@ -463,17 +478,16 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       };
       for (int j = 0; j < g.n; ++j, ++jg) {
         if ((int)(jg & 1u) != w) continue;
-        const uint32_t sc = lane_base + G::kSCol + (uint32_t)w * G::kT, pc = lane_base + G::kPCol + (uint32_t)w * (G::kT / 2);
+        const uint32_t b = jg % 3u, sc = lane_base + G::kSCol + b * G::kT, pc = lane_base + G::kPCol + (uint32_t)w * (G::kT / 2);
         const int32_t t0 = (g.t0 + j) * G::kT;
         const bool masked = t0 + G::kT > g.v.ctx;
-        tc_warp_wait_ready(sm32(&C.s_full[w]), (jg >> 1) & 1u, lim, abort_flag);
-        if (jg >= 2) wait_pv(jg - 2);  // P's buffer is free
+        tc_warp_wait_ready(sm32(&C.s_full[b]), (jg / 3u) & 1u, lim, abort_flag);
         tc_fence_after();
         if (live) {
-          uint64_t see[G::kT / 64];
+          uint64_t see[(G::kT + 63) / 64];
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < G::kT / 64; ++i)
+            for (int i = 0; i < (G::kT + 63) / 64; ++i)
               see[i] = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 + 64 * i - g.v.ctx);
           }
           bool probe = j == 0, settled = false;  // probe: for the maximum alone
@@ -507,6 +521,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
                   hi = ex2(hi);
                   part2[i & 1] = add2(part2[i & 1], pair_f32(lo, hi));
                   p[i] = pack_f32_bf16(lo, hi);
+                }
+                if (c == 0 && jg >= 2) {  // P's buffer is free
+                  wait_pv(jg - 2);
+                  tc_fence_after();
                 }
                 tmem_st16(pc + 16u * c, p);
               }
@@ -542,18 +560,20 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
           post(top);
           sum += part;
           tmem_wait_st();
+        } else if (jg >= 2) {
+          wait_pv(jg - 2);  // every warp keeps up with the barriers
         }
         if (masked && veiled) {
           // A value that is not finite would reach, as 0 x inf, the rows that do
           // not see its token: it is cleared here and given to the rows that do
           // see it when the output is written.  (The slot's earlier copy is known to
-          // have landed, as for the P V issuer: P V of the tile before the last is done.)
+          // have landed once P V of the tile before the last is done.)
           {
             const uint32_t at = ns + (uint32_t)v_pos(j, g.n), slot = at % G::kSlots;
             tc_warp_wait_ready(sm32(&C.full[slot]), (at / G::kSlots) & 1u, lim, abort_flag);
             __syncwarp();
-            uint8_t *vs = tr_smem + G::kRingOff + slot * kTrSlot;
-            for (int i = (warp & 3) * 32 + lane; i < (int)(kTrSlot / 16); i += 128) {
+            uint8_t *vs = tr_smem + G::kRingOff + slot * G::kSlot;
+            for (int i = (warp & 3) * 32 + lane; i < (int)(G::kSlot / 16); i += 128) {
               uint4 *q = reinterpret_cast<uint4 *>(vs) + i;
               const uint4 x = *q;
               uint32_t e[4] = {x.x, x.y, x.z, x.w};
@@ -574,14 +594,14 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(sm32(&C.s_free[w]));
+          mbar_arrive(sm32(&C.s_free[b]));
           mbar_arrive(sm32(&C.p_ready[w]));
         }
       }
       ns += (uint32_t)(2 * g.n);
       const uint32_t last = jg - 1;  // the part's last tile
       if (g.n > 0) {  // its S is done, and with it every one of this part: Q may go
-        tc_warp_wait_ready(sm32(&C.s_full[last & 1u]), (last >> 1) & 1u, lim, abort_flag);
+        tc_warp_wait_ready(sm32(&C.s_full[last % 3u]), (last / 3u) & 1u, lim, abort_flag);
         if (live && (int)(last & 1u) != w) rebase(receive());
       }
       TreeSeg next;
