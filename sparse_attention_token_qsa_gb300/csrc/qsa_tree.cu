@@ -166,8 +166,8 @@ struct TreeWalk {
   }
 };
 
-// Ring position of tile j's K and V among a part's n tiles: K0, K1, V0, K2, V1, ..., V(n-1), the order the MMAs take them in.
-__device__ __forceinline__ int k_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
+// Ring position of tile j's V among a part's n tiles, counted from the part's
+// first copy: K0, K1, V0, K2, V1, ..., V(n-1), about the order the MMAs take them in.
 __device__ __forceinline__ int v_pos(int j, int n) { return j + 1 < n ? 2 + 2 * j : 2 * n - 1; }
 
 __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
@@ -332,72 +332,86 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
   } else if (warp >= kTrMmaS) {
-    // ---- MMA issuers, one thread each
+    // ---- MMA issuers, one thread each.  What they do between MMAs is on the tensor
+    // pipe's time, so slots, buffers and phases are stepped, not divided.
     if (lane == 0) {
-      const bool is_s = warp == kTrMmaS;
-      // A descriptor's address sits in its low word: the steps of a tile add to it
-      // (shared memory ends below 2^18, so no carry leaves the address's 14 bits).
-      const uint32_t q_lo = (uint32_t)sw128_desc(sQ);
-      const uint32_t kDescHi = (uint32_t)(sw128_desc(0) >> 32);
-      uint32_t ns = 0, jg = 0, segs = 0;  // slots, tiles and parts before this part
       bool ok = true;
       auto wait = [&](uint64_t &bar, uint32_t parity) {
         ok = ok && tc_wait_ready(sm32(&bar), parity, lim, abort_flag);
         return ok;
       };
-      // Slot number i of the ring holds its copy.  A parity tells two phases apart,
-      // so the slot's copy before this one has to be known to have landed.  S of
-      // tile j (five slots; more are easier): that one is K, of a tile whose S this
-      // thread issued, or V of tile j - 4 at the latest, whose P V was waited for, or,
-      // where j begins a part, the last V of a part before the last, whose output was
-      // written before this part's Q was fetched.  P V of tile j: it is V, or K of an
-      // earlier tile.
-      auto landed = [&](uint32_t i) {
-        if (!wait(C.full[i % G::kSlots], (i / G::kSlots) & 1u)) return false;
+      uint32_t slot = 0, phase = 0;  // of the ring
+      auto step = [&](uint32_t n) {
+        slot += n;
+        if (slot >= (uint32_t)G::kSlots) {
+          slot -= (uint32_t)G::kSlots;
+          phase ^= 1u;
+        }
+      };
+      // The slot holds its copy.  A parity tells two phases apart, so the slot's copy
+      // before this one has to be known to have landed.  S of tile j (five slots; more
+      // are easier): that one is K, of a tile whose S this thread issued, or V of tile
+      // j - 4 at the latest, whose P V was waited for, or, where j begins a part, the
+      // last V of a part before the last, whose output was written before this part's
+      // Q was fetched.  P V of tile j: it is V, or K of an earlier tile.
+      auto landed = [&]() {
+        if (!wait(C.full[slot], phase)) return false;
         // the copies wrote through the generic proxy; the MMAs read through the async one
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_after();
         return true;
       };
-      while (ok && walk.next(g)) {
-        if (g.n == 0) continue;
-        if (is_s) {
-          if (!wait(C.q_full, segs & 1u)) break;
-        } else {  // the part before this one has left O
-          if (segs > 0 && !wait(C.o_free, (segs - 1) & 1u)) break;
-        }
-        for (int j = 0; j < g.n && ok; ++j) {
-          const uint32_t jj = jg + j;
-          const uint32_t i = ns + (uint32_t)(is_s ? k_pos(j) : v_pos(j, g.n));
-          const uint32_t kv = sRing + (i % G::kSlots) * G::kSlot;
-          if (is_s) {
-            const uint32_t b = jj % 3u;
-            if (jj >= 3 && !wait(C.s_free[b], (jj / 3u - 1u) & 1u)) break;  // tile j - 3 is read
-            if (jj >= 4 && !wait(C.pv_done[jj & 3u], ((jj >> 2) - 1u) & 1u)) break;
-            if (!landed(i)) break;
-            const uint32_t d = tmem + G::kSCol + b * G::kT, k_lo = (uint32_t)sw128_desc(kv);
+      // A descriptor's address sits in its low word: the steps of a tile add to it
+      // (shared memory ends below 2^18, so no carry leaves the address's 14 bits).
+      const uint32_t desc_hi = (uint32_t)(sw128_desc(0) >> 32);
+      uint32_t jg = 0, part = 0;  // tiles and parts before this one
+      if (warp == kTrMmaS) {
+        const uint32_t q_lo = (uint32_t)sw128_desc(sQ), r_lo = (uint32_t)sw128_desc(sRing);
+        uint32_t b = 0, b_phase = 1;  // S buffer, parity of its s_free phase before this use
+        while (ok && walk.next(g)) {
+          if (g.n == 0) continue;
+          if (!wait(C.q_full, part & 1u)) break;
+          ++part;
+          for (int j = 0; j < g.n; ++j, ++jg) {
+            if (jg >= 3 && !wait(C.s_free[b], b_phase)) break;  // tile j - 3 is read
+            if (HD == 256 && jg >= 4 && !wait(C.pv_done[jg & 3u], ((jg >> 2) & 1u) ^ 1u)) break;
+            if (j > 0) step(j == 1 ? 1u : 2u);
+            if (!landed()) break;
+            const uint32_t d = tmem + G::kSCol + b * G::kT, k_lo = r_lo + slot * (G::kSlot >> 4);
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
               const uint32_t in = (uint32_t)(kk & 3) * 2u;  // 32 bytes
-              mma_bf16(d, desc_of(q_lo + (uint32_t)(kk >> 2) * (G::kQBox >> 4) + in, kDescHi),
-                       desc_of(k_lo + (uint32_t)(kk >> 2) * (G::kBox >> 4) + in, kDescHi), G::kIdescS, kk > 0 ? 1u : 0u);
+              mma_bf16(d, desc_of(q_lo + (uint32_t)(kk >> 2) * (G::kQBox >> 4) + in, desc_hi),
+                       desc_of(k_lo + (uint32_t)(kk >> 2) * (G::kBox >> 4) + in, desc_hi), G::kIdescS, kk > 0 ? 1u : 0u);
             }
-            mma_commit(sm32(&C.empty[i % G::kSlots]));
+            mma_commit(sm32(&C.empty[slot]));
             mma_commit(sm32(&C.s_full[b]));
-          } else {
-            const uint32_t b = jj & 1u;
-            if (!wait(C.p_ready[b], (jj >> 1) & 1u) || !landed(i)) break;
-            const uint32_t p = tmem + G::kPCol + b * (G::kT / 2), v_lo = (uint32_t)sw128_mn_desc(kv, G::kBox);
+            if (++b == 3) {
+              b = 0;
+              b_phase ^= 1u;
+            }
+          }
+          step(g.n == 1 ? 2u : 3u);  // past V(n - 2) and V(n - 1)
+        }
+      } else {
+        const uint32_t r_lo = (uint32_t)sw128_mn_desc(sRing, G::kBox);
+        while (ok && walk.next(g)) {
+          if (g.n == 0) continue;
+          if (part > 0 && !wait(C.o_free, (part - 1) & 1u)) break;  // the part before has left O
+          ++part;
+          for (int j = 0; j < g.n; ++j, ++jg) {
+            if (!wait(C.p_ready[jg & 1u], (jg >> 1) & 1u)) break;
+            step(j + 1 < g.n ? 2u : 1u);
+            if (!landed()) break;
+            const uint32_t p = tmem + G::kPCol + (jg & 1u) * (G::kT / 2), v_lo = r_lo + slot * (G::kSlot >> 4);
 #pragma unroll
             for (int kk = 0; kk < G::kT / 16; ++kk)  // 16 tokens a step: 8 columns of P, 2 KiB of a V box
-              mma_bf16_ts(tmem, p + 8u * kk, desc_of(v_lo + 128u * kk, kDescHi), G::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(sm32(&C.empty[i % G::kSlots]));
-            mma_commit(sm32(&C.pv_done[jj & 3u]));
+              mma_bf16_ts(tmem, p + 8u * kk, desc_of(v_lo + 128u * kk, desc_hi), G::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(sm32(&C.empty[slot]));
+            mma_commit(sm32(&C.pv_done[jg & 3u]));
           }
+          step(1u);
         }
-        jg += (uint32_t)g.n;
-        ns += (uint32_t)(2 * g.n);
-        ++segs;
       }
       // every MMA this thread issued has finished before TMEM is freed
       mma_commit(sm32(&C.drain[warp - kTrMmaS]));
