@@ -643,6 +643,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         for (int c = 0; c < HD / 64; ++c) {
           const int d0 = w * (HD / 2) + c * 32;
           uint32_t o[32];
+          __syncwarp();
           if (g.n > 0) {
             tmem_ld32(lane_base + (uint32_t)d0, o);
             tmem_wait_ld32(o);

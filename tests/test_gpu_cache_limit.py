@@ -36,3 +36,30 @@ def test_tree_attention_gives_up_and_recovers():
         assert st[0] == 5
         got, st = run()
         assert st == (0, 0) and np.array_equal(got, want)
+
+
+def test_attention_mass_gives_up_and_recovers():
+    import sparse_attention_token_qsa_gb300 as qsa
+
+    default = qsa.qsa_wait_limit_cycles()
+    for hd, rows in ((128, 5), (128, 90), (256, 5), (256, 90)):
+        c = Cache(qi.rng_for(71, salt=hd + rows), [5000, 40], [rows, 9], 8, 2, hd, 16, "tree")
+        args = c.mass_args(dev(c.q), c.nq * hd)
+        lse = torch.full((c.n_rows, c.nq), 9.0, dtype=torch.float32, device="cuda")
+
+        def run():
+            mass = torch.zeros((2, 2, 5096), dtype=torch.float32, device="cuda")
+            st = qsa.new_status()
+            qsa.qsa_attn_mass(*args, hd ** -0.5, lse, None, 1.0, mass, 5096, st)
+            return mass.cpu().numpy(), qsa.qsa_read_status(st)
+
+        want, st = run()
+        assert st == (0, 0)
+        try:
+            qsa.qsa_set_wait_limit_cycles(1)
+            _, st = run()
+        finally:
+            qsa.qsa_set_wait_limit_cycles(default)
+        assert st[0] == 5
+        got, st = run()
+        assert st == (0, 0) and np.array_equal(got, want)
