@@ -452,54 +452,57 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
         if (g.cols > 0) {
           if (!wait(C.s_full[w], (at >> 1) & 1u)) break;
           tc_fence_after();
-          if (t0 + kMsT <= g.ctx) {  // every row attends every token
-            uint64_t acc[2] = {0ull, 0ull};
-#pragma unroll 2
-            for (int c = 0; c < cols16; c += 16) {
-              uint32_t sv[16];
-              tmem_ld16(lane_base + (uint32_t)c, sv);
-              const float4 *cv = reinterpret_cast<const float4 *>(C.colv + c);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v = cv[i];
-                float lo, hi;
-                unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, pair_f32(-v.x, -v.z)),
-                           lo, hi);
-                if (dull) {
-                  if (v.x == INFINITY) lo = -INFINITY;
-                  if (v.z == INFINITY) hi = -INFINITY;
-                }
-                acc[i & 1] = fma2(pair_f32(ex2(lo), ex2(hi)), pair_f32(v.y, v.w), acc[i & 1]);
+          const bool masked = t0 + kMsT > g.ctx;
+          const int32_t k0 = t0 + (warp & 3) * 32 - g.ctx;  // drafted index of the warp's first token
+          const int last_row = (int)fast_div(group_div, g.cols - 1 + g.h0);
+          uint64_t acc[2] = {0ull, 0ull};
+          auto add = [&](const uint32_t *sv, int c) {  // 16 pairs from c on
+            uint32_t sees = 0;
+            int i0 = 0;
+            if (masked) {  // lane i: which of the warp's 32 tokens the i-th row of these pairs sees
+              i0 = fast_div(group_div, c + g.h0);
+              if (i0 + lane <= last_row && lane < 16) {
+                const int32_t jr = list[i0 + lane];
+                sees = (uint32_t)sees64(a.seqs.mask ? a.seqs.mask + (int64_t)(g.row0 + jr) * a.seqs.mask_words : nullptr,
+                                        a.seqs.mask_words, jr, g.rows, k0);
               }
             }
-            float s0, s1;
-            unpair_f32(add2(acc[0], acc[1]), s0, s1);
-            sum = s0 + s1;
-          } else {
-            const int32_t k = t - g.ctx;  // drafted index, < 0: context
-            for (int c = 0; c < cols16; c += 16) {
-              uint32_t sv[16];
-              __syncwarp();
-              tmem_ld16(lane_base + (uint32_t)c, sv);
-              int32_t row_i = -1;
-              bool see = false;
+            const float4 *cv = reinterpret_cast<const float4 *>(C.colv + c);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int f = c + i;
-                if (f >= g.cols || !in) continue;
-                const int32_t li = fast_div(group_div, f + g.h0);
-                if (li != row_i) {
-                  row_i = li;
-                  const int32_t jr = list[li];
-                  const uint32_t *mrow =
-                      a.seqs.mask ? a.seqs.mask + (int64_t)(g.row0 + jr) * a.seqs.mask_words : nullptr;
-                  see = k < 0 || sees_draft(mrow, jr, k);
-                }
-                const float2 v = C.colv[f];
-                if (see && v.x != INFINITY) sum = fmaf(ex2(fmaf(__uint_as_float(sv[i]), c_hi, -v.x)), v.y, sum);
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = cv[i];
+              float lo, hi;
+              unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, pair_f32(-v.x, -v.z)),
+                         lo, hi);
+              if (dull) {
+                if (v.x == INFINITY) lo = -INFINITY;
+                if (v.z == INFINITY) hi = -INFINITY;
               }
+              if (masked) {
+                const uint32_t s0 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + g.h0) - i0);
+                const uint32_t s1 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + 1 + g.h0) - i0);
+                if (!((s0 >> lane) & 1u)) lo = -INFINITY;
+                if (!((s1 >> lane) & 1u)) hi = -INFINITY;
+              }
+              acc[i & 1] = fma2(pair_f32(ex2(lo), ex2(hi)), pair_f32(v.y, v.w), acc[i & 1]);
             }
+          };
+          int c = 0;
+          for (; c + 32 <= cols16; c += 32) {
+            uint32_t sv[32];
+            tmem_ld32(lane_base + (uint32_t)c, sv);
+            tmem_wait_ld32(sv);
+            add(sv, c);
+            add(sv + 16, c + 16);
           }
+          if (c < cols16) {
+            uint32_t sv[16];
+            tmem_ld16(lane_base + (uint32_t)c, sv);
+            add(sv, c);
+          }
+          float s0, s1;
+          unpair_f32(add2(acc[0], acc[1]), s0, s1);
+          sum = s0 + s1;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(sm32(&C.s_free[w]));
