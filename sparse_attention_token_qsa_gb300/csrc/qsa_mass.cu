@@ -20,6 +20,8 @@
 //
 // With few pairs the kernel is bound by reading K once from HBM; with many by the
 // products (M128 N256 K16 in 128 cycles) and the exponentials (16 a cycle and SM).
+#include <type_traits>
+
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"
@@ -243,6 +245,8 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
       off += g.n;
       left -= g.n;
       int32_t j = 0, last = 0;  // next row to look at; the row that the turn before cut
+      auto weigh = [&](int32_t jj) { return a.weight && jj < g.rows ? a.weight[g.row0 + jj] : 1.f; };
+      float ahead = weigh(lane);  // of row j + lane
       while (room()) {
         int32_t *list = C.list[qn % kMsQueue];
         int32_t found = 0;
@@ -252,7 +256,8 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
         }
         while (j < g.rows && (int64_t)found * a.group - g.h0 < NR) {
           const int32_t jj = j + lane;
-          const bool on = jj < g.rows && (a.weight == nullptr || a.weight[g.row0 + jj] != 0.f);
+          const bool on = jj < g.rows && ahead != 0.f;
+          const float next = weigh(jj + 32);
           const uint32_t bits = __ballot_sync(0xffffffffu, on);
           const int32_t want = (NR + g.h0 - found * a.group + a.group - 1) / a.group;  // rows still fitting
           const int32_t rank = __popc(bits & ((1u << lane) - 1u));
@@ -262,10 +267,12 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
             j += __ffs(at);
             last = j - 1;
             found += want;
+            ahead = weigh(j + lane);
           } else {
             if (bits) last = j + 31 - __clz(bits);
             j += 32;
             found += __popc(bits);
+            ahead = next;
           }
         }
         const int64_t have = (int64_t)found * a.group - g.h0;
@@ -400,6 +407,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
       if (g.cols > 0) {
         constexpr int kCh = HD / 8, kPer = 32 / kCh;  // 16-byte chunks a row, rows a warp copy
         const int ch = lane % kCh, sub = lane / kCh;
+#pragma unroll 8
         for (int f = warp * kPer + sub; f < cols16; f += kPer * kMsSum) {
           const uint32_t to = sQ + (uint32_t)(ch >> 3) * G::kQBox + (uint32_t)f * 128u + (uint32_t)(((ch & 7) ^ (f & 7)) << 4);
           const uint16_t *src = a.q;
@@ -456,10 +464,11 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
           const int32_t k0 = t0 + (warp & 3) * 32 - g.ctx;  // drafted index of the warp's first token
           const int last_row = (int)fast_div(group_div, g.cols - 1 + g.h0);
           uint64_t acc[2] = {0ull, 0ull};
-          auto add = [&](const uint32_t *sv, int c) {  // 16 pairs from c on
+          // 16 pairs from c on; `plain`: every one counts for every token
+          auto add = [&](auto plain, const uint32_t *sv, int c) {
             uint32_t sees = 0;
             int i0 = 0;
-            if (masked) {  // lane i: which of the warp's 32 tokens the i-th row of these pairs sees
+            if (!plain.value && masked) {  // lane i: which of the warp's 32 tokens the i-th row of these pairs sees
               i0 = fast_div(group_div, c + g.h0);
               if (i0 + lane <= last_row && lane < 16) {
                 const int32_t jr = list[i0 + lane];
@@ -474,32 +483,38 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
               float lo, hi;
               unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, pair_f32(-v.x, -v.z)),
                          lo, hi);
-              if (dull) {
+              if (!plain.value) {
                 if (v.x == INFINITY) lo = -INFINITY;
                 if (v.z == INFINITY) hi = -INFINITY;
-              }
-              if (masked) {
-                const uint32_t s0 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + g.h0) - i0);
-                const uint32_t s1 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + 1 + g.h0) - i0);
-                if (!((s0 >> lane) & 1u)) lo = -INFINITY;
-                if (!((s1 >> lane) & 1u)) hi = -INFINITY;
+                if (masked) {
+                  const uint32_t s0 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + g.h0) - i0);
+                  const uint32_t s1 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + 1 + g.h0) - i0);
+                  if (!((s0 >> lane) & 1u)) lo = -INFINITY;
+                  if (!((s1 >> lane) & 1u)) hi = -INFINITY;
+                }
               }
               acc[i & 1] = fma2(pair_f32(ex2(lo), ex2(hi)), pair_f32(v.y, v.w), acc[i & 1]);
             }
           };
-          int c = 0;
-          for (; c + 32 <= cols16; c += 32) {
-            uint32_t sv[32];
-            tmem_ld32(lane_base + (uint32_t)c, sv);
-            tmem_wait_ld32(sv);
-            add(sv, c);
-            add(sv + 16, c + 16);
-          }
-          if (c < cols16) {
-            uint32_t sv[16];
-            tmem_ld16(lane_base + (uint32_t)c, sv);
-            add(sv, c);
-          }
+          auto sweep = [&](auto plain) {
+            int c = 0;
+            for (; c + 32 <= cols16; c += 32) {
+              uint32_t sv[32];
+              __syncwarp();
+              tmem_ld32(lane_base + (uint32_t)c, sv);
+              tmem_wait_ld32(sv);
+              add(plain, sv, c);
+              add(plain, sv + 16, c + 16);
+            }
+            if (c < cols16) {
+              uint32_t sv[16];
+              __syncwarp();
+              tmem_ld16(lane_base + (uint32_t)c, sv);
+              add(plain, sv, c);
+            }
+          };
+          if (masked || dull) sweep(std::false_type{});
+          else sweep(std::true_type{});
           float s0, s1;
           unpair_f32(add2(acc[0], acc[1]), s0, s1);
           sum = s0 + s1;
