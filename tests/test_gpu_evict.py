@@ -133,3 +133,19 @@ def test_graph(qsa):
         torch.cuda.synchronize()
         check(mass, length, 200, 4, 40, 4, sel.cpu().numpy(), n_sel.cpu().numpy())
     assert qsa.qsa_read_status(st) == (0, 0)
+
+
+def test_runs_that_shared_memory_does_not_hold(qsa):
+    """A sequence whose share per CTA is past the cached keys: the mass is read again."""
+    rng = qi.rng_for(55)
+    most = 8 * 49152 + 2000
+    mass = draws(rng, "heavy", (1, 1, (most + 3) // 4 * 4))
+    mass[0, 0, ::3] = 0.0
+    for length, unit, keep in ((most, 1, 30000), (most - 5, 1, 300000)):
+        sel, n_sel, st = call(qsa, mass, [length], most, keep, 4, 64, unit)
+        assert st == (0, 0)
+        check(mass, [length], keep, 4, 64, unit, sel, n_sel)
+    wide = draws(rng, "ties", (1, 1, 4 * most))
+    sel, n_sel, st = call(qsa, wide, [4 * most], 4 * most, 8192, 4, 64, 4)
+    assert st == (0, 0)
+    check(wide, [4 * most], 8192, 4, 64, 4, sel, n_sel)
