@@ -110,7 +110,7 @@ def test_compact_refusals(lib):
     for kw in (dict(k=0), dict(k=U), dict(v=0), dict(v=U), dict(width=0), dict(width=516), dict(width=-8), dict(pages=-1),
                dict(table=0), dict(tl=-1), dict(tc=39), dict(tc=0), dict(page=0), dict(keep=0), dict(kc=258), dict(nk=0),
                dict(n=-1), dict(most=-1), dict(cols=-1), dict(nkv=0), dict(nkv=-1), dict(bk=U), dict(kb=0), dict(st=0),
-               dict(n=65536), dict(width=(1 << 24) + 8), dict(tl=1 << 28, tc=1 << 28)):
+               dict(n=65536), dict(width=(1 << 24) + 8), dict(tl=1 << 28, tc=1 << 28), dict(pages=1 << 27)):
         assert compact(lib, **kw) == 1, kw
 
 
