@@ -569,7 +569,7 @@ qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, 
   if ((int64_t)pool_pages * page_size > INT32_MAX || (int64_t)pool_pages * page_size > kMostElems / width ||
       (int64_t)table_len * page_size > INT32_MAX || keep_cols > kMostElems / n_seqs ||
       (mass && mass_cols > kMostElems / n_seqs / nkv) || (mass && nkv > 65535) || width > (1 << 24) ||
-      n_seqs > 65535 || ((int64_t)width / 16 + nkv + 5) * n_seqs > INT32_MAX)
+      n_seqs > 65535 || ((int64_t)width / 8 + nkv + 16) * n_seqs > INT32_MAX)
     return QSA_ERR_INVALID_VALUE;
   const qsa::CompactArgs a{k_pool, v_pool, width, pool_pages, qsa::make_fast_div(page_size), table,
                            table_len, table_cols, keep, keep_cols, n_keep, max_keep, first, mass,

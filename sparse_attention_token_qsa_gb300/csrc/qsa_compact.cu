@@ -5,14 +5,17 @@
 // first + j, so a token only moves towards the front.
 //
 // One CTA owns a narrow column slice of a sequence's K and V rows and walks the
-// list from the front in chunks of 32 KiB, up to five of them on their way into
+// list from the front in chunks of 32 KiB, up to three of them on their way into
 // shared memory (cp.async) at a time.  A later chunk's sources lie at or past its
-// own first destination, so only the loads of a chunk itself have to be over, in
-// every thread, before it is stored: one barrier a chunk.  A thread stores what it
-// loaded.  The slices never meet, and no row is moved twice.
+// own first destination, and what a chunk's destinations hold is only read by chunks
+// up to it: so a chunk's loads have to be over, in every thread, before it is
+// stored, and nothing else: one barrier a chunk.  A thread stores what it loaded.
+// The slices never meet, and no row is moved twice.
 //
-// The bound is HBM: every moved byte is read and written once.  Pool rows are looked
-// up once per token and CTA, ahead of the copies.
+// The bound is HBM: every moved byte is read and written once.  Whole rows per CTA,
+// a sequence's CTAs a cluster with a cluster barrier per round of chunks, took 274
+// us for what 64-byte slices and no cluster do in 102 (16 caches of 16k-65k tokens
+// cut to 8192).
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"
@@ -48,71 +51,86 @@ __device__ __forceinline__ void move_slice(int32_t n, Src src, Dst dst) {
 
 constexpr int kKeyVecs = 4;  // 64 bytes of a block key per CTA
 
-constexpr int kCoDepth = 5;                              // chunks in flight at most
+constexpr int kCoDepth = 3;                              // chunks in flight at most
 constexpr uint32_t kCoChunk = kCoThreads * kCoLoads * 16;  // bytes of a chunk
 
-// SV 16-byte vectors of each K row and of each V row per CTA.
-template <int SV>
+struct CompactGrid {
+  int32_t n_seqs, slices;
+  int32_t sv;                    // 16-byte vectors of a K (and of a V) row per slice
+  int32_t tokens;                // per chunk, at most one a thread
+  int32_t depth;                 // chunks in flight
+};
+
 __global__ void __launch_bounds__(kCoThreads)
-compact_kernel(const CompactArgs a, int32_t n_seqs, int32_t depth) {
+compact_kernel(const CompactArgs a, const CompactGrid cfg, const FastDiv lanes) {
   extern __shared__ __align__(16) uint8_t co_smem[];
   grid_dependency_sync();
   // every sequence's row slices first, then what is short: a CTA of those ahead of
   // a row slice would push it into a second wave
-  const int32_t vecs = a.width / 8, row_slices = (vecs + SV - 1) / SV;
-  const int32_t more = (int32_t)gridDim.x / n_seqs - row_slices, at = (int32_t)blockIdx.x - n_seqs * row_slices;
-  const int32_t s = at < 0 ? (int32_t)blockIdx.x / row_slices : at / more;
-  int32_t slice = at < 0 ? (int32_t)blockIdx.x % row_slices : row_slices + at % more;
+  const int32_t at = (int32_t)blockIdx.x - cfg.n_seqs * cfg.slices;
+  const int32_t more = a.nkv + (a.block_keys ? kHeadDim / 8 / kKeyVecs : 0);
+  const int32_t s = at < 0 ? (int32_t)blockIdx.x / cfg.slices : at / more;
+  int32_t slice = at < 0 ? (int32_t)blockIdx.x % cfg.slices : at % more;
+  const bool lead = at < 0 && slice == 0;
   const int32_t n = a.n_keep[s], first = a.first ? a.first[s] : 0;
   if (n < 0 || n > a.max_keep || first < 0 || (int64_t)first + n > (int64_t)a.table_len * a.page.d ||
       (a.mass && (int64_t)first + n > a.mass_cols)) {
-    if (threadIdx.x == 0 && slice == 0) report_error(a.status, kErrRowRange, s);
+    if (threadIdx.x == 0 && lead) report_error(a.status, kErrRowRange, s);
     return;
   }
   const int32_t *keep = a.keep + (int64_t)s * a.keep_cols;
   const int32_t *table = a.table + (int64_t)s * a.table_cols;
   const int64_t most = a.mass ? min((int64_t)a.mass_cols, (int64_t)a.table_len * a.page.d)
                               : (int64_t)a.table_len * a.page.d;
-  auto slot = [&](int32_t t) -> int64_t {
-    const int32_t pg = fast_div(a.page, t), phys = table[pg];
-    if (phys < 0 || phys >= a.pool_pages) return -1;
-    return (int64_t)phys * a.page.d + (t - pg * a.page.d);
-  };
   auto source = [&](int32_t j) -> int32_t {  // keep[j], or -1 where it may not move
     const int32_t t = keep[j];
     return t < first + j || t >= most ? -1 : t;
   };
-  if (slice < row_slices) {
-    constexpr int kLanes = 2 * SV, kRowsAtOnce = kCoThreads / kLanes, kChunk = kRowsAtOnce * kCoLoads;
-    const int c = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
-    const int32_t v = slice * SV + c % SV;
-    uint4 *pool = reinterpret_cast<uint4 *>(c < SV ? a.k_pool : a.v_pool) + v;
-    const int32_t chunks = (n + kChunk - 1) / kChunk;
-    // shared memory: depth chunks, then (source, destination) rows of depth + 2
+  if (at < 0) {
+    const int32_t vecs = a.width / 8, per = cfg.tokens, depth = cfg.depth, chunks = (n + per - 1) / per;
+    // this thread's vectors of a chunk: token, and column in the K or the V row
+    int32_t tok[kCoLoads];
+    uint4 *pool[kCoLoads];
+#pragma unroll
+    for (int i = 0; i < kCoLoads; ++i) {
+      const int32_t e = (int32_t)threadIdx.x + i * kCoThreads;
+      tok[i] = fast_div(lanes, e);
+      const int32_t c = e - tok[i] * lanes.d, v = slice * cfg.sv + (c < cfg.sv ? c : c - cfg.sv);
+      if (tok[i] >= per || v >= vecs) tok[i] = -1;
+      pool[i] = reinterpret_cast<uint4 *>(c < cfg.sv ? a.k_pool : a.v_pool) + v;
+    }
+    // Look-ups go by groups of `group` chunks, a token a thread: its number, the two
+    // pages, the rows.  Each step waits for the reads of the one before it, so the
+    // steps of a group lie a group apart (a chunk apart, every chunk took as long as a
+    // read under load, 2.5 us).  Shared memory: depth chunks, then the (source,
+    // destination) rows of a ring of groups: those of chunks k .. k + depth, one that
+    // is being written, and one.
+    const int32_t group = kCoThreads / per, groups_ahead = (group - 1 + depth) / group, slots = groups_ahead + 2;
     uint8_t *ring = co_smem + threadIdx.x * 16;
     int2 *rows = reinterpret_cast<int2 *>(co_smem + (size_t)depth * kCoChunk);
-    // A token a thread: its number, the two pages, the rows.  Each step waits for the
-    // reads of the one before it, so the steps of a chunk lie a chunk apart: a look-up
-    // made in one go took 3 us of every chunk.
+    const int32_t my_chunk = (int32_t)threadIdx.x / per, my_token = (int32_t)threadIdx.x - my_chunk * per;
     struct Look {
       int32_t t, px, py;
     };
-    auto token = [&](int32_t k) -> int32_t {  // -1: not moved
-      const int32_t j = k * kChunk + (int32_t)threadIdx.x;
-      return threadIdx.x < kChunk && j < n ? keep[j] : -1;
+    auto index = [&](int32_t q) -> int32_t {  // this thread's list entry of group q; n: none
+      const int64_t k = (int64_t)q * group + my_chunk;
+      return my_chunk < group && k < chunks ? min((int64_t)n, k * per + my_token) : n;
     };
-    auto pages = [&](int32_t k, int32_t t) -> Look {
-      const int32_t j = k * kChunk + (int32_t)threadIdx.x;
+    auto token = [&](int32_t q) -> int32_t {
+      const int32_t j = index(q);
+      return j < n ? keep[j] : -1;
+    };
+    auto pages = [&](int32_t q, int32_t t) -> Look {
+      const int32_t j = index(q);
       Look l = {t, -1, -1};
-      if (threadIdx.x < kChunk && j < n) {
+      if (j < n) {
         if (t >= first + j && t < most) l.px = table[fast_div(a.page, t)];
         l.py = table[fast_div(a.page, first + j)];
       }
       return l;
     };
-    auto put = [&](int32_t k, const Look &l) {
-      const int32_t j = k * kChunk + (int32_t)threadIdx.x;
-      if (threadIdx.x >= kChunk || k >= chunks) return;
+    auto put = [&](int32_t q, const Look &l) {  // -1: not moved
+      const int32_t j = index(q);
       int2 row = make_int2(-1, -1);
       if (j < n) {
         if (l.px >= 0 && l.px < a.pool_pages && l.py >= 0 && l.py < a.pool_pages) {
@@ -123,61 +141,75 @@ compact_kernel(const CompactArgs a, int32_t n_seqs, int32_t depth) {
           report_error(a.status, kErrTokenRange, s);
         }
       }
-      rows[(k % (depth + 2)) * kChunk + threadIdx.x] = row;
+      rows[(q % slots) * kCoThreads + threadIdx.x] = row;
     };
-    auto issue = [&](int32_t k) {  // chunk k into its place of the ring
-      if (k < chunks && v < vecs) {
+    // a chunk's place in the ring of chunks, and its rows
+    struct Place {
+      int32_t k = 0, chunk = 0, in_group = 0, slot = 0;
+    };
+    auto step = [&](Place &p) {
+      ++p.k;
+      if (++p.chunk == depth) p.chunk = 0;
+      if (++p.in_group == group) {
+        p.in_group = 0;
+        if (++p.slot == slots) p.slot = 0;
+      }
+    };
+    auto issue = [&](Place &p) {  // a chunk into its place of the ring
+      if (p.k < chunks) {
+        const int2 *r = rows + p.slot * kCoThreads + p.in_group * per;
 #pragma unroll
         for (int i = 0; i < kCoLoads; ++i) {
-          const int32_t from = rows[(k % (depth + 2)) * kChunk + r0 + i * kRowsAtOnce].x;
+          const int32_t from = tok[i] >= 0 ? r[tok[i]].x : -1;
           if (from >= 0)
-            cp_async16(sm32(ring + (size_t)(k % depth) * kCoChunk + i * kCoThreads * 16), pool + (int64_t)from * vecs, 16u);
+            cp_async16(sm32(ring + (size_t)p.chunk * kCoChunk + i * kCoThreads * 16), pool[i] + (int64_t)from * vecs, 16u);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
+      step(p);
     };
     int32_t ts[kCoDepth + 1];
     Look ls[kCoDepth + 1];
 #pragma unroll
-    for (int k = 0; k <= kCoDepth; ++k) ts[k] = k <= depth ? token(k) : -1;
-    int32_t far = token(depth + 1);
+    for (int q = 0; q <= kCoDepth; ++q) ts[q] = q <= groups_ahead ? token(q) : -1;
+    int32_t far = token(groups_ahead + 1);
 #pragma unroll
-    for (int k = 0; k <= kCoDepth; ++k)
-      if (k <= depth) ls[k] = pages(k, ts[k]);
-    Look ahead = pages(depth + 1, far);
-    far = token(depth + 2);
+    for (int q = 0; q <= kCoDepth; ++q)
+      if (q <= groups_ahead) ls[q] = pages(q, ts[q]);
+    Look ahead = pages(groups_ahead + 1, far);
+    far = token(groups_ahead + 2);
 #pragma unroll
-    for (int k = 0; k <= kCoDepth; ++k)
-      if (k <= depth) put(k, ls[k]);
+    for (int q = 0; q <= kCoDepth; ++q)
+      if (q <= groups_ahead) put(q, ls[q]);
     __syncthreads();
-    for (int32_t k = 0; k < depth; ++k) issue(k);
-    for (int32_t k = 0; k < chunks; ++k) {
-      switch (depth) {  // chunk k has landed, those behind it may be on their way
+    Place in, out;
+    for (int32_t k = 0; k < depth; ++k) issue(in);
+    for (int32_t q = 0; out.k < chunks; step(out)) {
+      switch (depth) {  // the chunk has landed, those behind it may be on their way
         case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
         case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
       }
       __syncthreads();
-      if (v < vecs) {
+      const int2 *r = rows + out.slot * kCoThreads + out.in_group * per;
 #pragma unroll
-        for (int i = 0; i < kCoLoads; ++i) {
-          const int32_t to = rows[(k % (depth + 2)) * kChunk + r0 + i * kRowsAtOnce].y;
-          if (to >= 0)
-            pool[(int64_t)to * vecs] =
-                *reinterpret_cast<const uint4 *>(ring + (size_t)(k % depth) * kCoChunk + i * kCoThreads * 16);
-        }
+      for (int i = 0; i < kCoLoads; ++i) {
+        const int32_t to = tok[i] >= 0 ? r[tok[i]].y : -1;
+        if (to >= 0)
+          pool[i][(int64_t)to * vecs] =
+              *reinterpret_cast<const uint4 *>(ring + (size_t)out.chunk * kCoChunk + i * kCoThreads * 16);
       }
-      issue(k + depth);
-      put(k + depth + 1, ahead);
-      ahead = pages(k + depth + 2, far);
-      far = token(k + depth + 3);
+      issue(in);
+      if (out.in_group == 0) {
+        put(q + groups_ahead + 1, ahead);
+        ahead = pages(q + groups_ahead + 2, far);
+        far = token(q + groups_ahead + 3);
+        ++q;
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
-  slice -= row_slices;
   if (slice < a.nkv) {
     if (a.mass == nullptr) return;
     float *m = a.mass + ((int64_t)s * a.nkv + slice) * a.mass_cols;
@@ -211,31 +243,35 @@ compact_kernel(const CompactArgs a, int32_t n_seqs, int32_t depth) {
       [&](int32_t j) { return key((first >> 2) + j); });
 }
 
-template <int SV>
-cudaError_t launch_compact(const CompactArgs &a, int32_t n_seqs, cudaStream_t stream) {
-  static PerDevice smem_attr;
-  constexpr int kRows = kCoThreads / (2 * SV) * kCoLoads;  // tokens per chunk
-  auto smem = [](int32_t depth) { return (size_t)depth * kCoChunk + (size_t)(depth + 2) * kRows * sizeof(int2); };
-  const cudaError_t e = set_smem_once(smem_attr, compact_kernel<SV>, smem(kCoDepth));
-  if (e != cudaSuccess) return e;
-  const int32_t row_slices = (a.width / 8 + SV - 1) / SV;
-  const int32_t keys = a.block_keys ? kHeadDim / 8 / kKeyVecs : 0;
-  const int64_t grid = (int64_t)(row_slices + a.nkv + keys) * n_seqs;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  // short lists leave shared memory to more CTAs
-  const int32_t chunks = (a.max_keep + kRows - 1) / kRows, depth = chunks < kCoDepth ? chunks : kCoDepth;
-  return launch_dependent(compact_kernel<SV>, dim3((unsigned)grid), dim3(kCoThreads), smem(depth), stream, 1u, a, n_seqs,
-                          depth);
+size_t compact_smem(int32_t depth, int32_t tokens) {
+  const int32_t group = kCoThreads / tokens;
+  return (size_t)depth * kCoChunk + (size_t)((group - 1 + depth) / group + 2) * kCoThreads * sizeof(int2);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_compact(const CompactArgs &a, int32_t n_seqs, cudaStream_t stream) {
-  // the widest slice (128, 64 or 32 bytes of K and of V) that still gives most SMs one
-  const int64_t vecs = (int64_t)a.width / 8 * n_seqs, want = (int64_t)device_sm_count() * 3 / 4;
-  if (vecs >= want * 8) return launch_compact<8>(a, n_seqs, stream);
-  if (vecs >= want * 4) return launch_compact<4>(a, n_seqs, stream);
-  return launch_compact<2>(a, n_seqs, stream);
+  // Slices: as wide as still gives every SM two CTAs, between 64 bytes and 1 KiB of a row
+  const int32_t vecs = a.width / 8;
+  const int64_t least = (vecs + 63) / 64, finest = vecs < 4 ? 1 : vecs / 4;
+  int64_t slices = 2 * device_sm_count() / n_seqs;
+  slices = slices > finest ? finest : slices < least ? least : slices;
+  CompactGrid g;
+  g.n_seqs = n_seqs;
+  g.sv = (int32_t)((vecs + slices - 1) / slices);
+  g.slices = (vecs + g.sv - 1) / g.sv;
+  g.tokens = kCoThreads * kCoLoads / (2 * g.sv);
+  if (g.tokens > kCoThreads) g.tokens = kCoThreads;  // a look-up per thread
+  const int32_t chunks = (a.max_keep + g.tokens - 1) / g.tokens;
+  g.depth = chunks < kCoDepth ? chunks : kCoDepth;  // short lists leave shared memory to more CTAs
+  static PerDevice smem_attr;
+  const cudaError_t e = set_smem_once(smem_attr, compact_kernel, compact_smem(kCoDepth, kCoThreads));
+  if (e != cudaSuccess) return e;
+  const int32_t more = a.nkv + (a.block_keys ? kHeadDim / 8 / kKeyVecs : 0);
+  const int64_t grid = (int64_t)n_seqs * (g.slices + more);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_dependent(compact_kernel, dim3((unsigned)grid), dim3(kCoThreads), compact_smem(g.depth, g.tokens), stream,
+                          1u, a, g, make_fast_div(2 * g.sv));
 }
 
 }  // namespace qsa
