@@ -82,6 +82,10 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t s = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  auto all_sync = [&]() {
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+  };
   for (int i = tid; i < 3 * kEvBins; i += kEvThreads) (&C.hist[0][0])[i] = 0u;
   if (tid == 0) C.bad = 0;
   grid_dependency_sync();
@@ -157,24 +161,34 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
       for (int o = 16; o; o >>= 1) zeros += __shfl_xor_sync(0xffffffffu, zeros, o);
       if (lane == 0 && zeros) atomicAdd(&C.hist[round][(kZeroKey >> kShift[round]) & (uint32_t)(bins - 1)], zeros);
     }
-    cluster.sync();  // every CTA's histogram (and, in round 0, its verdict) is there
+    all_sync();  // every CTA's histogram (and, in round 0, its verdict) is there
     if (round == 0) {
-      bool bad = false;
-      for (int32_t r = 0; r < ctas; ++r) bad |= *cluster.map_shared_rank(&C.bad, r) != 0;
+      bool bad = C.bad != 0;
+      for (int32_t r = 0; ctas > 1 && r < ctas; ++r) bad |= *cluster.map_shared_rank(&C.bad, r) != 0;
       if (bad) {  // the same in every CTA, none of which may leave while it is read
         if (tid == 0 && rank == 0) report_error(a.status, kErrNonFinite, s);
-        cluster.sync();
+        all_sync();
         return;
       }
     }
     if (none) break;
-    for (int i = tid; i < bins; i += kEvThreads) {
-      uint32_t sum = 0;
-      for (int32_t r = 0; r < ctas; ++r) sum += cluster.map_shared_rank(&C.hist[round][0], r)[i];
-      C.merged[i] = sum;
+    if (ctas > 1) {
+      uint32_t part[kEvBins / kEvThreads][kEvMaxCluster];  // every read of the others on its way at once
+#pragma unroll
+      for (int i = 0; i < bins / kEvThreads; ++i)
+#pragma unroll
+        for (int r = 0; r < kEvMaxCluster; ++r)
+          part[i][r] = r < ctas ? cluster.map_shared_rank(&C.hist[round][0], r)[tid + i * kEvThreads] : 0u;
+#pragma unroll
+      for (int i = 0; i < bins / kEvThreads; ++i) {
+        uint32_t sum = 0;
+#pragma unroll
+        for (int r = 0; r < kEvMaxCluster; ++r) sum += part[i][r];
+        C.merged[tid + i * kEvThreads] = sum;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    find_bin<kEvThreads>(C.merged, bins, need, C.warp_tot, &C.bin, &C.above);
+    find_bin<kEvThreads>(ctas > 1 ? C.merged : C.hist[round], bins, need, C.warp_tot, &C.bin, &C.above);
     prefix = (prefix << (round == 2 ? 10 : 11)) | (uint32_t)C.bin;
     need -= C.above;
     __syncthreads();  // bin and merged are written again in the next round
@@ -215,12 +229,14 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
     C.gt_all = gt_all;
     C.eq_all = eq_all;
   }
-  cluster.sync();
-  for (int32_t r = 0; r < rank; ++r) {
-    gt += *cluster.map_shared_rank(&C.gt_all, r);
-    eq += *cluster.map_shared_rank(&C.eq_all, r);
+  if (ctas > 1) {
+    cluster.sync();
+    for (int32_t r = 0; r < rank; ++r) {
+      gt += *cluster.map_shared_rank(&C.gt_all, r);
+      eq += *cluster.map_shared_rank(&C.eq_all, r);
+    }
+    cluster.sync();  // no CTA leaves while its counts are read
   }
-  cluster.sync();  // no CTA leaves while its counts are read
   for (int32_t b = w0; b < w1; b += 32) {
     const int32_t u = b + lane;
     const int st = state(u);
