@@ -7,16 +7,19 @@
 //
 // One thread-block cluster per sequence, a contiguous run of units per CTA.  The
 // mass is read once, into monotonic 32-bit keys in shared memory; three radix
-// rounds (11, 11 and 10 bits), their histograms added up over distributed shared
-// memory, find the key of the last unit that stays.  Exact zeros, which a cache
-// is full of, are counted by ballot and not by atomics on one bin.  A unit's place
-// in the list follows from two counts before it, larger keys and equal ones (of
-// which the first `ties` stay), taken per warp over its own run: no barrier while
-// the list is written.
+// rounds (11, 11 and 10 bits) find the key of the last unit that stays.  Over a
+// cluster the bins are searched in two steps, sums of 32 and then 32 bins, read
+// over distributed shared memory: reading all 2048 of every CTA took 2100 cycles a
+// round, the two reads 1600.  Exact zeros, which a cache is full of, are summed
+// over the warp and not by atomics on one bin.  A unit's place in the list follows
+// from two counts before it, larger keys and equal ones (of which the first `ties`
+// stay), taken per warp over its own run: no barrier while the list is written.
+// Positions inside a warp come from a shuffle scan: popc runs at half a lane a
+// cycle and eight of them a step were all that the writing waited for.
 //
-// 32 caches of 131k-262k tokens (48 MB of mass) take 19 us, 37 % of the copy
-// bandwidth; a cache of 4099 tokens 5 us, which is the chain of rounds and their
-// barriers.
+// 32 caches of 131k-262k tokens (48 MB of mass) take 22 us, 33 % of the copy
+// bandwidth: 5 us of them read the mass, the rest is the chain of rounds, their
+// barriers and the list.  A cache of 4099 tokens takes 6 us, all of it that chain.
 #include <cooperative_groups.h>
 
 #include "qsa_launch.h"
@@ -34,44 +37,52 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;          // of the first two rounds; the last has 1024
 constexpr int kEvMaxKeys = 49152;      // per CTA, in shared memory
 constexpr int kEvMaxCluster = 8;
+constexpr int kEvBatch = 4;            // loads of 16 bytes a thread has on their way for each KV head
+constexpr int kEvGroup = 32;           // bins that a coarse one sums
 
 struct EvictCtrl {
   uint32_t hist[3][kEvBins];
-  uint32_t merged[kEvBins];
+  uint32_t coarse[3][kEvBins / kEvGroup];
   uint32_t warp_tot[kEvWarps], gt[kEvWarps], eq[kEvWarps];
   uint32_t gt_all, eq_all, above;
   int32_t bin, bad;
 };
 constexpr size_t kEvKeysOff = (sizeof(EvictCtrl) + 15) / 16 * 16;
 
-// Keys of the (up to) four tokens from unit u0's first on: four units of one
-// token, or one unit of four.
+__device__ __forceinline__ float4 add4(float4 s, float4 x) {
+  return make_float4(__fadd_rn(s.x, x.x), __fadd_rn(s.y, x.y), __fadd_rn(s.z, x.z), __fadd_rn(s.w, x.w));
+}
+
+// Keys of four tokens' masses: four units of one token, or one unit of four.
+// Returns whether all are finite.
 template <int UNIT>
-__device__ __forceinline__ void unit_keys(const float *m, int64_t cols, int32_t nkv, int64_t t, uint32_t (&key)[4 / UNIT],
-                                          bool (&bad)[4 / UNIT]) {
-  float4 s = *reinterpret_cast<const float4 *>(m + t);
-  for (int h = 1; h < nkv; ++h) {
-    const float4 x = *reinterpret_cast<const float4 *>(m + h * cols + t);
-    s.x = __fadd_rn(s.x, x.x);
-    s.y = __fadd_rn(s.y, x.y);
-    s.z = __fadd_rn(s.z, x.z);
-    s.w = __fadd_rn(s.w, x.w);
-  }
+__device__ __forceinline__ bool unit_keys(float4 s, uint32_t (&key)[4 / UNIT], int units) {
   if constexpr (UNIT == 4) {
     const float f = __fadd_rn(__fadd_rn(__fadd_rn(s.x, s.y), s.z), s.w);
     key[0] = order_key(f);
-    bad[0] = !isfinite(f);
+    return isfinite(f);
   } else {
     key[0] = order_key(s.x);
     key[1] = order_key(s.y);
     key[2] = order_key(s.z);
     key[3] = order_key(s.w);
-    bad[0] = !isfinite(s.x);
-    bad[1] = !isfinite(s.y);
-    bad[2] = !isfinite(s.z);
-    bad[3] = !isfinite(s.w);
+    return isfinite(s.x) && (units <= 1 || isfinite(s.y)) && (units <= 2 || isfinite(s.z)) && (units <= 3 || isfinite(s.w));
   }
 }
+
+// The sum of the lanes' x up to this one.
+__device__ __forceinline__ uint32_t warp_upto(uint32_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// A protected unit's key lies above, the key past the last unit below, that of any
+// finite mass: neither needs a test after the first pass.
+constexpr uint32_t kProtected = 0xffffffffu, kNoUnit = 0u;
 
 template <int UNIT, bool CACHED>
 __global__ void __launch_bounds__(kEvThreads)
@@ -101,8 +112,8 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
     if (tid == 0 && rank == 0) a.n_sel[s] = len;
     return;
   }
-  // this CTA's units [u0, u1): a multiple of 1024, so that a warp's run is one of 32
-  const int32_t seg = ((units + ctas - 1) / ctas + 1023) & ~1023;
+  // this CTA's units [u0, u1), a whole number of warp steps of 128
+  const int32_t seg = ((units + ctas - 1) / ctas + 127) & ~127;
   const int32_t u0 = min((int64_t)units, (int64_t)rank * seg), u1 = min((int64_t)units, (int64_t)u0 + seg);
   const int32_t lo = a.n_first / UNIT, hi = units - a.n_last / UNIT;  // units in [lo, hi) compete
   const float *m = a.mass + (int64_t)s * a.nkv * a.mass_cols;
@@ -110,146 +121,231 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
   __syncthreads();
 
   // ---- round 0 while the mass is read: keys, their upper 11 bits, and what is not finite
-  const int32_t loads = (u1 - u0 + kPer - 1) / kPer;
+  const int32_t loads = ((u1 - u0 + 127) & ~127) / kPer;
   uint32_t zeros = 0;
-  bool any_bad = false;
-#pragma unroll 4
-  for (int32_t i = tid; i < loads; i += kEvThreads) {
-    uint32_t key[kPer];
-    bool bad[kPer];
-    unit_keys<UNIT>(m, a.mass_cols, a.nkv, ((int64_t)u0 + (int64_t)i * kPer) * UNIT, key, bad);
+  bool finite = true;
+  for (int32_t i0 = tid; i0 < loads; i0 += kEvBatch * kEvThreads) {
+    float4 sum[kEvBatch];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      const int32_t u = u0 + i * kPer + e;
-      if (u >= u1) continue;
-      any_bad |= bad[e];
-      if (CACHED) keys[u - u0] = key[e];
-      if (u < lo || u >= hi) continue;
-      if (key[e] == kZeroKey) ++zeros;
-      else atomicAdd(&C.hist[0][key[e] >> 21], 1u);
+    for (int b = 0; b < kEvBatch; ++b) {
+      const int32_t u = u0 + (i0 + b * kEvThreads) * kPer;
+      sum[b] = u < u1 ? *reinterpret_cast<const float4 *>(m + (int64_t)u * UNIT) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int32_t h = 1; h < a.nkv; ++h) {
+      float4 x[kEvBatch];
+#pragma unroll
+      for (int b = 0; b < kEvBatch; ++b) {
+        const int32_t u = u0 + (i0 + b * kEvThreads) * kPer;
+        x[b] = u < u1 ? *reinterpret_cast<const float4 *>(m + h * a.mass_cols + (int64_t)u * UNIT) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int b = 0; b < kEvBatch; ++b) sum[b] = add4(sum[b], x[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < kEvBatch; ++b) {
+      const int32_t i = i0 + b * kEvThreads, u = u0 + i * kPer;
+      if (i >= loads) break;
+      uint32_t key[kPer];
+      finite = unit_keys<UNIT>(sum[b], key, u1 - u) && finite;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (u + e >= u1) key[e] = kNoUnit;
+        else if (u + e < lo || u + e >= hi) key[e] = kProtected;
+        else if (key[e] == kZeroKey) ++zeros;
+        else atomicAdd(&C.hist[0][key[e] >> 21], 1u);
+      }
+      if constexpr (CACHED) {
+        if constexpr (UNIT == 4) keys[i] = key[0];
+        else reinterpret_cast<uint4 *>(keys)[i] = make_uint4(key[0], key[1], key[2], key[3]);
+      }
     }
   }
-  for (int o = 16; o; o >>= 1) zeros += __shfl_xor_sync(0xffffffffu, zeros, o);
-  if (lane == 0 && zeros) atomicAdd(&C.hist[0][kZeroKey >> 21], zeros);
-  if (any_bad) C.bad = 1;
+  auto add_zeros = [&](int round, int shift) {
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if (lane == 0 && zeros) atomicAdd(&C.hist[round][(kZeroKey >> shift) & (uint32_t)(kEvBins - 1)], zeros);
+    zeros = 0;
+  };
+  add_zeros(0, 21);
+  if (!finite) C.bad = 1;
 
-  auto key_at = [&](int32_t u) -> uint32_t {
-    if (CACHED) return keys[u - u0];
-    uint32_t key[kPer];
-    bool bad[kPer];
-    const int64_t t = (int64_t)u * UNIT;
-    unit_keys<UNIT>(m, a.mass_cols, a.nkv, t & ~(int64_t)3, key, bad);
-    if constexpr (UNIT == 4) return key[0];
-    return (t & 3) == 0 ? key[0] : (t & 3) == 1 ? key[1] : (t & 3) == 2 ? key[2] : key[3];
+  // four keys from unit u on (u - u0 a multiple of 4, u < u1)
+  auto keys_at = [&](int32_t u) -> uint4 {
+    if constexpr (CACHED) {
+      return *reinterpret_cast<const uint4 *>(keys + (u - u0));
+    } else {
+      uint32_t k[4];
+#pragma unroll
+      for (int e = 0; e < 4; e += kPer) {
+        uint32_t key[kPer] = {};
+        if (u + e < u1) {
+          const float *at = m + (int64_t)(u + e) * UNIT;
+          float4 sum = *reinterpret_cast<const float4 *>(at);
+          for (int32_t h = 1; h < a.nkv; ++h) sum = add4(sum, *reinterpret_cast<const float4 *>(at + h * a.mass_cols));
+          unit_keys<UNIT>(sum, key, kPer);
+        }
+#pragma unroll
+        for (int f = 0; f < kPer; ++f)
+          k[e + f] = u + e + f >= u1 ? kNoUnit : u + e + f < lo || u + e + f >= hi ? kProtected : key[f];
+      }
+      return make_uint4(k[0], k[1], k[2], k[3]);
+    }
   };
 
-  // ---- the key of the last unit that stays: the cut-th largest of those that compete
+  // one counter of all the CTAs, every read on its way at once
+  auto sum_ctas = [&](uint32_t *counter) -> uint32_t {
+    uint32_t part[kEvMaxCluster], sum = 0;
+#pragma unroll
+    for (int r = 0; r < kEvMaxCluster; ++r) part[r] = r < ctas ? *cluster.map_shared_rank(counter, r) : 0u;
+#pragma unroll
+    for (int r = 0; r < kEvMaxCluster; ++r) sum += part[r];
+    return sum;
+  };
+
+  // ---- the key of the last unit that stays: the need-th largest of those that compete
   uint32_t need = (uint32_t)(keep - lo - (units - hi)), prefix = 0;
   const bool none = need == 0;  // the protected units fill the budget
 #pragma unroll
   for (int round = 0; round < 3; ++round) {
-    constexpr int kShift[3] = {21, 10, 0};
-    const int bins = round == 2 ? 1024 : kEvBins;
-    if (round > 0 && !none) {
-      zeros = 0;
-      for (int32_t u = max(u0, lo) + tid; u < min(u1, hi); u += kEvThreads) {
-        const uint32_t k = key_at(u);
-        if ((k >> (round == 1 ? 21 : 10)) != prefix) continue;
-        if (k == kZeroKey) ++zeros;
-        else atomicAdd(&C.hist[round][(k >> kShift[round]) & (uint32_t)(bins - 1)], 1u);
+    constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+    if (round > 0) {
+      for (int32_t u = u0 + 4 * tid; u < u1; u += 4 * kEvThreads) {
+        const uint4 k4 = keys_at(u);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((k[e] >> (round == 1 ? 21 : 10)) != prefix) continue;
+          if (k[e] == kZeroKey) ++zeros;
+          else atomicAdd(&C.hist[round][(k[e] >> kShift[round]) & ((1u << kBits[round]) - 1u)], 1u);
+        }
       }
-      for (int o = 16; o; o >>= 1) zeros += __shfl_xor_sync(0xffffffffu, zeros, o);
-      if (lane == 0 && zeros) atomicAdd(&C.hist[round][(kZeroKey >> kShift[round]) & (uint32_t)(bins - 1)], zeros);
+      add_zeros(round, kShift[round]);
+    }
+    if (ctas > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int g = 2 * warp; g < 2 * warp + 2; ++g) {
+        const uint32_t n = __reduce_add_sync(0xffffffffu, C.hist[round][g * kEvGroup + lane]);
+        if (lane == 0) C.coarse[round][g] = n;
+      }
     }
     all_sync();  // every CTA's histogram (and, in round 0, its verdict) is there
     if (round == 0) {
       bool bad = C.bad != 0;
-      for (int32_t r = 0; ctas > 1 && r < ctas; ++r) bad |= *cluster.map_shared_rank(&C.bad, r) != 0;
+      if (ctas > 1) bad = __any_sync(0xffffffffu, lane < ctas && *cluster.map_shared_rank(&C.bad, lane < ctas ? lane : 0) != 0);
       if (bad) {  // the same in every CTA, none of which may leave while it is read
         if (tid == 0 && rank == 0) report_error(a.status, kErrNonFinite, s);
         all_sync();
         return;
       }
+      if (none) break;
     }
-    if (none) break;
-    if (ctas > 1) {
-      uint32_t part[kEvBins / kEvThreads][kEvMaxCluster];  // every read of the others on its way at once
-#pragma unroll
-      for (int i = 0; i < bins / kEvThreads; ++i)
-#pragma unroll
-        for (int r = 0; r < kEvMaxCluster; ++r)
-          part[i][r] = r < ctas ? cluster.map_shared_rank(&C.hist[round][0], r)[tid + i * kEvThreads] : 0u;
-#pragma unroll
-      for (int i = 0; i < bins / kEvThreads; ++i) {
-        uint32_t sum = 0;
-#pragma unroll
-        for (int r = 0; r < kEvMaxCluster; ++r) sum += part[i][r];
-        C.merged[tid + i * kEvThreads] = sum;
-      }
+    if (ctas == 1) {  // the bins from the top, two a thread
+      const int at = kEvBins / 2 - 1 - tid;
+      const uint2 n = reinterpret_cast<const uint2 *>(C.hist[round])[at];
+      uint32_t upto = warp_upto(n.x + n.y, lane);
+      if (lane == 31) C.warp_tot[warp] = upto;
       __syncthreads();
+      upto += __reduce_add_sync(0xffffffffu, lane < warp ? C.warp_tot[lane] : 0u);
+      const uint32_t above = upto - n.x - n.y;
+      if (above < need && need <= upto) {  // one thread's
+        const bool upper = need <= above + n.y;
+        C.bin = 2 * at + (upper ? 1 : 0);
+        C.above = upper ? above : above + n.y;
+      }
+    } else if (warp == 0) {
+      // One warp looks through the 64 groups and then the 32 bins of one: reading all
+      // the bins of the other CTAs takes longer than its chain of two reads.
+      uint32_t upper = sum_ctas(&C.coarse[round][63 - lane]), lower = sum_ctas(&C.coarse[round][31 - lane]);
+      uint32_t up = warp_upto(upper, lane);
+      const uint32_t low = warp_upto(lower, lane) + __shfl_sync(0xffffffffu, up, 31);
+      uint32_t hit = __ballot_sync(0xffffffffu, up >= need);
+      const bool in_upper = hit != 0;
+      if (!in_upper) {
+        up = low;
+        upper = lower;
+        hit = __ballot_sync(0xffffffffu, low >= need);
+      }
+      int src = (__ffs(hit) - 1) & 31;
+      const int at = ((in_upper ? 63 : 31) - src) * kEvGroup + 31 - lane;
+      const uint32_t n = sum_ctas(&C.hist[round][at]);
+      up = __shfl_sync(0xffffffffu, up - upper, src) + warp_upto(n, lane);
+      hit = __ballot_sync(0xffffffffu, up >= need);
+      src = (__ffs(hit) - 1) & 31;
+      if (lane == src) {
+        C.bin = at;
+        C.above = up - n;
+      }
     }
-    find_bin<kEvThreads>(ctas > 1 ? C.merged : C.hist[round], bins, need, C.warp_tot, &C.bin, &C.above);
-    prefix = (prefix << (round == 2 ? 10 : 11)) | (uint32_t)C.bin;
+    __syncthreads();
+    prefix = (prefix << kBits[round]) | (uint32_t)C.bin;
     need -= C.above;
-    __syncthreads();  // bin and merged are written again in the next round
   }
-  const uint32_t cut = prefix, ties = none ? 0u : need;
+  const uint32_t cut = none ? kProtected - 1u : prefix, ties = none ? 0u : need;
 
   // ---- counts before each warp's run, then the list
-  const int32_t run = seg / kEvWarps;
-  const int32_t w0 = u0 + warp * run, w1 = min(u1, w0 + run);
-  auto state = [&](int32_t u) -> int {  // 1: stays, 2: equal to the cut, 0: goes
-    if (u >= w1) return 0;
-    if (u < lo || u >= hi) return 1;
-    if (none) return 0;
-    const uint32_t k = key_at(u);
-    return k > cut ? 1 : k == cut ? 2 : 0;
-  };
+  const int32_t run = ((seg + kEvWarps - 1) / kEvWarps + 127) & ~127;
+  const int32_t w0 = min((int64_t)u1, (int64_t)u0 + warp * run), w1 = min((int64_t)u1, (int64_t)w0 + run);
   uint32_t gt = 0, eq = 0;
-  for (int32_t b = w0; b < w1; b += 32) {
-    const int st = state(b + lane);
-    gt += __popc(__ballot_sync(0xffffffffu, st == 1));
-    eq += __popc(__ballot_sync(0xffffffffu, st == 2));
+#pragma unroll 2
+  for (int32_t u = w0 + 4 * lane; u < w1; u += 128) {
+    const uint4 k = keys_at(u);
+    gt += (k.x > cut) + (k.y > cut) + (k.z > cut) + (k.w > cut);
+    eq += (k.x == cut) + (k.y == cut) + (k.z == cut) + (k.w == cut);
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     C.gt[warp] = gt;
     C.eq[warp] = eq;
   }
   __syncthreads();
-  gt = eq = 0;
-  uint32_t gt_all = 0, eq_all = 0;
-#pragma unroll
-  for (int i = 0; i < kEvWarps; ++i) {
-    gt += i < warp ? C.gt[i] : 0u;
-    eq += i < warp ? C.eq[i] : 0u;
-    gt_all += C.gt[i];
-    eq_all += C.eq[i];
-  }
-  if (tid == 0) {
-    C.gt_all = gt_all;
-    C.eq_all = eq_all;
-  }
+  const uint32_t w_gt = C.gt[lane], w_eq = C.eq[lane];
+  gt = __reduce_add_sync(0xffffffffu, lane < warp ? w_gt : 0u);
+  eq = __reduce_add_sync(0xffffffffu, lane < warp ? w_eq : 0u);
   if (ctas > 1) {
-    cluster.sync();
-    for (int32_t r = 0; r < rank; ++r) {
-      gt += *cluster.map_shared_rank(&C.gt_all, r);
-      eq += *cluster.map_shared_rank(&C.eq_all, r);
+    if (warp == 0) {
+      const uint32_t gt_all = __reduce_add_sync(0xffffffffu, w_gt), eq_all = __reduce_add_sync(0xffffffffu, w_eq);
+      if (lane == 0) {
+        C.gt_all = gt_all;
+        C.eq_all = eq_all;
+      }
     }
+    cluster.sync();
+    const bool before = lane < rank;
+    gt += __reduce_add_sync(0xffffffffu, before ? *cluster.map_shared_rank(&C.gt_all, before ? lane : 0) : 0u);
+    eq += __reduce_add_sync(0xffffffffu, before ? *cluster.map_shared_rank(&C.eq_all, before ? lane : 0) : 0u);
     cluster.sync();  // no CTA leaves while its counts are read
   }
-  for (int32_t b = w0; b < w1; b += 32) {
-    const int32_t u = b + lane;
-    const int st = state(u);
-    const uint32_t g = __ballot_sync(0xffffffffu, st == 1), q = __ballot_sync(0xffffffffu, st == 2);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t my_eq = eq + __popc(q & below);
-    const uint32_t at = gt + __popc(g & below) + min(my_eq, ties);
-    if (st == 1 || (st == 2 && my_eq < ties)) {
+  const bool wide = (reinterpret_cast<uintptr_t>(a.sel) & 15u) == 0 && (a.sel_cols & 3) == 0;
+  for (int32_t b = w0; b < w1; b += 128) {
+    const int32_t u = b + 4 * lane;
+    const uint4 k4 = u < w1 ? keys_at(u) : make_uint4(kNoUnit, kNoUnit, kNoUnit, kNoUnit);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    uint32_t mine = 0;  // larger keys in the lower half, equal ones in the upper
 #pragma unroll
-      for (int e = 0; e < UNIT; ++e) sel[(int64_t)at * UNIT + e] = u * UNIT + e;
+    for (int e = 0; e < 4; ++e) mine += k[e] > cut ? 1u : k[e] == cut ? 0x10000u : 0u;
+    if (!__any_sync(0xffffffffu, mine != 0)) continue;
+    const uint32_t upto = warp_upto(mine, lane), all = __shfl_sync(0xffffffffu, upto, 31);
+    uint32_t my_gt = gt + ((upto - mine) & 0xffffu), my_eq = eq + ((upto - mine) >> 16);
+    gt += all & 0xffffu;
+    eq += all >> 16;
+    if (mine == 0) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool more = k[e] > cut, same = k[e] == cut;
+      if (more || (same && my_eq < ties)) {
+        const int64_t at = (int64_t)(my_gt + min(my_eq, ties)) * UNIT;
+        const int32_t tok = (u + e) * UNIT;
+        if (UNIT == 4 && wide) {
+          *reinterpret_cast<int4 *>(sel + at) = make_int4(tok, tok + 1, tok + 2, tok + 3);
+        } else {
+#pragma unroll
+          for (int f = 0; f < UNIT; ++f) sel[at + f] = tok + f;
+        }
+      }
+      my_gt += more;
+      my_eq += same;
     }
-    gt += __popc(g);
-    eq += __popc(q);
   }
   if (rank == 0) {  // the tokens past the last whole unit
     if (tid < len - units * UNIT) sel[(int64_t)keep * UNIT + tid] = units * UNIT + tid;
@@ -273,10 +369,10 @@ cudaError_t launch_evict_select(const EvictArgs &a, int32_t n_seqs, cudaStream_t
   // CTAs per sequence: doubled while a run is longer than 4096 units and the launch
   // still has an SM for each, or while a run does not fit shared memory
   int32_t ctas = 1;
-  while (ctas < kEvMaxCluster && (units / ctas > kEvMaxKeys - 1024 ||
+  while (ctas < kEvMaxCluster && (units / ctas > kEvMaxKeys - 128 ||
                                   (units / ctas > 4096 && (int64_t)n_seqs * ctas * 2 <= (int64_t)device_sm_count())))
     ctas *= 2;
-  const int32_t keys = ((units + ctas - 1) / ctas + 1023) & ~1023;
+  const int32_t keys = ((units + ctas - 1) / ctas + 127) & ~127;
   if (a.unit == 4)
     return keys <= kEvMaxKeys ? launch_evict<4, true>(a, n_seqs, ctas, keys, stream)
                               : launch_evict<4, false>(a, n_seqs, ctas, keys, stream);
