@@ -12,9 +12,16 @@
 // of work is (sequence, KV head, 128 such rows); its tiles are a run of the
 // launch's linear list of tiles, of which every CTA (one per SM) takes an equal,
 // contiguous share, so ragged batches balance and one long context spreads over
-// the GPU.  A unit that lies in one CTA's share is written at once; the parts
-// of any other go to the workspace as (O, max, sum) and a second launch joins
-// them in a fixed order.
+// the GPU.  A unit that lies in one CTA's share is written at once; the parts of
+// any other go to the workspace as (O, max, sum) and a second launch joins them in
+// a fixed order.
+//
+// A unit counts kTrStart tiles more than it has, for its Q, its first tile's two
+// passes and its output: 24 sequences of 300 to 9001 tokens with 5 to 37 rows of 32
+// heads over 8 took 161 us without, 138 at 4 tiles, 135 at 8.  Where sequences have
+// several tiles of rows, a team of two or four CTAs shares a unit of as many: they
+// read the same K and V at the same time, so that these come from HBM once (64
+// rows of 16 heads over 2, 65471 tokens: 97 us one by one, 87 in twos, 84 in fours).
 //
 // Fourteen warps: two groups of four (warps 0-3 and 4-7) do the softmax, a row
 // per thread, tiles in turn; warps 8-11 copy K and V rows into a ring of
@@ -33,10 +40,15 @@
 // shared memory after each tile; a part's first tile is passed over twice, first
 // for its maximum.
 //
-// Decode (M = group rows of 128) is bound by HBM: the padded products take 2 x
-// 128 x 128 x head_dim x 2 flop per 128 tokens, under half the time their K and V
-// take to arrive.  Wide trees are bound by the softmax (128 exponentials a row and
-// tile) and the products.
+// Decode (M = group rows of 128) is bound by HBM: 16 sequences of 16k to 64k tokens
+// take 225 us, 95 % of the copy bandwidth.  With more rows the copies out of L2
+// bind: every tile of 128 rows reads its K and V, 32 KiB each, at the 33 bytes a
+// cycle and SM that the probe above moved, 2000 cycles a tile, of which the
+// exponentials (16 a cycle) take 512 or 768 and the products 1350 or 800; the 64
+// rows above run at 44 % of the bf16 rate, 128 rows of 32 heads over 8 at 41 %.
+// Two CTAs as a pair (MMAs of 256 rows, half of each tile a CTA) halve the copies,
+// but took 2500 cycles a tile; a third softmax group, a second issuer of S, tiles
+// of 128 tokens with fewer buffers were no faster either.
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"
@@ -50,8 +62,9 @@ constexpr int kTrProd = 4;     // producer warps
 constexpr int kTrMmaS = kTrSoft + kTrProd;  // issues S = Q K^T
 constexpr int kTrMmaO = kTrMmaS + 1;        // issues O += P V
 constexpr int kTrWarps = kTrMmaO + 1, kTrThreads = 32 * kTrWarps;
-constexpr int kTrRows = 128;   // rows of a unit: the MMA's M
+constexpr int kTrRowsLog = 7, kTrRows = 1 << kTrRowsLog;  // rows of a tile: the MMA's M
 constexpr int kTrMaxCtas = 160;
+constexpr int kTrStart = 8;     // what beginning a unit costs, in tiles
 constexpr float kTrSlack = 16.0f;  // log2 units a logit may pass the reference by
 constexpr long long kTrSpinLimit = 4000000000LL;
 
@@ -94,29 +107,30 @@ static_assert(tree_smem<256>() <= 232448 && tree_smem<128>() <= 232448, "227 KiB
 // What the plan below needs of a sequence.
 struct SeqTiles {
   SeqView v;
-  int32_t tiles, m_tiles;
-  int64_t count;  // tiles of all its units
+  int32_t tiles, m_tiles;  // of tokens; of rows, a team's together
+  int64_t count;  // tiles of all its units, their starts included
 };
 
 template <int T>
-__device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs &a, const SeqRaw &raw) {
+__device__ __forceinline__ SeqTiles seq_tiles(const TreeArgs &a, int team_log, const SeqRaw &raw) {
   SeqTiles q;
   q.v = view_seq(a.seqs, raw);
   q.tiles = q.v.rows > 0 ? (q.v.ctx + q.v.rows + T - 1) / T : 0;
-  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + kTrRows - 1) / kTrRows);
-  q.count = (int64_t)q.tiles * q.m_tiles * a.nkv;
+  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + (kTrRows << team_log) - 1) >> (kTrRowsLog + team_log));
+  q.count = q.tiles > 0 ? (int64_t)(q.tiles + kTrStart) * q.m_tiles * a.nkv : 0;
   return q;
 }
 
 // One CTA's part of one unit.
 struct TreeSeg {
-  int32_t s, kvh, mt;      // sequence, KV head, 128-row tile
+  int32_t s, kvh, mt;      // sequence, KV head, this CTA's tile of 128 rows
   int32_t t0, n;           // first tile, tiles to process
   bool whole, head;        // the unit's every tile; the unit began in an earlier CTA
+  bool empty;              // none of its tiles (a share that ends in a unit's start), or no rows
   SeqView v;
 };
 
-// Walks a CTA's share of the tile list, unit by unit (each role its own walk).
+// Walks a team's share of the tile list, unit by unit (each role its own walk).
 // A sequence's lengths are read one sequence ahead: under load a read takes
 // several thousand cycles.
 template <int T>
@@ -124,12 +138,13 @@ struct TreeWalk {
   const TreeArgs &a;
   int64_t left, off;
   int32_t s;
+  int team_log;
   SeqTiles q;
   SeqRaw ahead;
-  __device__ TreeWalk(const TreeArgs &a_, int32_t s_, int64_t off_, int64_t left_)
-      : a(a_), left(left_), off(off_), s(s_) {
+  __device__ TreeWalk(const TreeArgs &a_, int team_log_, int32_t s_, int64_t off_, int64_t left_)
+      : a(a_), left(left_), off(off_), s(s_), team_log(team_log_) {
     if (left <= 0) return;
-    q = seq_tiles<T>(a, read_seq(a.seqs, s));
+    q = seq_tiles<T>(a, team_log, read_seq(a.seqs, s));
     ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
   }
   __device__ bool next(TreeSeg &g) {
@@ -140,24 +155,28 @@ struct TreeWalk {
         left = 0;
         return false;
       }
-      q = seq_tiles<T>(a, ahead);
+      q = seq_tiles<T>(a, team_log, ahead);
       ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
     }
-    int32_t unit;  // (KV head, 128-row tile)
-    if ((off >> 31) == 0) unit = (int32_t)((uint32_t)off / (uint32_t)q.tiles);
-    else unit = (int32_t)(off / q.tiles);
-    g.t0 = (int32_t)(off - (int64_t)unit * q.tiles);
-    const int32_t take = (int32_t)min((int64_t)(q.tiles - g.t0), left);
-    off += take;
-    left -= take;
+    const int32_t length = q.tiles + kTrStart;
+    int32_t unit;  // (KV head, tile of team x 128 rows)
+    if ((off >> 31) == 0) unit = (int32_t)((uint32_t)off / (uint32_t)length);
+    else unit = (int32_t)(off / length);
+    const int32_t from = (int32_t)(off - (int64_t)unit * length);
+    const int32_t part = (int32_t)min((int64_t)(length - from), left);
+    off += part;
+    left -= part;
+    g.t0 = max(0, from - kTrStart);
+    const int32_t take = max(0, from + part - kTrStart) - g.t0;
     g.s = s;
     g.kvh = unit / q.m_tiles;
-    g.mt = unit - g.kvh * q.m_tiles;
+    g.mt = ((unit - g.kvh * q.m_tiles) << team_log) + (int32_t)(blockIdx.x & ((1u << team_log) - 1u));
     g.v = q.v;
     g.whole = take == q.tiles;
     g.head = g.t0 > 0;
-    g.n = take;
-    if (a.seqs.mask == nullptr) {  // no row of this tile sees past its last row's own token
+    g.empty = take == 0 || (int64_t)g.mt * kTrRows >= (int64_t)q.v.rows * a.group;
+    g.n = g.empty ? 0 : take;
+    if (a.seqs.mask == nullptr && !g.empty) {  // no row of this tile sees past its last row's own token
       const int64_t m_end = min((int64_t)(g.mt + 1) * kTrRows, (int64_t)q.v.rows * a.group);
       const int32_t end = (q.v.ctx + (int32_t)((m_end - 1) / a.group) + T) / T;
       g.n = max(0, min(take, end - g.t0));
@@ -174,7 +193,7 @@ __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) =
 
 template <int HD>
 __global__ void __launch_bounds__(kTrThreads, 1)
-tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, uint32_t q_and,
+tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_t part_rows, uint32_t q_and,
                  uint32_t q_xor, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml,
                  float *__restrict__ part_o) {
   using G = TreeGeom<HD>;
@@ -223,7 +242,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   const bool one_chunk = a.seqs.n_seqs <= kTrThreads;
   int64_t total = 0;
   if (!one_chunk) {
-    for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles<G::kT>(a, read_seq(a.seqs, s)).count;
+    for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles<G::kT>(a, team_log, read_seq(a.seqs, s)).count;
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) C.scan[warp] = total;
     __syncthreads();
@@ -231,11 +250,12 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
     for (int i = 0; i < kTrWarps; ++i) total += C.scan[i];
   }
   int64_t before = 0, per = 0, w0 = 0, share = 0;
+  const uint32_t teams = gridDim.x >> team_log;
   for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += kTrThreads) {
     const int32_t s = s0 + tid;
     int64_t count = 0;
     if (s < a.seqs.n_seqs) {
-      const SeqTiles q = seq_tiles<G::kT>(a, read_seq(a.seqs, s));
+      const SeqTiles q = seq_tiles<G::kT>(a, team_log, read_seq(a.seqs, s));
       count = q.count;
       if (blockIdx.x == 0 && !q.v.ok) report_error(a.status, kErrRowRange, s);
     }
@@ -254,8 +274,8 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       before += C.scan[i];
     }
     if (one_chunk) total = before;
-    per = (total >> 31) == 0 ? (int64_t)(((uint32_t)total + gridDim.x - 1u) / gridDim.x) : (total + gridDim.x - 1) / gridDim.x;
-    w0 = per * blockIdx.x;
+    per = (total >> 31) == 0 ? (int64_t)(((uint32_t)total + teams - 1u) / teams) : (total + teams - 1) / teams;
+    w0 = per * (blockIdx.x >> team_log);
     share = max((int64_t)0, min(per, total - w0));
     if (s < a.seqs.n_seqs && blockIdx.x == 0) base_out[s] = at;
     if (share > 0 && count > 0 && at <= w0 && w0 < at + count) {
@@ -270,7 +290,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
   tc_fence_after();
   const uint32_t tmem = C.tmem_base;
   const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
-  TreeWalk<G::kT> walk(a, C.found_seq, C.found_off, laid_out ? share : 0);
+  TreeWalk<G::kT> walk(a, team_log, C.found_seq, C.found_off, laid_out ? share : 0);
   TreeSeg g;
 
   if (warp >= kTrSoft && warp < kTrMmaS) {
@@ -483,6 +503,8 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
       const uint32_t *mrow = a.seqs.mask ? a.seqs.mask + (int64_t)row * a.seqs.mask_words : nullptr;
       // whether a row may be blind to a token that another one sees
       const bool veiled = g.v.rows > 1 || a.seqs.mask != nullptr;
+      TreeSeg next;
+      const bool more_next = walk.next(next);  // while the first S is on its way
       float top = -INFINITY, sum = 0.f;  // sum is relative to top
       auto rebase = [&](float t) {
         if (t != top) {
@@ -587,8 +609,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
             tc_warp_wait_ready(sm32(&C.full[slot]), (at / G::kSlots) & 1u, lim, abort_flag);
             __syncwarp();
             uint8_t *vs = tr_smem + G::kRingOff + slot * G::kSlot;
-            for (int i = (warp & 3) * 32 + lane; i < (int)(G::kSlot / 16); i += 128) {
-              uint4 *q = reinterpret_cast<uint4 *>(vs) + i;
+            const int first = max(0, g.v.ctx - t0), n = min(G::kT, g.v.ctx + g.v.rows - t0) - first;
+            for (int i = (warp & 3) * 32 + lane; i < n * (HD / 8); i += 128) {  // 16 bytes, in no order that matters
+              const int row = first + i / (HD / 8), ch = i % (HD / 8);
+              uint4 *q = reinterpret_cast<uint4 *>(vs + (ch >> 3) * G::kBox + row * 128 + (ch & 7) * 16);
               const uint4 x = *q;
               uint32_t e[4] = {x.x, x.y, x.z, x.w};
               bool hit = false;
@@ -618,15 +642,14 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
         tc_warp_wait_ready(sm32(&C.s_full[last % 3u]), (last / 3u) & 1u, lim, abort_flag);
         if (live && (int)(last & 1u) != w) rebase(receive());
       }
-      TreeSeg next;
-      more = walk.next(next);
+      more = more_next;
       if (more && next.n > 0) load_q(next);
       if (g.n > 0) {
         if (last > 0 && (int)(last & 1u) != w) wait_pv(last - 1);
         wait_pv(last);
         tc_fence_after();
       }
-      if (live) {
+      if (live && !g.empty) {
         C.sums[w][r] = sum;
         asm volatile("bar.sync %0, 64;" ::"r"(9 + (warp & 3)) : "memory");
         const float all = C.sums[0][r] + C.sums[1][r];
@@ -653,11 +676,11 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, u
           }
           if (!valid) continue;
           if (fix) {
-            // every token of the tiles that were cleared
-            const int32_t t_lo = max(g.t0, g.v.ctx / G::kT) * G::kT;
+            // every drafted token of this part
+            const int32_t t_lo = max(g.t0 * G::kT, g.v.ctx);
             const int32_t t_hi = min(g.v.ctx + g.v.rows, (g.t0 + g.n) * G::kT);
             for (int32_t t = t_lo; t < t_hi; ++t) {
-              if (t >= g.v.ctx && !sees_draft(mrow, j_row, t - g.v.ctx)) continue;
+              if (!sees_draft(mrow, j_row, t - g.v.ctx)) continue;
               const int64_t slot = token_slot(a.seqs, g.s, t);
               if (slot < 0) continue;
               const uint16_t *v = a.v_pool + (slot * a.nkv + g.kvh) * HD + d0;
@@ -708,7 +731,7 @@ constexpr int kJoinWarps = 8;
 
 template <int HD, int kGroups>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-tree_join_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, int32_t ctas,
+tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_t part_rows, int32_t teams,
                  const int64_t *__restrict__ base, const float2 *__restrict__ part_ml,
                  const float4 *__restrict__ part_o) {
   __shared__ float4 acc_s[kGroups > 1 ? kJoinWarps : 1][32];
@@ -720,17 +743,18 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, i
   const int32_t quad = blockIdx.y * 4 + (lane >> 3), kvh = blockIdx.z;
   const int32_t row = mg < (int64_t)a.seqs.n_rows * a.group ? fast_div(group_div, (int32_t)mg) : -1;
   const int32_t head = kvh * a.group + (int32_t)(mg - (int64_t)row * a.group);
-  int32_t c0 = 0, c1 = 0, r = 0;
+  int32_t c0 = 0, c1 = 0, r = 0, rank = 0;  // teams of the first and last part
   bool mine = false;
   if (row >= 0) {
     const int32_t s = seq_of_row(a.seqs, row);
-    const SeqTiles q = seq_tiles<TreeGeom<HD>::kT>(a, read_seq(a.seqs, s));
+    const SeqTiles q = seq_tiles<TreeGeom<HD>::kT>(a, team_log, read_seq(a.seqs, s));
     if (row >= q.v.row0 && row < q.v.row0 + q.v.rows) {
       const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
-      const int32_t mt = (int32_t)(m / kTrRows);
-      r = (int32_t)(m % kTrRows);
-      const int64_t per = (base[a.seqs.n_seqs] + ctas - 1) / ctas;
-      const int64_t u0 = base[s] + ((int64_t)kvh * q.m_tiles + mt) * q.tiles;
+      const int32_t mt = (int32_t)(m >> kTrRowsLog);
+      r = (int32_t)(m & (kTrRows - 1));
+      rank = mt & ((1 << team_log) - 1);
+      const int64_t per = (base[a.seqs.n_seqs] + teams - 1) / teams;
+      const int64_t u0 = base[s] + ((int64_t)kvh * q.m_tiles + (mt >> team_log)) * (q.tiles + kTrStart) + kTrStart;
       if (((u0 + q.tiles) >> 31) == 0) {
         c0 = (int32_t)((uint32_t)u0 / (uint32_t)per);
         c1 = (int32_t)((uint32_t)(u0 + q.tiles - 1) / (uint32_t)per);
@@ -741,10 +765,9 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int32_t part_rows, i
       mine = c0 != c1;
     }
   }
-  auto ml_at = [&](int32_t c) { return part_ml[((int64_t)c * 2 + (c == c0 ? 1 : 0)) * part_rows + r]; };
-  auto o_at = [&](int32_t c) {
-    return part_o[(((int64_t)c * 2 + (c == c0 ? 1 : 0)) * (HD / 4) + quad) * part_rows + r];
-  };
+  auto part_of = [&](int32_t c) { return (((int64_t)c << team_log) + rank) * 2 + (c == c0 ? 1 : 0); };
+  auto ml_at = [&](int32_t c) { return part_ml[part_of(c) * part_rows + r]; };
+  auto o_at = [&](int32_t c) { return part_o[(part_of(c) * (HD / 4) + quad) * part_rows + r]; };
   float top = -INFINITY, all = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (mine) {
@@ -817,10 +840,13 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   int64_t *base = reinterpret_cast<int64_t *>(ws);
   float2 *ml = reinterpret_cast<float2 *>(ws + base_bytes(a.seqs.n_seqs));
   float *o = reinterpret_cast<float *>(ws + base_bytes(a.seqs.n_seqs) + ml_bytes(part_rows));
-  const int ctas = device_sm_count() < kTrMaxCtas ? device_sm_count() : kTrMaxCtas;
+  // CTAs that take a unit's tiles of rows side by side
+  const int64_t mean_rows = (int64_t)a.seqs.n_rows * a.group / a.seqs.n_seqs;
+  const int team_log = mean_rows >= 448 ? 2 : mean_rows >= 192 ? 1 : 0;
+  const int ctas = ((device_sm_count() < kTrMaxCtas ? device_sm_count() : kTrMaxCtas) >> team_log) << team_log;
   const FastDiv group_div = make_fast_div(a.group);
   cudaError_t r = launch_dependent(tree_attn_kernel<HD>, dim3((unsigned)ctas), dim3(kTrThreads), tree_smem<HD>(), stream, 1u,
-                                   a, group_div, part_rows, q_and, q_xor, base, ml, o);
+                                   a, group_div, team_log, part_rows, q_and, q_xor, base, ml, o);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= TreeGeom<HD>::kT) return r;
   // One group of parts per warp where units outnumber the CTAs (few parts each),
@@ -831,7 +857,7 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   const int64_t blocks = many ? rows8 : (rows8 + kJoinWarps - 1) / kJoinWarps;
   return launch_dependent(many ? tree_join_kernel<HD, kJoinWarps> : tree_join_kernel<HD, 1>,
                           dim3((unsigned)blocks, HD / 16, (unsigned)a.nkv), dim3(32 * kJoinWarps), 0, stream, 1u, a,
-                          group_div, part_rows, (int32_t)ctas, base, ml, reinterpret_cast<const float4 *>(o));
+                          group_div, team_log, part_rows, (int32_t)(ctas >> team_log), base, ml, reinterpret_cast<const float4 *>(o));
 }
 
 }  // namespace
