@@ -14,12 +14,17 @@
 // weight 0 are left out of Q.
 //
 // Every CTA (one per SM) takes an equal, contiguous share of the launch's list of
-// (sequence, KV head, tile).  Fourteen warps: warps 0-3 and 4-7 sum a tile in
-// turn, warps 8-11 copy K, warp 12 issues the MMAs, warp 13 walks the share and
-// names the rows of each turn.
+// (sequence, KV head, tile).  Two groups of four warps sum a tile in turn, or, with
+// up to 256 pairs a turn, four groups, two to a tile, each with half of its pairs
+// (the second leaves its sums to the first through shared memory).  Four more warps
+// copy K, one issues the MMAs, one walks the share and names the rows of each turn.
 //
-// With few pairs the kernel is bound by reading K once from HBM; with many by the
-// products (M128 N256 K16 in 128 cycles) and the exponentials (16 a cycle and SM).
+// With few pairs the kernel is bound by reading K once from HBM: 16 sequences of
+// 16k to 64k tokens, a row of 16 heads over 2 each, take 104 us, 85 % of the copy
+// bandwidth.  With many a tile's sums take longest: 64 rows of the same heads over
+// 65471 tokens take 55 us with four groups, 62 with two; the products alone would
+// take 18 (M128 N256 K16 in 128 cycles), K out of L2 for two turns 14, and a turn
+// begins with 4000 cycles for its Q.  Four groups cost the few-pair case 4 %.
 #include <type_traits>
 
 #include "qsa_launch.h"
@@ -30,9 +35,7 @@ namespace qsa {
 
 namespace {
 
-constexpr int kMsSum = 8, kMsProd = 4;
-constexpr int kMsMma = kMsSum + kMsProd, kMsPlan = kMsMma + 1;
-constexpr int kMsWarps = kMsPlan + 1, kMsThreads = 32 * kMsWarps;
+constexpr int kMsProd = 4;
 constexpr int kMsT = 128;                  // tokens per tile: the MMA's M
 constexpr int kMsQueue = 2;
 constexpr uint32_t kMsBox = kMsT * 128;    // 64 dims of a tile: 16 KiB
@@ -45,6 +48,11 @@ struct MassGeom {
   static constexpr uint32_t kSlot = kB * kMsBox;
   static constexpr uint32_t kQBox = NR * 128;
   static constexpr uint32_t kRingOff = (HD / 64) * kQBox;
+  // Groups that sum a tile, each with its share of the pairs: with many pairs two
+  // groups left the exponentials waiting for one another's latency.
+  static constexpr int kSplit = NR == 256 ? 2 : 1;
+  static constexpr int kSum = 8 * kSplit;                    // warps that sum, then the producers
+  static constexpr int kMma = kSum + kMsProd, kPlan = kMma + 1, kWarps = kPlan + 1, kThreads = 32 * kWarps;
   static constexpr int kSlots = HD == 256 ? 5 : (NR == 256 ? 4 : 6);
   static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kSlot;
 };
@@ -59,14 +67,17 @@ struct MassTurn {
 
 template <int NR>
 struct MassCtrl {
-  float2 colv[NR];              // per pair: lse in log2 units, weight
+  float4 colv[NR / 2];          // per two pairs: -lse in log2 units, weights
   int32_t list[kMsQueue][NR + 2];  // the turn's rows, as offsets from row0
   uint64_t full[6], empty[6];
   uint64_t s_full[2], s_free[2];
   uint64_t q_full, cv_full, turn_done, drain;
   uint64_t turn_full[kMsQueue], turn_empty[kMsQueue];
+  // split tiles (256 pairs a turn alone): the second group's sums, a barrier a quarter
+  uint64_t part_full[NR == 256 ? 2 : 1][4];
+  float part[NR == 256 ? 2 : 1][NR == 256 ? kMsT : 1];
   MassTurn turn[kMsQueue];
-  int64_t scan[kMsWarps], found_off;
+  int64_t scan[32], found_off;
   int32_t found_seq, abort;
   int32_t dull[2];  // [turn parity]: the turn (from 1) some pair of which adds nothing
   uint32_t tmem_base;
@@ -95,7 +106,7 @@ __device__ __forceinline__ MassSeq mass_seq(const MassArgs &a, int32_t s) {
 }
 
 template <int HD, int NR>
-__global__ void __launch_bounds__(kMsThreads, 1)
+__global__ void __launch_bounds__(MassGeom<HD, NR>::kThreads, 1)
 attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
   using G = MassGeom<HD, NR>;
   extern __shared__ __align__(1024) uint8_t ms_smem[];
@@ -112,15 +123,16 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
-      mbar_init(sm32(&C.s_free[b]), kMsSum / 2);
+      mbar_init(sm32(&C.s_free[b]), 4 * G::kSplit);
     }
+    for (int b = 0; b < (int)(sizeof(C.part_full) / 8); ++b) mbar_init(sm32(&C.part_full[0][0]) + 8u * b, 1);
     for (int b = 0; b < kMsQueue; ++b) {
       mbar_init(sm32(&C.turn_full[b]), 1);
-      mbar_init(sm32(&C.turn_empty[b]), kMsPlan);  // every warp before the planner
+      mbar_init(sm32(&C.turn_empty[b]), G::kPlan);  // every warp before the planner
     }
-    mbar_init(sm32(&C.q_full), 32 * kMsSum);
-    mbar_init(sm32(&C.cv_full), kMsSum);
-    mbar_init(sm32(&C.turn_done), kMsSum);
+    mbar_init(sm32(&C.q_full), 32 * G::kSum);
+    mbar_init(sm32(&C.cv_full), G::kSum);
+    mbar_init(sm32(&C.turn_done), G::kSum);
     mbar_init(sm32(&C.drain), 1);
     C.abort = 0;
     C.dull[0] = C.dull[1] = 0;
@@ -130,7 +142,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
   }
   __syncthreads();
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
-  if (warp == kMsMma) {
+  if (warp == G::kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      sm32(&C.tmem_base)),
                  "r"(512u)
@@ -140,18 +152,18 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
 
   // ---- the plan: every sequence's tiles summed, then the sequence this CTA's
   // share starts in; one thread a sequence, in chunks where there are more
-  const bool one_chunk = a.seqs.n_seqs <= kMsThreads;
+  const bool one_chunk = a.seqs.n_seqs <= G::kThreads;
   int64_t total = 0;
   if (!one_chunk) {
-    for (int32_t s = tid; s < a.seqs.n_seqs; s += kMsThreads) total += mass_seq(a, s).count;
+    for (int32_t s = tid; s < a.seqs.n_seqs; s += G::kThreads) total += mass_seq(a, s).count;
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) C.scan[warp] = total;
     __syncthreads();
     total = 0;
-    for (int i = 0; i < kMsWarps; ++i) total += C.scan[i];
+    for (int i = 0; i < G::kWarps; ++i) total += C.scan[i];
   }
   int64_t before = 0, share = 0;
-  for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += kMsThreads) {
+  for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += G::kThreads) {
     const int32_t s = s0 + tid;
     int64_t count = 0;
     if (s < a.seqs.n_seqs) {
@@ -169,7 +181,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
     __syncthreads();
     int64_t at = before + incl - count;
 #pragma unroll
-    for (int i = 0; i < kMsWarps; ++i) {
+    for (int i = 0; i < G::kWarps; ++i) {
       at += i < warp ? C.scan[i] : 0;
       before += C.scan[i];
     }
@@ -206,7 +218,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
     if (one_thread || lane == 0) mbar_arrive(sm32(&C.turn_empty[(qn - 1) % kMsQueue]));
   };
 
-  if (warp == kMsPlan) {
+  if (warp == G::kPlan) {
     // ---- the share's turns: rows of weight 0 are passed over
     int64_t left = share, off = C.found_off;
     int32_t s = C.found_seq;
@@ -290,12 +302,12 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
       g.n = -1;
       push(g);
     }
-  } else if (warp >= kMsSum && warp < kMsMma) {
+  } else if (warp >= G::kSum && warp < G::kMma) {
     // ---- producers: warp p brings tokens 32p .. 32p + 31 of each tile's K, 512
     // bytes (kRows rows of a slot) an instruction; lane i looks up the pool row of
     // its token.
     constexpr int kCh = 8 * G::kB, kRows = 32 / kCh, kN = 32 / kRows;
-    const int p0 = (warp - kMsSum) * 32, ch = lane % kCh, hl = lane / kCh;
+    const int p0 = (warp - G::kSum) * 32, ch = lane % kCh, hl = lane / kCh;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * kMsBox + (uint32_t)(p0 + hl) * 128u;
     uint32_t slot = 0, phase = 1;
     MassTurn g;
@@ -334,7 +346,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
-  } else if (warp == kMsMma) {
+  } else if (warp == G::kMma) {
     // ---- MMA issuer (one thread): S^T of a tile, N = the turn's pairs rounded up to 16
     if (lane == 0) {
       auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -387,7 +399,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
     __syncwarp();
   } else {
     // ---- sums: thread = TMEM lane = token r of the tiles its group takes
-    const int w = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int w = (warp >> 2) / G::kSplit, half = (warp >> 2) % G::kSplit, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(w * NR);
     const float c_hi = (float)scale_log2;
     const double c_rel = scale_log2 != 0.0 ? (scale_log2 - (double)c_hi) / scale_log2 : 0.0;
@@ -396,7 +408,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
       ok = ok && tc_warp_wait_ready(sm32(&bar), parity, lim, abort_flag);
       return ok;
     };
-    uint32_t jg = 0, turn = 0, seen = 0;
+    uint32_t jg = 0, turn = 0, seen = 0, taken = 0;
     MassTurn g;
     while (take_turn(g, false)) {
       const int32_t *list = C.list[(qn - 1) % kMsQueue];
@@ -408,7 +420,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
         constexpr int kCh = HD / 8, kPer = 32 / kCh;  // 16-byte chunks a row, rows a warp copy
         const int ch = lane % kCh, sub = lane / kCh;
 #pragma unroll 8
-        for (int f = warp * kPer + sub; f < cols16; f += kPer * kMsSum) {
+        for (int f = warp * kPer + sub; f < cols16; f += kPer * G::kSum) {
           const uint32_t to = sQ + (uint32_t)(ch >> 3) * G::kQBox + (uint32_t)f * 128u + (uint32_t)(((ch & 7) ^ (f & 7)) << 4);
           const uint16_t *src = a.q;
           if (f < g.cols) {
@@ -435,7 +447,9 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
                             (lost == lost ? 1.0 + 0.6931471805599453 * lost : 1.0));
             }
           }
-          C.colv[f] = v;
+          float *at = reinterpret_cast<float *>(&C.colv[f >> 1]) + (f & 1);
+          at[0] = -v.x;
+          at[2] = v.y;
           if (v.x == INFINITY) *reinterpret_cast<volatile int32_t *>(&C.dull[turn & 1u]) = (int32_t)turn + 1;
         }
         __syncwarp();
@@ -447,15 +461,19 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
       // pairs that add nothing (padding, lse -inf) must not add NaN for a key that is
       // not finite either
       const bool dull = *reinterpret_cast<volatile int32_t *>(&C.dull[(turn - 1) & 1u]) == (int32_t)turn;
+      // this group's pairs
+      const int mid = G::kSplit == 2 ? (cols16 / 2 + 31) & ~31 : cols16;
+      const int c_lo = half ? mid : 0, c_hi = half ? cols16 : min(mid, cols16);
       float *mass = a.mass + ((int64_t)g.s * a.nkv + g.kvh) * a.mass_cols;
       for (int j = 0; j < g.n && ok; ++j) {
         // (a turn without pairs only scales: no tile of it is multiplied)
         const uint32_t at = g.cols > 0 ? jg + (uint32_t)j : (uint32_t)j;
         if ((int)(at & 1u) != w) continue;
+        if (half != 0 && g.cols == 0) continue;
         const int32_t t0 = (g.t0 + j) * kMsT, t = t0 + r;
         const bool in = t < g.ctx + g.rows;
         float old = 0.f;
-        if (in && (g.first ? t < g.ctx && a.carry != 0.f : true)) old = mass[t];
+        if (in && half == 0 && (g.first ? t < g.ctx && a.carry != 0.f : true)) old = mass[t];
         float sum = 0.f;
         if (g.cols > 0) {
           if (!wait(C.s_full[w], (at >> 1) & 1u)) break;
@@ -476,16 +494,16 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
                                         a.seqs.mask_words, jr, g.rows, k0);
               }
             }
-            const float4 *cv = reinterpret_cast<const float4 *>(C.colv + c);
+            const float4 *cv = C.colv + c / 2;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 v = cv[i];
               float lo, hi;
-              unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, pair_f32(-v.x, -v.z)),
+              unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, pair_f32(v.x, v.y)),
                          lo, hi);
               if (!plain.value) {
-                if (v.x == INFINITY) lo = -INFINITY;
-                if (v.z == INFINITY) hi = -INFINITY;
+                if (v.x == -INFINITY) lo = -INFINITY;
+                if (v.y == -INFINITY) hi = -INFINITY;
                 if (masked) {
                   const uint32_t s0 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + g.h0) - i0);
                   const uint32_t s1 = __shfl_sync(0xffffffffu, sees, fast_div(group_div, c + 2 * i + 1 + g.h0) - i0);
@@ -493,12 +511,12 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
                   if (!((s1 >> lane) & 1u)) hi = -INFINITY;
                 }
               }
-              acc[i & 1] = fma2(pair_f32(ex2(lo), ex2(hi)), pair_f32(v.y, v.w), acc[i & 1]);
+              acc[i & 1] = fma2(pair_f32(ex2(lo), ex2(hi)), pair_f32(v.z, v.w), acc[i & 1]);
             }
           };
           auto sweep = [&](auto plain) {
-            int c = 0;
-            for (; c + 32 <= cols16; c += 32) {
+            int c = c_lo;
+            for (; c + 32 <= c_hi; c += 32) {
               uint32_t sv[32];
               __syncwarp();
               tmem_ld32(lane_base + (uint32_t)c, sv);
@@ -506,7 +524,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
               add(plain, sv, c);
               add(plain, sv + 16, c + 16);
             }
-            if (c < cols16) {
+            if (c < c_hi) {
               uint32_t sv[16];
               __syncwarp();
               tmem_ld16(lane_base + (uint32_t)c, sv);
@@ -518,11 +536,26 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
           float s0, s1;
           unpair_f32(add2(acc[0], acc[1]), s0, s1);
           sum = s0 + s1;
+          if constexpr (G::kSplit == 2) {
+            // the second group's sums pass to the first (read before S's buffer is freed,
+            // so the next ones find the place empty)
+            uint64_t &bar = C.part_full[w][warp & 3];
+            if (half != 0) {
+              C.part[w][r] = sum;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sm32(&bar));
+            } else {
+              if (!wait(bar, taken & 1u)) break;
+              __syncwarp();
+              sum += C.part[w][r];
+            }
+            ++taken;
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(sm32(&C.s_free[w]));
         }
-        if (in) mass[t] = g.first ? fmaf(a.carry, old, sum) : old + sum;
+        if (in && half == 0) mass[t] = g.first ? fmaf(a.carry, old, sum) : old + sum;
       }
       if (!ok) break;
       if (g.cols > 0) jg += (uint32_t)g.n;
@@ -539,7 +572,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, C.found_seq);
-  if (warp == kMsMma)
+  if (warp == G::kMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -548,7 +581,7 @@ cudaError_t launch_mass(const MassArgs &a, cudaStream_t stream) {
   static PerDevice smem_attr;
   const cudaError_t e = set_smem_once(smem_attr, attn_mass_kernel<HD, NR>, mass_smem<HD, NR>());
   if (e != cudaSuccess) return e;
-  return launch_dependent(attn_mass_kernel<HD, NR>, dim3((unsigned)device_sm_count()), dim3(kMsThreads),
+  return launch_dependent(attn_mass_kernel<HD, NR>, dim3((unsigned)device_sm_count()), dim3(MassGeom<HD, NR>::kThreads),
                           mass_smem<HD, NR>(), stream, 1u, a, make_fast_div(a.group),
                           (double)a.scale * 1.4426950408889634);
 }
