@@ -127,7 +127,7 @@ def ref_tree(c, i, scale):
             g = h // c.group
             with np.errstate(all="ignore"):
                 s = (k[t, g] @ q[j, h]) * scale
-                delta = scale * (c.hd + 4) * 2 * U * float((np.abs(k[t, g]) @ np.abs(q[j, h])).max())
+                delta = abs(scale) * (c.hd + 4) * 2 * U * float((np.abs(k[t, g]) @ np.abs(q[j, h])).max())
                 top = s.max()
                 p = np.exp(s - top)
                 lse[j, h] = top + np.log(p.sum())
@@ -158,7 +158,7 @@ def ref_mass(c, i, scale, lse, weight, carry, old):
                     continue
                 t = vis[j]
                 s = (k[t, g] @ q[j, h]) * scale
-                delta = scale * (c.hd + 4) * 2 * U * (np.abs(k[t, g]) @ np.abs(q[j, h]))
+                delta = abs(scale) * (c.hd + 4) * 2 * U * (np.abs(k[t, g]) @ np.abs(q[j, h]))
                 p = w * np.exp(s - float(lse[j, h]))
                 got[g, t] += p
                 tol[g, t] += np.abs(p) * (2 * delta + 2 ** -20 + 4 * U * abs(float(lse[j, h])) + 2 * m * c.group * U)
