@@ -736,35 +736,42 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
                  const float4 *__restrict__ part_o) {
   __shared__ float4 acc_s[kGroups > 1 ? kJoinWarps : 1][32];
   __shared__ float2 ml_s[kGroups > 1 ? kJoinWarps : 1][32];
-  grid_dependency_sync();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int grp = warp % kGroups;
   const int64_t mg = ((int64_t)blockIdx.x * (kJoinWarps / kGroups) + warp / kGroups) * 8 + (lane & 7);
   const int32_t quad = blockIdx.y * 4 + (lane >> 3), kvh = blockIdx.z;
   const int32_t row = mg < (int64_t)a.seqs.n_rows * a.group ? fast_div(group_div, (int32_t)mg) : -1;
   const int32_t head = kvh * a.group + (int32_t)(mg - (int64_t)row * a.group);
-  int32_t c0 = 0, c1 = 0, r = 0, rank = 0;  // teams of the first and last part
-  bool mine = false;
+  // Where the row lies in the plan, while the launch before still runs: it wrote none
+  // of what this reads, and it began after everything before it was complete.
+  int32_t s = 0, r = 0, rank = 0, tiles = 0;
+  int64_t u0 = 0;  // the unit's first tile, from its sequence's first
   if (row >= 0) {
-    const int32_t s = seq_of_row(a.seqs, row);
+    s = seq_of_row(a.seqs, row);
     const SeqTiles q = seq_tiles<TreeGeom<HD>::kT>(a, team_log, read_seq(a.seqs, s));
     if (row >= q.v.row0 && row < q.v.row0 + q.v.rows) {
       const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
       const int32_t mt = (int32_t)(m >> kTrRowsLog);
       r = (int32_t)(m & (kTrRows - 1));
       rank = mt & ((1 << team_log) - 1);
-      const int64_t per = (base[a.seqs.n_seqs] + teams - 1) / teams;
-      const int64_t u0 = base[s] + ((int64_t)kvh * q.m_tiles + (mt >> team_log)) * (q.tiles + kTrStart) + kTrStart;
-      if (((u0 + q.tiles) >> 31) == 0) {
-        c0 = (int32_t)((uint32_t)u0 / (uint32_t)per);
-        c1 = (int32_t)((uint32_t)(u0 + q.tiles - 1) / (uint32_t)per);
-      } else {
-        c0 = (int32_t)(u0 / per);
-        c1 = (int32_t)((u0 + q.tiles - 1) / per);
-      }
-      mine = c0 != c1;
+      tiles = q.tiles;
+      u0 = ((int64_t)kvh * q.m_tiles + (mt >> team_log)) * (tiles + kTrStart) + kTrStart;
     }
   }
+  grid_dependency_sync();
+  int32_t c0 = 0, c1 = 0;  // teams of the first and last part
+  if (tiles > 0) {
+    const int64_t per = (base[a.seqs.n_seqs] + teams - 1) / teams;
+    u0 += base[s];
+    if (((u0 + tiles) >> 31) == 0) {
+      c0 = (int32_t)((uint32_t)u0 / (uint32_t)per);
+      c1 = (int32_t)((uint32_t)(u0 + tiles - 1) / (uint32_t)per);
+    } else {
+      c0 = (int32_t)(u0 / per);
+      c1 = (int32_t)((u0 + tiles - 1) / per);
+    }
+  }
+  const bool mine = c0 != c1;
   auto part_of = [&](int32_t c) { return (((int64_t)c << team_log) + rank) * 2 + (c == c0 ? 1 : 0); };
   auto ml_at = [&](int32_t c) { return part_ml[part_of(c) * part_rows + r]; };
   auto o_at = [&](int32_t c) { return part_o[(part_of(c) * (HD / 4) + quad) * part_rows + r]; };
