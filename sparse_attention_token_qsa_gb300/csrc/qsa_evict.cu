@@ -42,7 +42,7 @@ struct EvictCtrl {
   uint32_t hist[3][kEvBins];
   uint32_t coarse[3][kEvBins / kEvGroup];
   uint32_t warp_tot[kEvWarps], gt[kEvWarps], eq[kEvWarps];
-  uint32_t gt_all, eq_all, above;
+  uint32_t gt_all, eq_all, above, inside;
   int32_t bin, bad;
 };
 constexpr size_t kEvKeysOff = (sizeof(EvictCtrl) + 15) / 16 * 16;
@@ -202,6 +202,7 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
   // ---- the key of the last unit that stays: the need-th largest of those that compete
   uint32_t need = (uint32_t)(keep - lo - (units - hi)), prefix = 0;
   const bool none = need == 0;  // the protected units fill the budget
+  uint32_t cut = kProtected - 1u;
 #pragma unroll
   for (int round = 0; round < 3; ++round) {
     constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
@@ -249,6 +250,7 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
         const bool upper = need <= above + n.y;
         C.bin = 2 * at + (upper ? 1 : 0);
         C.above = upper ? above : above + n.y;
+        C.inside = upper ? n.y : n.x;
       }
     } else if (warp == 0) {
       // One warp looks through the 64 groups and then the 32 bins of one: reading all
@@ -272,24 +274,61 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
       if (lane == src) {
         C.bin = at;
         C.above = up - n;
+        C.inside = n;
       }
     }
     __syncthreads();
     prefix = (prefix << kBits[round]) | (uint32_t)C.bin;
     need -= C.above;
+    // Where the whole bin stays, every key from its lowest on does, and no bit more is
+    // needed: after two rounds that is the rule, keys that share 22 bits being few.
+    if (round < 2 && need == C.inside) {
+      cut = (prefix << (round == 0 ? 21 : 10)) - 1u;
+      need = 0;
+      break;
+    }
+    if (round == 2) cut = prefix;
   }
-  const uint32_t cut = none ? kProtected - 1u : prefix, ties = none ? 0u : need;
+  const uint32_t ties = none ? 0u : need;
 
   // ---- counts before each warp's run, then the list
-  const int32_t run = ((seg + kEvWarps - 1) / kEvWarps + 127) & ~127;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.sel) & 15u) == 0 && (a.sel_cols & 3) == 0;
+  auto put = [&](uint32_t at, int32_t u) {
+    int32_t *to = sel + (int64_t)at * UNIT;
+    const int32_t tok = u * UNIT;
+    if (UNIT == 4 && wide) {
+      *reinterpret_cast<int4 *>(to) = make_int4(tok, tok + 1, tok + 2, tok + 3);
+    } else {
+#pragma unroll
+      for (int f = 0; f < UNIT; ++f) to[f] = tok + f;
+    }
+  };
+  // Keys in shared memory: a lane takes `lane_run` units side by side, an odd number,
+  // which no two lanes read from one bank; what stays of them are the bits of two words.
+  // Otherwise a warp takes steps of 128 units, twice.
+  const int32_t lane_run = ((seg + kEvThreads - 1) / kEvThreads) | 1;
+  const int32_t run = CACHED ? 32 * lane_run : ((seg + kEvWarps - 1) / kEvWarps + 127) & ~127;
   const int32_t w0 = min((int64_t)u1, (int64_t)u0 + warp * run), w1 = min((int64_t)u1, (int64_t)w0 + run);
   uint32_t gt = 0, eq = 0;
-#pragma unroll 2
-  for (int32_t u = w0 + 4 * lane; u < w1; u += 128) {
-    const uint4 k = keys_at(u);
-    gt += (k.x > cut) + (k.y > cut) + (k.z > cut) + (k.w > cut);
-    eq += (k.x == cut) + (k.y == cut) + (k.z == cut) + (k.w == cut);
+  uint64_t gt_bits = 0, eq_bits = 0;
+  if constexpr (CACHED) {
+    const int32_t l0 = w0 + lane * lane_run, n = min(lane_run, w1 - l0);
+#pragma unroll 4
+    for (int32_t i = 0; i < n; ++i) {
+      const uint32_t k = keys[l0 - u0 + i];
+      gt_bits |= (uint64_t)(k > cut) << i;
+      eq_bits |= (uint64_t)(k == cut) << i;
+    }
+    gt = __popcll(gt_bits);
+    eq = __popcll(eq_bits);
+  } else {
+    for (int32_t u = w0 + 4 * lane; u < w1; u += 128) {
+      const uint4 k = keys_at(u);
+      gt += (k.x > cut) + (k.y > cut) + (k.z > cut) + (k.w > cut);
+      eq += (k.x == cut) + (k.y == cut) + (k.z == cut) + (k.w == cut);
+    }
   }
+  const uint32_t lane_gt = gt, lane_eq = eq;
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
@@ -314,7 +353,17 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
     eq += __reduce_add_sync(0xffffffffu, before ? *cluster.map_shared_rank(&C.eq_all, before ? lane : 0) : 0u);
     cluster.sync();  // no CTA leaves while its counts are read
   }
-  const bool wide = (reinterpret_cast<uintptr_t>(a.sel) & 15u) == 0 && (a.sel_cols & 3) == 0;
+  if constexpr (CACHED) {
+    uint32_t my_gt = gt + warp_upto(lane_gt, lane) - lane_gt, my_eq = eq + warp_upto(lane_eq, lane) - lane_eq;
+    const int32_t l0 = w0 + lane * lane_run;
+    for (uint64_t stay = gt_bits | eq_bits; stay; stay &= stay - 1) {
+      const int i = __ffsll((long long)stay) - 1;
+      const bool more = (gt_bits >> i) & 1u;
+      if (more || my_eq < ties) put(my_gt + min(my_eq, ties), l0 + i);
+      my_gt += more;
+      my_eq += !more;
+    }
+  } else
   for (int32_t b = w0; b < w1; b += 128) {
     const int32_t u = b + 4 * lane;
     const uint4 k4 = u < w1 ? keys_at(u) : make_uint4(kNoUnit, kNoUnit, kNoUnit, kNoUnit);
@@ -332,14 +381,7 @@ evict_kernel(const EvictArgs a, int32_t ctas) {
     for (int e = 0; e < 4; ++e) {
       const bool more = k[e] > cut, same = k[e] == cut;
       if (more || (same && my_eq < ties)) {
-        const int64_t at = (int64_t)(my_gt + min(my_eq, ties)) * UNIT;
-        const int32_t tok = (u + e) * UNIT;
-        if (UNIT == 4 && wide) {
-          *reinterpret_cast<int4 *>(sel + at) = make_int4(tok, tok + 1, tok + 2, tok + 3);
-        } else {
-#pragma unroll
-          for (int f = 0; f < UNIT; ++f) sel[at + f] = tok + f;
-        }
+        put(my_gt + min(my_eq, ties), u + e);
       }
       my_gt += more;
       my_eq += same;
