@@ -508,7 +508,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
       float top = -INFINITY, sum = 0.f;  // sum is relative to top
       auto rebase = [&](float t) {
         if (t != top) {
-          sum = top == -INFINITY ? 0.f : sum * ex2(top - t);
+          sum *= top == -INFINITY ? 0.f : ex2(top - t);  // (a NaN so far stays)
           top = t;
         }
       };

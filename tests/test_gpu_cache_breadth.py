@@ -117,6 +117,42 @@ def test_nonfinite_values_of_wide_trees(qsa):
         tree_check(c, out, lse)
 
 
+@pytest.mark.parametrize("hd", [128, 256])
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80])
+def test_keys_that_are_not_finite(qsa, hd, bad):
+    """Every key of the first tiles, one in the middle, or a drafted one: each row that
+    sees one gets NaN (its logit may be an infinity of either sign, or NaN), and lse too."""
+    rng = qi.rng_for(70, salt=hd)
+    for where in ("first", "one", "drafted"):
+        c = Cache(rng, [400, 60], [9, 3], 8, 2, hd, 16, "tree")
+        if where == "first":
+            c.k[c.slots(0, np.arange(200))] = bad
+        elif where == "one":
+            c.k[c.slots(0, np.array([250])), 5] = bad
+        else:
+            c.k[c.slots(0, np.array([403])), hd + 1] = bad
+        out, lse, st = tree_call(qsa, c)
+        assert st == (0, 0)
+        tree_check(c, out, lse)
+
+
+def test_refuses_tensors_of_another_device(qsa, monkeypatch):
+    c = Cache(qi.rng_for(71), [40], [2], 8, 2, 128, 16, "tree")
+    args = c.tree_args(dev(c.q), c.nq * c.hd)
+    out, st = torch.zeros((2, 1024), dtype=torch.int16, device="cuda"), qsa.new_status()
+    ws = qsa.new_tree_workspace(c.n, c.n_rows, c.nq, c.nkv, c.hd)
+    x = torch.zeros(64, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:0"):
+        qsa.qsa_tree_attn(*args, 1.0, out, 1024, None, st, ws)
+    with pytest.raises(ValueError, match="cuda:0"):
+        qsa.qsa_attn_mass(*c.mass_args(args[0], 1024), 1.0, x, None, 1.0, x, 64, st)
+    with pytest.raises(ValueError, match="cuda:0"):
+        qsa.qsa_evict_select(x, 64, 1, x, 1, 64, 4, 0, 0, 4, x, 64, x, st)
+    with pytest.raises(ValueError, match="cuda:0"):
+        qsa.qsa_cache_compact(x, x, 8, 1, x, 1, 1, 1, x, 1, x, 1, 1, None, None, 0, 0, None, None, st)
+
+
 def test_two_graphs_share_a_workspace(qsa):
     """Two captured calls of different shapes use the same workspace, replayed in turn on one stream."""
     cs = [Cache(qi.rng_for(67, salt=i), [3000 - 900 * i, 50], [6, 20 * i + 1], 16, 2, 256, 16, "tree") for i in range(2)]
