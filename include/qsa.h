@@ -544,9 +544,9 @@ qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
  * cache; with first = ctx_len and the accepted drafted tokens it joins a
  * verified path to its context.
  *  k_pool, v_pool, width, pool_pages, table, table_len, table_cols, page_size:
- *           as in qsa_gather_kv (pool_pages * page_size < 2^31).  No page may be in two sequences' tables among
- *           the tokens that are read or written here (table_cols = 0 is refused
- *           for n_seqs > 1).
+ *           as in qsa_gather_kv (pool_pages * page_size < 2^31).  No page may be
+ *           in two sequences' tables among the tokens that are read or written
+ *           here (table_cols = 0 is refused for n_seqs > 1).
  *  keep     DEVICE int32, row s at keep + s*keep_cols, its first n_keep[s] <=
  *           max_keep entries; keep[j] >= first + j (tokens only move towards the
  *           front; an ascending list of tokens from first on always does).

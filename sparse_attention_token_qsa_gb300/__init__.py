@@ -126,12 +126,42 @@ def _dev(t: torch.Tensor | None, name: str):
     return t.data_ptr()
 
 
+def _home(t, name: str) -> int:
+    """The device a cache operator works on: that of its first tensor, which has to be
+    the current one (the launch goes there, and the others' memory is not mapped)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    d = t.get_device()
+    if d < 0:
+        _dev(t, name)
+        return torch.cuda.current_device()
+    here = torch.cuda.current_device()
+    if d != here:
+        raise ValueError(f"{name} is on cuda:{d}, the current device is cuda:{here}")
+    return d
+
+
+def _at(t, name: str, home: int):
+    """_dev of a tensor that has to be on the operator's device, or pinned."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor):
+        d = t.get_device()
+        if d == home:
+            return t.data_ptr()
+        if d >= 0:
+            raise ValueError(f"{name} is on cuda:{d}, the other tensors on cuda:{home}")
+    return _dev(t, name)
+
+
+def _raw(stream, device: int) -> int:
+    """The cudaStream_t of a torch stream (default: the device's current one, asked for
+    without making a stream object: 3 us a call on a Grace core)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 def _stream(stream) -> int:
-    """The cudaStream_t of a torch stream (default: the current device's current
-    one, asked for without making a stream object: 3 us a call on a Grace core)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+    return _raw(stream, torch.cuda.current_device() if stream is None else 0)
 
 
 def _check(rc: int, where: str) -> None:
@@ -341,53 +371,58 @@ def new_tree_workspace(n_seqs: int, n_rows: int, nq: int, nkv: int, head_dim: in
 def qsa_tree_attn(q, q_stride, nq, nkv, head_dim, k_pool, v_pool, pool_pages, page_size, table,
                   table_len, table_cols, ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words,
                   scale, out, out_stride, lse, dev_status, workspace, stream=None) -> None:
-    ws, wsb = _ws(workspace)
-    _check(_lib.qsa_tree_attn(_dev(q, "q"), int(q_stride), int(nq), int(nkv), int(head_dim),
-                              _dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), int(pool_pages),
-                              int(page_size), _dev(table, "table"), int(table_len),
-                              int(table_cols), _dev(ctx_len, "ctx_len"),
-                              _dev(row_start, "row_start"), int(n_seqs), int(n_rows),
-                              _dev(tree_mask, "tree_mask"), int(mask_words), float(scale),
-                              _dev(out, "out"), int(out_stride), _dev(lse, "lse"),
-                              _dev(dev_status, "dev_status"), ws, int(wsb), _stream(stream)),
+    home = _home(q, "q")
+    ws = _at(workspace, "workspace", home)
+    wsb = 0 if ws is None else workspace.numel() * workspace.element_size()
+    _check(_lib.qsa_tree_attn(_at(q, "q", home), int(q_stride), int(nq), int(nkv), int(head_dim),
+                              _at(k_pool, "k_pool", home), _at(v_pool, "v_pool", home), int(pool_pages),
+                              int(page_size), _at(table, "table", home), int(table_len),
+                              int(table_cols), _at(ctx_len, "ctx_len", home),
+                              _at(row_start, "row_start", home), int(n_seqs), int(n_rows),
+                              _at(tree_mask, "tree_mask", home), int(mask_words), float(scale),
+                              _at(out, "out", home), int(out_stride), _at(lse, "lse", home),
+                              _at(dev_status, "dev_status", home), ws, wsb, _raw(stream, home)),
            "qsa_tree_attn")
 
 
 def qsa_attn_mass(q, q_stride, nq, nkv, head_dim, k_pool, pool_pages, page_size, table, table_len,
                   table_cols, ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words, scale,
                   lse, row_weight, carry, mass, mass_cols, dev_status, stream=None) -> None:
-    _check(_lib.qsa_attn_mass(_dev(q, "q"), int(q_stride), int(nq), int(nkv), int(head_dim),
-                              _dev(k_pool, "k_pool"), int(pool_pages), int(page_size),
-                              _dev(table, "table"), int(table_len), int(table_cols),
-                              _dev(ctx_len, "ctx_len"), _dev(row_start, "row_start"), int(n_seqs),
-                              int(n_rows), _dev(tree_mask, "tree_mask"), int(mask_words),
-                              float(scale), _dev(lse, "lse"), _dev(row_weight, "row_weight"),
-                              float(carry), _dev(mass, "mass"), int(mass_cols),
-                              _dev(dev_status, "dev_status"), _stream(stream)),
+    home = _home(q, "q")
+    _check(_lib.qsa_attn_mass(_at(q, "q", home), int(q_stride), int(nq), int(nkv), int(head_dim),
+                              _at(k_pool, "k_pool", home), int(pool_pages), int(page_size),
+                              _at(table, "table", home), int(table_len), int(table_cols),
+                              _at(ctx_len, "ctx_len", home), _at(row_start, "row_start", home), int(n_seqs),
+                              int(n_rows), _at(tree_mask, "tree_mask", home), int(mask_words),
+                              float(scale), _at(lse, "lse", home), _at(row_weight, "row_weight", home),
+                              float(carry), _at(mass, "mass", home), int(mass_cols),
+                              _at(dev_status, "dev_status", home), _raw(stream, home)),
            "qsa_attn_mass")
 
 
 def qsa_evict_select(mass, mass_cols, nkv, length, n_seqs, tokens, keep, n_first, n_last, unit,
                      sel, sel_cols, n_sel, dev_status, stream=None) -> None:
-    _check(_lib.qsa_evict_select(_dev(mass, "mass"), int(mass_cols), int(nkv),
-                                 _dev(length, "length"), int(n_seqs), int(tokens), int(keep),
-                                 int(n_first), int(n_last), int(unit), _dev(sel, "sel"),
-                                 int(sel_cols), _dev(n_sel, "n_sel"),
-                                 _dev(dev_status, "dev_status"), _stream(stream)),
+    home = _home(mass, "mass")
+    _check(_lib.qsa_evict_select(_at(mass, "mass", home), int(mass_cols), int(nkv),
+                                 _at(length, "length", home), int(n_seqs), int(tokens), int(keep),
+                                 int(n_first), int(n_last), int(unit), _at(sel, "sel", home),
+                                 int(sel_cols), _at(n_sel, "n_sel", home),
+                                 _at(dev_status, "dev_status", home), _raw(stream, home)),
            "qsa_evict_select")
 
 
 def qsa_cache_compact(k_pool, v_pool, width, pool_pages, table, table_len, table_cols, page_size,
                       keep, keep_cols, n_keep, n_seqs, max_keep, first, mass, mass_cols, nkv,
                       block_keys, key_base, dev_status, stream=None) -> None:
-    _check(_lib.qsa_cache_compact(_dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), int(width),
-                                  int(pool_pages), _dev(table, "table"), int(table_len),
-                                  int(table_cols), int(page_size), _dev(keep, "keep"),
-                                  int(keep_cols), _dev(n_keep, "n_keep"), int(n_seqs),
-                                  int(max_keep), _dev(first, "first"), _dev(mass, "mass"),
-                                  int(mass_cols), int(nkv), _dev(block_keys, "block_keys"),
-                                  _dev(key_base, "key_base"), _dev(dev_status, "dev_status"),
-                                  _stream(stream)),
+    home = _home(k_pool, "k_pool")
+    _check(_lib.qsa_cache_compact(_at(k_pool, "k_pool", home), _at(v_pool, "v_pool", home), int(width),
+                                  int(pool_pages), _at(table, "table", home), int(table_len),
+                                  int(table_cols), int(page_size), _at(keep, "keep", home),
+                                  int(keep_cols), _at(n_keep, "n_keep", home), int(n_seqs),
+                                  int(max_keep), _at(first, "first", home), _at(mass, "mass", home),
+                                  int(mass_cols), int(nkv), _at(block_keys, "block_keys", home),
+                                  _at(key_base, "key_base", home), _at(dev_status, "dev_status", home),
+                                  _raw(stream, home)),
            "qsa_cache_compact")
 
 
