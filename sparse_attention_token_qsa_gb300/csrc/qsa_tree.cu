@@ -725,21 +725,22 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
 }
 
 // Joins the parts of the units that several CTAs share.  A warp takes 8 rows x 4
-// quads of dims (a part's rows lie side by side) and every kGroups-th part, with
-// the running maximum of those; the groups' results are then added in order.
+// times kQuads quads of dims (a part's rows lie side by side) and every
+// kGroups-th part, two at a time with the running maximum: one trip to L2 for both
+// the maxima and the values.  The groups' results are then added in order.
 constexpr int kJoinWarps = 8;
 
-template <int HD, int kGroups>
+template <int HD, int kGroups, int kQuads>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_t part_rows, int32_t teams,
                  const int64_t *__restrict__ base, const float2 *__restrict__ part_ml,
                  const float4 *__restrict__ part_o) {
-  __shared__ float4 acc_s[kGroups > 1 ? kJoinWarps : 1][32];
+  __shared__ float4 acc_s[kGroups > 1 ? kJoinWarps : 1][kQuads][32];
   __shared__ float2 ml_s[kGroups > 1 ? kJoinWarps : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int grp = warp % kGroups;
   const int64_t mg = ((int64_t)blockIdx.x * (kJoinWarps / kGroups) + warp / kGroups) * 8 + (lane & 7);
-  const int32_t quad = blockIdx.y * 4 + (lane >> 3), kvh = blockIdx.z;
+  const int32_t quad = blockIdx.y * (4 * kQuads) + (lane >> 3), kvh = blockIdx.z;
   const int32_t row = mg < (int64_t)a.seqs.n_rows * a.group ? fast_div(group_div, (int32_t)mg) : -1;
   const int32_t head = kvh * a.group + (int32_t)(mg - (int64_t)row * a.group);
   // Where the row lies in the plan, while the launch before still runs: it wrote none
@@ -773,49 +774,68 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   }
   const bool mine = c0 != c1;
   auto part_of = [&](int32_t c) { return (((int64_t)c << team_log) + rank) * 2 + (c == c0 ? 1 : 0); };
-  auto ml_at = [&](int32_t c) { return part_ml[part_of(c) * part_rows + r]; };
-  auto o_at = [&](int32_t c) { return part_o[(part_of(c) * (HD / 4) + quad) * part_rows + r]; };
+  const float2 none = make_float2(-INFINITY, 0.f);
   float top = -INFINITY, all = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kQuads];
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [](float4 &s, const float4 &x, float w) {
+    s.x = fmaf(x.x, w, s.x);
+    s.y = fmaf(x.y, w, s.y);
+    s.z = fmaf(x.z, w, s.z);
+    s.w = fmaf(x.w, w, s.w);
+  };
+  auto scaled = [](const float4 &x, float w) { return make_float4(x.x * w, x.y * w, x.z * w, x.w * w); };
   if (mine) {
-    for (int32_t c = c0 + grp; c <= c1; c += kGroups) top = fmaxf(top, ml_at(c).x);
-    const float use = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-    for (int32_t c = c0 + grp; c <= c1; c += kGroups) {
-      const float2 ml = ml_at(c);
-      const float4 x = o_at(c);
-      const float w = ex2(ml.x - use);
-      all = fmaf(ml.y, w, all);
-      acc.x = fmaf(x.x, w, acc.x);
-      acc.y = fmaf(x.y, w, acc.y);
-      acc.z = fmaf(x.z, w, acc.z);
-      acc.w = fmaf(x.w, w, acc.w);
+    for (int32_t c = c0 + grp; c <= c1; c += 2 * kGroups) {
+      float2 ml[2];
+      float4 x[2][kQuads];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool there = e == 0 || c + kGroups <= c1;
+        const int64_t part = part_of(there ? c + e * kGroups : c);
+        ml[e] = there ? part_ml[part * part_rows + r] : none;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+          x[e][i] = there ? part_o[(part * (HD / 4) + quad + 4 * i) * part_rows + r] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      const float now = fmaxf(top, fmaxf(ml[0].x, ml[1].x)), use = now == -INFINITY ? 0.f : now;
+      const float w = ex2(top - use), w0 = ex2(ml[0].x - use), w1 = ex2(ml[1].x - use);
+      top = now;
+      all = fmaf(ml[1].y, w1, fmaf(ml[0].y, w0, all * w));
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        acc[i] = scaled(acc[i], w);
+        add(acc[i], x[0][i], w0);
+        add(acc[i], x[1][i], w1);
+      }
     }
   }
   if constexpr (kGroups > 1) {
-    acc_s[warp][lane] = acc;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) acc_s[warp][i][lane] = acc[i];
     ml_s[warp][lane] = make_float2(top, all);
     __syncthreads();
     if (grp != 0) return;
-    for (int i = 0; i < kGroups; ++i) top = fmaxf(top, ml_s[warp + i][lane].x);
+    for (int g = 1; g < kGroups; ++g) top = fmaxf(top, ml_s[warp + g][lane].x);
     const float use = top == -INFINITY ? 0.f : top;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
     all = 0.f;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const float w = ex2(ml_s[warp + i][lane].x - use);
-      const float4 x = acc_s[warp + i][lane];
-      all = fmaf(ml_s[warp + i][lane].y, w, all);
-      acc.x = fmaf(x.x, w, acc.x);
-      acc.y = fmaf(x.y, w, acc.y);
-      acc.z = fmaf(x.z, w, acc.z);
-      acc.w = fmaf(x.w, w, acc.w);
+    for (int i = 0; i < kQuads; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float w = ex2(ml_s[warp + g][lane].x - use);
+      all = fmaf(ml_s[warp + g][lane].y, w, all);
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) add(acc[i], acc_s[warp + g][i][lane], w);
     }
   }
   if (!mine) return;
   const float inv = all == 0.f ? 0.f : 1.f / all;
-  *reinterpret_cast<uint2 *>(a.out + (int64_t)row * a.out_stride + (int64_t)head * HD + 4 * quad) =
-      make_uint2(pack_f32_bf16(acc.x * inv, acc.y * inv), pack_f32_bf16(acc.z * inv, acc.w * inv));
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i)
+    *reinterpret_cast<uint2 *>(a.out + (int64_t)row * a.out_stride + (int64_t)head * HD + 4 * (quad + 4 * i)) =
+        make_uint2(pack_f32_bf16(acc[i].x * inv, acc[i].y * inv), pack_f32_bf16(acc[i].z * inv, acc[i].w * inv));
   if (quad == 0 && a.lse)
     a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
 }
@@ -862,8 +882,14 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   const int64_t units = (int64_t)a.nkv * (((int64_t)a.seqs.n_rows * a.group + kTrRows - 1) / kTrRows);
   const bool many = ctas >= 8 * units;
   const int64_t blocks = many ? rows8 : (rows8 + kJoinWarps - 1) / kJoinWarps;
-  return launch_dependent(many ? tree_join_kernel<HD, kJoinWarps> : tree_join_kernel<HD, 1>,
-                          dim3((unsigned)blocks, HD / 16, (unsigned)a.nkv), dim3(32 * kJoinWarps), 0, stream, 1u, a,
+  // Four quads a thread keep more reads on their way where blocks come in waves (64
+  // rows of 65k tokens: 77.0 us, 80.6 with one); one where they are few (12.1 us for a
+  // row of 515 tokens, 12.8 with four).
+  const bool few = many && rows8 * a.nkv * (HD / 16) <= device_sm_count();
+  return launch_dependent(few    ? tree_join_kernel<HD, kJoinWarps, 1>
+                          : many ? tree_join_kernel<HD, kJoinWarps, 4>
+                                 : tree_join_kernel<HD, 1, 4>,
+                          dim3((unsigned)blocks, few ? HD / 16 : HD / 64, (unsigned)a.nkv), dim3(32 * kJoinWarps), 0, stream, 1u, a,
                           group_div, team_log, part_rows, (int32_t)(ctas >> team_log), base, ml, reinterpret_cast<const float4 *>(o));
 }
 
