@@ -38,6 +38,7 @@ namespace {
 constexpr int kMsProd = 4;
 constexpr int kMsT = 128;                  // tokens per tile: the MMA's M
 constexpr int kMsQueue = 2;
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;  // log2(e) in two words
 constexpr uint32_t kMsBox = kMsT * 128;    // 64 dims of a tile: 16 KiB
 constexpr long long kMsSpinLimit = 4000000000LL;
 
@@ -107,7 +108,7 @@ __device__ __forceinline__ MassSeq mass_seq(const MassArgs &a, int32_t s) {
 
 template <int HD, int NR>
 __global__ void __launch_bounds__(MassGeom<HD, NR>::kThreads, 1)
-attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
+attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel) {
   using G = MassGeom<HD, NR>;
   extern __shared__ __align__(1024) uint8_t ms_smem[];
   MassCtrl<NR> &C = *reinterpret_cast<MassCtrl<NR> *>(ms_smem + G::kCtrlOff);
@@ -151,53 +152,66 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
   }
 
   // ---- the plan: every sequence's tiles summed, then the sequence this CTA's
-  // share starts in; one thread a sequence, in chunks where there are more
-  const bool one_chunk = a.seqs.n_seqs <= G::kThreads;
-  int64_t total = 0;
-  if (!one_chunk) {
-    for (int32_t s = tid; s < a.seqs.n_seqs; s += G::kThreads) total += mass_seq(a, s).count;
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) C.scan[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int i = 0; i < G::kWarps; ++i) total += C.scan[i];
-  }
-  int64_t before = 0, share = 0;
-  for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += G::kThreads) {
-    const int32_t s = s0 + tid;
-    int64_t count = 0;
-    if (s < a.seqs.n_seqs) {
-      const MassSeq q = mass_seq(a, s);
-      count = q.count;
-      if (blockIdx.x == 0 && !q.v.ok) report_error(a.status, kErrRowRange, s);
+  // share starts in.  Up to 32 sequences, a lane each, every warp for itself; else a
+  // thread each, in chunks.
+  int64_t total = 0, found_off = 0;
+  int32_t found_seq = a.seqs.n_seqs;
+  TileShare part = {0, 0, 0};
+  auto tiles_of = [&](int32_t s, bool report) -> int64_t {
+    if (s >= a.seqs.n_seqs) return 0;
+    const MassSeq q = mass_seq(a, s);
+    if (report && !q.v.ok) report_error(a.status, kErrRowRange, s);
+    return q.count;
+  };
+  if (a.seqs.n_seqs <= 32) {
+    const int64_t count = tiles_of(lane, blockIdx.x == 0 && warp == 0), incl = warp_scan(count, lane), at = incl - count;
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    part = tile_share(total, gridDim.x, blockIdx.x);
+    const uint32_t hit = __ballot_sync(0xffffffffu, part.n > 0 && count > 0 && at <= part.first && part.first < incl);
+    if (hit != 0) {
+      found_seq = __ffs(hit) - 1;
+      found_off = part.first - __shfl_sync(0xffffffffu, at, found_seq);
     }
-    int64_t incl = count;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+  } else {
+    const bool one_chunk = a.seqs.n_seqs <= G::kThreads;
+    if (!one_chunk) {
+      for (int32_t s = tid; s < a.seqs.n_seqs; s += G::kThreads) total += tiles_of(s, false);
+      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      if (lane == 0) C.scan[warp] = total;
+      __syncthreads();
+      total = 0;
+      for (int i = 0; i < G::kWarps; ++i) total += C.scan[i];
     }
-    __syncthreads();
-    if (lane == 31) C.scan[warp] = incl;
-    __syncthreads();
-    int64_t at = before + incl - count;
+    int64_t before = 0;
+    for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += G::kThreads) {
+      const int32_t s = s0 + tid;
+      const int64_t count = tiles_of(s, blockIdx.x == 0), incl = warp_scan(count, lane);
+      __syncthreads();
+      if (lane == 31) C.scan[warp] = incl;
+      __syncthreads();
+      int64_t at = before + incl - count;
 #pragma unroll
-    for (int i = 0; i < G::kWarps; ++i) {
-      at += i < warp ? C.scan[i] : 0;
-      before += C.scan[i];
+      for (int i = 0; i < G::kWarps; ++i) {
+        at += i < warp ? C.scan[i] : 0;
+        before += C.scan[i];
+      }
+      if (one_chunk) total = before;
+      part = tile_share(total, gridDim.x, blockIdx.x);
+      if (part.n > 0 && count > 0 && at <= part.first && part.first < at + count) {
+        C.found_seq = s;
+        C.found_off = part.first - at;
+      }
+      if (blockIdx.x != 0 && before > part.first) break;
     }
-    if (one_chunk) total = before;
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x, w0 = per * blockIdx.x;
-    share = max((int64_t)0, min(per, total - w0));
-    if (share > 0 && count > 0 && at <= w0 && w0 < at + count) {
-      C.found_seq = s;
-      C.found_off = w0 - at;
-    }
-    if (blockIdx.x != 0 && before > w0) break;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = C.tmem_base;
+  if (a.seqs.n_seqs > 32) {
+    found_seq = C.found_seq;
+    found_off = C.found_off;
+  }
   const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
 
   // The next turn of the share (a whole warp, or the issuer's one thread).
@@ -220,8 +234,8 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
 
   if (warp == G::kPlan) {
     // ---- the share's turns: rows of weight 0 are passed over
-    int64_t left = share, off = C.found_off;
-    int32_t s = C.found_seq;
+    int64_t left = part.n, off = found_off;
+    int32_t s = found_seq;
     auto push = [&](const MassTurn &g) {  // (the list is written)
       __syncwarp();
       if (lane == 0) {
@@ -401,9 +415,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
     // ---- sums: thread = TMEM lane = token r of the tiles its group takes
     const int w = (warp >> 2) / G::kSplit, half = (warp >> 2) % G::kSplit, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(w * NR);
-    const float c_hi = (float)scale_log2;
-    const double c_rel = scale_log2 != 0.0 ? (scale_log2 - (double)c_hi) / scale_log2 : 0.0;
-    const uint64_t c2 = pair_f32(c_hi, c_hi);
+    const uint64_t c2 = pair_f32(c, c);
     auto wait = [&](uint64_t &bar, uint32_t parity) {
       ok = ok && tc_warp_wait_ready(sm32(&bar), parity, lim, abort_flag);
       return ok;
@@ -439,12 +451,14 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
             const float lse = a.lse[row * a.nq + g.kvh * a.group + f + g.h0 - i * a.group];
             if (lse != -INFINITY) {
               // exp(scale s - lse) = 2^(s c - l): what c and l lose to f32 goes into the
-              // weight, c's share at s c = l, where the token that matters lies
-              const double l = (double)lse * 1.4426950408889634;
-              v.x = (float)l;
-              const double lost = (double)v.x - l + c_rel * l;  // log2 units, under 2^-17 of l
-              v.y = (float)((a.weight ? (double)a.weight[row] : 1.0) *
-                            (lost == lost ? 1.0 + 0.6931471805599453 * lost : 1.0));
+              // weight, c's share at s c = l, where the token that matters lies.  l is
+              // the product of lse and log2(e), the latter in two words; its f32
+              // rounding and the rest are exact but for the rest's own rounding.
+              v.x = __fmul_rn(lse, kLog2eHi);
+              const float rest = fmaf(lse, kLog2eHi, -v.x) + lse * kLog2eLo;
+              const float lost = fmaf(c_rel, v.x, -rest);  // log2 units, under 2^-22 of l
+              const float w = a.weight ? a.weight[row] : 1.f;
+              v.y = lost == lost ? fmaf(w, 0.69314718f * lost, w) : w;
             }
           }
           float *at = reinterpret_cast<float *>(&C.colv[f >> 1]) + (f & 1);
@@ -480,13 +494,15 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
           tc_fence_after();
           const bool masked = t0 + kMsT > g.ctx;
           const int32_t k0 = t0 + (warp & 3) * 32 - g.ctx;  // drafted index of the warp's first token
-          const int last_row = (int)fast_div(group_div, g.cols - 1 + g.h0);
           uint64_t acc[2] = {0ull, 0ull};
           // 16 pairs from c on; `plain`: every one counts for every token
           auto add = [&](auto plain, const uint32_t *sv, int c) {
             uint32_t sees = 0;
             int i0 = 0;
-            if (!plain.value && masked) {  // lane i: which of the warp's 32 tokens the i-th row of these pairs sees
+            if (!plain.value) asm volatile("" : "+r"(c));
+            if (!plain.value && masked) {
+              const int last_row = (int)fast_div(group_div, g.cols - 1 + g.h0);
+              // lane i: which of the warp's 32 tokens the i-th row of these pairs sees
               i0 = fast_div(group_div, c + g.h0);
               if (i0 + lane <= last_row && lane < 16) {
                 const int32_t jr = list[i0 + lane];
@@ -571,7 +587,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, double scale_log2) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, C.found_seq);
+  if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found_seq);
   if (warp == G::kMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
@@ -581,9 +597,12 @@ cudaError_t launch_mass(const MassArgs &a, cudaStream_t stream) {
   static PerDevice smem_attr;
   const cudaError_t e = set_smem_once(smem_attr, attn_mass_kernel<HD, NR>, mass_smem<HD, NR>());
   if (e != cudaSuccess) return e;
+  // the logits' factor in log2 units, and what its f32 rounding lost, relative to it
+  const double scale_log2 = (double)a.scale * 1.4426950408889634;
+  const float c = (float)scale_log2;
+  const float c_rel = scale_log2 != 0.0 ? (float)((scale_log2 - (double)c) / scale_log2) : 0.f;
   return launch_dependent(attn_mass_kernel<HD, NR>, dim3((unsigned)device_sm_count()), dim3(MassGeom<HD, NR>::kThreads),
-                          mass_smem<HD, NR>(), stream, 1u, a, make_fast_div(a.group),
-                          (double)a.scale * 1.4426950408889634);
+                          mass_smem<HD, NR>(), stream, 1u, a, make_fast_div(a.group), c, c_rel);
 }
 
 }  // namespace

@@ -99,4 +99,27 @@ __device__ __forceinline__ int32_t seq_of_row(const CachedSeqs &c, int32_t row) 
   return lo;
 }
 
+// A CTA's (or team's) share of a list of `total` tiles cut into equal runs.
+struct TileShare {
+  int64_t per, first, n;
+};
+
+__device__ __forceinline__ TileShare tile_share(int64_t total, uint32_t sharers, uint32_t at) {
+  TileShare h;
+  h.per = (total >> 31) == 0 ? (int64_t)(((uint32_t)total + sharers - 1u) / sharers) : (total + sharers - 1) / sharers;
+  h.first = h.per * at;
+  h.n = max((int64_t)0, min(h.per, total - h.first));
+  return h;
+}
+
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
 }  // namespace qsa

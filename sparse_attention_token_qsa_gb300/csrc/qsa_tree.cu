@@ -237,52 +237,61 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   }
 
   // ---- the plan: every sequence's tiles summed, then the sequence this CTA's
-  // share starts in (CTA 0 also leaves the sums for the joining launch); one
-  // thread a sequence, in chunks where there are more
-  const bool one_chunk = a.seqs.n_seqs <= kTrThreads;
-  int64_t total = 0;
-  if (!one_chunk) {
-    for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += seq_tiles<G::kT>(a, team_log, read_seq(a.seqs, s)).count;
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) C.scan[warp] = total;
-    __syncthreads();
-    total = 0;
-    for (int i = 0; i < kTrWarps; ++i) total += C.scan[i];
-  }
-  int64_t before = 0, per = 0, w0 = 0, share = 0;
-  const uint32_t teams = gridDim.x >> team_log;
-  for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += kTrThreads) {
-    const int32_t s = s0 + tid;
-    int64_t count = 0;
-    if (s < a.seqs.n_seqs) {
-      const SeqTiles q = seq_tiles<G::kT>(a, team_log, read_seq(a.seqs, s));
-      count = q.count;
-      if (blockIdx.x == 0 && !q.v.ok) report_error(a.status, kErrRowRange, s);
+  // share starts in (CTA 0 also leaves the sums for the joining launch).  Up to 32
+  // sequences, a lane each, every warp for itself; else a thread each, in chunks.
+  int64_t total = 0, found_off = 0;
+  int32_t found_seq = a.seqs.n_seqs;
+  TileShare share = {0, 0, 0};
+  const uint32_t teams = gridDim.x >> team_log, my_team = blockIdx.x >> team_log;
+  auto tiles_of = [&](int32_t s, bool report) -> int64_t {
+    if (s >= a.seqs.n_seqs) return 0;
+    const SeqTiles q = seq_tiles<G::kT>(a, team_log, read_seq(a.seqs, s));
+    if (report && !q.v.ok) report_error(a.status, kErrRowRange, s);
+    return q.count;
+  };
+  if (a.seqs.n_seqs <= 32) {
+    const bool writes = blockIdx.x == 0 && warp == 0;
+    const int64_t count = tiles_of(lane, writes), incl = warp_scan(count, lane), at = incl - count;
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    share = tile_share(total, teams, my_team);
+    if (writes && lane < a.seqs.n_seqs) base_out[lane] = at;
+    const uint32_t hit = __ballot_sync(0xffffffffu, share.n > 0 && count > 0 && at <= share.first && share.first < incl);
+    if (hit != 0) {
+      found_seq = __ffs(hit) - 1;
+      found_off = share.first - __shfl_sync(0xffffffffu, at, found_seq);
     }
-    int64_t incl = count;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+  } else {
+    const bool one_chunk = a.seqs.n_seqs <= kTrThreads;
+    if (!one_chunk) {
+      for (int32_t s = tid; s < a.seqs.n_seqs; s += kTrThreads) total += tiles_of(s, false);
+      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      if (lane == 0) C.scan[warp] = total;
+      __syncthreads();
+      total = 0;
+      for (int i = 0; i < kTrWarps; ++i) total += C.scan[i];
     }
-    __syncthreads();
-    if (lane == 31) C.scan[warp] = incl;
-    __syncthreads();
-    int64_t at = before + incl - count;
+    int64_t before = 0;
+    for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += kTrThreads) {
+      const int32_t s = s0 + tid;
+      const int64_t count = tiles_of(s, blockIdx.x == 0), incl = warp_scan(count, lane);
+      __syncthreads();
+      if (lane == 31) C.scan[warp] = incl;
+      __syncthreads();
+      int64_t at = before + incl - count;
 #pragma unroll
-    for (int i = 0; i < kTrWarps; ++i) {
-      at += i < warp ? C.scan[i] : 0;
-      before += C.scan[i];
+      for (int i = 0; i < kTrWarps; ++i) {
+        at += i < warp ? C.scan[i] : 0;
+        before += C.scan[i];
+      }
+      if (one_chunk) total = before;
+      share = tile_share(total, teams, my_team);
+      if (s < a.seqs.n_seqs && blockIdx.x == 0) base_out[s] = at;
+      if (share.n > 0 && count > 0 && at <= share.first && share.first < at + count) {
+        C.found_seq = s;
+        C.found_off = share.first - at;
+      }
+      if (blockIdx.x != 0 && before > share.first) break;
     }
-    if (one_chunk) total = before;
-    per = (total >> 31) == 0 ? (int64_t)(((uint32_t)total + teams - 1u) / teams) : (total + teams - 1) / teams;
-    w0 = per * (blockIdx.x >> team_log);
-    share = max((int64_t)0, min(per, total - w0));
-    if (s < a.seqs.n_seqs && blockIdx.x == 0) base_out[s] = at;
-    if (share > 0 && count > 0 && at <= w0 && w0 < at + count) {
-      C.found_seq = s;
-      C.found_off = w0 - at;
-    }
-    if (blockIdx.x != 0 && before > w0) break;
   }
   if (blockIdx.x == 0 && tid == 0) base_out[a.seqs.n_seqs] = total;
   tc_fence_before();
@@ -290,7 +299,11 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   tc_fence_after();
   const uint32_t tmem = C.tmem_base;
   const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
-  TreeWalk<G::kT> walk(a, team_log, C.found_seq, C.found_off, laid_out ? share : 0);
+  if (a.seqs.n_seqs > 32) {
+    found_seq = C.found_seq;
+    found_off = C.found_off;
+  }
+  TreeWalk<G::kT> walk(a, team_log, found_seq, found_off, laid_out ? share.n : 0);
   TreeSeg g;
 
   if (warp >= kTrSoft && warp < kTrMmaS) {
@@ -719,7 +732,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, C.found_seq);
+  if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found_seq);
   if (warp == kTrMmaS)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
