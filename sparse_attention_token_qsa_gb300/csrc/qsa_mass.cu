@@ -14,17 +14,17 @@
 // weight 0 are left out of Q.
 //
 // Every CTA (one per SM) takes an equal, contiguous share of the launch's list of
-// (sequence, KV head, tile).  Two groups of four warps sum a tile in turn, or, with
-// up to 256 pairs a turn, four groups, two to a tile, each with half of its pairs
-// (the second leaves its sums to the first through shared memory).  Four more warps
-// copy K, one issues the MMAs, one walks the share and names the rows of each turn.
+// (sequence, KV head, tile), in which beginning a (sequence, KV head) counts as some
+// tiles more.  Fourteen warps: warps 0-3 and 4-7 sum a tile in turn, warps 8-11 copy
+// K, warp 12 issues the MMAs, warp 13 walks the share and names the rows of each turn.
 //
 // With few pairs the kernel is bound by reading K once from HBM: 16 sequences of
 // 16k to 64k tokens, a row of 16 heads over 2 each, take 104 us, 85 % of the copy
-// bandwidth.  With many a tile's sums take longest: 64 rows of the same heads over
-// 65471 tokens take 55 us with four groups, 62 with two; the products alone would
-// take 18 (M128 N256 K16 in 128 cycles), K out of L2 for two turns 14, and a turn
-// begins with 4000 cycles for its Q.  Four groups cost the few-pair case 4 %.
+// bandwidth.  With many: 64 rows of the same heads over 65471 tokens take 42 us.  The
+// products alone would take 18 (M128 N256 K16 in 128 cycles); a turn begins with 4000
+// cycles for its Q (128 KiB at the rate L2 gives an SM), and a tile's sums wait for one another's latency (TMEM load,
+// exponential).  Four groups, two to a tile, took 45 us, and so did the exchange of
+// their sums.
 #include <type_traits>
 
 #include "qsa_launch.h"
@@ -35,7 +35,9 @@ namespace qsa {
 
 namespace {
 
-constexpr int kMsProd = 4;
+constexpr int kMsSum = 8, kMsProd = 4;
+constexpr int kMsMma = kMsSum + kMsProd, kMsPlan = kMsMma + 1;
+constexpr int kMsWarps = kMsPlan + 1, kMsThreads = 32 * kMsWarps;
 constexpr int kMsT = 128;                  // tokens per tile: the MMA's M
 constexpr int kMsQueue = 2;
 constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f;  // log2(e) in two words
@@ -49,11 +51,11 @@ struct MassGeom {
   static constexpr uint32_t kSlot = kB * kMsBox;
   static constexpr uint32_t kQBox = NR * 128;
   static constexpr uint32_t kRingOff = (HD / 64) * kQBox;
-  // Groups that sum a tile, each with its share of the pairs: with many pairs two
-  // groups left the exponentials waiting for one another's latency.
-  static constexpr int kSplit = NR == 256 ? 2 : 1;
-  static constexpr int kSum = 8 * kSplit;                    // warps that sum, then the producers
-  static constexpr int kMma = kSum + kMsProd, kPlan = kMma + 1, kWarps = kPlan + 1, kThreads = 32 * kWarps;
+  // What beginning a (sequence, KV head) costs, in tiles: its turns' pairs and Q, its
+  // masked tile.  3 sequences of 15k to 25k tokens with 33 to 40 rows of 32 heads over 8:
+  // 41 us without, 39.4 at 2, 38.5 at 3 and 4; 6 of 2k to 5k: 35, 32.8, 31.5, 35; 20 of
+  // 500 to 3000 with 1 to 4 rows: 14.3 without, 14.1 at 1, 13.4 at 2.
+  static constexpr int kStart = NR == 256 ? 3 : 2;
   static constexpr int kSlots = HD == 256 ? 5 : (NR == 256 ? 4 : 6);
   static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kSlot;
 };
@@ -74,11 +76,8 @@ struct MassCtrl {
   uint64_t s_full[2], s_free[2];
   uint64_t q_full, cv_full, turn_done, drain;
   uint64_t turn_full[kMsQueue], turn_empty[kMsQueue];
-  // split tiles (256 pairs a turn alone): the second group's sums, a barrier a quarter
-  uint64_t part_full[NR == 256 ? 2 : 1][4];
-  float part[NR == 256 ? 2 : 1][NR == 256 ? kMsT : 1];
   MassTurn turn[kMsQueue];
-  int64_t scan[32], found_off;
+  int64_t scan[kMsWarps], found_off;
   int32_t found_seq, abort;
   int32_t dull[2];  // [turn parity]: the turn (from 1) some pair of which adds nothing
   uint32_t tmem_base;
@@ -94,6 +93,7 @@ struct MassSeq {
   int64_t count;
 };
 
+template <class G>
 __device__ __forceinline__ MassSeq mass_seq(const MassArgs &a, int32_t s) {
   MassSeq q;
   q.v = view_seq(a.seqs, s);
@@ -102,12 +102,12 @@ __device__ __forceinline__ MassSeq mass_seq(const MassArgs &a, int32_t s) {
     q.v.rows = 0;
   }
   q.tiles = q.v.rows > 0 ? (q.v.ctx + q.v.rows + kMsT - 1) / kMsT : 0;
-  q.count = (int64_t)q.tiles * a.nkv;
+  q.count = q.tiles > 0 ? (int64_t)(q.tiles + G::kStart) * a.nkv : 0;
   return q;
 }
 
 template <int HD, int NR>
-__global__ void __launch_bounds__(MassGeom<HD, NR>::kThreads, 1)
+__global__ void __launch_bounds__(kMsThreads, 1)
 attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel) {
   using G = MassGeom<HD, NR>;
   extern __shared__ __align__(1024) uint8_t ms_smem[];
@@ -124,16 +124,15 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
-      mbar_init(sm32(&C.s_free[b]), 4 * G::kSplit);
+      mbar_init(sm32(&C.s_free[b]), kMsSum / 2);
     }
-    for (int b = 0; b < (int)(sizeof(C.part_full) / 8); ++b) mbar_init(sm32(&C.part_full[0][0]) + 8u * b, 1);
     for (int b = 0; b < kMsQueue; ++b) {
       mbar_init(sm32(&C.turn_full[b]), 1);
-      mbar_init(sm32(&C.turn_empty[b]), G::kPlan);  // every warp before the planner
+      mbar_init(sm32(&C.turn_empty[b]), kMsPlan);  // every warp before the planner
     }
-    mbar_init(sm32(&C.q_full), 32 * G::kSum);
-    mbar_init(sm32(&C.cv_full), G::kSum);
-    mbar_init(sm32(&C.turn_done), G::kSum);
+    mbar_init(sm32(&C.q_full), 32 * kMsSum);
+    mbar_init(sm32(&C.cv_full), kMsSum);
+    mbar_init(sm32(&C.turn_done), kMsSum);
     mbar_init(sm32(&C.drain), 1);
     C.abort = 0;
     C.dull[0] = C.dull[1] = 0;
@@ -143,7 +142,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
   }
   __syncthreads();
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
-  if (warp == G::kMma) {
+  if (warp == kMsMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      sm32(&C.tmem_base)),
                  "r"(512u)
@@ -159,7 +158,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
   TileShare part = {0, 0, 0};
   auto tiles_of = [&](int32_t s, bool report) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
-    const MassSeq q = mass_seq(a, s);
+    const MassSeq q = mass_seq<G>(a, s);
     if (report && !q.v.ok) report_error(a.status, kErrRowRange, s);
     return q.count;
   };
@@ -173,17 +172,17 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
       found_off = part.first - __shfl_sync(0xffffffffu, at, found_seq);
     }
   } else {
-    const bool one_chunk = a.seqs.n_seqs <= G::kThreads;
+    const bool one_chunk = a.seqs.n_seqs <= kMsThreads;
     if (!one_chunk) {
-      for (int32_t s = tid; s < a.seqs.n_seqs; s += G::kThreads) total += tiles_of(s, false);
+      for (int32_t s = tid; s < a.seqs.n_seqs; s += kMsThreads) total += tiles_of(s, false);
       for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       if (lane == 0) C.scan[warp] = total;
       __syncthreads();
       total = 0;
-      for (int i = 0; i < G::kWarps; ++i) total += C.scan[i];
+      for (int i = 0; i < kMsWarps; ++i) total += C.scan[i];
     }
     int64_t before = 0;
-    for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += G::kThreads) {
+    for (int32_t s0 = 0; s0 < a.seqs.n_seqs; s0 += kMsThreads) {
       const int32_t s = s0 + tid;
       const int64_t count = tiles_of(s, blockIdx.x == 0), incl = warp_scan(count, lane);
       __syncthreads();
@@ -191,7 +190,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
       __syncthreads();
       int64_t at = before + incl - count;
 #pragma unroll
-      for (int i = 0; i < G::kWarps; ++i) {
+      for (int i = 0; i < kMsWarps; ++i) {
         at += i < warp ? C.scan[i] : 0;
         before += C.scan[i];
       }
@@ -232,7 +231,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
     if (one_thread || lane == 0) mbar_arrive(sm32(&C.turn_empty[(qn - 1) % kMsQueue]));
   };
 
-  if (warp == G::kPlan) {
+  if (warp == kMsPlan) {
     // ---- the share's turns: rows of weight 0 are passed over
     int64_t left = part.n, off = found_off;
     int32_t s = found_seq;
@@ -251,25 +250,28 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
       return ok;
     };
     while (left > 0 && ok) {
-      MassSeq q = mass_seq(a, s);
+      MassSeq q = mass_seq<G>(a, s);
       while (off >= q.count) {
         off -= q.count;
         if (++s >= a.seqs.n_seqs) break;
-        q = mass_seq(a, s);
+        q = mass_seq<G>(a, s);
       }
       if (s >= a.seqs.n_seqs) break;  // (a share ends inside the last sequence)
       MassTurn g;
       g.s = s;
-      g.kvh = (int32_t)(off / q.tiles);
-      g.t0 = (int32_t)(off - (int64_t)g.kvh * q.tiles);
-      g.n = (int32_t)min((int64_t)(q.tiles - g.t0), left);
+      const int32_t length = q.tiles + G::kStart;
+      g.kvh = (off >> 31) == 0 ? (int32_t)((uint32_t)off / (uint32_t)length) : (int32_t)(off / length);
+      const int32_t from = (int32_t)(off - (int64_t)g.kvh * length), run = (int32_t)min((int64_t)(length - from), left);
+      g.t0 = max(0, from - G::kStart);
+      g.n = max(0, from + run - G::kStart) - g.t0;
+      off += run;
+      left -= run;
+      if (g.n == 0) continue;  // a share that ends in a start
       g.row0 = q.v.row0;
       g.rows = q.v.rows;
       g.ctx = q.v.ctx;
       g.first = 1;
       g.h0 = 0;
-      off += g.n;
-      left -= g.n;
       int32_t j = 0, last = 0;  // next row to look at; the row that the turn before cut
       auto weigh = [&](int32_t jj) { return a.weight && jj < g.rows ? a.weight[g.row0 + jj] : 1.f; };
       float ahead = weigh(lane);  // of row j + lane
@@ -316,12 +318,12 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
       g.n = -1;
       push(g);
     }
-  } else if (warp >= G::kSum && warp < G::kMma) {
+  } else if (warp >= kMsSum && warp < kMsMma) {
     // ---- producers: warp p brings tokens 32p .. 32p + 31 of each tile's K, 512
     // bytes (kRows rows of a slot) an instruction; lane i looks up the pool row of
     // its token.
     constexpr int kCh = 8 * G::kB, kRows = 32 / kCh, kN = 32 / kRows;
-    const int p0 = (warp - G::kSum) * 32, ch = lane % kCh, hl = lane / kCh;
+    const int p0 = (warp - kMsSum) * 32, ch = lane % kCh, hl = lane / kCh;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * kMsBox + (uint32_t)(p0 + hl) * 128u;
     uint32_t slot = 0, phase = 1;
     MassTurn g;
@@ -360,7 +362,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
-  } else if (warp == G::kMma) {
+  } else if (warp == kMsMma) {
     // ---- MMA issuer (one thread): S^T of a tile, N = the turn's pairs rounded up to 16
     if (lane == 0) {
       auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -413,14 +415,14 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
     __syncwarp();
   } else {
     // ---- sums: thread = TMEM lane = token r of the tiles its group takes
-    const int w = (warp >> 2) / G::kSplit, half = (warp >> 2) % G::kSplit, r = (warp & 3) * 32 + lane;
+    const int w = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(w * NR);
     const uint64_t c2 = pair_f32(c, c);
     auto wait = [&](uint64_t &bar, uint32_t parity) {
       ok = ok && tc_warp_wait_ready(sm32(&bar), parity, lim, abort_flag);
       return ok;
     };
-    uint32_t jg = 0, turn = 0, seen = 0, taken = 0;
+    uint32_t jg = 0, turn = 0, seen = 0;
     MassTurn g;
     while (take_turn(g, false)) {
       const int32_t *list = C.list[(qn - 1) % kMsQueue];
@@ -432,7 +434,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
         constexpr int kCh = HD / 8, kPer = 32 / kCh;  // 16-byte chunks a row, rows a warp copy
         const int ch = lane % kCh, sub = lane / kCh;
 #pragma unroll 8
-        for (int f = warp * kPer + sub; f < cols16; f += kPer * G::kSum) {
+        for (int f = warp * kPer + sub; f < cols16; f += kPer * kMsSum) {
           const uint32_t to = sQ + (uint32_t)(ch >> 3) * G::kQBox + (uint32_t)f * 128u + (uint32_t)(((ch & 7) ^ (f & 7)) << 4);
           const uint16_t *src = a.q;
           if (f < g.cols) {
@@ -475,19 +477,15 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
       // pairs that add nothing (padding, lse -inf) must not add NaN for a key that is
       // not finite either
       const bool dull = *reinterpret_cast<volatile int32_t *>(&C.dull[(turn - 1) & 1u]) == (int32_t)turn;
-      // this group's pairs
-      const int mid = G::kSplit == 2 ? (cols16 / 2 + 31) & ~31 : cols16;
-      const int c_lo = half ? mid : 0, c_hi = half ? cols16 : min(mid, cols16);
       float *mass = a.mass + ((int64_t)g.s * a.nkv + g.kvh) * a.mass_cols;
       for (int j = 0; j < g.n && ok; ++j) {
         // (a turn without pairs only scales: no tile of it is multiplied)
         const uint32_t at = g.cols > 0 ? jg + (uint32_t)j : (uint32_t)j;
         if ((int)(at & 1u) != w) continue;
-        if (half != 0 && g.cols == 0) continue;
         const int32_t t0 = (g.t0 + j) * kMsT, t = t0 + r;
         const bool in = t < g.ctx + g.rows;
         float old = 0.f;
-        if (in && half == 0 && (g.first ? t < g.ctx && a.carry != 0.f : true)) old = mass[t];
+        if (in && (g.first ? t < g.ctx && a.carry != 0.f : true)) old = mass[t];
         float sum = 0.f;
         if (g.cols > 0) {
           if (!wait(C.s_full[w], (at >> 1) & 1u)) break;
@@ -531,8 +529,8 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
             }
           };
           auto sweep = [&](auto plain) {
-            int c = c_lo;
-            for (; c + 32 <= c_hi; c += 32) {
+            int c = 0;
+            for (; c + 32 <= cols16; c += 32) {
               uint32_t sv[32];
               __syncwarp();
               tmem_ld32(lane_base + (uint32_t)c, sv);
@@ -540,7 +538,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
               add(plain, sv, c);
               add(plain, sv + 16, c + 16);
             }
-            if (c < c_hi) {
+            if (c < cols16) {
               uint32_t sv[16];
               __syncwarp();
               tmem_ld16(lane_base + (uint32_t)c, sv);
@@ -552,26 +550,11 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
           float s0, s1;
           unpair_f32(add2(acc[0], acc[1]), s0, s1);
           sum = s0 + s1;
-          if constexpr (G::kSplit == 2) {
-            // the second group's sums pass to the first (read before S's buffer is freed,
-            // so the next ones find the place empty)
-            uint64_t &bar = C.part_full[w][warp & 3];
-            if (half != 0) {
-              C.part[w][r] = sum;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(sm32(&bar));
-            } else {
-              if (!wait(bar, taken & 1u)) break;
-              __syncwarp();
-              sum += C.part[w][r];
-            }
-            ++taken;
-          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(sm32(&C.s_free[w]));
         }
-        if (in && half == 0) mass[t] = g.first ? fmaf(a.carry, old, sum) : old + sum;
+        if (in) mass[t] = g.first ? fmaf(a.carry, old, sum) : old + sum;
       }
       if (!ok) break;
       if (g.cols > 0) jg += (uint32_t)g.n;
@@ -588,7 +571,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found_seq);
-  if (warp == G::kMma)
+  if (warp == kMsMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -601,7 +584,7 @@ cudaError_t launch_mass(const MassArgs &a, cudaStream_t stream) {
   const double scale_log2 = (double)a.scale * 1.4426950408889634;
   const float c = (float)scale_log2;
   const float c_rel = scale_log2 != 0.0 ? (float)((scale_log2 - (double)c) / scale_log2) : 0.f;
-  return launch_dependent(attn_mass_kernel<HD, NR>, dim3((unsigned)device_sm_count()), dim3(MassGeom<HD, NR>::kThreads),
+  return launch_dependent(attn_mass_kernel<HD, NR>, dim3((unsigned)device_sm_count()), dim3(kMsThreads),
                           mass_smem<HD, NR>(), stream, 1u, a, make_fast_div(a.group), c, c_rel);
 }
 
