@@ -37,8 +37,8 @@
 // maximum.  f32 and bf16 keep their relative precision under any such reference,
 // so it only moves (O and the sums rescaled, the tile's pass taken again) when a
 // logit passes it by 2^16.  The groups tell each other a row's reference through
-// shared memory after each tile; a part's first tile is passed over twice, first
-// for its maximum.
+// shared memory after each tile; of a group's first tile in a part the first
+// columns are passed over beforehand, for a maximum to begin with.
 //
 // Decode (M = group rows of 128) is bound by HBM: 16 sequences of 16k to 64k tokens
 // take 225 us, 95 % of the copy bandwidth.  With more rows the copies out of L2
@@ -539,7 +539,9 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
             for (int i = 0; i < (G::kT + 63) / 64; ++i)
               see[i] = sees64(mrow, a.seqs.mask_words, j_row, g.v.rows, t0 + 64 * i - g.v.ctx);
           }
-          bool probe = j == 0, settled = false;  // probe: for the maximum alone
+          // probe: for a maximum alone, of the first columns that a row sees any of
+          bool probe = j < 2, told = j == 0;  // told: of what the tile before left
+          float t = -INFINITY;
           float part;
           while (true) {
             const float use = top == -INFINITY ? 0.f : top;
@@ -560,7 +562,9 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
 #pragma unroll
               for (int i = 0; i < 16; ++i)
                 mx[i & 1] = max3(mx[i & 1], __uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1]));
-              if (!probe) {
+              if (probe) {
+                if (__all_sync(0xffffffffu, !valid || fmaxf(mx[0], mx[1]) != -INFINITY)) break;
+              } else {
                 uint32_t p[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -581,9 +585,9 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
             float s0, s1;
             unpair_f32(add2(part2[0], part2[1]), s0, s1);
             part = s0 + s1;
-            if (settled) break;
             // what the other group's tile left, and whether this one passes it
-            const float t = j > 0 ? receive() : -INFINITY;
+            if (!told) t = receive();
+            told = true;
             const float mine = fmaxf(mx[0], mx[1]);
             const float want = mine == -INFINITY ? -INFINITY : mine * a.scale_log2;
             const bool move = valid && (want > t + kTrSlack || (t == -INFINITY && want != -INFINITY));
@@ -601,10 +605,11 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                 tmem_st16(lane_base + (uint32_t)(c * 16), o);
               }
+              tmem_wait_st();
             }
             rebase(now);
+            t = now;
             probe = false;
-            settled = true;
           }
           post(top);
           sum += part;
