@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import qsa_inputs as qi
-from cache_cases import Cache, dev, keep_units, ref_mass, ref_tree
+from cache_cases import Cache, dev, f64, keep_units, ref_mass, ref_tree
 from test_gpu_compact import Pool
 from test_gpu_compact import call as compact_call
 from test_gpu_compact import same, want as compact_want
@@ -134,6 +134,24 @@ def test_keys_that_are_not_finite(qsa, hd, bad):
         out, lse, st = tree_call(qsa, c)
         assert st == (0, 0)
         tree_check(c, out, lse)
+
+
+@pytest.mark.parametrize("hd", [128, 256])
+@pytest.mark.parametrize("at", [0, 31, 32, 33, 63, 64, 95, 96, 127, 191, 192, 250])
+def test_a_token_far_above_the_others(qsa, hd, at):
+    """One key some 200 log2 units above the rest, at the edges of columns and tiles, and a
+    second one 30 below it further on."""
+    rng = qi.rng_for(72, salt=hd + at)
+    c = Cache(rng, [260], [3], 8, 2, hd, 16, "tree", q_std=0.25)
+    scale = hd ** -0.5
+    for g in range(2):
+        q = f64(c.q[0]).reshape(8, hd)[4 * g:4 * g + 4].sum(0)
+        for t, units in ((at, 200.0), (min(at + 70, 259), 170.0)):
+            k = q / (q @ q) * 4 * units * np.log(2) / scale
+            c.k[c.slots(0, np.array([t]))[0], g * hd:(g + 1) * hd] = qi.to_bf16_bits(k.astype(np.float32))
+    out, lse, st = tree_call(qsa, c)
+    assert st == (0, 0)
+    tree_check(c, out, lse)
 
 
 def test_refuses_tensors_of_another_device(qsa, monkeypatch):
