@@ -562,7 +562,8 @@ qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
  *  that is no multiple of 4 or a negative key_base with block_keys:
  *  QSA_ERR_ROW_RANGE, the sequence (or its block keys) left alone; an entry
  *  below first + j or past the table (or mass_cols), an entry of the page table
- *  outside the pool, or a broken block: QSA_ERR_TOKEN_RANGE, that entry not moved.
+ *  outside the pool, or a broken block: QSA_ERR_TOKEN_RANGE, that entry not moved
+ *  (of an entry that fails by its page, or by its block, K and V, or the block key).
  */
 qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, int32_t pool_pages,
                              const int32_t *table, int32_t table_len, int64_t table_cols,

@@ -14,8 +14,8 @@
 //
 // The bound is HBM: every moved byte is read and written once.  Whole rows per CTA,
 // a sequence's CTAs a cluster with a cluster barrier per round of chunks, took 274
-// us for what 64-byte slices and no cluster do in 102 (16 caches of 16k-65k tokens
-// cut to 8192).
+// us for what 64-byte slices and no cluster do in 110 (16 caches of 16k-65k tokens
+// cut to 8192; 75 % of the copy bandwidth).
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"

@@ -15,9 +15,9 @@
 // from two counts before it, larger keys and equal ones (of which the first `ties`
 // stay), taken per warp over its own run: no barrier while the list is written.
 //
-// 32 caches of 131k-262k tokens (48 MB of mass) take 22 us, 33 % of the copy
-// bandwidth: 5 us of them read the mass, the rest is the chain of rounds, their
-// barriers and the list.  A cache of 4099 tokens takes 6 us, all of it that chain.
+// 32 caches of 131k-262k tokens (48 MB of mass) take 21 us, 34 % of the copy
+// bandwidth: 5.5 us of them read the mass, the rest is the chain of rounds, their
+// barriers and the list.  A cache of 4099 tokens takes 5 us, all of it that chain.
 #include <cooperative_groups.h>
 
 #include "qsa_launch.h"

@@ -22,9 +22,8 @@
 // 16k to 64k tokens, a row of 16 heads over 2 each, take 104 us, 85 % of the copy
 // bandwidth.  With many: 64 rows of the same heads over 65471 tokens take 42 us.  The
 // products alone would take 18 (M128 N256 K16 in 128 cycles); a turn begins with 4000
-// cycles for its Q (128 KiB at the rate L2 gives an SM), and a tile's sums wait for one another's latency (TMEM load,
-// exponential).  Four groups, two to a tile, took 45 us, and so did the exchange of
-// their sums.
+// cycles for its Q (128 KiB at the rate L2 gives an SM), and a tile's sums wait for
+// one another's latency (TMEM load, exponential).  Four groups, two to a tile, took 45.
 #include <type_traits>
 
 #include "qsa_launch.h"

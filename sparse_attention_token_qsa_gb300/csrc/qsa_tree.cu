@@ -16,12 +16,14 @@
 // any other go to the workspace as (O, max, sum) and a second launch joins them in
 // a fixed order.
 //
-// A unit counts kTrStart tiles more than it has, for its Q, its first tile's two
-// passes and its output: 24 sequences of 300 to 9001 tokens with 5 to 37 rows of 32
-// heads over 8 took 161 us without, 138 at 4 tiles, 135 at 8.  Where sequences have
+// A unit counts kTrStart tiles more than it has, for its Q, its first tile's maximum
+// and its output: 24 sequences of 300 to 9001 tokens with 5 to 37 rows of 32 heads
+// over 8 take 119 us at 4 tiles, 117 at 6, 115 at 8 (before the first maximum was
+// taken of few columns: 161 without, 138 at 4, 135 at 8).  Where sequences have
 // several tiles of rows, a team of two or four CTAs shares a unit of as many: they
-// read the same K and V at the same time, so that these come from HBM once (64
-// rows of 16 heads over 2, 65471 tokens: 97 us one by one, 87 in twos, 84 in fours).
+// read the same K and V at the same time, so that these come from HBM once (64 rows
+// of 16 heads over 2, 65471 tokens: 97 us one by one, 87 in twos, 84 in fours, when the
+// join took 5 us more than now).
 //
 // Fourteen warps: two groups of four (warps 0-3 and 4-7) do the softmax, a row
 // per thread, tiles in turn; warps 8-11 copy K and V rows into a ring of
@@ -41,14 +43,15 @@
 // columns are passed over beforehand, for a maximum to begin with.
 //
 // Decode (M = group rows of 128) is bound by HBM: 16 sequences of 16k to 64k tokens
-// take 225 us, 95 % of the copy bandwidth.  With more rows the copies out of L2
-// bind: every tile of 128 rows reads its K and V, 32 KiB each, at the 33 bytes a
-// cycle and SM that the probe above moved, 2000 cycles a tile, of which the
-// exponentials (16 a cycle) take 512 or 768 and the products 1350 or 800; the 64
-// rows above run at 44 % of the bf16 rate, 128 rows of 32 heads over 8 at 41 %.
-// Two CTAs as a pair (MMAs of 256 rows, half of each tile a CTA) halve the copies,
-// but took 2500 cycles a tile; a third softmax group, a second issuer of S, tiles
-// of 128 tokens with fewer buffers were no faster either.
+// take 225 us, 95 % of the copy bandwidth.  With more rows no unit is busy all the
+// time: the 64 rows above take 78 us, 46 % of the bf16 rate, 4 sequences' 128 rows of 32
+// heads over 8 take 99, 45 %.  A tile's products take 1350 cycles (800 at head_dim
+// 128), its copies 2000 (1500) at the 33 bytes a cycle and SM of the probe above, its
+// exponentials under 800, and a group's chain of barrier tests (over 100 cycles each
+// beside the copies), TMEM loads and stores about 3000 for every other tile.
+// Measured and no faster: two CTAs as a pair (MMAs of 256 rows, half of each tile a
+// CTA), a third softmax group, a second issuer of S, tiles of 128 tokens with fewer
+// buffers, K by TMA boxes of 8 tokens, the next unit's Q ahead.
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"
