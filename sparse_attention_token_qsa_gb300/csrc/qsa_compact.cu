@@ -5,7 +5,7 @@
 // first + j, so a token only moves towards the front.
 //
 // One CTA owns a narrow column slice of a sequence's K and V rows and walks the
-// list from the front in chunks of 32 KiB, up to three of them on their way into
+// list from the front in chunks of 16 or 32 KiB, up to three of them on their way into
 // shared memory (cp.async) at a time.  A later chunk's sources lie at or past its
 // own first destination, and what a chunk's destinations hold is only read by chunks
 // up to it: so a chunk's loads have to be over, in every thread, before it is
@@ -14,8 +14,8 @@
 //
 // The bound is HBM: every moved byte is read and written once.  Whole rows per CTA,
 // a sequence's CTAs a cluster with a cluster barrier per round of chunks, took 274
-// us for what 64-byte slices and no cluster do in 110 (16 caches of 16k-65k tokens
-// cut to 8192; 75 % of the copy bandwidth).
+// us for what 64-byte slices and no cluster do in 101 (16 caches of 16k-65k tokens
+// cut to 8192; 81 % of the copy bandwidth).
 #include "qsa_launch.h"
 #include "qsa_paged.cuh"
 #include "qsa_tc_cache.cuh"
@@ -25,18 +25,18 @@ namespace qsa {
 namespace {
 
 constexpr int kCoThreads = 512;
-constexpr int kCoLoads = 4;  // per thread and chunk
+constexpr int kMoveLoads = 4;  // of what is short, per thread and chunk
 
 // Moves of one sequence's list: element (j, c) goes from src(j) to dst(j).
 template <typename T, int VECS, typename Src, typename Dst>
 __device__ __forceinline__ void move_slice(int32_t n, Src src, Dst dst) {
-  constexpr int kChunk = kCoThreads * kCoLoads / VECS;
+  constexpr int kChunk = kCoThreads * kMoveLoads / VECS;
   const int c = threadIdx.x % VECS, j0 = threadIdx.x / VECS;
   for (int32_t b = 0; b < n; b += kChunk) {
-    T x[kCoLoads];
-    T *to[kCoLoads];
+    T x[kMoveLoads];
+    T *to[kMoveLoads];
 #pragma unroll
-    for (int i = 0; i < kCoLoads; ++i) {
+    for (int i = 0; i < kMoveLoads; ++i) {
       const int32_t j = b + j0 + i * (kCoThreads / VECS);
       const T *from = j < n ? src(j) : nullptr;
       to[i] = from ? dst(j) : nullptr;
@@ -44,15 +44,14 @@ __device__ __forceinline__ void move_slice(int32_t n, Src src, Dst dst) {
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kCoLoads; ++i)
+    for (int i = 0; i < kMoveLoads; ++i)
       if (to[i]) to[i][c] = x[i];
   }
 }
 
 constexpr int kKeyVecs = 4;  // 64 bytes of a block key per CTA
 
-constexpr int kCoDepth = 3;                              // chunks in flight at most
-constexpr uint32_t kCoChunk = kCoThreads * kCoLoads * 16;  // bytes of a chunk
+constexpr int kCoDepth = 3;  // chunks in flight at most
 
 struct CompactGrid {
   int32_t n_seqs, slices;
@@ -61,8 +60,11 @@ struct CompactGrid {
   int32_t depth;                 // chunks in flight
 };
 
+// A chunk is LOADS vectors of 16 bytes a thread.
+template <int LOADS>
 __global__ void __launch_bounds__(kCoThreads)
 compact_kernel(const CompactArgs a, const CompactGrid cfg, const FastDiv lanes) {
+  constexpr uint32_t kCoChunk = kCoThreads * LOADS * 16;
   extern __shared__ __align__(16) uint8_t co_smem[];
   grid_dependency_sync();
   // every sequence's row slices first, then what is short: a CTA of those ahead of
@@ -89,10 +91,10 @@ compact_kernel(const CompactArgs a, const CompactGrid cfg, const FastDiv lanes) 
   if (at < 0) {
     const int32_t vecs = a.width / 8, per = cfg.tokens, depth = cfg.depth, chunks = (n + per - 1) / per;
     // this thread's vectors of a chunk: token, and column in the K or the V row
-    int32_t tok[kCoLoads];
-    uint4 *pool[kCoLoads];
+    int32_t tok[LOADS];
+    uint4 *pool[LOADS];
 #pragma unroll
-    for (int i = 0; i < kCoLoads; ++i) {
+    for (int i = 0; i < LOADS; ++i) {
       const int32_t e = (int32_t)threadIdx.x + i * kCoThreads;
       tok[i] = fast_div(lanes, e);
       const int32_t c = e - tok[i] * lanes.d, v = slice * cfg.sv + (c < cfg.sv ? c : c - cfg.sv);
@@ -159,7 +161,7 @@ compact_kernel(const CompactArgs a, const CompactGrid cfg, const FastDiv lanes) 
       if (p.k < chunks) {
         const int2 *r = rows + p.slot * kCoThreads + p.in_group * per;
 #pragma unroll
-        for (int i = 0; i < kCoLoads; ++i) {
+        for (int i = 0; i < LOADS; ++i) {
           const int32_t from = tok[i] >= 0 ? r[tok[i]].x : -1;
           if (from >= 0)
             cp_async16(sm32(ring + (size_t)p.chunk * kCoChunk + i * kCoThreads * 16), pool[i] + (int64_t)from * vecs, 16u);
@@ -193,7 +195,7 @@ compact_kernel(const CompactArgs a, const CompactGrid cfg, const FastDiv lanes) 
       __syncthreads();
       const int2 *r = rows + out.slot * kCoThreads + out.in_group * per;
 #pragma unroll
-      for (int i = 0; i < kCoLoads; ++i) {
+      for (int i = 0; i < LOADS; ++i) {
         const int32_t to = tok[i] >= 0 ? r[tok[i]].y : -1;
         if (to >= 0)
           pool[i][(int64_t)to * vecs] =
@@ -243,9 +245,22 @@ compact_kernel(const CompactArgs a, const CompactGrid cfg, const FastDiv lanes) 
       [&](int32_t j) { return key((first >> 2) + j); });
 }
 
-size_t compact_smem(int32_t depth, int32_t tokens) {
-  const int32_t group = kCoThreads / tokens;
-  return (size_t)depth * kCoChunk + (size_t)((group - 1 + depth) / group + 2) * kCoThreads * sizeof(int2);
+template <int LOADS>
+cudaError_t launch_compact(const CompactArgs &a, CompactGrid g, int64_t grid, cudaStream_t stream) {
+  g.tokens = kCoThreads * LOADS / (2 * g.sv);
+  if (g.tokens > kCoThreads) g.tokens = kCoThreads;  // a look-up per thread
+  const int32_t chunks = (a.max_keep + g.tokens - 1) / g.tokens;
+  g.depth = chunks < kCoDepth ? chunks : kCoDepth;  // short lists leave shared memory to more CTAs
+  auto smem = [](int32_t depth, int32_t tokens) {
+    const int32_t group = kCoThreads / tokens;
+    return (size_t)depth * kCoThreads * LOADS * 16 +
+           (size_t)((group - 1 + depth) / group + 2) * kCoThreads * sizeof(int2);
+  };
+  static PerDevice smem_attr;
+  const cudaError_t e = set_smem_once(smem_attr, compact_kernel<LOADS>, smem(kCoDepth, kCoThreads));
+  if (e != cudaSuccess) return e;
+  return launch_dependent(compact_kernel<LOADS>, dim3((unsigned)grid), dim3(kCoThreads), smem(g.depth, g.tokens), stream, 1u,
+                          a, g, make_fast_div(2 * g.sv));
 }
 
 }  // namespace
@@ -256,22 +271,17 @@ cudaError_t launch_cache_compact(const CompactArgs &a, int32_t n_seqs, cudaStrea
   const int64_t least = (vecs + 63) / 64, finest = vecs < 4 ? 1 : vecs / 4;
   int64_t slices = 2 * device_sm_count() / n_seqs;
   slices = slices > finest ? finest : slices < least ? least : slices;
-  CompactGrid g;
+  CompactGrid g = {};
   g.n_seqs = n_seqs;
   g.sv = (int32_t)((vecs + slices - 1) / slices);
   g.slices = (vecs + g.sv - 1) / g.sv;
-  g.tokens = kCoThreads * kCoLoads / (2 * g.sv);
-  if (g.tokens > kCoThreads) g.tokens = kCoThreads;  // a look-up per thread
-  const int32_t chunks = (a.max_keep + g.tokens - 1) / g.tokens;
-  g.depth = chunks < kCoDepth ? chunks : kCoDepth;  // short lists leave shared memory to more CTAs
-  static PerDevice smem_attr;
-  const cudaError_t e = set_smem_once(smem_attr, compact_kernel, compact_smem(kCoDepth, kCoThreads));
-  if (e != cudaSuccess) return e;
   const int32_t more = a.nkv + (a.block_keys ? kHeadDim / 8 / kKeyVecs : 0);
   const int64_t grid = (int64_t)n_seqs * (g.slices + more);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_dependent(compact_kernel, dim3((unsigned)grid), dim3(kCoThreads), compact_smem(g.depth, g.tokens), stream,
-                          1u, a, g, make_fast_div(2 * g.sv));
+  // Chunks of 32 KiB where a CTA has an SM to itself (4 caches cut to 8192: 51 us, 57 with
+  // 16 KiB), else of 16 (16 caches: 101 us, 110 with 32 KiB and 137 with 8).
+  return (int64_t)n_seqs * g.slices <= device_sm_count() ? launch_compact<4>(a, g, grid, stream)
+                                                         : launch_compact<2>(a, g, grid, stream);
 }
 
 }  // namespace qsa
