@@ -12,7 +12,8 @@ import qsa_inputs as qi
 from cache_cases import Cache, dev, f64, keep_units, ref_mass, ref_tree
 from test_gpu_compact import Pool
 from test_gpu_compact import call as compact_call
-from test_gpu_compact import same, want as compact_want
+from test_gpu_compact import same, whole_blocks
+from test_gpu_compact import want as compact_want
 from test_gpu_evict import call as evict_call
 from test_gpu_mass import call as mass_call
 from test_gpu_mass import check as mass_check
@@ -271,3 +272,14 @@ def test_lists_for_many_sequences(qsa):
         for i in range(1000):
             want = keep_units(mass[i], int(length[i]), keep, first, last, unit)
             assert n_sel[i] == len(want) and np.array_equal(sel[i, :len(want)], want)
+
+
+@pytest.mark.parametrize("n,tokens,page,width,nkv", [(40, 300, 16, 512, 2), (160, 90, 7, 136, 1), (12, 900, 64, 1024, 8)])
+def test_moves_of_many_sequences(qsa, n, tokens, page, width, nkv):
+    """More slices than SMs, with block keys; lists of every length from nothing on."""
+    rng = qi.rng_for(73, salt=n)
+    p = Pool(rng, n, tokens, page, width, nkv, True)
+    lists = [whole_blocks(rng, tokens, int(rng.integers(0, tokens // 4 + 1)) if i else 0, 0) for i in range(n)]
+    got = compact_call(qsa, p, lists, None)
+    assert got[4] == (0, 0)
+    same(got[:4], compact_want(p, lists, None))
