@@ -89,7 +89,8 @@ __device__ __forceinline__ bool sees_draft(const uint32_t *mrow, int32_t j, int3
   return mrow == nullptr ? k <= j : (mrow[k >> 5] >> (k & 31)) & 1u;
 }
 
-// The sequence whose rows hold `row`: the last s with row_start[s] <= row.
+// The sequence whose rows hold `row` where the starts ascend: the last s with
+// row_start[s] <= row.
 __device__ __forceinline__ int32_t seq_of_row(const CachedSeqs &c, int32_t row) {
   int32_t lo = 0, hi = c.n_seqs;
   while (hi - lo > 1) {

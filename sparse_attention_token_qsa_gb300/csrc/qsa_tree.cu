@@ -100,7 +100,7 @@ struct TreeCtrl {
   uint64_t pv_done[4];            // tile % 4
   uint64_t q_full, o_free, drain[2];
   int64_t scan[kTrWarps], found_off;
-  int32_t found_seq, bad[2], abort;
+  int32_t found_seq, bad[2], abort, broken;
   uint32_t tmem_base;
 };
 template <int HD>
@@ -224,7 +224,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
     for (int b = 0; b < 4; ++b) mbar_init(sm32(&C.pv_done[b]), 1);
     mbar_init(sm32(&C.q_full), 32 * kTrSoft);
     mbar_init(sm32(&C.o_free), kTrSoft);
-    C.abort = 0;
+    C.abort = C.broken = 0;
     C.found_seq = a.seqs.n_seqs;
     C.found_off = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -240,8 +240,9 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   }
 
   // ---- the plan: every sequence's tiles summed, then the sequence this CTA's
-  // share starts in (CTA 0 also leaves the sums for the joining launch).  Up to 32
-  // sequences, a lane each, every warp for itself; else a thread each, in chunks.
+  // share starts in (CTA 0 also leaves the sums for the joining launch, and whether some
+  // sequence is left out).  Up to 32 sequences, a lane each, every warp for itself; else a
+  // thread each, in chunks.
   int64_t total = 0, found_off = 0;
   int32_t found_seq = a.seqs.n_seqs;
   TileShare share = {0, 0, 0};
@@ -249,7 +250,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   auto tiles_of = [&](int32_t s, bool report) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
     const SeqTiles q = seq_tiles<G::kT>(a, team_log, read_seq(a.seqs, s));
-    if (report && !q.v.ok) report_error(a.status, kErrRowRange, s);
+    if (report && !q.v.ok) {
+      report_error(a.status, kErrRowRange, s);
+      *reinterpret_cast<volatile int32_t *>(&C.broken) = 1;
+    }
     return q.count;
   };
   if (a.seqs.n_seqs <= 32) {
@@ -296,10 +300,13 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
       if (blockIdx.x != 0 && before > share.first) break;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) base_out[a.seqs.n_seqs] = total;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (blockIdx.x == 0 && tid == 0) {
+    base_out[a.seqs.n_seqs] = total;
+    base_out[a.seqs.n_seqs + 1] = C.broken;
+  }
   const uint32_t tmem = C.tmem_base;
   const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
   if (a.seqs.n_seqs > 32) {
@@ -768,19 +775,23 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   // of what this reads, and it began after everything before it was complete.
   int32_t s = 0, r = 0, rank = 0, tiles = 0;
   int64_t u0 = 0;  // the unit's first tile, from its sequence's first
-  if (row >= 0) {
-    s = seq_of_row(a.seqs, row);
-    const SeqTiles q = seq_tiles<TreeGeom<HD>::kT>(a, team_log, read_seq(a.seqs, s));
-    if (row >= q.v.row0 && row < q.v.row0 + q.v.rows) {
-      const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
-      const int32_t mt = (int32_t)(m >> kTrRowsLog);
-      r = (int32_t)(m & (kTrRows - 1));
-      rank = mt & ((1 << team_log) - 1);
-      tiles = q.tiles;
-      u0 = ((int64_t)kvh * q.m_tiles + (mt >> team_log)) * (tiles + kTrStart) + kTrStart;
-    }
-  }
+  auto place = [&](int32_t at) {  // whether the row is one of sequence `at`
+    const SeqTiles q = seq_tiles<TreeGeom<HD>::kT>(a, team_log, read_seq(a.seqs, at));
+    if (row < q.v.row0 || row >= q.v.row0 + q.v.rows) return;
+    const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
+    const int32_t mt = (int32_t)(m >> kTrRowsLog);
+    s = at;
+    r = (int32_t)(m & (kTrRows - 1));
+    rank = mt & ((1 << team_log) - 1);
+    tiles = q.tiles;
+    u0 = ((int64_t)kvh * q.m_tiles + (mt >> team_log)) * (tiles + kTrStart) + kTrStart;
+  };
+  if (row >= 0) place(seq_of_row(a.seqs, row));
   grid_dependency_sync();
+  // Where a sequence was left out, the starts may not ascend, and the search above may
+  // have missed a good one: every sequence is looked at.
+  if (row >= 0 && tiles == 0 && base[a.seqs.n_seqs + 1] != 0)
+    for (int32_t i = 0; i < a.seqs.n_seqs && tiles == 0; ++i) place(i);
   int32_t c0 = 0, c1 = 0;  // teams of the first and last part
   if (tiles > 0) {
     const int64_t per = (base[a.seqs.n_seqs] + teams - 1) / teams;
@@ -861,11 +872,12 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
     a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
 }
 
-// The workspace: the sequences' first tiles, then the parts' (max, sum) and O.
+// The workspace: the sequences' first tiles, their sum, whether one was left out; then the
+// parts' (max, sum) and O.
 int32_t part_rows_of(int64_t n_rows, int32_t group) {
   return (int32_t)(n_rows * group < kTrRows ? n_rows * group : kTrRows);
 }
-int64_t base_bytes(int32_t n_seqs) { return ((int64_t)(n_seqs + 1) * 8 + 255) / 256 * 256; }
+int64_t base_bytes(int32_t n_seqs) { return ((int64_t)(n_seqs + 2) * 8 + 255) / 256 * 256; }
 int64_t ml_bytes(int32_t part_rows) { return ((int64_t)kTrMaxCtas * 2 * part_rows * 8 + 255) / 256 * 256; }
 
 template <int HD>
