@@ -483,7 +483,8 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
       tc_warp_wait_ready(sm32(&C.pv_done[i & 3u]), (i >> 2) & 1u, lim, abort_flag);
     };
     // This warp's rows of a part's Q into shared memory.  The copies arrive on
-    // q_full by themselves; a sign or a zero scale has to pass through registers.
+    // q_full by themselves; a sign or a zero scale has to pass through registers, and the
+    // arrival of a thread's copies would not wait for its stores: it arrives behind them.
     auto load_q = [&](const TreeSeg &e) {
       const int64_t m0 = (int64_t)e.mt * kTrRows;
       const int rows = (int)min((int64_t)kTrRows, (int64_t)e.v.rows * a.group - m0);
@@ -508,7 +509,8 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
           *reinterpret_cast<uint4 *>(tr_smem + to) = v;
         }
       }
-      cp_async_arrive(sm32(&C.q_full));
+      if (plain) cp_async_arrive(sm32(&C.q_full));
+      else mbar_arrive(sm32(&C.q_full));
     };
     uint32_t jg = 0, ns = 0;
     int32_t seg = 0;
