@@ -501,7 +501,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
         if (plain) {
           cp_async16(sQ + to, src, 16u);
         } else {
-          uint4 v = ldg_nc_v4(src);
+          uint4 v = *reinterpret_cast<const uint4 *>(src);
           v.x = (v.x & q_and) ^ q_xor;
           v.y = (v.y & q_and) ^ q_xor;
           v.z = (v.z & q_and) ^ q_xor;
@@ -758,13 +758,15 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
 // times kQuads quads of dims (a part's rows lie side by side) and every
 // kGroups-th part, two at a time with the running maximum: one trip to L2 for both
 // the maxima and the values.  The groups' results are then added in order.
+// The plan and the parts are written while this launch is already resident, so they
+// are no __restrict__ arguments: nothing may read them ahead of the wait, or as if no
+// one wrote them.
 constexpr int kJoinWarps = 8;
 
 template <int HD, int kGroups, int kQuads>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_t part_rows, int32_t teams,
-                 const int64_t *__restrict__ base, const float2 *__restrict__ part_ml,
-                 const float4 *__restrict__ part_o) {
+                 const int64_t *base, const float2 *part_ml, const float4 *part_o) {
   __shared__ float4 acc_s[kGroups > 1 ? kJoinWarps : 1][kQuads][32];
   __shared__ float2 ml_s[kGroups > 1 ? kJoinWarps : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
