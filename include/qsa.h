@@ -91,9 +91,11 @@ const char *qsa_status_string(int32_t status);
  * The limit of the bounded device waits a caller may shorten, in SM clock
  * cycles (default 4e9, about 2 s at 2 GHz): the streaming scorers' waits for
  * the block keys they copy into shared memory and for their MMAs
- * (qsa_score_rows on the SIMT and QSA_SCORE_STREAM paths), and the fused
+ * (qsa_score_rows on the SIMT and QSA_SCORE_STREAM paths), the fused
  * decode step's waits for its key copies, its MMAs and its barrier over a
- * row's CTAs (qsa_decode_index_select).  A wait
+ * row's CTAs (qsa_decode_index_select), and the waits of tree attention and
+ * attention mass for their copies, their MMAs and the buffers that these pass
+ * on (qsa_tree_attn, qsa_attn_mass: what they then leave is said there).  A wait
  * that reaches the limit records QSA_ERR_TIMEOUT with its row in dev_status
  * and the row's output is left unspecified (a fused decode call may then
  * leave its workspace dirty: zero it before the next call); the CTA first
@@ -464,7 +466,9 @@ qsa_status qsa_qk_proj(const uint16_t *x, int64_t x_stride, const uint16_t *w, i
  *  n_rows, the table or the mask is QSA_ERR_ROW_RANGE (with the sequence's
  *  index) and its rows are left alone; a table entry outside the pool is
  *  QSA_ERR_TOKEN_RANGE (the sequence's index) and its sequence's output is
- *  unspecified.  Refused: pool_pages * page_size * nkv or table_len * page_size
+ *  unspecified; a wait that gives up is QSA_ERR_TIMEOUT, with the index of the
+ *  first sequence that the CTA had a part of, and leaves out and lse of every
+ *  sequence of the call unspecified.  Refused: pool_pages * page_size * nkv or table_len * page_size
  *  past 31 bits, n_seqs > 65535, a small or unaligned workspace.
  */
 qsa_status qsa_tree_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
@@ -499,7 +503,10 @@ int64_t qsa_tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int
  *  The sums run in f32 in an order that the arguments alone decide.
  *  Device errors as in qsa_tree_attn; more cached tokens than mass_cols is
  *  QSA_ERR_ROW_RANGE.  A sequence that reports QSA_ERR_TOKEN_RANGE has
- *  unspecified mass.
+ *  unspecified mass.  So has every sequence with rows after QSA_ERR_TIMEOUT:
+ *  the sums are added in place, and some tokens then have theirs and others
+ *  not.  Such a mass cannot be taken on with; it has to be put back from a copy,
+ *  or started again.
  */
 qsa_status qsa_attn_mass(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
                          int32_t head_dim, const uint16_t *k_pool, int32_t pool_pages,

@@ -176,7 +176,7 @@ def qsa_version() -> int:
 def qsa_set_wait_limit_cycles(cycles: int) -> None:
     """The limit, in SM clock cycles, of the waits a caller may shorten (the
     streaming scorers' key-copy, operand and accumulator waits, the fused decode
-    step's waits and barrier)."""
+    step's waits and barrier, the waits of tree attention and attention mass)."""
     _check(_lib.qsa_set_wait_limit_cycles(int(cycles)), "qsa_set_wait_limit_cycles")
 
 

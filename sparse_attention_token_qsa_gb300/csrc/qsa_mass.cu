@@ -214,7 +214,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
 
   // The next turn of the share (a whole warp, or the issuer's one thread).
   uint32_t qn = 0;
-  bool ok = laid_out;
+  bool ok = laid_out && part.n > 0;  // (a CTA without a share has nothing to wait for)
   auto take_turn = [&](MassTurn &g, bool one_thread) -> bool {
     const uint32_t e = qn % kMsQueue, par = (qn / kMsQueue) & 1u;
     ok = ok && (one_thread ? tc_wait_ready(sm32(&C.turn_full[e]), par, lim, abort_flag)
@@ -569,7 +569,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found_seq);
+  if (tid == 0 && part.n > 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found_seq);
   if (warp == kMsMma)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }

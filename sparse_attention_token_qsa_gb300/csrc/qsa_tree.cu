@@ -749,7 +749,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found_seq);
+  if (tid == 0 && share.n > 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found_seq);
   if (warp == kTrMmaS)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }

@@ -1,9 +1,10 @@
-"""What a bad sequence leaves of the others."""
+"""What a bad sequence, or a wait that runs out, leaves of the others and of the status word."""
 import numpy as np
 import pytest
+import torch
 
 import qsa_inputs as qi
-from cache_cases import Cache
+from cache_cases import Cache, dev
 from test_gpu_mass import call as mass_call
 from test_gpu_tree import call as tree_call
 
@@ -41,3 +42,31 @@ def test_starts_that_do_not_ascend_leave_the_good_sequences(qsa, n, hd):
     _, mass, st = mass_call(qsa, c, lse, old=old)
     assert st[0] == 3 and st[1] in (mid - 1, mid)
     assert np.array_equal(mass, wmass)
+
+
+@pytest.mark.parametrize("hd", [128, 256])
+@pytest.mark.parametrize("rows", [1, 60])
+def test_a_timeout_names_a_sequence_of_the_call(qsa, hd, rows):
+    """Most CTAs have no share of two short sequences: they have nothing to wait for, and
+    those that do name a sequence with rows."""
+    default = qsa.qsa_wait_limit_cycles()
+    c = Cache(qi.rng_for(81, salt=hd + rows), [7, 300, 9, 40], [0, rows, 0, 2], 8, 2, hd, 16, "tree")
+    lse = dev(np.zeros((c.n_rows, c.nq), np.float32))
+    args = c.mass_args(dev(c.q), c.nq * hd)
+    targs = c.tree_args(dev(c.q), c.nq * hd)
+    out = torch.zeros((c.n_rows, c.nq * hd), dtype=torch.int16, device="cuda")
+    ws = qsa.new_tree_workspace(c.n, c.n_rows, c.nq, c.nkv, hd)
+    mass = torch.zeros((c.n, c.nkv, 400), dtype=torch.float32, device="cuda")
+    try:
+        qsa.qsa_set_wait_limit_cycles(1)
+        for _ in range(10):
+            st = qsa.new_status()
+            qsa.qsa_attn_mass(*args, hd ** -0.5, lse, None, 1.0, mass, 400, st)
+            st = qsa.qsa_read_status(st)
+            assert st[0] == 5 and st[1] in (1, 3)
+            st = qsa.new_status()
+            qsa.qsa_tree_attn(*targs, hd ** -0.5, out, c.nq * hd, None, st, ws)
+            st = qsa.qsa_read_status(st)
+            assert st[0] == 5 and st[1] in (1, 3)
+    finally:
+        qsa.qsa_set_wait_limit_cycles(default)
