@@ -346,6 +346,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
         for (int c = 0; c < G::kC; ++c) {
           ok = ok && tc_warp_wait_ready(sm32(&C.empty[slot]), phase, lim, abort_flag);
           if (!ok) break;
+          __syncwarp();
           const uint16_t *src = a.k_pool + c * (64 * G::kB) + ch * 8;
 #pragma unroll
           for (int k = 0; k < kN; ++k)  // row p0 + kRows k + hl, its 16-byte chunks swizzled by row % 8
@@ -427,6 +428,7 @@ attn_mass_kernel(const MassArgs a, const FastDiv group_div, float c, float c_rel
       const int32_t *list = C.list[(qn - 1) % kMsQueue];
       // ---- the turn's Q and what belongs to its pairs, once the turn before is over
       if (seen > 0 && !wait(C.turn_done, (seen - 1) & 1u)) break;
+      __syncwarp();
       ++seen;
       const int cols16 = (g.cols + 15) & ~15;
       if (g.cols > 0) {

@@ -30,7 +30,9 @@ __device__ __forceinline__ bool mbar_test(uint32_t mb, uint32_t parity) {
   return ok != 0;
 }
 
-// tc_wait and tc_warp_wait with the completed phase's case in line.
+// tc_wait and tc_warp_wait with the completed phase's case in line.  Where lane 0 waits
+// for its warp, the shuffle that tells the others orders no memory: a __syncwarp has to
+// follow where they then touch shared or global memory.
 __device__ __forceinline__ bool tc_wait_ready(uint32_t mb, uint32_t parity, long long limit,
                                               volatile int32_t *abort_flag) {
   return mbar_test(mb, parity) || tc_wait(mb, parity, limit, abort_flag);

@@ -348,6 +348,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
           ok = false;
           return;
         }
+        __syncwarp();
         const uint16_t *src = pool + ch * 8;
 #pragma unroll
         for (int k = 0; k < kN; ++k)  // row p0 + kRows k + hl, its 16-byte chunks swizzled by row % 8
@@ -670,6 +671,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
       const uint32_t last = jg - 1;  // the part's last tile
       if (g.n > 0) {  // its S is done, and with it every one of this part: Q may go
         tc_warp_wait_ready(sm32(&C.s_full[last % 3u]), (last / 3u) & 1u, lim, abort_flag);
+        __syncwarp();
         if (live && (int)(last & 1u) != w) rebase(receive());
       }
       more = more_next;
