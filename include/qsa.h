@@ -480,7 +480,9 @@ qsa_status qsa_tree_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_
                          int64_t out_stride, float *lse, int32_t *dev_status, void *workspace,
                          int64_t workspace_bytes, void *stream);
 
-/* Bytes of the workspace qsa_tree_attn needs; -1 for arguments it refuses. */
+/* Bytes of the workspace qsa_tree_attn needs; -1 for arguments it refuses.  They
+ * grow with n_seqs, n_rows, nq / nkv and head_dim: one made for the largest of each
+ * serves every call below them (fewer KV heads for the same nq need more). */
 int64_t qsa_tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int32_t nkv,
                                  int32_t head_dim);
 

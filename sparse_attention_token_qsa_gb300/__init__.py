@@ -363,9 +363,13 @@ def qsa_tree_workspace_bytes(n_seqs: int, n_rows: int, nq: int, nkv: int, head_d
 
 def new_tree_workspace(n_seqs: int, n_rows: int, nq: int, nkv: int, head_dim: int,
                        device="cuda") -> torch.Tensor:
-    """A workspace for qsa_tree_attn calls of at most these sizes."""
-    n = max(16, qsa_tree_workspace_bytes(n_seqs, n_rows, nq, nkv, head_dim))
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    """A workspace for qsa_tree_attn calls of at most these n_seqs, n_rows and head_dim, and
+    of at most nq / nkv query heads a KV head."""
+    n = qsa_tree_workspace_bytes(n_seqs, n_rows, nq, nkv, head_dim)
+    if n < 0:
+        raise ValueError(f"no tree workspace for n_seqs={n_seqs}, n_rows={n_rows}, nq={nq}, nkv={nkv}, "
+                         f"head_dim={head_dim}")
+    return torch.empty(max(16, n), dtype=torch.uint8, device=device)
 
 
 def qsa_tree_attn(q, q_stride, nq, nkv, head_dim, k_pool, v_pool, pool_pages, page_size, table,
