@@ -468,8 +468,8 @@ qsa_status qsa_qk_proj(const uint16_t *x, int64_t x_stride, const uint16_t *w, i
  *  QSA_ERR_TOKEN_RANGE (the sequence's index) and its sequence's output is
  *  unspecified; a wait that gives up is QSA_ERR_TIMEOUT, with the index of the
  *  first sequence that the CTA had a part of, and leaves out and lse of every
- *  sequence of the call unspecified.  Refused: pool_pages * page_size * nkv or table_len * page_size
- *  past 31 bits, n_seqs > 65535, a small or unaligned workspace.
+ *  sequence of the call unspecified.  Refused: pool_pages * page_size * nkv, table_len * page_size or
+ *  n_rows * nq past 31 bits, n_seqs or nkv > 65535, a small or unaligned workspace.
  */
 qsa_status qsa_tree_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
                          int32_t head_dim, const uint16_t *k_pool, const uint16_t *v_pool,
@@ -496,7 +496,7 @@ int64_t qsa_tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int
  *  q ... scale  as in qsa_tree_attn (the same rows, cache and masks).
  *  lse      DEVICE f32 [n_rows, nq], as qsa_tree_attn wrote it; a head with lse
  *           -inf adds nothing.
- *  row_weight  DEVICE f32 [n_rows] or NULL (= 1): a row of weight 0 (a
+ *  row_weight  DEVICE f32 [n_rows], finite, or NULL (= 1): a row of weight 0 (a
  *           rejected draft) adds nothing, whatever its logits are.
  *  carry    finite, >= 0: the share of the mass that stays; 0 does not read it.
  *  mass     DEVICE f32 [n_seqs, nkv, mass_cols], 16-byte aligned, mass_cols a
@@ -540,6 +540,7 @@ qsa_status qsa_attn_mass(const uint16_t *q, int64_t q_stride, int32_t nq, int32_
  *  Device errors: a length outside [0, tokens] is QSA_ERR_ROW_RANGE, a
  *  non-finite unit mass of a sequence that is cut QSA_ERR_NONFINITE (both with
  *  the sequence's index); its row of sel and its n_sel are left alone.
+ *  Refused: n_seqs > 2^20, nkv > 65535, tokens > 2^31 - 65537.
  */
 qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
                             const int32_t *length, int32_t n_seqs, int32_t tokens, int32_t keep,
@@ -573,6 +574,7 @@ qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
  *  below first + j or past the table (or mass_cols), an entry of the page table
  *  outside the pool, or a broken block: QSA_ERR_TOKEN_RANGE, that entry not moved
  *  (of an entry that fails by its page, or by its block, K and V, or the block key).
+ *  Refused: n_seqs or nkv > 65535, width > 2^24, table_len * page_size past 31 bits.
  */
 qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, int32_t pool_pages,
                              const int32_t *table, int32_t table_len, int64_t table_cols,

@@ -448,7 +448,7 @@ qsa_status check_cached(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t
   if (tree_mask != nullptr && mask_words == 0) return QSA_ERR_INVALID_VALUE;
   if (!q || !k_pool || !table || !ctx_len || !row_start || !dev_status) return QSA_ERR_INVALID_VALUE;
   if (!aligned16(q) || !aligned16(k_pool)) return QSA_ERR_INVALID_VALUE;
-  // a pool row is one KV head of one token; TMA numbers them with 32 bits
+  // a pool row is one KV head of one token; the kernels' copies number them with 32 bits
   if ((int64_t)pool_pages * page_size > INT32_MAX / nkv ||
       (int64_t)table_len * page_size > INT32_MAX - 256 || (int64_t)n_rows * nq > INT32_MAX ||
       (int64_t)n_rows * q_stride > kMostElems || n_seqs > 65535 || nkv > 65535 ||
