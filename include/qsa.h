@@ -493,6 +493,9 @@ int64_t qsa_tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int
  *                 + sum_j row_weight[j] * sum_{h in group g} exp(scale q_jh . k_tg - lse[j, h])
  * over the rows j of sequence s that attend token t.  Drafted tokens start at
  * zero, so a cache that grows needs no clearing.  What qsa_evict_select reads.
+ * It is the weight of attention over every cached token.  For rows that attended a
+ * selected list (qsa_sparse_attn returns no lse) it takes a qsa_tree_attn call for
+ * lse, and is then the weight that dense attention would have given.
  *  q ... scale  as in qsa_tree_attn (the same rows, cache and masks).
  *  lse      DEVICE f32 [n_rows, nq], as qsa_tree_attn wrote it; a head with lse
  *           -inf adds nothing.
@@ -568,6 +571,18 @@ qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
  *           4b+2, 4b+3) and first a multiple of 4.
  *  key_base  DEVICE int64 [n_seqs], or NULL (= 0) for one sequence.
  *  What lies past the moved tokens is left as it is.
+ *  Afterwards token t of a sequence is the cache's t-th, no longer the sequence's.
+ *  Let D be the tokens dropped so far (true length - cached length; a multiple of
+ *  4 where unit 4 and moves of whole blocks dropped them).  qsa_tree_attn,
+ *  qsa_attn_mass, qsa_evict_select, qsa_mask_tokens, qsa_gather_kv and
+ *  qsa_sparse_attn take cached tokens and lengths (q and K carry their true
+ *  rotation already).  Of the calls that rotate:
+ *   - qsa_score_rows: pos the true position, visible_len the cached length;
+ *     qsa_select_mask: pos the cached position (visible_len - 1).
+ *   - qsa_pool_blocks, qsa_index_select, qsa_decode_index_select: cached blocks
+ *     and positions, with cos_t and sin_t D rows on and table_rows D less (one
+ *     sequence a call, or several with the same D).
+ *  Block keys cannot follow moves that break blocks (unit 1).
  *  Device errors: n_keep or first out of range (also past mass_cols), a first
  *  that is no multiple of 4 or a negative key_base with block_keys:
  *  QSA_ERR_ROW_RANGE, the sequence (or its block keys) left alone; an entry
