@@ -128,7 +128,10 @@ def _dev(t: torch.Tensor | None, name: str):
 
 def _home(t, name: str) -> int:
     """The device a cache operator works on: that of its first tensor, which has to be
-    the current one (the launch goes there, and the others' memory is not mapped)."""
+    the current one (the launch goes there, and the others' memory is not mapped).  None,
+    which the library takes for nothing to do and refuses otherwise: the current one."""
+    if t is None:
+        return torch.cuda.current_device()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     d = t.get_device()

@@ -70,3 +70,21 @@ def test_a_timeout_names_a_sequence_of_the_call(qsa, hd, rows):
             assert st[0] == 5 and st[1] in (1, 3)
     finally:
         qsa.qsa_set_wait_limit_cycles(default)
+
+
+def test_calls_with_nothing_to_do_take_no_tensors(qsa):
+    """As in the library's other calls: no sequences or rows and no tensors is no error, and
+    the same call with rows is refused."""
+    def calls(n):
+        yield lambda: qsa.qsa_tree_attn(None, 0, 8, 2, 128, None, None, 0, 16, None, 0, 0, None, None, n, n, None, 0, 1.0, None,
+                                        0, None, None, None)
+        yield lambda: qsa.qsa_attn_mass(None, 0, 8, 2, 128, None, 0, 16, None, 0, 0, None, None, n, n, None, 0, 1.0, None, None,
+                                        1.0, None, 0, None)
+        yield lambda: qsa.qsa_evict_select(None, 0, 2, None, n, 0, 4, 0, 0, 4, None, 0, None, None)
+        yield lambda: qsa.qsa_cache_compact(None, None, 512, 0, None, 0, 0, 16, None, 0, None, n, n, None, None, 0, 0, None,
+                                            None, None)
+    for f in calls(0):
+        f()
+    for f in calls(1):
+        with pytest.raises(qsa.QsaError):
+            f()
