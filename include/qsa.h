@@ -459,6 +459,8 @@ qsa_status qsa_qk_proj(const uint16_t *x, int64_t x_stride, const uint16_t *w, i
  *  what the cache holds past a sequence's tokens.
  *  Logits, softmax and sums run in f32; the weights are rounded to bf16 for the
  *  weighted sum of V alone (the normaliser and lse use them unrounded).
+ *  The work is shared out for sequences of like width, here and in qsa_attn_mass: a
+ *  wide chunk of a prompt costs less in a call of its own than beside single rows.
  *  workspace  DEVICE scratch of at least qsa_tree_workspace_bytes(...) bytes,
  *           16-byte aligned; its contents on entry do not matter.  Calls that
  *           share one must be stream-ordered.

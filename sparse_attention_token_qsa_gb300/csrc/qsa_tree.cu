@@ -17,13 +17,17 @@
 // a fixed order.
 //
 // A unit counts kTrStart tiles more than it has, for its Q, its first tile's maximum
-// and its output: 24 sequences of 300 to 9001 tokens with 5 to 37 rows of 32 heads
-// over 8 take 119 us at 4 tiles, 117 at 6, 115 at 8 (before the first maximum was
-// taken of few columns: 161 without, 138 at 4, 135 at 8).  Where sequences have
-// several tiles of rows, a team of two or four CTAs shares a unit of as many: they
-// read the same K and V at the same time, so that these come from HBM once (64 rows
-// of 16 heads over 2, 65471 tokens: 97 us one by one, 87 in twos, 84 in fours, when the
-// join took 5 us more than now).
+// and its output.  At 4, 6, 8 and 12 tiles, 24 sequences of 300 to 9001 tokens with 5 to
+// 37 rows of 32 heads over 8 take 115, 112, 111 and 113 us, with 24 rows each 104, 103,
+// 104 and 105, with 48 each 164, 159, 159 and 161; 64 rows alone over 100 to 2000 tokens
+// 94, 91, 93 and 94; 4 sequences of 128 rows over 7k to 16k 115, 114, 116 and 118.
+// Where sequences have several tiles of rows, a team of two or four CTAs shares a unit of
+// as many: they read the same K and V at the same time, so that these come from HBM
+// once.  One by one, in twos and in fours: those 4 sequences (four tiles) 131, 119 and
+// 116 us, the 24 with 48 rows (two tiles) 181, 160 and 273, 64 rows of 16 heads over 2
+// over 65k tokens 79 each way.  A tile that a team's CTA does not have costs as much as
+// one that it has: 24 sequences of 96 rows (three tiles) 268, 313 and 285, and a chunk of
+// 512 rows beside 15 single rows over 64k tokens 351, 540 and 988.
 //
 // Fourteen warps: two groups of four (warps 0-3 and 4-7) do the softmax, a row
 // per thread, tiles in turn; warps 8-11 copy K and V rows into a ring of
@@ -43,9 +47,9 @@
 // columns are passed over beforehand, for a maximum to begin with.
 //
 // Decode (M = group rows of 128) is bound by HBM: 16 sequences of 16k to 64k tokens
-// take 225 us, 95 % of the copy bandwidth.  With more rows no unit is busy all the
-// time: the 64 rows above take 78 us, 46 % of the bf16 rate, 4 sequences' 128 rows of 32
-// heads over 8 take 99, 45 %.  A tile's products take 1350 cycles (800 at head_dim
+// take 227 us, 94 % of the copy bandwidth.  With more rows no unit is busy all the
+// time: a tree of 64 rows over 65471 tokens takes 80 us, 45 % of the bf16 rate, 4 trees of
+// 128 rows of 32 heads over 8 take 100, 44 %.  A tile's products take 1350 cycles (800 at head_dim
 // 128), its copies 2000 (1500) at the 33 bytes a cycle and SM of the probe above, its
 // exponentials under 800, and a group's chain of barrier tests (over 100 cycles each
 // beside the copies), TMEM loads and stores about 3000 for every other tile.
@@ -585,6 +589,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
                   unpair_f32(fma2(pair_f32(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), c2, m2), lo, hi);
                   lo = ex2(lo);
                   hi = ex2(hi);
+                  // The sums keep 32 bits, as lse has to; P is rounded to bf16, the type
+                  // that the MMA takes beside V's.  Each weight is then off by half a
+                  // bf16 step at most, as the output is by its own rounding: 0.0023 of
+                  // the output's norm against 64 bits, 0.0017 if P had 32 bits.
                   part2[i & 1] = add2(part2[i & 1], pair_f32(lo, hi));
                   p[i] = pack_f32_bf16(lo, hi);
                 }
@@ -906,7 +914,9 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   int64_t *base = reinterpret_cast<int64_t *>(ws);
   float2 *ml = reinterpret_cast<float2 *>(ws + base_bytes(a.seqs.n_seqs));
   float *o = reinterpret_cast<float *>(ws + base_bytes(a.seqs.n_seqs) + ml_bytes(part_rows));
-  // CTAs that take a unit's tiles of rows side by side
+  // CTAs that take a unit's tiles of rows side by side: from one and a half tiles a
+  // sequence on two, from three and a half four.  The lengths are the device's, so the
+  // host goes by the mean over the call (measured both ways at the head of this file).
   const int64_t mean_rows = (int64_t)a.seqs.n_rows * a.group / a.seqs.n_seqs;
   const int team_log = mean_rows >= 448 ? 2 : mean_rows >= 192 ? 1 : 0;
   const int ctas = ((device_sm_count() < kTrMaxCtas ? device_sm_count() : kTrMaxCtas) >> team_log) << team_log;
@@ -922,8 +932,8 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   const bool many = ctas >= 8 * units;
   const int64_t blocks = many ? rows8 : (rows8 + kJoinWarps - 1) / kJoinWarps;
   // Four quads a thread keep more reads on their way where blocks come in waves (64
-  // rows of 65k tokens: 77.0 us, 80.6 with one); one where they are few (12.1 us for a
-  // row of 515 tokens, 12.8 with four).
+  // rows of 65k tokens: 79.8 us, 82.9 with one); one where they are few (12.0 us for a
+  // row of 515 tokens, 12.9 with four).
   const bool few = many && rows8 * a.nkv * (HD / 16) <= device_sm_count();
   return launch_dependent(few    ? tree_join_kernel<HD, kJoinWarps, 1>
                           : many ? tree_join_kernel<HD, kJoinWarps, 4>
