@@ -104,7 +104,7 @@ struct TreeCtrl {
   uint64_t pv_done[4];            // tile % 4
   uint64_t q_full, o_free, drain[2];
   int64_t scan[kTrWarps], found_off;
-  int32_t found_seq, bad[2], abort, broken;
+  int32_t found_seq, bad[2], abort;
   uint32_t tmem_base;
 };
 template <int HD>
@@ -202,7 +202,7 @@ template <int HD>
 __global__ void __launch_bounds__(kTrThreads, 1)
 tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_t part_rows, uint32_t q_and,
                  uint32_t q_xor, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml,
-                 float *__restrict__ part_o) {
+                 float *__restrict__ part_o, int32_t *__restrict__ row_seq) {
   using G = TreeGeom<HD>;
   extern __shared__ __align__(1024) uint8_t tr_smem[];
   TreeCtrl &C = *reinterpret_cast<TreeCtrl *>(tr_smem + G::kCtrlOff);
@@ -228,7 +228,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
     for (int b = 0; b < 4; ++b) mbar_init(sm32(&C.pv_done[b]), 1);
     mbar_init(sm32(&C.q_full), 32 * kTrSoft);
     mbar_init(sm32(&C.o_free), kTrSoft);
-    C.abort = C.broken = 0;
+    C.abort = 0;
     C.found_seq = a.seqs.n_seqs;
     C.found_off = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -244,9 +244,8 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   }
 
   // ---- the plan: every sequence's tiles summed, then the sequence this CTA's
-  // share starts in (CTA 0 also leaves the sums for the joining launch, and whether some
-  // sequence is left out).  Up to 32 sequences, a lane each, every warp for itself; else a
-  // thread each, in chunks.
+  // share starts in (CTA 0 also leaves the sums for the joining launch).  Up to 32
+  // sequences, a lane each, every warp for itself; else a thread each, in chunks.
   int64_t total = 0, found_off = 0;
   int32_t found_seq = a.seqs.n_seqs;
   TileShare share = {0, 0, 0};
@@ -254,10 +253,7 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   auto tiles_of = [&](int32_t s, bool report) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
     const SeqTiles q = seq_tiles<G::kT>(a, team_log, read_seq(a.seqs, s));
-    if (report && !q.v.ok) {
-      report_error(a.status, kErrRowRange, s);
-      *reinterpret_cast<volatile int32_t *>(&C.broken) = 1;
-    }
+    if (report && !q.v.ok) report_error(a.status, kErrRowRange, s);
     return q.count;
   };
   if (a.seqs.n_seqs <= 32) {
@@ -304,13 +300,10 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
       if (blockIdx.x != 0 && before > share.first) break;
     }
   }
+  if (blockIdx.x == 0 && tid == 0) base_out[a.seqs.n_seqs] = total;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (blockIdx.x == 0 && tid == 0) {
-    base_out[a.seqs.n_seqs] = total;
-    base_out[a.seqs.n_seqs + 1] = C.broken;
-  }
   const uint32_t tmem = C.tmem_base;
   const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
   if (a.seqs.n_seqs > 32) {
@@ -376,6 +369,11 @@ tree_attn_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
 #pragma unroll
           for (int k = 0; k < kN; ++k) rv[k] = rk[k];
         }
+      }
+      if (warp == kTrSoft && !g.whole && !g.empty) {  // the rows of a part, for the join
+        const int64_t m0 = (int64_t)g.mt * kTrRows, m1 = min(m0 + kTrRows, (int64_t)g.v.rows * a.group);
+        const int32_t end = fast_div(group_div, (int32_t)m1 - 1);
+        for (int32_t j = fast_div(group_div, (int32_t)m0) + lane; j <= end; j += 32) row_seq[g.v.row0 + j] = g.s;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
@@ -776,7 +774,7 @@ constexpr int kJoinWarps = 8;
 template <int HD, int kGroups, int kQuads>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_t part_rows, int32_t teams,
-                 const int64_t *base, const float2 *part_ml, const float4 *part_o) {
+                 const int64_t *base, const float2 *part_ml, const float4 *part_o, const int32_t *row_seq) {
   __shared__ float4 acc_s[kGroups > 1 ? kJoinWarps : 1][kQuads][32];
   __shared__ float2 ml_s[kGroups > 1 ? kJoinWarps : 1][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -802,10 +800,13 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   };
   if (row >= 0) place(seq_of_row(a.seqs, row));
   grid_dependency_sync();
-  // Where a sequence was left out, the starts may not ascend, and the search above may
-  // have missed a good one: every sequence is looked at.
-  if (row >= 0 && tiles == 0 && base[a.seqs.n_seqs + 1] != 0)
-    for (int32_t i = 0; i < a.seqs.n_seqs && tiles == 0; ++i) place(i);
+  // Where bad sequences' starts do not ascend, the search above may have missed a good
+  // one: who wrote a part of the row left its sequence.  (A row without parts has what an
+  // earlier call left there, which names its sequence or is no place for it.)
+  if (row >= 0 && tiles == 0) {
+    const int32_t at = row_seq[row];
+    if (at >= 0 && at < a.seqs.n_seqs) place(at);
+  }
   int32_t c0 = 0, c1 = 0;  // teams of the first and last part
   if (tiles > 0) {
     const int64_t per = (base[a.seqs.n_seqs] + teams - 1) / teams;
@@ -886,12 +887,13 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
     a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
 }
 
-// The workspace: the sequences' first tiles, their sum, whether one was left out; then the
-// parts' (max, sum) and O.
+// The workspace: the sequences' first tiles and their sum, the parts' (max, sum) and O, the
+// sequence of each row that has parts.
 int32_t part_rows_of(int64_t n_rows, int32_t group) {
   return (int32_t)(n_rows * group < kTrRows ? n_rows * group : kTrRows);
 }
-int64_t base_bytes(int32_t n_seqs) { return ((int64_t)(n_seqs + 2) * 8 + 255) / 256 * 256; }
+int64_t base_bytes(int32_t n_seqs) { return ((int64_t)(n_seqs + 1) * 8 + 255) / 256 * 256; }
+int64_t o_bytes(int32_t part_rows, int32_t head_dim) { return (int64_t)kTrMaxCtas * 2 * part_rows * head_dim * 4; }
 int64_t ml_bytes(int32_t part_rows) { return ((int64_t)kTrMaxCtas * 2 * part_rows * 8 + 255) / 256 * 256; }
 
 template <int HD>
@@ -914,6 +916,7 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   int64_t *base = reinterpret_cast<int64_t *>(ws);
   float2 *ml = reinterpret_cast<float2 *>(ws + base_bytes(a.seqs.n_seqs));
   float *o = reinterpret_cast<float *>(ws + base_bytes(a.seqs.n_seqs) + ml_bytes(part_rows));
+  int32_t *row_seq = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(o) + o_bytes(part_rows, HD));
   // CTAs that take a unit's tiles of rows side by side: from one and a half tiles a
   // sequence on two, from three and a half four.  The lengths are the device's, so the
   // host goes by the mean over the call (measured both ways at the head of this file).
@@ -922,7 +925,7 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
   const int ctas = ((device_sm_count() < kTrMaxCtas ? device_sm_count() : kTrMaxCtas) >> team_log) << team_log;
   const FastDiv group_div = make_fast_div(a.group);
   cudaError_t r = launch_dependent(tree_attn_kernel<HD>, dim3((unsigned)ctas), dim3(kTrThreads), tree_smem<HD>(), stream, 1u,
-                                   a, group_div, team_log, part_rows, q_and, q_xor, base, ml, o);
+                                   a, group_div, team_log, part_rows, q_and, q_xor, base, ml, o, row_seq);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= TreeGeom<HD>::kT) return r;
   // One group of parts per warp where units outnumber the CTAs (few parts each),
@@ -939,14 +942,15 @@ cudaError_t launch_hd(const TreeArgs &args, cudaStream_t stream) {
                           : many ? tree_join_kernel<HD, kJoinWarps, 4>
                                  : tree_join_kernel<HD, 1, 4>,
                           dim3((unsigned)blocks, few ? HD / 16 : HD / 64, (unsigned)a.nkv), dim3(32 * kJoinWarps), 0, stream, 1u, a,
-                          group_div, team_log, part_rows, (int32_t)(ctas >> team_log), base, ml, reinterpret_cast<const float4 *>(o));
+                          group_div, team_log, part_rows, (int32_t)(ctas >> team_log), base, ml, reinterpret_cast<const float4 *>(o),
+                          row_seq);
 }
 
 }  // namespace
 
 int64_t tree_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t group, int32_t head_dim) {
   const int32_t rows = part_rows_of(n_rows, group);
-  return base_bytes(n_seqs) + ml_bytes(rows) + (int64_t)kTrMaxCtas * 2 * rows * head_dim * 4;
+  return base_bytes(n_seqs) + ml_bytes(rows) + o_bytes(rows, head_dim) + (int64_t)n_rows * 4;
 }
 
 cudaError_t launch_tree_attn(const TreeArgs &a, int32_t head_dim, cudaStream_t stream) {

@@ -44,6 +44,30 @@ def test_starts_that_do_not_ascend_leave_the_good_sequences(qsa, n, hd):
     assert np.array_equal(mass, wmass)
 
 
+def test_many_rows_of_a_bad_sequence(qsa):
+    """Twenty thousand sequences, one of which claims thirty thousand rows that it may not
+    have, beside starts that do not ascend: rows that no sequence has cost the join little."""
+    n, more = 20000, 30000
+    c = Cache(qi.rng_for(88), np.full(n, 3), np.zeros(n, int), 8, 2, 128, 16, "chain")
+    ctx, rows = c.ctx, c.rows
+    ctx[n - 2], rows[n - 2], rows[n - 1] = 9001, 4, 1
+    c = Cache(qi.rng_for(89), ctx, rows, 8, 2, 128, 16, "chain")
+    c.q = np.concatenate([c.q, np.zeros((more, 8 * 128), np.uint16)])
+    c.n_rows += more
+    want, wlse, st = tree_call(qsa, c)
+    assert st == (0, 0)
+    c.row_start[n // 2] = c.n_rows - 1  # the one before has all rows, and a context too long for its table
+    c.ctx[n // 2 - 1] = c.table_len * 16
+    t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    t0.record()
+    out, lse, st = tree_call(qsa, c)
+    t1.record()
+    t1.synchronize()
+    assert st[0] == 3 and st[1] in (n // 2 - 1, n // 2)
+    assert np.array_equal(out, want) and np.array_equal(lse, wlse)
+    assert t0.elapsed_time(t1) < 5000  # with the copies
+
+
 @pytest.mark.parametrize("hd", [128, 256])
 @pytest.mark.parametrize("rows", [1, 60])
 def test_a_timeout_names_a_sequence_of_the_call(qsa, hd, rows):
