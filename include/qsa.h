@@ -470,8 +470,9 @@ qsa_status qsa_qk_proj(const uint16_t *x, int64_t x_stride, const uint16_t *w, i
  *  QSA_ERR_TOKEN_RANGE (the sequence's index) and its sequence's output is
  *  unspecified; a wait that gives up is QSA_ERR_TIMEOUT, with the index of the
  *  first sequence that the CTA had a part of, and leaves out and lse of every
- *  sequence of the call unspecified.  Refused: pool_pages * page_size * nkv, table_len * page_size or
- *  n_rows * nq past 31 bits, n_seqs or nkv > 65535, a small or unaligned workspace.
+ *  sequence of the call unspecified.  Refused: pool_pages * page_size * nkv,
+ *  table_len * page_size or n_rows * nq past 31 bits, n_seqs or nkv > 65535, a
+ *  small or unaligned workspace.
  */
 qsa_status qsa_tree_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
                          int32_t head_dim, const uint16_t *k_pool, const uint16_t *v_pool,
@@ -579,8 +580,9 @@ qsa_status qsa_evict_select(const float *mass, int64_t mass_cols, int32_t nkv,
  *  qsa_attn_mass, qsa_evict_select, qsa_mask_tokens, qsa_gather_kv and
  *  qsa_sparse_attn take cached tokens and lengths (q and K carry their true
  *  rotation already).  Of the calls that rotate:
- *   - qsa_score_rows: pos the true position, visible_len the cached length;
- *     qsa_select_mask: pos the cached position (visible_len - 1).
+ *   - qsa_score_rows: pos the true position, visible_len the cached length with
+ *     the row's own token; qsa_select_mask: pos the cached position
+ *     (visible_len - 1).
  *   - qsa_pool_blocks, qsa_index_select, qsa_decode_index_select: cached blocks
  *     and positions, with cos_t and sin_t D rows on and table_rows D less (one
  *     sequence a call, or several with the same D).

@@ -19,7 +19,7 @@
 // A unit counts kTrStart tiles more than it has, for its Q, its first tile's maximum
 // and its output.  At 4, 6, 8 and 12 tiles, 24 sequences of 300 to 9001 tokens with 5 to
 // 37 rows of 32 heads over 8 take 115, 112, 111 and 113 us, with 24 rows each 104, 103,
-// 104 and 105, with 48 each 164, 159, 159 and 161; 64 rows alone over 100 to 2000 tokens
+// 104 and 105, with 48 each 164, 159, 159 and 161; 64 single rows over 100 to 2000 tokens
 // 94, 91, 93 and 94; 4 sequences of 128 rows over 7k to 16k 115, 114, 116 and 118.
 // Where sequences have several tiles of rows, a team of two or four CTAs shares a unit of
 // as many: they read the same K and V at the same time, so that these come from HBM
@@ -46,13 +46,13 @@
 // shared memory after each tile; of a group's first tile in a part the first
 // columns are passed over beforehand, for a maximum to begin with.
 //
-// Decode (M = group rows of 128) is bound by HBM: 16 sequences of 16k to 64k tokens
-// take 227 us, 94 % of the copy bandwidth.  With more rows no unit is busy all the
-// time: a tree of 64 rows over 65471 tokens takes 80 us, 45 % of the bf16 rate, 4 trees of
-// 128 rows of 32 heads over 8 take 100, 44 %.  A tile's products take 1350 cycles (800 at head_dim
-// 128), its copies 2000 (1500) at the 33 bytes a cycle and SM of the probe above, its
-// exponentials under 800, and a group's chain of barrier tests (over 100 cycles each
-// beside the copies), TMEM loads and stores about 3000 for every other tile.
+// Decode (M = group rows of 128) is bound by HBM: 16 sequences of 16k to 64k tokens take
+// 227 us, 94 % of the copy bandwidth.  With more rows no unit is busy all the time: a
+// tree of 64 rows over 65471 tokens takes 80 us, 45 % of the bf16 rate, 4 trees of 128
+// rows of 32 heads over 8 take 100, 44 %.  A tile's products take 1350 cycles (800 at
+// head_dim 128), its copies 2000 (1500) at the 33 bytes a cycle and SM of the probe
+// above, its exponentials under 800, and a group's chain of barrier tests (over 100
+// cycles each beside the copies), TMEM loads and stores about 3000 for every other tile.
 // Measured and no faster: two CTAs as a pair (MMAs of 256 rows, half of each tile a
 // CTA), a third softmax group, a second issuer of S, tiles of 128 tokens with fewer
 // buffers, K by TMA boxes of 8 tokens, the next unit's Q ahead.
@@ -787,7 +787,7 @@ tree_join_kernel(const TreeArgs a, const FastDiv group_div, int team_log, int32_
   // of what this reads, and it began after everything before it was complete.
   int32_t s = 0, r = 0, rank = 0, tiles = 0;
   int64_t u0 = 0;  // the unit's first tile, from its sequence's first
-  auto place = [&](int32_t at) {  // whether the row is one of sequence `at`
+  auto place = [&](int32_t at) {  // where the row lies, if sequence `at` has it
     const SeqTiles q = seq_tiles<TreeGeom<HD>::kT>(a, team_log, read_seq(a.seqs, at));
     if (row < q.v.row0 || row >= q.v.row0 + q.v.rows) return;
     const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
