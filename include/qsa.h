@@ -67,8 +67,9 @@ typedef enum {
     QSA_ERR_ROW_RANGE = 3,     /* device: pos, visible_len (or key_base) out of range */
     QSA_ERR_NONFINITE = 4,     /* device: NaN/Inf score in a truncating row */
     QSA_ERR_TIMEOUT = 5,       /* device: a bounded wait gave up */
-    QSA_ERR_TOKEN_RANGE = 6    /* device: a gathered token or its page lies outside
+    QSA_ERR_TOKEN_RANGE = 6,   /* device: a gathered token or its page lies outside
                                   the page table or the pool */
+    QSA_ERR_NO_PAGES = 7       /* device: a step needs more pages than are free */
 } qsa_status;
 
 /* Which scorer qsa_score_rows_with runs. */
@@ -602,6 +603,149 @@ qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, 
                              const int32_t *first, float *mass, int64_t mass_cols, int32_t nkv,
                              uint16_t *block_keys, const int64_t *key_base, int32_t *dev_status,
                              void *stream);
+
+/*
+ * The pages, rows and slots of a step: each sequence's page table is brought to the
+ * length that its cached and its new tokens need, and every new token gets its row,
+ * its position and its place in the pool.  The row_start it writes is the one that
+ * qsa_qkv_write, qsa_cache8_attn, qsa_tree_attn and qsa_attn_mass take, with the same
+ * ctx_len and table; slot serves a caller that writes K and V itself.
+ *  ctx_len  DEVICE int32 [n_seqs]: cached tokens (of a cache that was cut, or whose
+ *           drafts were rejected: what is left of them).
+ *  new_rows DEVICE int32 [n_seqs]: tokens the step adds.
+ *  table    DEVICE int32: sequence s's page table at table + s*table_cols,
+ *           table_len entries, the first held[s] of them its pages.
+ *  held     DEVICE int32 [n_seqs]; held_out the same after the call:
+ *           ceil((ctx_len + new_rows) / page_size).  held_out may be held itself.
+ *  free_pages  DEVICE int32 [pool_pages], a stack of n_free[0] free pages, its top
+ *           last.  First the pages that sequences no longer need (entries held_out to
+ *           held - 1 of their tables) are put on it, in the order of sequences and
+ *           entries; then those that sequences need are taken off it in that order.
+ *           n_free_out[0] is its height after the call; it may be n_free itself.
+ *           Table entries past held_out and stack entries past the height are left as
+ *           they come.
+ *  max_rows rows that slot, pos and row_seq hold.
+ *  row_start  DEVICE int32 [n_seqs + 1]: sequence s's first row, and their sum.
+ *  slot     DEVICE int32 [max_rows]: the pool row (page * page_size + place in it) of
+ *           each row's token, -1 behind the last row.
+ *  pos      DEVICE int32 [max_rows]: ctx_len + the row's index in its sequence, 0 behind
+ *           the last row; or NULL.
+ *  row_seq  DEVICE int32 [max_rows]: each row's sequence, -1 behind the last; or NULL.
+ *  Device errors: a sequence whose lengths contradict the table (negative ones, more
+ *  tokens than table_len pages hold, held outside [0, table_len]) is
+ *  QSA_ERR_ROW_RANGE with its index, has no rows and keeps its pages.  More rows than
+ *  max_rows (QSA_ERR_ROW_RANGE), more pages than are free (QSA_ERR_NO_PAGES), both with
+ *  the first sequence that has no room, or a stack that would not fit pool_pages entries
+ *  (QSA_ERR_TOKEN_RANGE, sequence 0): the call then plans nothing, row_start is zero, and
+ *  tables, pages and heights stay as they were.  A page outside the pool among those
+ *  given back, taken or used by a row is QSA_ERR_TOKEN_RANGE with the sequence's index; a
+ *  slot in it is -1.
+ *  Refused: n_seqs > 65535, pool_pages * page_size or table_len * page_size past 31
+ *  bits, table_cols = 0 with several sequences.
+ */
+qsa_status qsa_page_plan(const int32_t *ctx_len, const int32_t *new_rows, int32_t n_seqs,
+                         int32_t page_size, int32_t pool_pages, int32_t *table, int32_t table_len,
+                         int64_t table_cols, const int32_t *held, int32_t *held_out,
+                         int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out,
+                         int32_t max_rows, int32_t *row_start, int32_t *slot, int32_t *pos,
+                         int32_t *row_seq, int32_t *dev_status, void *stream);
+
+/*
+ * The query and key heads of new tokens normed and rotated, and their K and V written
+ * into the paged cache, in bf16 or in 8 bits.  What qsa_tree_attn, qsa_sparse_attn
+ * (bf16) and qsa_cache8_attn (8 bits) then read.
+ *  q, k, v  DEVICE bf16, row i at q + i*q_stride (nq heads of head_dim values), k +
+ *           i*k_stride and v + i*v_stride (nkv heads): one projection's row, or three.
+ *           16-byte aligned, strides multiples of 8.
+ *  q_norm_w, k_norm_w  DEVICE bf16 [head_dim], 16-byte aligned: every head x becomes
+ *           x / sqrt(mean(x^2) + eps) * (1 + w), as the indexer's; NULL: not normed.
+ *  cos_t, sin_t, table_rows  the tables of qsa_rope_tables: dims i and i + 32 of a head,
+ *           i < 32, are turned by the angle of its position, the others pass.
+ *  pos      DEVICE int32 [n_rows]: each row's position (the depth of a tree's token, the
+ *           true position after a cut), or NULL: ctx_len + its index in the sequence.
+ *  ctx_len, row_start, n_seqs, n_rows, pool_pages, page_size, table, table_len,
+ *           table_cols: as in qsa_tree_attn; row j of sequence s is token ctx_len[s] + j
+ *           of its cache.
+ *  k_scale, v_scale  both NULL: k_pool and v_pool are DEVICE bf16 [pool_pages *
+ *           page_size, nkv, head_dim] (page_size any), 16-byte aligned.
+ *           Else the pools are e4m3 of that shape and the scales DEVICE f32
+ *           [pool_pages * page_size / unit, nkv]: block b of the pool's rows, rows
+ *           unit*b to unit*b + unit - 1, holds value * scale.  unit is 16, 32, 64 or 128
+ *           and divides page_size (it is not looked at for bf16 pools).
+ *           A block's scale is the smallest power of two s with |x| <= 448 s for
+ *           every finite new value x of the head in the block (0 if they are all 0),
+ *           and no less than its earlier scale where tokens before the new ones are in
+ *           the block: those are then divided by the new one and rounded again.  A NaN or
+ *           an infinity is held as NaN.
+ *  q_out    DEVICE bf16, row i at q_out + i*out_stride (nq*head_dim values), 16-byte
+ *           aligned, out_stride a multiple of 8; q itself with q_stride is allowed.
+ *  Everything runs in f32 and is rounded once, to bf16 or e4m3.  head_dim is 128 or 256.
+ *  Rows outside every sequence, and what the cache holds past its new tokens, are left
+ *  alone.  Sequences must not share a page that new tokens go to.
+ *  Device errors: a sequence whose rows or context contradict n_rows or the table is
+ *  QSA_ERR_ROW_RANGE (with its index) and is left alone; a position outside
+ *  [0, table_rows) is QSA_ERR_ROW_RANGE (the sequence's index), that row's q_out, K and V
+ *  left alone; a table entry outside the pool QSA_ERR_TOKEN_RANGE (the sequence's
+ *  index), its tokens' K and V not written.
+ *  Refused: what qsa_tree_attn refuses of these, one scale without the other, a unit that
+ *  does not divide page_size.
+ */
+qsa_status qsa_qkv_write(const uint16_t *q, int64_t q_stride, int32_t nq, const uint16_t *k,
+                         int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t nkv,
+                         int32_t head_dim, const uint16_t *q_norm_w, const uint16_t *k_norm_w,
+                         float eps, const uint16_t *cos_t, const uint16_t *sin_t,
+                         int32_t table_rows, const int32_t *pos, const int32_t *ctx_len,
+                         const int32_t *row_start, int32_t n_seqs, int32_t n_rows, void *k_pool,
+                         void *v_pool, float *k_scale, float *v_scale, int32_t unit,
+                         int32_t pool_pages, int32_t page_size, const int32_t *table,
+                         int32_t table_len, int64_t table_cols, uint16_t *q_out,
+                         int64_t out_stride, int32_t *dev_status, void *stream);
+
+/*
+ * qsa_tree_attn over a cache held in 8 bits (qsa_qkv_write writes it), and with a window
+ * over the tokens that a row looks back at.
+ *  q ... scale, out, out_stride, lse  as in qsa_tree_attn, but
+ *  k_pool, v_pool  DEVICE e4m3 [pool_pages * page_size, nkv, head_dim], 16-byte aligned;
+ *  k_scale, v_scale  DEVICE f32 [pool_pages * page_size / unit, nkv]: K and V are the
+ *           pools' values times their block's scale.  Scales are finite and >= 0, powers
+ *           of two or not.
+ *  unit     16, 32, 64 or 128, a divisor of page_size.
+ *  window, n_first  window 0: every row sees its context whole.  Else a row at cached
+ *           position p sees context token t iff t < n_first or p - t < window, where p
+ *           is ctx_len + j for row j without a tree_mask (which then holds for drafted
+ *           tokens t <= p too), and ctx_len + max(0, c - 1) for a row whose tree_mask
+ *           names c drafted tokens of its sequence (those are seen whatever the window).
+ *           Cached tokens that no row sees are not read.
+ *  A row that attends no token gets zeros, and lse -inf.  What a row does not see does
+ *  not reach its output, NaN though it be.
+ *  Products, softmax and sums run in f32.  A row's weights times their block's V scale
+ *  enter the weighted sum as two e4m3 terms, relative to the row's largest: off by at
+ *  most 2^-8 of themselves, or 2^-18 of the largest; those of 2^-96 of it and less may
+ *  count as nothing.  q is split likewise, exact but for what is below 2^-17 of its
+ *  head's largest value.  The normaliser and lse use the f32 weights.
+ *  workspace  DEVICE scratch of qsa_cache8_workspace_bytes(...) bytes, 16-byte aligned;
+ *           its contents on entry do not matter.  Calls that share one must be
+ *           stream-ordered.
+ *  Device errors and refusals as in qsa_tree_attn (its product bounds too), and: a scale
+ *  that is negative or not finite among tokens that are read is QSA_ERR_NONFINITE with
+ *  the sequence's index, whose output is then unspecified.  Refused: another unit, a
+ *  negative window or n_first.
+ */
+qsa_status qsa_cache8_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
+                           int32_t head_dim, const uint8_t *k_pool, const uint8_t *v_pool,
+                           const float *k_scale, const float *v_scale, int32_t unit,
+                           int32_t pool_pages, int32_t page_size, const int32_t *table,
+                           int32_t table_len, int64_t table_cols, const int32_t *ctx_len,
+                           const int32_t *row_start, int32_t n_seqs, int32_t n_rows,
+                           const uint32_t *tree_mask, int32_t mask_words, int32_t n_first,
+                           int32_t window, float scale, uint16_t *out, int64_t out_stride,
+                           float *lse, int32_t *dev_status, void *workspace,
+                           int64_t workspace_bytes, void *stream);
+
+/* Bytes of the workspace qsa_cache8_attn needs; -1 for arguments it refuses.  They grow
+ * as qsa_tree_workspace_bytes does. */
+int64_t qsa_cache8_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int32_t nkv,
+                                   int32_t head_dim);
 
 /* Zero a DEVICE status word (stream-ordered). */
 qsa_status qsa_reset_status(int32_t *dev_status, void *stream);

@@ -26,6 +26,7 @@ QSA_ERR_ROW_RANGE = 3
 QSA_ERR_NONFINITE = 4
 QSA_ERR_TIMEOUT = 5
 QSA_ERR_TOKEN_RANGE = 6
+QSA_ERR_NO_PAGES = 7
 
 QSA_SCORE_AUTO = 0
 QSA_SCORE_SIMT = 1
@@ -40,6 +41,7 @@ EXPORTED = ("qsa_version", "qsa_status_string", "qsa_rope_tables", "qsa_pool_blo
             "qsa_decode_workspace_bytes", "qsa_decode_index_select", "qsa_mask_tokens",
             "qsa_gather_kv", "qsa_sparse_attn", "qsa_qk_proj", "qsa_tree_attn",
             "qsa_tree_workspace_bytes", "qsa_attn_mass", "qsa_evict_select", "qsa_cache_compact",
+            "qsa_page_plan", "qsa_qkv_write", "qsa_cache8_attn", "qsa_cache8_workspace_bytes",
             "qsa_reset_status",
             "qsa_read_status", "qsa_set_wait_limit_cycles", "qsa_wait_limit_cycles")
 
@@ -88,6 +90,13 @@ def _load() -> ctypes.CDLL:
         "qsa_evict_select": ([P, i64, i32, P, i32, i32, i32, i32, i32, i32, P, i64, P, P, P], i32),
         "qsa_cache_compact": ([P, P, i32, i32, P, i32, i64, i32, P, i64, P, i32, i32, P, P, i64,
                                i32, P, P, P, P], i32),
+        "qsa_page_plan": ([P, P, i32, i32, i32, P, i32, i64, P, P, P, P, P, i32, P, P, P, P, P, P],
+                          i32),
+        "qsa_qkv_write": ([P, i64, i32, P, i64, P, i64, i32, i32, P, P, f32, P, P, i32, P, P, P, i32,
+                           i32, P, P, P, P, i32, i32, i32, P, i32, i64, P, i64, P, P], i32),
+        "qsa_cache8_attn": ([P, i64, i32, i32, i32, P, P, P, P, i32, i32, i32, P, i32, i64, P, P, i32,
+                             i32, P, i32, i32, i32, f32, P, i64, P, P, P, i64, P], i32),
+        "qsa_cache8_workspace_bytes": ([i32, i32, i32, i32, i32], i64),
         "qsa_reset_status": ([P, P], i32),
         "qsa_read_status": ([P, P, P, P], i32),
         "qsa_set_wait_limit_cycles": ([i64], i32),
@@ -431,6 +440,76 @@ def qsa_cache_compact(k_pool, v_pool, width, pool_pages, table, table_len, table
                                   _at(key_base, "key_base", home), _at(dev_status, "dev_status", home),
                                   _raw(stream, home)),
            "qsa_cache_compact")
+
+
+def qsa_page_plan(ctx_len, new_rows, n_seqs, page_size, pool_pages, table, table_len, table_cols,
+                  held, held_out, free_pages, n_free, n_free_out, max_rows, row_start, slot, pos,
+                  row_seq, dev_status, stream=None) -> None:
+    home = _home(ctx_len, "ctx_len")
+    _check(_lib.qsa_page_plan(_at(ctx_len, "ctx_len", home), _at(new_rows, "new_rows", home),
+                              int(n_seqs), int(page_size), int(pool_pages), _at(table, "table", home),
+                              int(table_len), int(table_cols), _at(held, "held", home),
+                              _at(held_out, "held_out", home), _at(free_pages, "free_pages", home),
+                              _at(n_free, "n_free", home), _at(n_free_out, "n_free_out", home),
+                              int(max_rows), _at(row_start, "row_start", home), _at(slot, "slot", home),
+                              _at(pos, "pos", home), _at(row_seq, "row_seq", home),
+                              _at(dev_status, "dev_status", home), _raw(stream, home)),
+           "qsa_page_plan")
+
+
+def qsa_qkv_write(q, q_stride, nq, k, k_stride, v, v_stride, nkv, head_dim, q_norm_w, k_norm_w, eps,
+                  cos_t, sin_t, table_rows, pos, ctx_len, row_start, n_seqs, n_rows, k_pool, v_pool,
+                  k_scale, v_scale, unit, pool_pages, page_size, table, table_len, table_cols,
+                  q_out, out_stride, dev_status, stream=None) -> None:
+    home = _home(q, "q")
+    _check(_lib.qsa_qkv_write(_at(q, "q", home), int(q_stride), int(nq), _at(k, "k", home), int(k_stride),
+                              _at(v, "v", home), int(v_stride), int(nkv), int(head_dim),
+                              _at(q_norm_w, "q_norm_w", home), _at(k_norm_w, "k_norm_w", home),
+                              float(eps), _at(cos_t, "cos_t", home), _at(sin_t, "sin_t", home),
+                              int(table_rows), _at(pos, "pos", home), _at(ctx_len, "ctx_len", home),
+                              _at(row_start, "row_start", home), int(n_seqs), int(n_rows),
+                              _at(k_pool, "k_pool", home), _at(v_pool, "v_pool", home),
+                              _at(k_scale, "k_scale", home), _at(v_scale, "v_scale", home), int(unit),
+                              int(pool_pages), int(page_size), _at(table, "table", home), int(table_len),
+                              int(table_cols), _at(q_out, "q_out", home), int(out_stride),
+                              _at(dev_status, "dev_status", home), _raw(stream, home)),
+           "qsa_qkv_write")
+
+
+def qsa_cache8_workspace_bytes(n_seqs: int, n_rows: int, nq: int, nkv: int, head_dim: int) -> int:
+    return int(_lib.qsa_cache8_workspace_bytes(int(n_seqs), int(n_rows), int(nq), int(nkv),
+                                               int(head_dim)))
+
+
+def new_cache8_workspace(n_seqs: int, n_rows: int, nq: int, nkv: int, head_dim: int,
+                         device="cuda") -> torch.Tensor:
+    """A workspace for qsa_cache8_attn calls of at most these n_seqs, n_rows and head_dim, and
+    of at most nq / nkv query heads a KV head."""
+    n = qsa_cache8_workspace_bytes(n_seqs, n_rows, nq, nkv, head_dim)
+    if n < 0:
+        raise ValueError(f"no workspace for n_seqs={n_seqs}, n_rows={n_rows}, nq={nq}, nkv={nkv}, "
+                         f"head_dim={head_dim}")
+    return torch.empty(max(16, n), dtype=torch.uint8, device=device)
+
+
+def qsa_cache8_attn(q, q_stride, nq, nkv, head_dim, k_pool, v_pool, k_scale, v_scale, unit, pool_pages,
+                    page_size, table, table_len, table_cols, ctx_len, row_start, n_seqs, n_rows,
+                    tree_mask, mask_words, n_first, window, scale, out, out_stride, lse, dev_status,
+                    workspace, stream=None) -> None:
+    home = _home(q, "q")
+    ws = _at(workspace, "workspace", home)
+    wsb = 0 if ws is None else workspace.numel() * workspace.element_size()
+    _check(_lib.qsa_cache8_attn(_at(q, "q", home), int(q_stride), int(nq), int(nkv), int(head_dim),
+                                _at(k_pool, "k_pool", home), _at(v_pool, "v_pool", home),
+                                _at(k_scale, "k_scale", home), _at(v_scale, "v_scale", home), int(unit),
+                                int(pool_pages), int(page_size), _at(table, "table", home),
+                                int(table_len), int(table_cols), _at(ctx_len, "ctx_len", home),
+                                _at(row_start, "row_start", home), int(n_seqs), int(n_rows),
+                                _at(tree_mask, "tree_mask", home), int(mask_words), int(n_first),
+                                int(window), float(scale), _at(out, "out", home), int(out_stride),
+                                _at(lse, "lse", home), _at(dev_status, "dev_status", home), ws, wsb,
+                                _raw(stream, home)),
+           "qsa_cache8_attn")
 
 
 def qsa_reset_status(dev_status, stream=None) -> None:

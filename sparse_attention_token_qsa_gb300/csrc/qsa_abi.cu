@@ -116,6 +116,7 @@ const char *qsa_status_string(int32_t status) {
     case QSA_ERR_NONFINITE: return "non-finite score in a truncating row";
     case QSA_ERR_TIMEOUT: return "a bounded device wait gave up";
     case QSA_ERR_TOKEN_RANGE: return "a selected token or its page lies outside the page table or the pool";
+    case QSA_ERR_NO_PAGES: return "a step needs more pages than are free";
     default: return "unknown status";
   }
 }
@@ -575,6 +576,119 @@ qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, 
                            table_len, table_cols, keep, keep_cols, n_keep, max_keep, first, mass,
                            mass_cols, mass ? nkv : 0, block_keys, key_base, dev_status};
   return from_cuda(qsa::launch_cache_compact(a, n_seqs, (cudaStream_t)stream));
+}
+
+namespace {
+
+// log2 of the tokens of a scale's block, or -1.
+int unit_log_of(int32_t unit) {
+  for (int l = 4; l <= 7; ++l)
+    if (unit == 1 << l) return l;
+  return -1;
+}
+
+}  // namespace
+
+qsa_status qsa_page_plan(const int32_t *ctx_len, const int32_t *new_rows, int32_t n_seqs,
+                         int32_t page_size, int32_t pool_pages, int32_t *table, int32_t table_len,
+                         int64_t table_cols, const int32_t *held, int32_t *held_out,
+                         int32_t *free_pages, const int32_t *n_free, int32_t *n_free_out,
+                         int32_t max_rows, int32_t *row_start, int32_t *slot, int32_t *pos,
+                         int32_t *row_seq, int32_t *dev_status, void *stream) {
+  if (n_seqs < 0 || pool_pages < 0 || table_len < 0 || table_cols < 0 || max_rows < 0)
+    return QSA_ERR_INVALID_VALUE;
+  if (n_seqs == 0) return QSA_OK;
+  if (page_size <= 0 || pool_pages == 0 || table_len == 0) return QSA_ERR_INVALID_VALUE;
+  // a table shared by several sequences would have them overwrite each other
+  if (table_cols != 0 ? table_cols < table_len : n_seqs > 1) return QSA_ERR_INVALID_VALUE;
+  if (!ctx_len || !new_rows || !table || !held || !held_out || !free_pages || !n_free || !n_free_out ||
+      !row_start || (!slot && max_rows > 0) || !dev_status)
+    return QSA_ERR_INVALID_VALUE;
+  if (n_seqs > 65535 || (int64_t)pool_pages * page_size > INT32_MAX ||
+      (int64_t)table_len * page_size > INT32_MAX - 256 || table_cols > kMostElems / n_seqs)
+    return QSA_ERR_INVALID_VALUE;
+  const qsa::PlanArgs a{ctx_len, new_rows, n_seqs, pool_pages, qsa::make_fast_div(page_size), table, table_len, table_cols,
+                        held, held_out, free_pages, n_free, n_free_out, max_rows, row_start, slot, pos, row_seq, dev_status};
+  return from_cuda(qsa::launch_page_plan(a, (cudaStream_t)stream));
+}
+
+qsa_status qsa_qkv_write(const uint16_t *q, int64_t q_stride, int32_t nq, const uint16_t *k,
+                         int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t nkv,
+                         int32_t head_dim, const uint16_t *q_norm_w, const uint16_t *k_norm_w,
+                         float eps, const uint16_t *cos_t, const uint16_t *sin_t,
+                         int32_t table_rows, const int32_t *pos, const int32_t *ctx_len,
+                         const int32_t *row_start, int32_t n_seqs, int32_t n_rows, void *k_pool,
+                         void *v_pool, float *k_scale, float *v_scale, int32_t unit,
+                         int32_t pool_pages, int32_t page_size, const int32_t *table,
+                         int32_t table_len, int64_t table_cols, uint16_t *q_out,
+                         int64_t out_stride, int32_t *dev_status, void *stream) {
+  bool empty;
+  const qsa_status st =
+      check_cached(q, q_stride, nq, nkv, head_dim, static_cast<const uint16_t *>(k_pool), pool_pages, page_size, table,
+                   table_len, table_cols, ctx_len, row_start, n_seqs, n_rows, nullptr, 0, 1.0f, dev_status, &empty);
+  if (st != QSA_OK) return st;
+  if (k_stride < 0 || v_stride < 0 || out_stride < 0 || table_rows < 0 || !eps_ok(eps)) return QSA_ERR_INVALID_VALUE;
+  if (empty) return QSA_OK;
+  // a table shared by several sequences would have them overwrite each other
+  if (table_cols == 0 && n_seqs > 1) return QSA_ERR_INVALID_VALUE;
+  if (!k || !v || !v_pool || !q_out || !cos_t || !sin_t || !aligned16(k) || !aligned16(v) || !aligned16(v_pool) ||
+      !aligned16(q_out) || !aligned16(cos_t) || !aligned16(sin_t) || (q_norm_w && !aligned16(q_norm_w)) ||
+      (k_norm_w && !aligned16(k_norm_w)))
+    return QSA_ERR_INVALID_VALUE;
+  const int64_t kv_row = (int64_t)nkv * head_dim, q_row = (int64_t)nq * head_dim;
+  if (k_stride < kv_row || v_stride < kv_row || out_stride < q_row || (k_stride & 7) != 0 || (v_stride & 7) != 0 ||
+      (out_stride & 7) != 0 || (int64_t)n_rows * k_stride > kMostElems || (int64_t)n_rows * v_stride > kMostElems ||
+      (int64_t)n_rows * out_stride > kMostElems || nq > (1 << 20))
+    return QSA_ERR_INVALID_VALUE;
+  if ((k_scale == nullptr) != (v_scale == nullptr)) return QSA_ERR_INVALID_VALUE;
+  const int unit_log = k_scale ? unit_log_of(unit) : 4;
+  if (unit_log < 0 || (k_scale && page_size % unit != 0)) return QSA_ERR_INVALID_VALUE;
+  const qsa::WriteArgs a{{pool_pages, qsa::make_fast_div(page_size), table, table_len, table_cols, ctx_len, row_start, n_seqs,
+                          n_rows, nullptr, 0},
+                         q, k, v, q_stride, k_stride, v_stride, nq, nkv, q_norm_w, k_norm_w, eps, cos_t, sin_t, table_rows,
+                         pos, k_pool, v_pool, k_scale, v_scale, unit_log, q_out, out_stride, dev_status};
+  return from_cuda(qsa::launch_qkv_write(a, head_dim, (cudaStream_t)stream));
+}
+
+int64_t qsa_cache8_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, int32_t nkv,
+                                   int32_t head_dim) {
+  if (n_seqs < 0 || n_rows < 0 || nq <= 0 || nkv <= 0 || nq % nkv != 0 ||
+      (head_dim != 128 && head_dim != 256))
+    return -1;
+  return qsa::cache8_workspace_bytes(n_seqs, n_rows, nq / nkv, head_dim);
+}
+
+qsa_status qsa_cache8_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,
+                           int32_t head_dim, const uint8_t *k_pool, const uint8_t *v_pool,
+                           const float *k_scale, const float *v_scale, int32_t unit,
+                           int32_t pool_pages, int32_t page_size, const int32_t *table,
+                           int32_t table_len, int64_t table_cols, const int32_t *ctx_len,
+                           const int32_t *row_start, int32_t n_seqs, int32_t n_rows,
+                           const uint32_t *tree_mask, int32_t mask_words, int32_t n_first,
+                           int32_t window, float scale, uint16_t *out, int64_t out_stride,
+                           float *lse, int32_t *dev_status, void *workspace,
+                           int64_t workspace_bytes, void *stream) {
+  bool empty;
+  const qsa_status st =
+      check_cached(q, q_stride, nq, nkv, head_dim, reinterpret_cast<const uint16_t *>(k_pool), pool_pages, page_size, table,
+                   table_len, table_cols, ctx_len, row_start, n_seqs, n_rows, tree_mask, mask_words, scale, dev_status,
+                   &empty);
+  if (st != QSA_OK) return st;
+  if (out_stride < 0 || workspace_bytes < 0 || n_first < 0 || window < 0) return QSA_ERR_INVALID_VALUE;
+  if (empty) return QSA_OK;
+  const int unit_log = unit_log_of(unit);
+  if (unit_log < 0 || page_size % unit != 0) return QSA_ERR_INVALID_VALUE;
+  if (!v_pool || !k_scale || !v_scale || !out || !aligned16(v_pool) || !aligned16(out) ||
+      out_stride < (int64_t)nq * head_dim || (out_stride & 7) != 0 || (int64_t)n_rows * out_stride > kMostElems)
+    return QSA_ERR_INVALID_VALUE;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < qsa_cache8_workspace_bytes(n_seqs, n_rows, nq, nkv, head_dim))
+    return QSA_ERR_INVALID_VALUE;
+  const qsa::Cache8Args a{{pool_pages, qsa::make_fast_div(page_size), table, table_len, table_cols, ctx_len, row_start, n_seqs,
+                           n_rows, tree_mask, mask_words},
+                          q, q_stride, nq, nkv, nq / nkv, k_pool, v_pool, k_scale, v_scale, unit_log, n_first, window,
+                          scale * 1.4426950408889634f, out, out_stride, lse, dev_status, workspace, qsa::wait_limit_cycles()};
+  return from_cuda(qsa::launch_cache8_attn(a, head_dim, (cudaStream_t)stream));
 }
 
 qsa_status qsa_reset_status(int32_t *dev_status, void *stream) {

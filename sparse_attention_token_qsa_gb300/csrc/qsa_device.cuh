@@ -30,6 +30,7 @@ enum : int32_t {
   kErrNonFinite = 4,
   kErrTimeout = 5,
   kErrTokenRange = 6,
+  kErrNoPages = 7,
 };
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t h16) { return __uint_as_float(h16 << 16); }

@@ -206,4 +206,63 @@ struct CompactArgs {
 };
 cudaError_t launch_cache_compact(const CompactArgs &a, int32_t n_seqs, cudaStream_t stream);
 
+// The pages, rows and slots of a step (qsa_plan.cu).
+struct PlanArgs {
+  const int32_t *ctx_len, *new_rows;
+  int32_t n_seqs, pool_pages;
+  FastDiv page;
+  int32_t *table;
+  int32_t table_len;
+  int64_t table_cols;
+  const int32_t *held;
+  int32_t *held_out, *free_pages;
+  const int32_t *n_free;
+  int32_t *n_free_out;
+  int32_t max_rows;
+  int32_t *row_start, *slot, *pos, *row_seq;  // pos, row_seq: nullptr where not wanted
+  int32_t *status;
+};
+cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t stream);
+
+// Normed and rotated query and key heads, K and V into the cache (qsa_write.cu).
+struct WriteArgs {
+  CachedSeqs seqs;
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  int32_t nq, nkv;
+  const uint16_t *q_norm_w, *k_norm_w;  // nullptr: no norm
+  float eps;
+  const uint16_t *cos_t, *sin_t;
+  int32_t table_rows;
+  const int32_t *pos;  // nullptr: ctx + index
+  void *k_pool, *v_pool;
+  float *k_scale, *v_scale;  // nullptr: bf16 pools
+  int32_t unit_log;
+  uint16_t *q_out;
+  int64_t out_stride;
+  int32_t *status;
+};
+cudaError_t launch_qkv_write(const WriteArgs &a, int32_t head_dim, cudaStream_t stream);
+
+// Attention over a cache held in 8 bits (qsa_cache8.cu).
+struct Cache8Args {
+  CachedSeqs seqs;
+  const uint16_t *q;
+  int64_t q_stride;
+  int32_t nq, nkv, group;
+  const uint8_t *k_pool, *v_pool;
+  const float *k_scale, *v_scale;
+  int32_t unit_log;
+  int32_t n_first, window;  // window 0: none
+  float scale_log2;         // scale * log2(e)
+  uint16_t *out;
+  int64_t out_stride;
+  float *lse;  // nullptr: not written
+  int32_t *status;
+  void *ws;
+  long long wait_limit;
+};
+int64_t cache8_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t group, int32_t head_dim);
+cudaError_t launch_cache8_attn(const Cache8Args &a, int32_t head_dim, cudaStream_t stream);
+
 }  // namespace qsa

@@ -1,0 +1,224 @@
+// The pages, rows and slots of a step.
+//
+// need_s = ceil((ctx_s + new_s) / page).  The pages [need_s, held_s) go on a stack of
+// free ones, in the order of sequences and entries; the pages [held_s, need_s) come off it
+// in that order, the i-th from place H - 1 - i of the stack's height H; row j of
+// sequence s is token ctx_s + j, in page table[s][(ctx_s + j) / page].
+//
+// Whole numbers only, and little of them: three passes over the sequences' lengths and
+// one over the rows, 12 bytes each.  What costs is the chain: lengths, sums over the
+// sequences, the stack, the tables, the rows.  One CTA does a small step, a cluster of
+// eight a large one, whose CTAs all sum the lengths, move the pages of their own warps'
+// sequences and fill their own run of rows, with a cluster barrier where one reads what
+// another wrote; so the lengths, heights and tables may be updated in place, and a step
+// is one launch.
+#include "qsa_launch.h"
+
+namespace qsa {
+
+namespace {
+
+constexpr int kPlThreads = 1024, kPlWarps = kPlThreads / 32, kPlCtas = 8;
+
+struct PlanSeq {
+  int32_t rows, back, take, held;
+  bool ok;
+};
+
+__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs &a, int32_t s) {
+  PlanSeq p = {0, 0, 0, 0, true};
+  if (s >= a.n_seqs) return p;
+  const int32_t ctx = a.ctx_len[s], rows = a.new_rows[s];
+  p.held = a.held[s];
+  p.ok = ctx >= 0 && rows >= 0 && p.held >= 0 && p.held <= a.table_len &&
+         (int64_t)ctx + rows <= (int64_t)a.table_len * a.page.d;
+  if (!p.ok) return p;
+  p.rows = rows;
+  const int32_t kv = ctx + rows, need = kv > 0 ? fast_div(a.page, kv - 1) + 1 : 0;
+  p.back = max(0, p.held - need);
+  p.take = max(0, need - p.held);
+  return p;
+}
+
+// How many of the 32 lanes' ascending values are <= x (each lane its own x).
+__device__ __forceinline__ int lanes_upto(int64_t value, int64_t x) {
+  int n = 0;
+#pragma unroll
+  for (int step = 16; step; step >>= 1)
+    if (__shfl_sync(0xffffffffu, value, n + step - 1) <= x) n += step;
+  if (__shfl_sync(0xffffffffu, value, n) <= x) ++n;  // (n <= 31 here)
+  return n;
+}
+
+__device__ __forceinline__ void plan_barrier() {
+  if (gridDim.x == 1) {
+    __syncthreads();
+    return;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+struct PlanSums {
+  int64_t rows, back, take;
+};
+
+__global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a) {
+  __shared__ int64_t scan[3][kPlWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x, ranks = gridDim.x;  // the grid is one cluster
+  grid_dependency_sync();
+
+  // this thread's sequence of a chunk, and the sums before it; adds the chunk to `before`
+  auto chunk = [&](int32_t s, PlanSeq &p, PlanSums &before) -> PlanSums {
+    p = plan_seq(a, s);
+    const int64_t r = warp_scan(p.rows, lane), b = warp_scan(p.back, lane), t = warp_scan(p.take, lane);
+    __syncthreads();
+    if (lane == 31) {
+      scan[0][warp] = r;
+      scan[1][warp] = b;
+      scan[2][warp] = t;
+    }
+    __syncthreads();
+    PlanSums at = {before.rows + r - p.rows, before.back + b - p.back, before.take + t - p.take};
+    for (int i = 0; i < kPlWarps; ++i) {
+      const int64_t x = scan[0][i], y = scan[1][i], z = scan[2][i];
+      if (i < warp) {
+        at.rows += x;
+        at.back += y;
+        at.take += z;
+      }
+      before.rows += x;
+      before.back += y;
+      before.take += z;
+    }
+    return at;
+  };
+
+  PlanSums all = {0, 0, 0};
+  PlanSeq p;
+  PlanSums at = {0, 0, 0};
+  for (int32_t s0 = 0; s0 < a.n_seqs; s0 += kPlThreads) {
+    at = chunk(s0 + tid, p, all);
+    if (rank == 0 && !p.ok) report_error(a.status, kErrRowRange, s0 + tid);
+  }
+  const bool one_chunk = a.n_seqs <= kPlThreads;  // p and at stay good
+  const int64_t free0 = *a.n_free, height = free0 + all.back;
+  const bool stack_ok = free0 >= 0 && height <= a.pool_pages, rows_ok = all.rows <= a.max_rows;
+  const bool ok = stack_ok && rows_ok && all.take <= height;
+
+  // item(s, i, k): the i-th of sequence s's `count` items, the k-th of all
+  auto each = [&](int32_t s, int32_t count, int64_t first, auto &&item) {
+    const int64_t incl = warp_scan(count, lane), total = __shfl_sync(0xffffffffu, incl, 31);
+    const int64_t base = __shfl_sync(0xffffffffu, first, 0);
+    for (int64_t i0 = 0; i0 < total; i0 += 32) {
+      const int64_t i = i0 + lane;
+      const int src = min(lanes_upto(incl, i), 31);
+      const int64_t begin = __shfl_sync(0xffffffffu, incl - count, src);
+      const int32_t seq = __shfl_sync(0xffffffffu, s, src);
+      if (i < total) item(seq, (int32_t)(i - begin), base + i);
+    }
+  };
+  auto mine = [&](int32_t s0) { return (uint32_t)(s0 / 32 + warp) % ranks == rank; };
+
+  if (ok && all.back > 0) {
+    PlanSums sums = {0, 0, 0};
+    for (int32_t s0 = 0; s0 < a.n_seqs; s0 += kPlThreads) {
+      if (!one_chunk) at = chunk(s0 + tid, p, sums);
+      if (!mine(s0)) continue;
+      each(s0 + tid, p.back, at.back, [&](int32_t s, int32_t i, int64_t k) {
+        const int32_t kv = a.ctx_len[s] + a.new_rows[s];
+        const int32_t entry = (kv > 0 ? fast_div(a.page, kv - 1) + 1 : 0) + i;
+        const int32_t page = a.table[(int64_t)s * a.table_cols + entry];
+        if (page < 0 || page >= a.pool_pages) report_error(a.status, kErrTokenRange, s);
+        a.free_pages[free0 + k] = page;
+      });
+    }
+    plan_barrier();
+  }
+  {
+    PlanSums sums = {0, 0, 0};
+    for (int32_t s0 = 0; s0 < a.n_seqs; s0 += kPlThreads) {
+      const int32_t s = s0 + tid;
+      if (!one_chunk) at = chunk(s, p, sums);
+      if (rank == 0 && s < a.n_seqs) {
+        a.row_start[s] = ok ? (int32_t)at.rows : 0;
+        if (s == a.n_seqs - 1) a.row_start[s + 1] = ok ? (int32_t)all.rows : 0;
+        if (!ok) {
+          if (!stack_ok) {
+            if (s == 0) report_error(a.status, kErrTokenRange, 0);
+          } else if (!rows_ok) {
+            if (at.rows <= a.max_rows && at.rows + p.rows > a.max_rows) report_error(a.status, kErrRowRange, s);
+          } else if (at.take <= height && at.take + p.take > height) {
+            report_error(a.status, kErrNoPages, s);
+          }
+        }
+      }
+      if (!ok || !mine(s0)) continue;
+      each(s, p.take, at.take, [&](int32_t seq, int32_t i, int64_t k) {
+        const int32_t page = __ldcg(a.free_pages + (height - 1 - k));
+        if (page < 0 || page >= a.pool_pages) report_error(a.status, kErrTokenRange, seq);
+        a.table[(int64_t)seq * a.table_cols + a.held[seq] + i] = page;
+      });
+    }
+  }
+  plan_barrier();
+
+  // everyone has read the lengths and heights: they may be written in place
+  for (int64_t s = (int64_t)rank * kPlThreads + tid; s < a.n_seqs; s += (int64_t)ranks * kPlThreads) {
+    const PlanSeq q = plan_seq(a, (int32_t)s);
+    a.held_out[s] = !ok || !q.ok ? a.held[s] : q.held - q.back + q.take;
+  }
+  if (rank == 0 && tid == 0) *a.n_free_out = ok ? (int32_t)(height - all.take) : (int32_t)free0;
+
+  // a run of rows per warp, 32 at a time; `base`: a sequence no later than theirs
+  const int64_t rows = ok ? all.rows : 0;
+  const int64_t warps = (int64_t)ranks * kPlWarps;
+  const int64_t per = (((int64_t)a.max_rows + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t r0 = ((int64_t)rank * kPlWarps + warp) * per, r1 = min((int64_t)a.max_rows, r0 + per);
+  int32_t base = 0;
+  if (r0 < rows) {  // the last sequence that starts at or before r0
+    int32_t hi = a.n_seqs;
+    while (hi - base > 1) {
+      const int32_t step = (hi - base + 31) / 32, probe = base + lane * step;
+      const uint32_t hit = __ballot_sync(0xffffffffu, probe < hi && __ldcg(a.row_start + probe) <= r0);
+      base += (31 - __clz((int)hit)) * step;
+      hi = min(hi, base + step);
+    }
+  }
+  for (int64_t i0 = r0; i0 < r1; i0 += 32) {
+    const int64_t r = i0 + lane;
+    int32_t seq = -1;
+    bool open = r < rows;
+    while (__any_sync(0xffffffffu, open)) {
+      const int64_t end = __ldcg(a.row_start + min(base + 1 + lane, a.n_seqs));
+      const int n = lanes_upto(end, r);
+      if (open && n < 32) {
+        seq = base + n;
+        open = false;
+      }
+      if (__any_sync(0xffffffffu, open)) base += 32;
+    }
+    if (i0 < rows) base = max(base, __reduce_max_sync(0xffffffffu, seq));
+    if (r >= r1) continue;
+    int32_t slot = -1, t = 0;
+    if (seq >= 0) {
+      t = a.ctx_len[seq] + (int32_t)(r - __ldcg(a.row_start + seq));
+      const int32_t pg = fast_div(a.page, t), page = __ldcg(a.table + (int64_t)seq * a.table_cols + pg);
+      if (page >= 0 && page < a.pool_pages) slot = page * a.page.d + (t - pg * a.page.d);
+      else report_error(a.status, kErrTokenRange, seq);
+    }
+    a.slot[r] = slot;
+    if (a.pos) a.pos[r] = t;
+    if (a.row_seq) a.row_seq[r] = seq;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t stream) {
+  const unsigned ctas = a.n_seqs > 256 || a.max_rows > 8192 ? kPlCtas : 1;
+  return launch_dependent(page_plan_kernel, dim3(ctas), dim3(kPlThreads), 0, stream, ctas, a);
+}
+
+}  // namespace qsa
