@@ -35,16 +35,18 @@ namespace qsa {
 namespace {
 
 constexpr int kC8Soft = 8, kC8Prod = 4, kC8MmaS = kC8Soft + kC8Prod, kC8MmaO = kC8MmaS + 1;
-constexpr int kC8Warps = 16, kC8Threads = 32 * kC8Warps;  // (the last two only make up a warpgroup)
-constexpr int kC8SoftRegs = 160, kC8OtherRegs = 96;  // of 128 a thread at the launch
-static_assert(2 * kC8SoftRegs + 2 * kC8OtherRegs <= 4 * 128, "registers of the launch's four warpgroups");
+constexpr int kC8Scale = kC8MmaO + 1;  // brings the scales
+constexpr int kC8Plan = kC8Scale + 1;  // walks the CTA's share
+constexpr int kC8Warps = kC8Plan + 1, kC8Threads = 32 * kC8Warps;
+constexpr int kC8Readers = kC8Plan;    // warps that take the walk's parts
+constexpr int kC8Segs = 4;             // parts it is ahead by
 constexpr int kC8T = 128;        // tokens of a tile: the MMAs' M
 constexpr int kC8MostRows = 64;  // rows of a unit at most
 constexpr int kC8MaxCtas = 160;
 constexpr int kC8Start = 4;      // what beginning a unit costs, in tiles
 constexpr float kC8Unset = -1e30f;    // a row's reference before it has seen a token
 constexpr float kC8Nobody = 1e30f;    // ... of a column without a row: its weights are 0
-constexpr float kC8Head = 5.f;        // log2 of a largest w when the reference is set
+constexpr float kC8Head = 4.f;        // log2 of a largest w when the reference is set
 constexpr float kC8Least = 0x1p-92f;  // a V scale below counts as this for the reference
 constexpr long long kC8SpinLimit = 4000000000LL;
 
@@ -52,42 +54,38 @@ template <int HD, int R>
 struct C8Geom {
   static constexpr int kN = 2 * R;               // columns: hi terms, lo terms
   static constexpr int kHalves = HD / 128;
+  // Up to 32 rows the softmax groups take tiles in turn, each with a sum, references and an
+  // O of its own, joined at the part's end; of 64 each takes half of every tile's rows.
+  static constexpr bool kTurns = R < 64;
+  static constexpr int kCols = kTurns ? R : R / 2;  // a group's rows of a tile
+  static constexpr int kOs = kTurns ? 2 : 1, kMix = kTurns ? 2 * R : 1;
   static constexpr uint32_t kQBox = kN * 128, kBox = kC8T * 128, kSlot = kC8T * HD;
   static constexpr int kSlots = HD == 256 ? 5 : 10;
   static constexpr int kS = R < 64 ? 4 : HD == 256 ? 2 : 3;  // S buffers
+  // Registers of the softmax's threads and of the others, of 128 a thread at the launch: 32
+  // rows a thread do not fit those, and every spilled value would queue behind the copies.
+  static constexpr int kSoftRegs = kCols < 32 ? 128 : 168, kOtherRegs = 256 - kSoftRegs;
+  static constexpr int kScales = 4;  // tiles whose scales are held
   static constexpr uint32_t kQBytes = (kHalves * kQBox + 1023) / 1024 * 1024;
   static constexpr uint32_t kPOff = kQBytes, kRingOff = kPOff + 2 * kBox, kCtrlOff = kRingOff + kSlots * kSlot;
-  static constexpr uint32_t kSCol = kHalves * kN;  // TMEM: O of each half, then S
+  static constexpr uint32_t kOCols = kHalves * kN, kSCol = kOs * kOCols;  // TMEM: O's halves, then S
   static_assert(kSCol + kS * kN <= 512, "TMEM has 512 columns");
   // kind::f8f6f4, D f32, A and B e4m3, M = 128, N = kN; O: A and B MN-major
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kN >> 3) << 17) | ((128u >> 4) << 24);
   static constexpr uint32_t kIdescO = kIdescS | (1u << 15) | (1u << 16);
 };
 
-struct C8Ctrl {
-  float factor[kC8MostRows];  // log2 units a unit of S and ks
-  float less_ref[kC8MostRows];  // the reference, negated
-  float alpha[kC8MostRows], inv[kC8MostRows];
-  int32_t depth[kC8MostRows];
-  float red[kC8Soft][kC8MostRows / 2];
-  uint64_t full[10], empty[10];
-  uint64_t s_full[4], s_free[4], p_ready[2], pv_done[4];
-  uint64_t q_full, o_free, drain[2];
-  int32_t bad[2], abort;
-  uint32_t tmem_base;
-};
-union C8Scratch {  // the plan is made before anything else
-  C8Ctrl c;
-  ShareScratch share;
-};
-template <int HD, int R>
-constexpr size_t c8_smem() { return C8Geom<HD, R>::kCtrlOff + sizeof(C8Ctrl) + 16; }
-static_assert(c8_smem<256, 64>() <= 232448 && c8_smem<128, 64>() <= 232448, "227 KiB per CTA");
-
 struct C8Seq {
   SeqView v;
   int32_t tiles, m_tiles;  // in every unit's list; units of rows, a team's together
   int64_t count;           // tiles of all its units, their starts included
+};
+
+// How the launch shares its work out.
+struct C8Plan {
+  FastDiv group_div;
+  int32_t team_log;  // log2 of the CTAs that take units of rows side by side
+  int32_t span;      // rows of a sequence that a unit holds of, at most
 };
 
 // Tiles that hold the first tokens (all of them where there is no window).
@@ -97,59 +95,66 @@ __device__ __forceinline__ int32_t first_tiles(const Cache8Args &a, const SeqVie
 
 // The units' lists have one length: that of the longest where a window cuts them.
 template <int R>
-__device__ __forceinline__ C8Seq c8_seq(const Cache8Args &a, int team_log, const SeqRaw &raw) {
+__device__ __forceinline__ C8Seq c8_seq(const Cache8Args &a, const C8Plan &p, const SeqRaw &raw) {
+  constexpr int kLog = R == 8 ? 3 : R == 16 ? 4 : R == 32 ? 5 : 6;
+  static_assert(1 << kLog == R, "rows of a unit");
   C8Seq q;
   q.v = view_seq(a.seqs, raw);
   q.tiles = q.v.rows > 0 ? (q.v.ctx + q.v.rows + kC8T - 1) / kC8T : 0;
   if (a.window > 0 && q.tiles > 0) {
-    const int64_t span = (int64_t)a.window + (a.seqs.mask ? q.v.rows : R / a.group + 2);
+    const int64_t span = (int64_t)a.window + (a.seqs.mask ? q.v.rows : p.span);
     q.tiles = (int32_t)min((int64_t)q.tiles, first_tiles(a, q.v) + (span + kC8T - 1) / kC8T + 1);
   }
-  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + ((int64_t)R << team_log) - 1) / ((int64_t)R << team_log));
+  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + (R << p.team_log) - 1) >> (kLog + p.team_log));
   q.count = q.tiles > 0 ? (int64_t)(q.tiles + kC8Start) * q.m_tiles * a.nkv : 0;
   return q;
 }
 
 // One CTA's part of one unit.
 struct C8Seg {
-  int32_t s, kvh, mt;   // sequence, KV head, this CTA's unit of R rows
-  int32_t n;            // tiles to process
-  int32_t first, gap;   // tile i of the part is token tile first + i, gap more from `near` on
-  int32_t near;
-  int32_t back;         // no row sees the tokens from n_first to before `back`
-  bool whole, head;     // the unit's every tile; the unit began in an earlier CTA
-  bool empty;           // none of its tiles (a share that ends in a unit's start), or no rows
-  SeqView v;
+  int32_t s, kvh, m0;         // sequence, KV head, this CTA's unit's first row
+  int32_t n;                  // tiles to process
+  int32_t first, gap, near;   // tile i of the part is token tile first + i, gap more from `near` on
+  int32_t back;               // no row sees the tokens from n_first to before `back`
+  int32_t row0, rows, ctx;    // the sequence's
+  int32_t flags;
+  enum : int32_t {
+    kWhole = 1,  // the unit's every tile
+    kHead = 2,   // the unit began in an earlier CTA
+    kEmpty = 4,  // none of its tiles (a share that ends in a unit's start), or no rows
+    kEnd = 8     // no part: the walk is over
+  };
   __device__ int32_t tile(int i) const { return first + i + (i >= near ? gap : 0); }
-  // whether token t of tile i < n is there and may be seen by a row (others are not read)
-  __device__ bool wants(const Cache8Args &a, int32_t t) const { return t < v.ctx + v.rows && (t < a.n_first || t >= back); }
+  // whether token t may be seen by a row (others are not read)
+  __device__ bool wants(const Cache8Args &a, int32_t t) const { return t < ctx + rows && (t < a.n_first || t >= back); }
 };
 
-// Walks a team's share of the list, unit by unit (each role its own walk), the
-// sequences' lengths read one sequence ahead.
+// Walks a team's share of the list, unit by unit, the sequences' lengths read one ahead.
 template <int R>
 struct C8Walk {
   const Cache8Args &a;
+  const C8Plan &p;
   int64_t left, off;
   int32_t s;
-  int team_log;
   C8Seq q;
   SeqRaw ahead;
-  __device__ C8Walk(const Cache8Args &a_, int team_log_, int32_t s_, int64_t off_, int64_t left_)
-      : a(a_), left(left_), off(off_), s(s_), team_log(team_log_) {
+  __device__ C8Walk(const Cache8Args &a_, const C8Plan &p_, int32_t s_, int64_t off_, int64_t left_)
+      : a(a_), p(p_), left(left_), off(off_), s(s_) {
     if (left <= 0) return;
-    q = c8_seq<R>(a, team_log, read_seq(a.seqs, s));
+    q = c8_seq<R>(a, p, read_seq(a.seqs, s));
     ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
   }
-  __device__ bool next(C8Seg &g) {
-    if (left <= 0) return false;
+  __device__ C8Seg next() {
+    C8Seg g = {};
+    g.flags = C8Seg::kEnd;
+    if (left <= 0) return g;
     while (off >= q.count) {
       off -= q.count;
       if (++s >= a.seqs.n_seqs) {
         left = 0;
-        return false;
+        return g;
       }
-      q = c8_seq<R>(a, team_log, ahead);
+      q = c8_seq<R>(a, p, ahead);
       ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
     }
     const int32_t length = q.tiles + kC8Start;
@@ -163,35 +168,67 @@ struct C8Walk {
     const int32_t i0 = max(0, from - kC8Start), take = max(0, from + part - kC8Start) - i0;
     g.s = s;
     g.kvh = unit / q.m_tiles;
-    g.mt = ((unit - g.kvh * q.m_tiles) << team_log) + (int32_t)(blockIdx.x & ((1u << team_log) - 1u));
-    g.v = q.v;
-    g.whole = take == q.tiles;
-    g.head = i0 > 0;
-    const int64_t m0 = (int64_t)g.mt * R, m_all = (int64_t)q.v.rows * a.group;
-    g.empty = take == 0 || m0 >= m_all;
-    g.n = 0;
-    if (g.empty) return true;
+    const int32_t mt = ((unit - g.kvh * q.m_tiles) << p.team_log) + (int32_t)(blockIdx.x & ((1u << p.team_log) - 1u));
+    g.row0 = q.v.row0;
+    g.rows = q.v.rows;
+    g.ctx = q.v.ctx;
+    g.first = i0;
+    const int64_t m0 = (int64_t)mt * R, m_all = (int64_t)q.v.rows * a.group;
+    g.flags = (take == q.tiles ? C8Seg::kWhole : 0) | (i0 > 0 ? C8Seg::kHead : 0);
+    if (take == 0 || m0 >= m_all) {
+      g.flags |= C8Seg::kEmpty;
+      return g;
+    }
     // the token tiles that this unit's rows see any of: those of the first tokens, and from
     // `back` (its first row's oldest) to `end` (its last row's newest)
+    g.m0 = (int32_t)m0;
     const bool chain = a.seqs.mask == nullptr;
-    const int32_t j0 = (int32_t)(m0 / a.group), j1 = (int32_t)((min(m0 + R, m_all) - 1) / a.group);
+    const int32_t j0 = fast_div(p.group_div, (int32_t)m0), j1 = fast_div(p.group_div, (int32_t)(min(m0 + R, m_all) - 1));
     const int32_t end = (q.v.ctx + (chain ? j1 + 1 : q.v.rows) + kC8T - 1) / kC8T;
-    g.near = g.gap = g.back = 0;
     if (a.window > 0) {
       g.near = min(end, first_tiles(a, q.v));
       g.back = max(0, q.v.ctx + (chain ? j0 : 0) - (a.window - 1));
       g.gap = max(0, min(g.back / kC8T, end) - g.near);
     }
     g.n = max(0, min(take, end - g.gap - i0));
-    g.first = i0;
     g.near = max(0, g.near - i0);
-    return true;
+    return g;
   }
 };
+
+template <int kScales, int kMix>
+struct C8Ctrl {
+  float factor[kC8MostRows];    // log2 units a unit of S and ks
+  float less_ref[kC8MostRows];  // [group][its rows]: the reference, negated
+  float alpha[kC8MostRows];     // [group][its rows]: what a move multiplies by
+  float mix[kMix], inv[kC8MostRows];  // ... and, at a part's end, the groups' join, and 1 / sum
+  int64_t where[kC8MostRows];   // a row's place in the output
+  int32_t depth[kC8MostRows];
+  C8Seg segs[kC8Segs];
+  float scales[kScales][2][8];  // [tile % kScales][K, V][16 tokens]
+  uint64_t full[10], empty[10], scaled[kScales];
+  uint64_t s_full[4], s_free[4], p_ready[2], pv_done[4];
+  uint64_t q_full, o_free, drain[2], seg_full[kC8Segs], seg_free[kC8Segs];
+  int32_t bad[2], abort;
+  uint32_t tmem_base;
+};
+template <int kScales, int kMix>
+union C8Scratch {  // the plan is made before anything else
+  C8Ctrl<kScales, kMix> c;
+  ShareScratch share;
+};
+template <int HD, int R>
+constexpr size_t c8_smem() { return C8Geom<HD, R>::kCtrlOff + sizeof(C8Scratch<C8Geom<HD, R>::kScales, C8Geom<HD, R>::kMix>); }
+static_assert(c8_smem<256, 64>() <= 232448 && c8_smem<128, 64>() <= 232448, "227 KiB per CTA");
 
 // Ring position of tile j's V among a part's n tiles, counted from the part's first copy:
 // K0, K1, V0, K2, V1, ..., V(n-1), about the order the MMAs take them in.
 __device__ __forceinline__ int c8_v_pos(int j, int n) { return j + 1 < n ? 2 + 2 * j : 2 * n - 1; }
+
+// 4 bytes from global to shared memory, asynchronously; bytes 0: zeros.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void mma_e4m3(uint32_t dtmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -232,12 +269,21 @@ __device__ __forceinline__ void tmem_ready(uint32_t *v) {
   for (int i = 4; i < K; i += 4) asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3])::"memory");
 }
 
-__device__ __forceinline__ void tmem_scale1(uint32_t taddr, float by) {
-  uint32_t x;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x)::"memory");
-  x = __float_as_uint(__uint_as_float(x) * by);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(x) : "memory");
+// A column of O's halves (`half` columns apart) and its lo term (`lo` columns on), times `by`.
+template <int kHalves>
+__device__ __forceinline__ void tmem_scale(uint32_t taddr, uint32_t half, uint32_t lo, float by) {
+  uint32_t x[2 * kHalves];
+#pragma unroll
+  for (int i = 0; i < 2 * kHalves; ++i)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x[i]) : "r"(taddr + (i >> 1) * half + (i & 1) * lo));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 2 * kHalves; ++i) {
+    asm volatile("" : "+r"(x[i])::"memory");
+    x[i] = __float_as_uint(__uint_as_float(x[i]) * by);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr + (i >> 1) * half + (i & 1) * lo), "r"(x[i])
+                 : "memory");
+  }
 }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -246,12 +292,24 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// A float's place in the order of signed integers, and back.
-__device__ __forceinline__ int32_t ordered(float x) {
-  const int32_t i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7FFFFFFF);
+// K values of each lane joined over the lanes: lane i gets the K-th of value i / (32 / K).
+// Half of the values change lanes in each step, so that all are joined at once.
+template <int K, typename Join>
+__device__ __forceinline__ float over_lanes(float (&x)[K], int lane, Join &&join) {
+  int o = 16;
+#pragma unroll
+  for (int half = K / 2; half > 0; half /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = upper ? x[i + half] : x[i], give = upper ? x[i] : x[i + half];
+      x[i] = join(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (int p = 16 / K; p > 0; p /= 2) x[0] = join(x[0], __shfl_xor_sync(0xffffffffu, x[0], p));
+  return x[0];
 }
-__device__ __forceinline__ float unordered(int32_t i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
 
 // Two values as e4m3 terms hi + lo / 16.  Through f16: its eleven bits hold hi's four and
 // the four that lo rounds to (2^-12 of the value is lost beside lo's 2^-9).
@@ -281,18 +339,31 @@ __device__ __forceinline__ bool any_of_group(int g, bool x) {  // over a softmax
       : "memory");
   return r != 0;
 }
+// ... over both groups
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, 3, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ void group_sync(int g) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + g) : "memory"); }
 
 __device__ __forceinline__ bool nan8(uint32_t byte) { return (byte & 0x7Fu) == 0x7Fu; }
 
 template <int HD, int R>
 __global__ void __launch_bounds__(kC8Threads, 1)
-cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, int64_t *__restrict__ base_out,
-                   float2 *__restrict__ part_ml, float *__restrict__ part_o, int32_t *__restrict__ row_seq) {
+cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml, float *__restrict__ part_o, int32_t *__restrict__ row_seq) {
   using G = C8Geom<HD, R>;
   extern __shared__ __align__(1024) uint8_t c8_shared[];
-  C8Scratch &both = *reinterpret_cast<C8Scratch *>(c8_shared + G::kCtrlOff);
-  C8Ctrl &C = both.c;
+  auto &both = *reinterpret_cast<C8Scratch<G::kScales, G::kMix> *>(c8_shared + G::kCtrlOff);
+  auto &C = both.c;
   const uint32_t sQ = sm32(c8_shared), sP = sm32(c8_shared + G::kPOff), sRing = sm32(c8_shared + G::kRingOff);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long lim = a.wait_limit > 0 ? a.wait_limit : kC8SpinLimit;
@@ -300,10 +371,10 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
 
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
   // ---- the plan (CTA 0 also leaves the sums for the joining launch)
-  const uint32_t teams = gridDim.x >> team_log, my_team = blockIdx.x >> team_log;
+  const uint32_t teams = gridDim.x >> plan.team_log, my_team = blockIdx.x >> plan.team_log;
   const FoundShare found = find_share(a.seqs.n_seqs, kC8Threads, teams, my_team, both.share, [&](int32_t s) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
-    return c8_seq<R>(a, team_log, read_seq(a.seqs, s)).count;
+    return c8_seq<R>(a, plan, read_seq(a.seqs, s)).count;
   });
   if (blockIdx.x == 0) {
     int64_t before = 0;
@@ -311,7 +382,7 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
       const int32_t s = s0 + lane;
       int64_t count = 0;
       if (s < a.seqs.n_seqs) {
-        const C8Seq q = c8_seq<R>(a, team_log, read_seq(a.seqs, s));
+        const C8Seq q = c8_seq<R>(a, plan, read_seq(a.seqs, s));
         if (!q.v.ok) report_error(a.status, kErrRowRange, s);
         count = q.count;
       }
@@ -327,15 +398,20 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
       mbar_init(sm32(&C.full[i]), 32 * kC8Prod);
       mbar_init(sm32(&C.empty[i]), 1);
     }
+    for (int i = 0; i < G::kScales; ++i) mbar_init(sm32(&C.scaled[i]), 32);
     for (int b = 0; b < 4; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
-      mbar_init(sm32(&C.s_free[b]), kC8Soft);
+      mbar_init(sm32(&C.s_free[b]), kC8Soft / G::kOs);
       mbar_init(sm32(&C.pv_done[b]), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(sm32(&C.p_ready[b]), kC8Soft);
+      mbar_init(sm32(&C.p_ready[b]), kC8Soft / G::kOs);
       mbar_init(sm32(&C.drain[b]), 1);
       C.bad[b] = 0;
+    }
+    for (int i = 0; i < kC8Segs; ++i) {
+      mbar_init(sm32(&C.seg_full[i]), 1);
+      mbar_init(sm32(&C.seg_free[i]), kC8Readers);
     }
     mbar_init(sm32(&C.q_full), kC8Soft);
     mbar_init(sm32(&C.o_free), kC8Soft);
@@ -352,77 +428,169 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
   tc_fence_after();
   const uint32_t tmem = C.tmem_base;
   const bool laid_out = (sQ & 1023u) == 0;  // the swizzle needs it; the declaration asks for it
-  if (warp < kC8Soft) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kC8SoftRegs));
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kC8OtherRegs));
-  C8Walk<R> walk(a, team_log, found.seq, found.off, laid_out ? found.share.n : 0);
-  C8Seg g;
+  // A warp's next part.  False where the wait for it gave up.
+  uint32_t segs_taken = 0;
+  auto take_seg = [&](C8Seg &g) -> bool {
+    const uint32_t i = segs_taken % kC8Segs;
+    const bool ok = tc_warp_wait_ready(sm32(&C.seg_full[i]), (segs_taken / kC8Segs) & 1u, lim, abort_flag);
+    __syncwarp();
+    if (ok) g = C.segs[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm32(&C.seg_free[i]));
+    ++segs_taken;
+    return ok;
+  };
 
   if (warp >= kC8Soft && warp < kC8MmaS) {
+    if constexpr (G::kOtherRegs < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+    C8Seg g;
     // ---- producers: warp p brings 32 of a tile's tokens, 512 bytes an instruction (kRows
-    // rows); lane i looks up the pool row of its token.  A slot's barrier takes each
-    // thread's arrival when its copies have landed, so the whole ring may be in flight.
-    constexpr int kCh = HD / 16, kRows = 32 / kCh, kN = 32 / kRows;
+    // rows).  A block's tokens, and so 16 of a tile's from a multiple of 16 on, lie in one
+    // page: two look-ups a tile, read two tiles ahead (under load a read takes several
+    // thousand cycles).  A slot's barrier takes each thread's arrival when its copies have
+    // landed, so the whole ring may be in flight.
+    constexpr int kCh = HD / 16, kRows = 32 / kCh, kN = 16 / kRows;  // chunks of a row, copies of 16 tokens
     const int p0 = (warp - kC8Soft) * 32, ch = lane % kCh, hl = lane / kCh;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * G::kBox + (uint32_t)(p0 + hl) * 128u;
+    const int64_t pitch = (int64_t)a.nkv * HD;
     uint32_t ns = 0;
     bool ok = true;
-    while (ok && walk.next(g)) {
-      auto fetch = [&](int j) -> int32_t {  // pool row of this lane's token of tile j, -1: zeros
-        if (j >= g.n) return -1;
-        const int32_t t = g.tile(j) * kC8T + p0 + lane;
-        if (!g.wants(a, t)) return -1;
-        const int64_t slot = token_slot(a.seqs, g.s, t);
-        if (slot < 0) report_error(a.status, kErrTokenRange, g.s);
-        return slot < 0 ? -1 : (int32_t)(slot * a.nkv + g.kvh);
+    while (ok && take_seg(g) && !(g.flags & C8Seg::kEnd)) {
+      const int32_t kv = g.ctx + g.rows;
+      const int64_t mine = (int64_t)g.kvh * HD + ch * 16 + hl * pitch;
+      struct Pages {
+        int32_t t0, page[2], at[2];  // of tile j: its first token here, its pages, the first token's place in them
       };
-      // Pool rows of this thread's copies of a slot, spread from the lanes that looked them
-      // up before the slot is waited for.
-      auto spread = [&](int32_t y, int32_t (&r)[kN]) {
+      auto fetch = [&](int j) -> Pages {
+        Pages y = {kv, {0, 0}, {0, 0}};
+        if (j >= g.n) return y;
+        y.t0 = g.tile(j) * kC8T + p0;
 #pragma unroll
-        for (int k = 0; k < kN; ++k) r[k] = __shfl_sync(0xffffffffu, y, kRows * k + hl);
+        for (int i = 0; i < 2; ++i) {
+          const int32_t t = y.t0 + 16 * i, pg = fast_div(a.seqs.page, t);
+          y.at[i] = t - pg * a.seqs.page.d;
+          if (t < kv) y.page[i] = a.seqs.table[(int64_t)g.s * a.seqs.table_cols + pg];
+        }
+        return y;
       };
-      auto bring = [&](const uint8_t *pool, const int32_t (&r)[kN]) {
+      auto bring = [&](const uint8_t *pool, const Pages &y) {
         const uint32_t slot = ns % G::kSlots;
         if (!tc_warp_wait_ready(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
           ok = false;
           return;
         }
         __syncwarp();
-        const uint8_t *src = pool + ch * 16;
 #pragma unroll
-        for (int k = 0; k < kN; ++k)  // row p0 + kRows k + hl, its 16-byte chunks swizzled by row % 8
-          cp_async16(dst0 + slot * G::kSlot + (uint32_t)(k * kRows) * 128u + (uint32_t)(((ch & 7) ^ ((kRows * k + hl) & 7)) << 4),
-                     src + (int64_t)max(r[k], 0) * HD, r[k] >= 0 ? 16u : 0u);
+        for (int i = 0; i < 2; ++i) {
+          const bool there = (uint32_t)y.page[i] < (uint32_t)a.seqs.pool_pages;
+          const uint8_t *src = pool + (int64_t)(there ? y.page[i] * a.seqs.page.d + y.at[i] : 0) * pitch + mine;
+          const uint32_t dst = dst0 + slot * G::kSlot + (uint32_t)i * 16u * 128u;
+          const int32_t t = y.t0 + 16 * i;
+          // row p0 + 16 i + kRows k + hl, its 16-byte chunks swizzled by row % 8
+          auto to = [&](int k) { return dst + (uint32_t)(k * kRows) * 128u + (uint32_t)(((ch & 7) ^ ((kRows * k + hl) & 7)) << 4); };
+          if (there && t + 16 <= kv && (t + 16 <= a.n_first || t >= g.back)) {  // all of them
+#pragma unroll
+            for (int k = 0; k < kN; ++k) cp_async16(to(k), src + k * kRows * pitch, 16u);
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < kN; ++k) {
+              const bool read = there && g.wants(a, t + kRows * k + hl);
+              cp_async16(to(k), read ? src + k * kRows * pitch : pool, read ? 16u : 0u);
+            }
+          }
+        }
         cp_async_arrive(sm32(&C.full[slot]));
         ++ns;
       };
       if (g.n > 0) {
-        int32_t rv[kN], rk[kN];
-        int32_t y = fetch(0);
-        spread(y, rv);
-        y = fetch(1);
-        bring(a.k_pool, rv);
+        Pages yv = fetch(0), yk = fetch(1);
+        bring(a.k_pool, yv);
         for (int j = 0; j < g.n && ok; ++j) {
-          spread(y, rk);
-          y = fetch(j + 2);
-          if (j + 1 < g.n) bring(a.k_pool, rk);
-          if (ok) bring(a.v_pool, rv);
-#pragma unroll
-          for (int k = 0; k < kN; ++k) rv[k] = rk[k];
+          const Pages later = fetch(j + 2);
+          if (j + 1 < g.n) bring(a.k_pool, yk);
+          if (ok) bring(a.v_pool, yv);
+          yv = yk;
+          yk = later;
         }
       }
-      if (warp == kC8Soft && !g.whole && !g.empty) {  // the rows of a part, for the join
-        const int64_t m0 = (int64_t)g.mt * R, m1 = min(m0 + R, (int64_t)g.v.rows * a.group);
-        const int32_t end = fast_div(group_div, (int32_t)m1 - 1);
-        for (int32_t j = fast_div(group_div, (int32_t)m0) + lane; j <= end; j += 32) row_seq[g.v.row0 + j] = g.s;
+      if (warp == kC8Soft && !(g.flags & (C8Seg::kWhole | C8Seg::kEmpty))) {  // the rows of a part, for the join
+        const int32_t end = fast_div(plan.group_div, min(g.m0 + R, g.rows * a.group) - 1);
+        for (int32_t j = fast_div(plan.group_div, g.m0) + lane; j <= end; j += 32) row_seq[g.row0 + j] = g.s;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
-  } else if (warp > kC8MmaO) {
-    // nothing to do
   } else if (warp >= kC8MmaS) {
+    if constexpr (G::kOtherRegs < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+    if (warp == kC8Plan) {
+      // ---- the walk
+      C8Walk<R> walk(a, plan, found.seq, found.off, laid_out ? found.share.n : 0);
+      for (uint32_t k = 0;; ++k) {
+        const C8Seg g = walk.next();
+        if (k >= kC8Segs && !tc_warp_wait_ready(sm32(&C.seg_free[k % kC8Segs]), ((k / kC8Segs) & 1u) ^ 1u, lim, abort_flag)) break;
+        __syncwarp();
+        if (lane == 0) {
+          C.segs[k % kC8Segs] = g;
+          mbar_arrive(sm32(&C.seg_full[k % kC8Segs]));
+        }
+        if (g.flags & C8Seg::kEnd) break;
+      }
+    } else if (warp == kC8Scale) {
+      // ---- the scales: lane i < 8 brings the K scale of a tile's tokens 16 i to 16 i + 15,
+      // lane i + 8 their V scale, once the tile four before it is weighed: P V of it is done.
+      uint32_t jg = 0;
+      bool ok = true;
+      C8Seg g;
+      while (ok && take_seg(g) && !(g.flags & C8Seg::kEnd)) {
+        const int32_t kv = g.ctx + g.rows;
+        const float *scales = lane < 8 ? a.k_scale : a.v_scale;
+        auto fetch = [&](int j, int32_t &at) -> int32_t {  // the page of a token that is read, its place there (-1: none)
+          at = -1;
+          if (j >= g.n || lane >= 16) return -1;
+          int32_t t = g.tile(j) * kC8T + 16 * (lane & 7);
+          if (!g.wants(a, t)) {
+            if (t >= kv || t + 16 <= g.back || g.back >= kv) return -1;
+            t = g.back;  // the first of them that is
+          }
+          const int32_t pg = fast_div(a.seqs.page, t);
+          at = t - pg * a.seqs.page.d;
+          return a.seqs.table[(int64_t)g.s * a.seqs.table_cols + pg];
+        };
+        int32_t at = 0, at1 = 0, at2 = 0;
+        int32_t page = fetch(0, at), page1 = fetch(1, at1);
+        for (int j = 0; j < g.n; ++j, ++jg) {
+          const int32_t page2 = fetch(j + 2, at2);
+          if (jg >= 4 && !tc_warp_wait_ready(sm32(&C.pv_done[jg & 3u]), ((jg >> 2) & 1u) ^ 1u, lim, abort_flag)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          if (lane < 16) {
+            const bool there = (uint32_t)page < (uint32_t)a.seqs.pool_pages;
+            if (!there && at >= 0) report_error(a.status, kErrTokenRange, g.s);
+            const int64_t block = there ? (int64_t)((page * a.seqs.page.d + at) >> a.unit_log) * a.nkv + g.kvh : 0;
+            cp_async4(sm32(&C.scales[jg % G::kScales][lane >> 3][lane & 7]), scales + block, there ? 4u : 0u);
+          }
+          cp_async_arrive(sm32(&C.scaled[jg % G::kScales]));
+          page = page1;
+          at = at1;
+          page1 = page2;
+          at1 = at2;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
     // ---- MMA issuers, one thread each
-    if (lane == 0) {
+    if (lane == 0 && warp <= kC8MmaO) {
+      C8Seg g;
+      auto take_one = [&]() -> bool {
+        const uint32_t i = segs_taken % kC8Segs;
+        if (!tc_wait_ready(sm32(&C.seg_full[i]), (segs_taken / kC8Segs) & 1u, lim, abort_flag)) return false;
+        g.n = C.segs[i].n;
+        g.flags = C.segs[i].flags;
+        mbar_arrive(sm32(&C.seg_free[i]));
+        ++segs_taken;
+        return !(g.flags & C8Seg::kEnd);
+      };
       bool ok = true;
       auto wait = [&](uint64_t &bar, uint32_t parity) {
         ok = ok && tc_wait_ready(sm32(&bar), parity, lim, abort_flag);
@@ -454,7 +622,7 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
       if (warp == kC8MmaS) {
         const uint32_t q_lo = (uint32_t)sw128_desc(sQ), r_lo = (uint32_t)sw128_desc(sRing);
         uint32_t b = 0, b_phase = 1;  // S buffer, parity of its s_free phase before this use
-        while (ok && walk.next(g)) {
+        while (ok && take_one()) {
           if (g.n == 0) continue;
           if (!wait(C.q_full, part & 1u)) break;
           ++part;
@@ -481,7 +649,7 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
         }
       } else {
         const uint32_t r_lo = (uint32_t)sw128_mn_desc(sRing, 0), p_lo = (uint32_t)sw128_mn_desc(sP, 0);
-        while (ok && walk.next(g)) {
+        while (ok && take_one()) {
           if (g.n == 0) continue;
           if (part > 0 && !wait(C.o_free, (part - 1) & 1u)) break;  // the part before has left O
           ++part;
@@ -489,13 +657,14 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
             if (!wait(C.p_ready[jg & 1u], (jg >> 1) & 1u)) break;
             step(j + 1 < g.n ? 2u : 1u);
             if (!landed()) break;
+            const uint32_t o = tmem + (G::kTurns ? (jg & 1u) * G::kOCols : 0u);
             const uint32_t p = p_lo + (jg & 1u) * (G::kBox >> 4), v_lo = r_lo + slot * (G::kSlot >> 4);
 #pragma unroll
             for (int h = 0; h < G::kHalves; ++h)
 #pragma unroll
               for (int kk = 0; kk < kC8T / 32; ++kk)  // 32 tokens a step: 4 KiB of V's and of P's rows
-                mma_e4m3(tmem + (uint32_t)h * G::kN, desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi),
-                         desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+                mma_e4m3(o + (uint32_t)h * G::kN, desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi),
+                         desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
             mma_commit(sm32(&C.empty[slot]));
             mma_commit(sm32(&C.pv_done[jg & 3u]));
           }
@@ -508,26 +677,43 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
     }
     __syncwarp();
   } else {
-    // ---- softmax: group w has rows [w R/2, w R/2 + R/2) of every tile, thread tk the
-    // tile's token tk (TMEM lane) and, at the end, dims tk and tk + 128.  After an abort
+    if constexpr (G::kSoftRegs > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftRegs));
+    // ---- softmax: thread tk has the tile's token tk (TMEM lane) and, at the end, dims tk
+    // and tk + 128.  Group w takes every other tile, or its rows of each.  After an abort
     // every wait returns at once, and the loops and barriers run on to the end.
-    constexpr int kHalf = R / 2, kAtOnce = kHalf < 16 ? kHalf : 16;  // its rows, rows of a TMEM load
-    const int w = warp >> 2, wq = warp & 3, tk = wq * 32 + lane, n0 = w * kHalf;
+    constexpr int kCols = G::kCols, kAtOnce = kCols < 16 ? kCols : 16;  // rows of a TMEM load
+    const int w = warp >> 2, wq = warp & 3, tk = wq * 32 + lane;
+    const int n0 = G::kTurns ? 0 : w * kCols;  // this group's first row
+    float *const less_ref = C.less_ref + w * kCols, *const alpha = C.alpha + w * kCols;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t my_o = lane_base + (G::kTurns ? w * G::kOCols : (uint32_t)n0);
+    // P V of tile i.  A warp has waited for tile i - 4 (or a later one) by then, so of a
+    // barrier no phase but the last two is ever in question.
     auto wait_pv = [&](uint32_t i) { tc_warp_wait_ready(sm32(&C.pv_done[i & 3u]), (i >> 2) & 1u, lim, abort_flag); };
     // This warp's rows of a part's Q, split into two e4m3 terms, with what goes with a row.
     auto load_q = [&](const C8Seg &e) {
-      const int64_t m0 = (int64_t)e.mt * R, m_all = (int64_t)e.v.rows * a.group;
+      const int32_t m_all = e.rows * a.group;
       constexpr int kLanes = HD / 8, kPer = 32 / kLanes;  // lanes a row, rows a warp takes at once
+      constexpr int kTimes = (R + kC8Soft * kPer - 1) / (kC8Soft * kPer), kBatch = kTimes < 4 ? kTimes : 4;
       const int ch = lane % kLanes, sub = lane / kLanes;
+      auto row_of = [&](int i) { return (i * kC8Soft + warp) * kPer + sub; };
 #pragma unroll 1
-      for (int i = wq * kPer; i < kHalf; i += 4 * kPer) {
-        const int n = n0 + i + sub;
-        const bool mine = i + sub < kHalf, valid = mine && m0 + n < m_all;
-        const int32_t m = valid ? (int32_t)(m0 + n) : 0, j = fast_div(group_div, m);
+      for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int n = row_of(i0 + i);
+        const bool valid = n < R && e.m0 + n < m_all;
+        const int32_t m = valid ? e.m0 + n : 0, j = fast_div(plan.group_div, m);
         const int32_t head = e.kvh * a.group + (m - j * a.group);
+        raw[i] = valid ? ldg_v4(a.q + (int64_t)(e.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int n = row_of(i0 + i);
+        const bool mine = n < R, valid = mine && e.m0 + n < m_all;
         float x[8], amax = 0.f;
-        unpack8(valid ? ldg_v4(a.q + (int64_t)(e.v.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch) : make_uint4(0, 0, 0, 0), x);
+        unpack8(raw[i], x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
 #pragma unroll
@@ -549,104 +735,115 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
           *reinterpret_cast<uint2 *>(at(R + n)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
         int32_t depth = 0;
-        if (a.window > 0 && a.seqs.mask != nullptr && valid) {  // the row's drafted tokens, over its lanes
-          const uint32_t *mrow = a.seqs.mask + (int64_t)(e.v.row0 + j) * a.seqs.mask_words;
-          for (int32_t k = ch; 32 * k < e.v.rows; k += kLanes) {
-            const int32_t over = e.v.rows - 32 * k;
-            depth += __popc(over >= 32 ? mrow[k] : mrow[k] & ((1u << over) - 1u));
+        if (a.window > 0 && a.seqs.mask != nullptr) {  // the row's drafted tokens, over its lanes
+          if (valid) {
+            const int32_t j = fast_div(plan.group_div, e.m0 + n);
+            const uint32_t *mrow = a.seqs.mask + (int64_t)(e.row0 + j) * a.seqs.mask_words;
+            for (int32_t k = ch; 32 * k < e.rows; k += kLanes) {
+              const int32_t over = e.rows - 32 * k;
+              depth += __popc(over >= 32 ? mrow[k] : mrow[k] & ((1u << over) - 1u));
+            }
           }
-        }
-        if (a.window > 0 && a.seqs.mask != nullptr) {
 #pragma unroll
           for (int o = kLanes / 2; o; o >>= 1) depth += __shfl_xor_sync(0xffffffffu, depth, o);
         }
         if (mine && ch == 0) {
           C.factor[n] = a.scale_log2 * s;
-          C.less_ref[n] = valid ? -kC8Unset : -kC8Nobody;
           C.depth[n] = max(0, depth - 1);
+#pragma unroll
+          for (int o = 0; o < G::kOs; ++o) C.less_ref[o * kCols + n] = valid ? -kC8Unset : -kC8Nobody;
         }
+      }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(sm32(&C.q_full));
     };
-    uint32_t jg = 0, ns = 0;
+    uint32_t jg = 0, ns = 0, loaded = 0;  // tiles, copies and parts with tiles before this one
     int32_t seg = 0;
-    bool more = walk.next(g);
+    // the next part, unless a wait of one of the softmax's warps gave up
+    C8Seg g;
+    auto advance = [&](C8Seg &to) -> bool {
+      const bool ok = take_seg(to);
+      return !soft_any(!ok) && !(to.flags & C8Seg::kEnd);
+    };
+    bool more = advance(g);
     if (more && g.n > 0) load_q(g);
     while (more) {
       ++seg;
-      const int64_t m0 = (int64_t)g.mt * R, m_all = (int64_t)g.v.rows * a.group;
-      const int32_t kv = g.v.ctx + g.v.rows;
-      const bool chain = a.seqs.mask == nullptr;
+      const int32_t m0 = g.m0, m_all = g.rows * a.group, kv = g.ctx + g.rows;
+      const bool chain = a.seqs.mask == nullptr, empty = (g.flags & C8Seg::kEmpty) != 0;
       // whether a row may be blind to a token that another one sees, or that is read beside its own
-      const bool veiled = g.v.rows > 1 || !chain || a.window > 0;
-      const int32_t j0 = g.empty ? 0 : fast_div(group_div, (int32_t)m0);
-      const int32_t j1 = g.empty ? 0 : fast_div(group_div, (int32_t)(min(m0 + R, m_all) - 1));
+      const bool veiled = g.rows > 1 || !chain || a.window > 0;
+      const int32_t j0 = fast_div(plan.group_div, m0), j1 = fast_div(plan.group_div, max(0, min(m0 + R, m_all) - 1));
       // tokens below `clear` and, of a window, from `old` on or below n_first are seen by every row
-      const int32_t clear = chain ? g.v.ctx + j0 + 1 : g.v.ctx;
-      const int32_t old = a.window > 0 ? g.v.ctx + (chain ? j1 : g.v.rows - 1) - (a.window - 1) : 0;
+      const int32_t clear = chain ? g.ctx + j0 + 1 : g.ctx;
+      const int32_t old = a.window > 0 ? g.ctx + (chain ? j1 : g.rows - 1) - (a.window - 1) : 0;
       auto is_masked = [&](int32_t t0) { return t0 + kC8T > clear || (t0 < old && t0 + kC8T > a.n_first); };
-      // whether row n sees token t
-      auto sees = [&](int n, int32_t t) -> bool {
-        if (m0 + n >= m_all || t >= kv) return false;
-        const int32_t j = fast_div(group_div, (int32_t)(m0 + n));
-        const bool drafted = t >= g.v.ctx;
-        if (!chain && drafted)
-          return sees_draft(a.seqs.mask + (int64_t)(g.v.row0 + j) * a.seqs.mask_words, j, t - g.v.ctx);
-        const int32_t at = g.v.ctx + (chain ? j : C.depth[n]);
-        return t <= at && (a.window == 0 || t < a.n_first || at - t < a.window);
+      // the columns of rows [from, to) of the sequence, among this group's
+      auto columns = [&](int32_t from, int32_t to) -> uint32_t {
+        const int lo = min(max(from * a.group - m0 - n0, 0), kCols), hi = min(max(to * a.group - m0 - n0, 0), kCols);
+        if (lo >= hi) return 0u;
+        return (hi >= 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
       };
-      // K and V scales of this thread's token: their block two tiles ahead, they one
-      auto block_of = [&](int j) -> int32_t {
-        if (j >= g.n) return -1;
-        const int32_t t = g.tile(j) * kC8T + tk;
-        if (!g.wants(a, t)) return -1;
-        const int64_t slot = token_slot(a.seqs, g.s, t);
-        return slot < 0 ? -1 : (int32_t)((slot >> a.unit_log) * a.nkv) + g.kvh;
-      };
-      float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
-      int32_t block = block_of(0);
-      if (block >= 0) {
-        ks_next = a.k_scale[block];
-        vs_next = a.v_scale[block];
-      }
-      block = block_of(1);
-      uint64_t sum2[kHalf / 2];
-#pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) sum2[i] = 0ull;
-      for (int j = 0; j < g.n; ++j, ++jg) {
-        ks = ks_next;
-        vs = vs_next;
-        ks_next = vs_next = 0.f;
-        if (block >= 0) {
-          ks_next = a.k_scale[block];
-          vs_next = a.v_scale[block];
+      // which of this group's rows see token t
+      auto sees = [&](int32_t t) -> uint32_t {
+        if (t >= kv) return 0u;
+        const int32_t k = t - g.ctx;
+        if (chain) {  // row j: k <= j, and j - k < window or t < n_first
+          const bool near = a.window > 0 && t >= a.n_first;
+          return columns(max(k, 0), near ? max(0, min(g.rows, k + a.window)) : g.rows);
         }
-        block = block_of(j + 2);
+        uint32_t s = 0u;
+        if (k >= 0) {
+          const int32_t end = fast_div(plan.group_div, min(m0 + n0 + kCols, m_all) - 1) + 1;
+          for (int32_t j = fast_div(plan.group_div, min(m0 + n0, m_all - 1)); j < end; ++j)
+            if (sees_draft(a.seqs.mask + (int64_t)(g.row0 + j) * a.seqs.mask_words, j, k)) s |= columns(j, j + 1);
+          return s;
+        }
+        s = columns(0, g.rows);
+        if (a.window > 0 && t >= a.n_first) {
+#pragma unroll 1
+          for (int i = 0; i < kCols; ++i)
+            if (C.depth[n0 + i] - k >= a.window) s &= ~(1u << i);
+        }
+        return s;
+      };
+      uint64_t sum2[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) sum2[i] = 0ull;
+      const uint32_t jg0 = jg;
+      if (g.n > 0) {  // what the other warps have left of the part's rows
+        tc_warp_wait_ready(sm32(&C.q_full), loaded & 1u, lim, abort_flag);
+        __syncwarp();
+        ++loaded;
+      }
+      for (int j = 0; j < g.n; ++j, ++jg) {
+        if (G::kTurns && (int)(jg & 1u) != w) continue;
         const uint32_t b = jg % (uint32_t)G::kS, sc = lane_base + G::kSCol + b * G::kN + n0;
         const int32_t t0 = g.tile(j) * kC8T;
         const bool masked = is_masked(t0);
-        uint32_t see = 0xFFFFFFFFu;
-        if (masked) {
-          see = 0u;
-#pragma unroll 4
-          for (int i = 0; i < kHalf; ++i) see |= sees(n0 + i, t0 + tk) ? 1u << i : 0u;
-        }
+        const uint32_t see = masked ? sees(t0 + tk) : 0xFFFFFFFFu;
+        tc_warp_wait_ready(sm32(&C.scaled[jg % G::kScales]), (jg / (uint32_t)G::kScales) & 1u, lim, abort_flag);
+        tc_warp_wait_ready(sm32(&C.s_full[b]), (jg / (uint32_t)G::kS) & 1u, lim, abort_flag);
+        tc_fence_after();
+        __syncwarp();
+        float ks = C.scales[jg % G::kScales][0][tk >> 4], vs = C.scales[jg % G::kScales][1][tk >> 4];
         if (!(ks >= 0.f && ks < INFINITY && vs >= 0.f && vs < INFINITY)) {
           if (see != 0u) report_error(a.status, kErrNonFinite, g.s);
           ks = vs = 0.f;
         }
         const float vx = fmaxf(vs, kC8Least);
-        tc_warp_wait_ready(sm32(&C.s_full[b]), (jg / (uint32_t)G::kS) & 1u, lim, abort_flag);
-        tc_fence_after();
-        float x[kHalf];
-        const uint64_t ks2 = pair_f32(ks, ks), sixteenth = pair_f32(0.0625f, 0.0625f);
-        // Logits in log2 units, rounded as they are: a reference taken from them is then met
-        // exactly, however large they are.
-        auto logits = [&]() {
+        uint8_t *const p_tile = c8_shared + G::kPOff + (jg & 1u) * G::kBox;
+        float x[kCols];
+        // Twice where references move: of the rows whose largest w of this tile is over 2^8,
+        // or of all in a part's first tile.
+        for (bool move = j < G::kOs;; move = true) {
+          // Logits in log2 units, rounded as they are: a reference taken from them is then met
+          // exactly, however large they are.
+          const uint64_t ks2 = pair_f32(ks, ks), sixteenth = pair_f32(0.0625f, 0.0625f);
 #pragma unroll
-          for (int c = 0; c < kHalf; c += kAtOnce) {
+          for (int c = 0; c < kCols; c += kAtOnce) {
             uint32_t hi[kAtOnce], lo[kAtOnce];
             tmem_cols<kAtOnce>(sc + c, hi);
             tmem_cols<kAtOnce>(sc + R + c, lo);
@@ -660,13 +857,48 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
               unpair_f32(mul2(mul2(s2, ks2), f2), x[c + i], x[c + i + 1]);
             }
           }
-        };
-        auto weights = [&]() -> float {  // exp of the logits relative to the references; their largest
+          if (move) {
+            const float lv = log2f(vx);
+            float l[kCols];
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) l[i] = ((see >> i) & 1u) ? x[i] + lv : -INFINITY;
+            const float top = over_lanes<kCols>(l, lane, [](float p, float q) { return fmaxf(p, q); });
+            // the warps' maxima meet in this group's bytes of the tile's P, which is written later
+            if (jg >= 2) wait_pv(jg - 2);
+            __syncwarp();
+            auto spot = [&](int q, int i) {
+              const int row = q * 32 + i;
+              return reinterpret_cast<float *>(p_tile + row * 128 + (((n0 >> 4) ^ (row & 7)) << 4));
+            };
+            if (lane % (32 / kCols) == 0) *spot(wq, lane / (32 / kCols)) = top;
+            group_sync(w);
+            if (tk < kCols) {
+              const float most = fmaxf(fmaxf(*spot(0, tk), *spot(1, tk)), fmaxf(*spot(2, tk), *spot(3, tk)));
+              const float was = -less_ref[tk], now = most - kC8Head;
+              const bool moves = most > was + 8.f;
+              alpha[tk] = moves ? ex2(was - now) : 1.f;
+              if (moves) less_ref[tk] = -now;
+            }
+            group_sync(w);
+            if (j >= G::kOs) {  // O and the sums hold the earlier tiles of this part
+#pragma unroll
+              for (int i = 0; i < kCols / 2; ++i) sum2[i] = mul2(sum2[i], pair_f32(alpha[2 * i], alpha[2 * i + 1]));
+              wait_pv(jg - G::kOs);
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < kCols; ++i) {
+                const float by = alpha[i];
+                if (by != 1.f) tmem_scale<G::kHalves>(my_o + i, G::kN, R, by);
+              }
+              tmem_wait_st();
+            }
+          }
+          // exp of the logits relative to the references
           float most = 0.f;
 #pragma unroll
-          for (int i = 0; i < kHalf; i += 2) {
+          for (int i = 0; i < kCols; i += 2) {
             float lo, hi;
-            unpair_f32(add2(pair_f32(x[i], x[i + 1]), pair_f32(C.less_ref[n0 + i], C.less_ref[n0 + i + 1])), lo, hi);
+            unpair_f32(add2(pair_f32(x[i], x[i + 1]), pair_f32(less_ref[i], less_ref[i + 1])), lo, hi);
             x[i] = ex2(lo);
             x[i + 1] = ex2(hi);
             if (masked) {
@@ -675,83 +907,42 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
             }
             most = max3(most, x[i], x[i + 1]);
           }
-          return most;
-        };
-        logits();
-        const float most = weights();
-        if (any_of_group(w, most * vx > 448.f)) {
-          // references move: of the rows whose largest w of this tile is over 2^8
-          logits();
-          const float lv = log2f(vx);
-#pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            const float l = ((see >> i) & 1u) ? x[i] + lv : -INFINITY;
-            const float top = unordered(__reduce_max_sync(0xffffffffu, ordered(l != l ? -INFINITY : l)));
-            if (lane == i) C.red[warp][i] = top;
-          }
-          group_sync(w);
-          if (tk < kHalf) {
-            const float l = fmaxf(fmaxf(C.red[4 * w][tk], C.red[4 * w + 1][tk]), fmaxf(C.red[4 * w + 2][tk], C.red[4 * w + 3][tk]));
-            const float was = -C.less_ref[n0 + tk], now = l - kC8Head;
-            const bool move = l > was + 8.f;
-            C.alpha[n0 + tk] = move ? ex2(was - now) : 1.f;
-            if (move) C.less_ref[n0 + tk] = -now;
-          }
-          group_sync(w);
-          if (j > 0) {  // O holds the earlier tiles of this part
-            wait_pv(jg - 1);
-            tc_fence_after();
-          }
-#pragma unroll
-          for (int i = 0; i < kHalf / 2; ++i) sum2[i] = mul2(sum2[i], pair_f32(C.alpha[n0 + 2 * i], C.alpha[n0 + 2 * i + 1]));
-          if (j > 0) {
-#pragma unroll 1
-            for (int i = 0; i < kHalf; ++i) {
-              const float by = C.alpha[n0 + i];
-              if (by == 1.f) continue;
-#pragma unroll
-              for (int h = 0; h < G::kHalves; ++h) {
-                tmem_scale1(lane_base + (uint32_t)(h * G::kN + n0 + i), by);
-                tmem_scale1(lane_base + (uint32_t)(h * G::kN + R + n0 + i), by);
-              }
-            }
-            tmem_wait_st();
-          }
-          weights();
+          if (move || !any_of_group(w, most * vx > 448.f)) break;
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm32(&C.s_free[b]));
         if (jg >= 2) wait_pv(jg - 2);  // P's buffer is free
         // The row of the P buffer that is this token's: the group's bytes of hi and of lo.
         // The sums keep 32 bits, as lse has to; the weights go to the two terms above.
-        uint8_t *prow = c8_shared + G::kPOff + (jg & 1u) * G::kBox + tk * 128;
-        uint32_t ph[(kHalf + 3) / 4], pl[(kHalf + 3) / 4];
-#pragma unroll
-        for (int i = 0; i < kHalf; i += 4) {
-          uint32_t h[2], l[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint64_t p2 = pair_f32(x[i + 2 * k], x[i + 2 * k + 1]);
-            float w0, w1;
-            unpair_f32(mul2(p2, pair_f32(vs, vs)), w0, w1);
-            split_e4m3(w0, w1, h[k], l[k]);
-            sum2[i / 2 + k] = add2(sum2[i / 2 + k], p2);
-          }
-          ph[i / 4] = h[0] | h[1] << 16;
-          pl[i / 4] = l[0] | l[1] << 16;
-        }
+        uint8_t *prow = p_tile + tk * 128;
+        constexpr int kPut = kCols < 16 ? kCols : 16;  // bytes at once
         auto put = [&](int col, const uint32_t *v) {
-          if constexpr (kHalf >= 16) {
-#pragma unroll
-            for (int c = 0; c < kHalf / 16; ++c)
-              *reinterpret_cast<uint4 *>(prow + ((((col >> 4) + c) ^ (tk & 7)) << 4)) =
-                  make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-          } else if constexpr (kHalf == 8) {
-            *reinterpret_cast<uint2 *>(prow + (((col >> 4) ^ (tk & 7)) << 4) + (col & 8)) = make_uint2(v[0], v[1]);
-          } else {
-            *reinterpret_cast<uint32_t *>(prow + (((col >> 4) ^ (tk & 7)) << 4) + (col & 12)) = v[0];
-          }
+          uint8_t *at = prow + (((col >> 4) ^ (tk & 7)) << 4) + (col & 15);
+          if constexpr (kPut == 16) *reinterpret_cast<uint4 *>(at) = make_uint4(v[0], v[1], v[2], v[3]);
+          else *reinterpret_cast<uint2 *>(at) = make_uint2(v[0], v[1]);
         };
-        put(n0, ph);
-        put(R + n0, pl);
+        const uint64_t vs2 = pair_f32(vs, vs);
+#pragma unroll
+        for (int c = 0; c < kCols; c += kPut) {
+          uint32_t ph[kPut / 4], pl[kPut / 4];
+#pragma unroll
+          for (int i = 0; i < kPut; i += 4) {
+            uint32_t h[2], l[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t p2 = pair_f32(x[c + i + 2 * k], x[c + i + 2 * k + 1]);
+              float w0, w1;
+              unpair_f32(mul2(p2, vs2), w0, w1);
+              split_e4m3(w0, w1, h[k], l[k]);
+              sum2[(c + i) / 2 + k] = add2(sum2[(c + i) / 2 + k], p2);
+            }
+            ph[i / 4] = h[0] | h[1] << 16;
+            pl[i / 4] = l[0] | l[1] << 16;
+          }
+          put(n0 + c, ph);
+          put(R + n0 + c, pl);
+        }
         if (masked && veiled) {
           // A NaN of V would reach, as 0 x NaN, the rows that do not see its token: it is
           // cleared here and given to the rows that do see it when the output is written.
@@ -761,19 +952,17 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
           tc_warp_wait_ready(sm32(&C.full[slot]), (at / G::kSlots) & 1u, lim, abort_flag);
           __syncwarp();
           uint4 *vt = reinterpret_cast<uint4 *>(c8_shared + G::kRingOff + slot * G::kSlot);
-          for (int i = warp * 32 + lane; i < (int)(G::kSlot / 16); i += 32 * kC8Soft) {
-            const uint4 x = vt[i];
-            uint32_t e[4] = {x.x, x.y, x.z, x.w};
-            bool hit = false;
+          for (int i = G::kTurns ? tk : tid; i < (int)(G::kSlot / 16); i += 32 * kC8Soft / G::kOs) {
+            const uint4 y = vt[i];
+            uint32_t e[4] = {y.x, y.y, y.z, y.w}, hit = 0u;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) hit |= ((e[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // a byte's seven bits all set
+            if (hit != 0u) {
 #pragma unroll
-              for (int c = 0; c < 32; c += 8)
-                if (nan8(e[k] >> c)) {
-                  e[k] &= ~(0xFFu << c);
-                  hit = true;
-                }
-            if (hit) {
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t z = ((e[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                e[k] &= ~((z >> 7) * 0xFFu);
+              }
               vt[i] = make_uint4(e[0], e[1], e[2], e[3]);
               *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) = seg;
             }
@@ -782,104 +971,127 @@ cache8_attn_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(sm32(&C.s_free[b]));
-          mbar_arrive(sm32(&C.p_ready[jg & 1u]));
-        }
+        if (lane == 0) mbar_arrive(sm32(&C.p_ready[jg & 1u]));
       }
       ns += (uint32_t)(2 * g.n);
-      C8Seg next;
-      const bool more_next = walk.next(next);
-      if (!g.empty) {
-        // the rows' sums over this group's threads, in a fixed order
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) {
-          float even, odd;
-          unpair_f32(sum2[i / 2], even, odd);
-          float x = i & 1 ? odd : even;
-#pragma unroll
-          for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == i) C.red[warp][i] = x;
-        }
-      }
-      const int64_t part = (int64_t)blockIdx.x * 2 + (g.head ? 0 : 1);
-      group_sync(w);
-      if (!g.empty && tk < kHalf) {
-        const int n = n0 + tk;
-        const float all = (C.red[4 * w][tk] + C.red[4 * w + 1][tk]) + (C.red[4 * w + 2][tk] + C.red[4 * w + 3][tk]);
-        const float ref = g.n > 0 ? -C.less_ref[n] : kC8Unset;
-        C.inv[n] = all == 0.f ? 0.f : 1.f / all;
-        if (m0 + n < m_all) {
-          if (!g.whole) {
-            part_ml[part * R + n] = make_float2(ref, all);
-          } else if (a.lse) {
-            const int32_t m = (int32_t)(m0 + n), j = fast_div(group_div, m);
-            a.lse[(int64_t)(g.v.row0 + j) * a.nq + g.kvh * a.group + (m - j * a.group)] =
-                all == 0.f ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
-          }
-        }
-      }
       bool fix = false;
       if (g.n > 0) {  // S and P V of every tile are done: Q may go, O may be read
+        if (G::kTurns && g.n > 1) wait_pv(jg - 2);
         wait_pv(jg - 1);
         tc_fence_after();
         __syncwarp();
         fix = *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) == seg;
       }
-      if (fix) {  // rare: rows that see a cleared NaN; the rows' depths are still this part's
-        for (int i = 0; i < kHalf; ++i) {
-          for (int h = 0; h < G::kHalves; ++h) {
-            bool hit = false;
-            for (int j = 0; j < g.n; ++j) {
-              const int32_t t0 = g.tile(j) * kC8T;
-              if (!is_masked(t0)) continue;
-              for (int32_t t = t0; t < min(kv, t0 + kC8T); ++t) {
-                if (!sees(n0 + i, t)) continue;
-                const int64_t slot = token_slot(a.seqs, g.s, t);
-                hit = hit || (slot >= 0 && nan8(a.v_pool[(slot * a.nkv + g.kvh) * HD + h * 128 + tk]));
-              }
-            }
-            uint32_t x;
-            __syncwarp();
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(lane_base + (uint32_t)(h * G::kN + n0 + i)));
-            asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x)::"memory");
-            if (hit) x = 0x7FC00000u;
-            asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(lane_base + (uint32_t)(h * G::kN + n0 + i)), "r"(x) : "memory");
-          }
-        }
-        tmem_wait_st();
+      // the first tile of a part went to group jg0 % 2: whether a group had one
+      auto has = [&](int o) { return G::kTurns ? g.n > (int)((jg0 + (uint32_t)o) & 1u) : g.n > 0; };
+      const int64_t part = (int64_t)blockIdx.x * 2 + ((g.flags & C8Seg::kHead) ? 0 : 1);
+      const bool whole = (g.flags & C8Seg::kWhole) != 0;
+      float(*const sums)[kCols] = reinterpret_cast<float(*)[kCols]>(c8_shared + G::kPOff);  // P is read
+      if (!empty) {
+        // the rows' sums over this group's threads, in a fixed order
+        float sum[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; i += 2) unpair_f32(sum2[i / 2], sum[i], sum[i + 1]);
+        const float mine = over_lanes<kCols>(sum, lane, [](float p, float q) { return p + q; });
+        if (lane % (32 / kCols) == 0) sums[warp][lane / (32 / kCols)] = mine;
       }
-      group_sync(w);  // the part's references, sums and depths are read
-      more = more_next;
-      if (more && next.n > 0) load_q(next);
-      if (!g.empty) {
+      soft_sync();
+      if (!empty && tid < R) {
+        const int n = tid;
+        float ref = kC8Unset, all = 0.f;
+        auto sum_of = [&](int o, int i) { return (sums[4 * o][i] + sums[4 * o + 1][i]) + (sums[4 * o + 2][i] + sums[4 * o + 3][i]); };
+        if constexpr (G::kTurns) {
+          const float r0 = has(0) ? -C.less_ref[n] : kC8Unset, r1 = has(1) ? -C.less_ref[kCols + n] : kC8Unset;
+          ref = fmaxf(r0, r1);
+          const float by0 = ex2(r0 - ref), by1 = ex2(r1 - ref);
+          C.mix[n] = by0;
+          C.mix[kCols + n] = by1;
+          if (has(0)) all = sum_of(0, n) * by0;
+          if (has(1)) all = fmaf(sum_of(1, n), by1, all);
+        } else if (g.n > 0) {
+          ref = -C.less_ref[n];
+          all = sum_of(n / kCols, n % kCols);
+        }
+        C.inv[n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
+        int64_t where = -1;
+        if (m0 + n < m_all) {
+          const int32_t j = fast_div(plan.group_div, m0 + n), head = g.kvh * a.group + (m0 + n - j * a.group);
+          where = whole ? (int64_t)(g.row0 + j) * a.out_stride + (int64_t)head * HD : (part * R + n) * HD;
+          if (!whole) part_ml[part * R + n] = make_float2(ref, all);
+          else if (a.lse)
+            a.lse[(int64_t)(g.row0 + j) * a.nq + head] = all == 0.f ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
+        }
+        C.where[n] = where;
+      }
+      C8Seg next;
+      const bool more_next = advance(next);
+      more = more_next;  // (its barrier: the part's references and sums are read)
+      const bool load = more && next.n > 0;
+      if (load && !fix) load_q(next);  // (the depths of a part to be mended are still wanted)
+      if (!empty) {
+        constexpr int kRows = R / 2, kOut = kRows < 16 ? kRows : 16;  // a group's rows of the output, at once
+        const int first = w * kRows;
 #pragma unroll 1
         for (int h = 0; h < G::kHalves; ++h) {
           const int d = h * 128 + tk;
 #pragma unroll 1
-          for (int c = 0; c < kHalf; c += kAtOnce) {
-            uint32_t hi[kAtOnce], lo[kAtOnce];
-            if (g.n > 0) {
-              tmem_cols<kAtOnce>(lane_base + (uint32_t)(h * G::kN + n0 + c), hi);
-              tmem_cols<kAtOnce>(lane_base + (uint32_t)(h * G::kN + R + n0 + c), lo);
-              tmem_ready<kAtOnce>(hi);
-              tmem_ready<kAtOnce>(lo);
+          for (int c = first; c < first + kRows; c += kOut) {
+            float x[kOut];
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) x[i] = 0.f;
+#pragma unroll
+            for (int o = 0; o < G::kOs; ++o) {
+              if (!has(o)) continue;
+              uint32_t hi[kOut], lo[kOut];
+              const uint32_t at = lane_base + (uint32_t)o * G::kOCols + (uint32_t)(h * G::kN + c);
+              tmem_cols<kOut>(at, hi);
+              tmem_cols<kOut>(at + R, lo);
+              tmem_ready<kOut>(hi);
+              tmem_ready<kOut>(lo);
+#pragma unroll
+              for (int i = 0; i < kOut; ++i) {
+                const float y = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                x[i] = G::kTurns ? fmaf(y, C.mix[o * kCols + c + i], x[i]) : y;
+              }
             }
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-              const int n = n0 + c + i;
-              if (m0 + n >= m_all) break;
-              const float x = g.n > 0 ? fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i])) : 0.f;
-              if (g.whole) {
-                const int32_t m = (int32_t)(m0 + n), j = fast_div(group_div, m);
-                a.out[(int64_t)(g.v.row0 + j) * a.out_stride + (int64_t)(g.kvh * a.group + (m - j * a.group)) * HD + d] =
-                    (uint16_t)f32_to_bf16(x * C.inv[n]);
-              } else {
-                part_o[(part * R + n) * HD + d] = x;
-              }
+            for (int i = 0; i < kOut; ++i) {
+              const int64_t where = C.where[c + i];
+              if (where < 0) continue;
+              const float y = x[i] * C.inv[c + i];
+              if (whole) a.out[where + d] = (uint16_t)f32_to_bf16(y);
+              else part_o[where + d] = y;
             }
           }
         }
+      }
+      if (fix) {  // rare: the rows of this thread's dims that see a cleared NaN
+        const int first = w * (R / 2);
+        for (int n = first; n < first + R / 2 && m0 + n < m_all; ++n) {
+          const int32_t j = fast_div(plan.group_div, m0 + n);
+          const uint32_t *mrow = chain ? nullptr : a.seqs.mask + (int64_t)(g.row0 + j) * a.seqs.mask_words;
+          const int32_t at = g.ctx + (chain ? j : C.depth[n]);
+#pragma unroll 1
+          for (int h = 0; h < G::kHalves; ++h) {
+            bool hit = false;
+            for (int i = 0; i < g.n; ++i) {
+              const int32_t t0 = g.tile(i) * kC8T;
+              if (!is_masked(t0)) continue;
+              for (int32_t t = t0; t < min(kv, t0 + kC8T); ++t) {
+                const bool drafted = t >= g.ctx;
+                if (drafted && !sees_draft(mrow, j, t - g.ctx)) continue;
+                if (a.window > 0 && t >= a.n_first && at - t >= a.window && (chain || !drafted)) continue;
+                const int64_t slot = token_slot(a.seqs, g.s, t);
+                hit = hit || (slot >= 0 && nan8(a.v_pool[(slot * a.nkv + g.kvh) * HD + h * 128 + tk]));
+              }
+            }
+            if (!hit) continue;
+            if (whole) a.out[C.where[n] + h * 128 + tk] = 0x7FC0u;
+            else part_o[C.where[n] + h * 128 + tk] = __int_as_float(0x7FC00000);
+          }
+        }
+        soft_sync();
+        if (load) load_q(next);
       }
       tc_fence_before();
       __syncwarp();
@@ -904,7 +1116,7 @@ constexpr int kC8JoinWarps = 8;
 
 template <int HD, int R, int kGroups>
 __global__ void __launch_bounds__(32 * kC8JoinWarps)
-cache8_join_kernel(const Cache8Args a, const FastDiv group_div, int team_log, int32_t teams, const int64_t *base,
+cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t teams, const int64_t *base,
                    const float2 *part_ml, const float4 *part_o, const int32_t *row_seq) {
   constexpr int kQuads = HD / 128;
   __shared__ float4 acc_s[kGroups > 1 ? kC8JoinWarps : 1][kQuads][32];
@@ -912,22 +1124,22 @@ cache8_join_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp % kGroups;
   const int64_t mg = (int64_t)blockIdx.x * (kC8JoinWarps / kGroups) + warp / kGroups;
   const int32_t kvh = blockIdx.y;
-  const int32_t row = mg < (int64_t)a.seqs.n_rows * a.group ? fast_div(group_div, (int32_t)mg) : -1;
+  const int32_t row = mg < (int64_t)a.seqs.n_rows * a.group ? fast_div(plan.group_div, (int32_t)mg) : -1;
   const int32_t head = kvh * a.group + (int32_t)(mg - (int64_t)row * a.group);
   // Where the row lies in the plan, while the launch before still runs: it wrote none of
   // what this reads, and it began after everything before it was complete.
   int32_t s = 0, r = 0, rank = 0, tiles = 0;
   int64_t u0 = 0;  // the unit's first tile, from its sequence's first
   auto place = [&](int32_t at) {  // where the row lies, if sequence `at` has it
-    const C8Seq q = c8_seq<R>(a, team_log, read_seq(a.seqs, at));
+    const C8Seq q = c8_seq<R>(a, plan, read_seq(a.seqs, at));
     if (row < q.v.row0 || row >= q.v.row0 + q.v.rows) return;
     const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
     const int32_t mt = (int32_t)(m / R);
     s = at;
     r = (int32_t)(m % R);
-    rank = mt & ((1 << team_log) - 1);
+    rank = mt & ((1 << plan.team_log) - 1);
     tiles = q.tiles;
-    u0 = ((int64_t)kvh * q.m_tiles + (mt >> team_log)) * (tiles + kC8Start) + kC8Start;
+    u0 = ((int64_t)kvh * q.m_tiles + (mt >> plan.team_log)) * (tiles + kC8Start) + kC8Start;
   };
   if (row >= 0) place(seq_of_row(a.seqs, row));
   grid_dependency_sync();
@@ -964,7 +1176,7 @@ cache8_join_kernel(const Cache8Args a, const FastDiv group_div, int team_log, in
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         const int32_t at = c + e * kGroups;
-        const int64_t part = (((int64_t)min(at, c1) << team_log) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
+        const int64_t part = (((int64_t)min(at, c1) << plan.team_log) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
         ml[e] = part_ml[part * R + r];
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) x[e][i] = part_o[(part * R + r) * (HD / 4) + 32 * i + lane];
@@ -1041,9 +1253,9 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
   const int64_t mean_rows = (int64_t)a.seqs.n_rows * a.group / a.seqs.n_seqs;
   const int team_log = R < 64 ? 0 : mean_rows >= 224 ? 2 : mean_rows >= 96 ? 1 : 0;
   const int ctas = ((device_sm_count() < kC8MaxCtas ? device_sm_count() : kC8MaxCtas) >> team_log) << team_log;
-  const FastDiv group_div = make_fast_div(a.group);
+  const C8Plan plan = {make_fast_div(a.group), team_log, R / a.group + 2};
   cudaError_t r = launch_dependent(cache8_attn_kernel<HD, R>, dim3((unsigned)ctas), dim3(kC8Threads), c8_smem<HD, R>(), stream, 1u, a,
-                                   group_div, team_log, base, ml, o, row_seq);
+                                   plan, base, ml, o, row_seq);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kC8T) return r;
   // One group of parts per warp where units outnumber the CTAs (few parts each), eight
@@ -1052,7 +1264,7 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
   const bool many = ctas >= 8 * units;
   return launch_dependent(many ? cache8_join_kernel<HD, R, kC8JoinWarps> : cache8_join_kernel<HD, R, 1>,
                           dim3((unsigned)(many ? rows : (rows + kC8JoinWarps - 1) / kC8JoinWarps), (unsigned)a.nkv),
-                          dim3(32 * kC8JoinWarps), 0, stream, 1u, a, group_div, team_log, (int32_t)(ctas >> team_log), base, ml,
+                          dim3(32 * kC8JoinWarps), 0, stream, 1u, a, plan, (int32_t)(ctas >> team_log), base, ml,
                           reinterpret_cast<const float4 *>(o), row_seq);
 }
 
