@@ -48,6 +48,7 @@ constexpr float kC8Unset = -1e30f;    // a row's reference before it has seen a 
 constexpr float kC8Nobody = 1e30f;    // ... of a column without a row: its weights are 0
 constexpr float kC8Head = 4.f;        // log2 of a largest w when the reference is set
 constexpr float kC8Least = 0x1p-92f;  // a V scale below counts as this for the reference
+constexpr uint32_t kC8SuspendNs = 2000;  // a wait's sleep at most (it ends early when its phase completes)
 constexpr long long kC8SpinLimit = 4000000000LL;
 
 template <int HD, int R>
@@ -224,6 +225,37 @@ static_assert(c8_smem<256, 64>() <= 232448 && c8_smem<128, 64>() <= 232448, "227
 // Ring position of tile j's V among a part's n tiles, counted from the part's first copy:
 // K0, K1, V0, K2, V1, ..., V(n-1), about the order the MMAs take them in.
 __device__ __forceinline__ int c8_v_pos(int j, int n) { return j + 1 < n ? 2 + 2 * j : 2 * n - 1; }
+
+// Bounded wait on a phase.  Every role's loop has several and they share the instruction
+// cache, so it is short: one instruction that sleeps until the phase completes or some time
+// has passed, then a look at the abort flag and the clock.
+__device__ __forceinline__ bool phase_done(uint32_t mb, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(mb), "r"(parity), "r"(kC8SuspendNs)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool one_wait(uint32_t mb, uint32_t parity, long long limit, volatile int32_t *abort_flag) {
+  if (phase_done(mb, parity)) return true;
+  const long long t0 = clock64();
+  while (!phase_done(mb, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// ... of a warp, each lane for itself, the verdict the warp's.
+__device__ __forceinline__ bool warp_wait(uint32_t mb, uint32_t parity, long long limit, volatile int32_t *abort_flag) {
+  return __all_sync(0xffffffffu, one_wait(mb, parity, limit, abort_flag));
+}
 
 // 4 bytes from global to shared memory, asynchronously; bytes 0: zeros.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
@@ -432,7 +464,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
   uint32_t segs_taken = 0;
   auto take_seg = [&](C8Seg &g) -> bool {
     const uint32_t i = segs_taken % kC8Segs;
-    const bool ok = tc_warp_wait_ready(sm32(&C.seg_full[i]), (segs_taken / kC8Segs) & 1u, lim, abort_flag);
+    const bool ok = warp_wait(sm32(&C.seg_full[i]), (segs_taken / kC8Segs) & 1u, lim, abort_flag);
     __syncwarp();
     if (ok) g = C.segs[i];
     __syncwarp();
@@ -453,7 +485,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     const int p0 = (warp - kC8Soft) * 32, ch = lane % kCh, hl = lane / kCh;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * G::kBox + (uint32_t)(p0 + hl) * 128u;
     const int64_t pitch = (int64_t)a.nkv * HD;
-    uint32_t ns = 0;
+    const int64_t step = kRows * pitch;
+    uint32_t slot = 0u, phase = 0u;
     bool ok = true;
     while (ok && take_seg(g) && !(g.flags & C8Seg::kEnd)) {
       const int32_t kv = g.ctx + g.rows;
@@ -473,44 +506,59 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
         return y;
       };
-      auto bring = [&](const uint8_t *pool, const Pages &y) {
-        const uint32_t slot = ns % G::kSlots;
-        if (!tc_warp_wait_ready(sm32(&C.empty[slot]), ((ns / G::kSlots) & 1u) ^ 1u, lim, abort_flag)) {
+      // copies in the ring's order: K0, K1, V0, K2, V1, ..., V(n - 1)
+      Pages yv = fetch(0), yk = yv, later = fetch(1);
+      int j = 0;         // the tile of V's next copy; K's is one on
+      bool is_k = true;  // of this copy
+      for (int i = 0; i < 2 * g.n; ++i) {
+        const Pages y = is_k ? yk : yv;
+        const uint8_t *const pool = is_k ? a.k_pool : a.v_pool;
+        if (!warp_wait(sm32(&C.empty[slot]), phase ^ 1u, lim, abort_flag)) {
           ok = false;
-          return;
+          break;
         }
-        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool there = (uint32_t)y.page[i] < (uint32_t)a.seqs.pool_pages;
-          const uint8_t *src = pool + (int64_t)(there ? y.page[i] * a.seqs.page.d + y.at[i] : 0) * pitch + mine;
-          const uint32_t dst = dst0 + slot * G::kSlot + (uint32_t)i * 16u * 128u;
-          const int32_t t = y.t0 + 16 * i;
-          // row p0 + 16 i + kRows k + hl, its 16-byte chunks swizzled by row % 8
+        for (int e = 0; e < 2; ++e) {
+          const bool there = (uint32_t)y.page[e] < (uint32_t)a.seqs.pool_pages;
+          const uint8_t *src = pool + (int64_t)(there ? y.page[e] * a.seqs.page.d + y.at[e] : 0) * pitch + mine;
+          const uint32_t dst = dst0 + slot * G::kSlot + (uint32_t)e * 16u * 128u;
+          const int32_t t = y.t0 + 16 * e;
+          // row p0 + 16 e + kRows k + hl, its 16-byte chunks swizzled by row % 8
           auto to = [&](int k) { return dst + (uint32_t)(k * kRows) * 128u + (uint32_t)(((ch & 7) ^ ((kRows * k + hl) & 7)) << 4); };
           if (there && t + 16 <= kv && (t + 16 <= a.n_first || t >= g.back)) {  // all of them
 #pragma unroll
-            for (int k = 0; k < kN; ++k) cp_async16(to(k), src + k * kRows * pitch, 16u);
+            for (int k = 0; k < kN; ++k) {
+              cp_async16(to(k), src, 16u);
+              src += step;
+            }
           } else {
 #pragma unroll 1
             for (int k = 0; k < kN; ++k) {
               const bool read = there && g.wants(a, t + kRows * k + hl);
-              cp_async16(to(k), read ? src + k * kRows * pitch : pool, read ? 16u : 0u);
+              cp_async16(to(k), read ? src + k * step : pool, read ? 16u : 0u);
             }
           }
         }
         cp_async_arrive(sm32(&C.full[slot]));
-        ++ns;
-      };
-      if (g.n > 0) {
-        Pages yv = fetch(0), yk = fetch(1);
-        bring(a.k_pool, yv);
-        for (int j = 0; j < g.n && ok; ++j) {
-          const Pages later = fetch(j + 2);
-          if (j + 1 < g.n) bring(a.k_pool, yk);
-          if (ok) bring(a.v_pool, yv);
-          yv = yk;
+        if (++slot == (uint32_t)G::kSlots) {
+          slot = 0u;
+          phase ^= 1u;
+        }
+        // the next copy
+        if (i == 0 ? g.n > 1 : !is_k && j + 2 < g.n) {
+          if (i > 0) {
+            yv = yk;
+            ++j;
+          }
+          is_k = true;
           yk = later;
+          later = fetch(j + 2);
+        } else {
+          if (i > 0 && !is_k) {
+            yv = yk;
+            ++j;
+          }
+          is_k = false;
         }
       }
       if (warp == kC8Soft && !(g.flags & (C8Seg::kWhole | C8Seg::kEmpty))) {  // the rows of a part, for the join
@@ -526,7 +574,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       C8Walk<R> walk(a, plan, found.seq, found.off, laid_out ? found.share.n : 0);
       for (uint32_t k = 0;; ++k) {
         const C8Seg g = walk.next();
-        if (k >= kC8Segs && !tc_warp_wait_ready(sm32(&C.seg_free[k % kC8Segs]), ((k / kC8Segs) & 1u) ^ 1u, lim, abort_flag)) break;
+        if (k >= kC8Segs && !warp_wait(sm32(&C.seg_free[k % kC8Segs]), ((k / kC8Segs) & 1u) ^ 1u, lim, abort_flag)) break;
         __syncwarp();
         if (lane == 0) {
           C.segs[k % kC8Segs] = g;
@@ -559,7 +607,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         int32_t page = fetch(0, at), page1 = fetch(1, at1);
         for (int j = 0; j < g.n; ++j, ++jg) {
           const int32_t page2 = fetch(j + 2, at2);
-          if (jg >= 4 && !tc_warp_wait_ready(sm32(&C.pv_done[jg & 3u]), ((jg >> 2) & 1u) ^ 1u, lim, abort_flag)) {
+          if (jg >= 4 && !warp_wait(sm32(&C.pv_done[jg & 3u]), ((jg >> 2) & 1u) ^ 1u, lim, abort_flag)) {
             ok = false;
             break;
           }
@@ -584,7 +632,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       C8Seg g;
       auto take_one = [&]() -> bool {
         const uint32_t i = segs_taken % kC8Segs;
-        if (!tc_wait_ready(sm32(&C.seg_full[i]), (segs_taken / kC8Segs) & 1u, lim, abort_flag)) return false;
+        if (!one_wait(sm32(&C.seg_full[i]), (segs_taken / kC8Segs) & 1u, lim, abort_flag)) return false;
         g.n = C.segs[i].n;
         g.flags = C.segs[i].flags;
         mbar_arrive(sm32(&C.seg_free[i]));
@@ -593,7 +641,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       };
       bool ok = true;
       auto wait = [&](uint64_t &bar, uint32_t parity) {
-        ok = ok && tc_wait_ready(sm32(&bar), parity, lim, abort_flag);
+        ok = ok && one_wait(sm32(&bar), parity, lim, abort_flag);
         return ok;
       };
       uint32_t slot = 0, phase = 0;  // of the ring
@@ -689,7 +737,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     const uint32_t my_o = lane_base + (G::kTurns ? w * G::kOCols : (uint32_t)n0);
     // P V of tile i.  A warp has waited for tile i - 4 (or a later one) by then, so of a
     // barrier no phase but the last two is ever in question.
-    auto wait_pv = [&](uint32_t i) { tc_warp_wait_ready(sm32(&C.pv_done[i & 3u]), (i >> 2) & 1u, lim, abort_flag); };
+    auto wait_pv = [&](uint32_t i) { warp_wait(sm32(&C.pv_done[i & 3u]), (i >> 2) & 1u, lim, abort_flag); };
     // This warp's rows of a part's Q, split into two e4m3 terms, with what goes with a row.
     auto load_q = [&](const C8Seg &e) {
       const int32_t m_all = e.rows * a.group;
@@ -814,7 +862,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       for (int i = 0; i < kCols / 2; ++i) sum2[i] = 0ull;
       const uint32_t jg0 = jg;
       if (g.n > 0) {  // what the other warps have left of the part's rows
-        tc_warp_wait_ready(sm32(&C.q_full), loaded & 1u, lim, abort_flag);
+        warp_wait(sm32(&C.q_full), loaded & 1u, lim, abort_flag);
         __syncwarp();
         ++loaded;
       }
@@ -824,8 +872,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         const int32_t t0 = g.tile(j) * kC8T;
         const bool masked = is_masked(t0);
         const uint32_t see = masked ? sees(t0 + tk) : 0xFFFFFFFFu;
-        tc_warp_wait_ready(sm32(&C.scaled[jg % G::kScales]), (jg / (uint32_t)G::kScales) & 1u, lim, abort_flag);
-        tc_warp_wait_ready(sm32(&C.s_full[b]), (jg / (uint32_t)G::kS) & 1u, lim, abort_flag);
+        warp_wait(sm32(&C.scaled[jg % G::kScales]), (jg / (uint32_t)G::kScales) & 1u, lim, abort_flag);
+        warp_wait(sm32(&C.s_full[b]), (jg / (uint32_t)G::kS) & 1u, lim, abort_flag);
         tc_fence_after();
         __syncwarp();
         float ks = C.scales[jg % G::kScales][0][tk >> 4], vs = C.scales[jg % G::kScales][1][tk >> 4];
@@ -894,19 +942,21 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             }
           }
           // exp of the logits relative to the references
-          float most = 0.f;
 #pragma unroll
           for (int i = 0; i < kCols; i += 2) {
             float lo, hi;
             unpair_f32(add2(pair_f32(x[i], x[i + 1]), pair_f32(less_ref[i], less_ref[i + 1])), lo, hi);
             x[i] = ex2(lo);
             x[i + 1] = ex2(hi);
-            if (masked) {
-              if (!((see >> i) & 1u)) x[i] = 0.f;
-              if (!((see >> i) & 2u)) x[i + 1] = 0.f;
-            }
-            most = max3(most, x[i], x[i + 1]);
           }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              if (!((see >> i) & 1u)) x[i] = 0.f;
+          }
+          float most = 0.f;
+#pragma unroll
+          for (int i = 0; i < kCols; i += 2) most = max3(most, x[i], x[i + 1]);
           if (move || !any_of_group(w, most * vx > 448.f)) break;
         }
         tc_fence_before();
@@ -949,7 +999,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           // (The slot's earlier copy is known to have landed once P V of the tile before the
           // last is done.)
           const uint32_t at = ns + (uint32_t)c8_v_pos(j, g.n), slot = at % G::kSlots;
-          tc_warp_wait_ready(sm32(&C.full[slot]), (at / G::kSlots) & 1u, lim, abort_flag);
+          warp_wait(sm32(&C.full[slot]), (at / G::kSlots) & 1u, lim, abort_flag);
           __syncwarp();
           uint4 *vt = reinterpret_cast<uint4 *>(c8_shared + G::kRingOff + slot * G::kSlot);
           for (int i = G::kTurns ? tk : tid; i < (int)(G::kSlot / 16); i += 32 * kC8Soft / G::kOs) {
