@@ -226,6 +226,12 @@ static_assert(c8_smem<256, 64>() <= 232448 && c8_smem<128, 64>() <= 232448, "227
 // K0, K1, V0, K2, V1, ..., V(n-1), about the order the MMAs take them in.
 __device__ __forceinline__ int c8_v_pos(int j, int n) { return j + 1 < n ? 2 + 2 * j : 2 * n - 1; }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Bounded wait on a phase.  Every role's loop has several and they share the instruction
 // cache, so it is short: one instruction that sleeps until the phase completes or some time
 // has passed, then a look at the abort flag and the clock.
@@ -318,6 +324,14 @@ __device__ __forceinline__ void tmem_scale(uint32_t taddr, uint32_t half, uint32
   }
 }
 
+__device__ __forceinline__ void tmem_scale1(uint32_t taddr, float by) {
+  uint32_t x;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x)::"memory");
+  x = __float_as_uint(__uint_as_float(x) * by);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(x) : "memory");
+}
+
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -397,7 +411,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
   auto &both = *reinterpret_cast<C8Scratch<G::kScales, G::kMix> *>(c8_shared + G::kCtrlOff);
   auto &C = both.c;
   const uint32_t sQ = sm32(c8_shared), sP = sm32(c8_shared + G::kPOff), sRing = sm32(c8_shared + G::kRingOff);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const long long lim = a.wait_limit > 0 ? a.wait_limit : kC8SpinLimit;
   volatile int32_t *abort_flag = &C.abort;
 
@@ -627,23 +641,20 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    // ---- MMA issuers, one thread each
-    if (lane == 0 && warp <= kC8MmaO) {
+    // ---- MMA issuers: the warp steps through its tiles, one elected lane issues
+    if (warp <= kC8MmaO) {
       C8Seg g;
-      auto take_one = [&]() -> bool {
-        const uint32_t i = segs_taken % kC8Segs;
-        if (!one_wait(sm32(&C.seg_full[i]), (segs_taken / kC8Segs) & 1u, lim, abort_flag)) return false;
-        g.n = C.segs[i].n;
-        g.flags = C.segs[i].flags;
-        mbar_arrive(sm32(&C.seg_free[i]));
-        ++segs_taken;
-        return !(g.flags & C8Seg::kEnd);
-      };
       bool ok = true;
       auto wait = [&](uint64_t &bar, uint32_t parity) {
-        ok = ok && one_wait(sm32(&bar), parity, lim, abort_flag);
+        ok = ok && warp_wait(sm32(&bar), parity, lim, abort_flag);
         return ok;
       };
+      auto take_one = [&]() -> bool {
+        if (!take_seg(g)) return false;
+        g.n = __shfl_sync(0xffffffffu, g.n, 0);
+        return !(g.flags & C8Seg::kEnd);
+      };
+      const bool lead = elect_one();
       uint32_t slot = 0, phase = 0;  // of the ring
       auto step = [&](uint32_t n) {
         slot += n;
@@ -654,7 +665,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       };
       // The slot holds its copy.  A parity tells two phases apart, so the slot's copy
       // before this one has to be known to have landed.  S of tile j: that one is K, of a
-      // tile whose S this thread issued, or V of tile j - 4 or an earlier one, whose P V
+      // tile whose S this warp issued, or V of tile j - 4 or an earlier one, whose P V
       // was waited for, or, in a part's first tiles, V of a part before the last, whose
       // output was written before this part's Q was fetched.  P V of tile j: it is V, or K
       // of an earlier tile.
@@ -680,6 +691,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             if (j > 0) step(j == 1 ? 1u : 2u);
             if (!landed()) break;
             const uint32_t d = tmem + G::kSCol + b * G::kN, k_lo = r_lo + slot * (G::kSlot >> 4);
+            if (lead) {
 #pragma unroll
             for (int kk = 0; kk < HD / 32; ++kk) {
               const uint32_t in = (uint32_t)(kk & 3) * 2u;  // 32 bytes
@@ -688,6 +700,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             }
             mma_commit(sm32(&C.empty[slot]));
             mma_commit(sm32(&C.s_full[b]));
+            }
+            __syncwarp();
             if (++b == (uint32_t)G::kS) {
               b = 0;
               b_phase ^= 1u;
@@ -707,6 +721,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             if (!landed()) break;
             const uint32_t o = tmem + (G::kTurns ? (jg & 1u) * G::kOCols : 0u);
             const uint32_t p = p_lo + (jg & 1u) * (G::kBox >> 4), v_lo = r_lo + slot * (G::kSlot >> 4);
+            if (lead) {
 #pragma unroll
             for (int h = 0; h < G::kHalves; ++h)
 #pragma unroll
@@ -715,13 +730,16 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
                          desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
             mma_commit(sm32(&C.empty[slot]));
             mma_commit(sm32(&C.pv_done[jg & 3u]));
+            }
+            __syncwarp();
           }
           step(1u);
         }
       }
-      // every MMA this thread issued has finished before TMEM is freed
-      mma_commit(sm32(&C.drain[warp - kC8MmaS]));
-      tc_wait(sm32(&C.drain[warp - kC8MmaS]), 0u, kC8SpinLimit, nullptr);
+      // every MMA this warp issued has finished before TMEM is freed
+      if (lead) mma_commit(sm32(&C.drain[warp - kC8MmaS]));
+      __syncwarp();
+      if (lane == 0) tc_wait(sm32(&C.drain[warp - kC8MmaS]), 0u, kC8SpinLimit, nullptr);
     }
     __syncwarp();
   } else {
@@ -807,17 +825,67 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(sm32(&C.q_full));
     };
-    uint32_t jg = 0, ns = 0, loaded = 0;  // tiles, copies and parts with tiles before this one
     int32_t seg = 0;
+    // Whether group o had a tile of part g, whose first went to group jg0 % 2.
+    uint32_t jg = 0, ns = 0, loaded = 0, jg0 = 0;  // tiles, copies and parts with tiles before this one
+    C8Seg g = {}, next;
+    g.flags = C8Seg::kEmpty;
+    auto has = [&](int o) { return G::kTurns ? g.n > (int)((jg0 + (uint32_t)o) & 1u) : g.n > 0; };
+    auto write_out = [&]() {
+      if (!(g.flags & C8Seg::kEmpty)) {
+        const bool whole = (g.flags & C8Seg::kWhole) != 0;
+        constexpr int kRows = R / 2, kOut = kRows < 16 ? kRows : 16;  // a group's rows of the output, at once
+        const int first = w * kRows;
+#pragma unroll 1
+        for (int h = 0; h < G::kHalves; ++h) {
+          const int d = h * 128 + tk;
+#pragma unroll 1
+          for (int c = first; c < first + kRows; c += kOut) {
+            float x[kOut];
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) x[i] = 0.f;
+#pragma unroll
+            for (int o = 0; o < G::kOs; ++o) {
+              if (!has(o)) continue;
+              uint32_t hi[kOut], lo[kOut];
+              const uint32_t at = lane_base + (uint32_t)o * G::kOCols + (uint32_t)(h * G::kN + c);
+              tmem_cols<kOut>(at, hi);
+              tmem_cols<kOut>(at + R, lo);
+              tmem_ready<kOut>(hi);
+              tmem_ready<kOut>(lo);
+#pragma unroll
+              for (int i = 0; i < kOut; ++i) {
+                const float y = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                x[i] = G::kTurns ? fmaf(y, C.mix[o * kCols + c + i], x[i]) : y;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kOut; ++i) {
+              const int64_t where = C.where[c + i];
+              if (where < 0) continue;
+              const float y = x[i] * C.inv[c + i];
+              if (whole) a.out[where + d] = (uint16_t)f32_to_bf16(y);
+              else part_o[where + d] = y;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && g.n > 0) mbar_arrive(sm32(&C.o_free));
+    };
     // the next part, unless a wait of one of the softmax's warps gave up
-    C8Seg g;
     auto advance = [&](C8Seg &to) -> bool {
       const bool ok = take_seg(to);
       return !soft_any(!ok) && !(to.flags & C8Seg::kEnd);
     };
-    bool more = advance(g);
-    if (more && g.n > 0) load_q(g);
-    while (more) {
+    // Parts overlap: the next one's Q is fetched before this one's output is written.
+    bool more = advance(next);
+    while (true) {
+      if (more && next.n > 0) load_q(next);
+      write_out();
+      if (!more) break;
+      g = next;
       ++seg;
       const int32_t m0 = g.m0, m_all = g.rows * a.group, kv = g.ctx + g.rows;
       const bool chain = a.seqs.mask == nullptr, empty = (g.flags & C8Seg::kEmpty) != 0;
@@ -860,7 +928,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       uint64_t sum2[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) sum2[i] = 0ull;
-      const uint32_t jg0 = jg;
+      jg0 = jg;
       if (g.n > 0) {  // what the other warps have left of the part's rows
         warp_wait(sm32(&C.q_full), loaded & 1u, lim, abort_flag);
         __syncwarp();
@@ -1032,8 +1100,33 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         __syncwarp();
         fix = *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) == seg;
       }
-      // the first tile of a part went to group jg0 % 2: whether a group had one
-      auto has = [&](int o) { return G::kTurns ? g.n > (int)((jg0 + (uint32_t)o) & 1u) : g.n > 0; };
+      if (fix) {  // rare: the rows of this thread's dims that see a cleared NaN
+        const int first = w * (R / 2);
+#pragma unroll 1
+        for (int n = first; n < first + R / 2 && m0 + n < m_all; ++n) {
+          const int32_t j = fast_div(plan.group_div, m0 + n);
+          const uint32_t *mrow = chain ? nullptr : a.seqs.mask + (int64_t)(g.row0 + j) * a.seqs.mask_words;
+          const int32_t at = g.ctx + (chain ? j : C.depth[n]);
+#pragma unroll 1
+          for (int h = 0; h < G::kHalves; ++h) {
+            bool hit = false;
+            for (int i = 0; i < g.n; ++i) {
+              const int32_t t0 = g.tile(i) * kC8T;
+              if (!is_masked(t0)) continue;
+              for (int32_t t = t0; t < min(kv, t0 + kC8T); ++t) {
+                const bool drafted = t >= g.ctx;
+                if (drafted && !sees_draft(mrow, j, t - g.ctx)) continue;
+                if (a.window > 0 && t >= a.n_first && at - t >= a.window && (chain || !drafted)) continue;
+                const int64_t slot = token_slot(a.seqs, g.s, t);
+                hit = hit || (slot >= 0 && nan8(a.v_pool[(slot * a.nkv + g.kvh) * HD + h * 128 + tk]));
+              }
+            }
+            __syncwarp();
+            tmem_scale1(lane_base + (has(0) ? 0u : G::kOCols) + (uint32_t)(h * G::kN + n), hit ? NAN : 1.f);
+          }
+        }
+        tmem_wait_st();
+      }
       const int64_t part = (int64_t)blockIdx.x * 2 + ((g.flags & C8Seg::kHead) ? 0 : 1);
       const bool whole = (g.flags & C8Seg::kWhole) != 0;
       float(*const sums)[kCols] = reinterpret_cast<float(*)[kCols]>(c8_shared + G::kPOff);  // P is read
@@ -1073,80 +1166,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
         C.where[n] = where;
       }
-      C8Seg next;
-      const bool more_next = advance(next);
-      more = more_next;  // (its barrier: the part's references and sums are read)
-      const bool load = more && next.n > 0;
-      if (load && !fix) load_q(next);  // (the depths of a part to be mended are still wanted)
-      if (!empty) {
-        constexpr int kRows = R / 2, kOut = kRows < 16 ? kRows : 16;  // a group's rows of the output, at once
-        const int first = w * kRows;
-#pragma unroll 1
-        for (int h = 0; h < G::kHalves; ++h) {
-          const int d = h * 128 + tk;
-#pragma unroll 1
-          for (int c = first; c < first + kRows; c += kOut) {
-            float x[kOut];
-#pragma unroll
-            for (int i = 0; i < kOut; ++i) x[i] = 0.f;
-#pragma unroll
-            for (int o = 0; o < G::kOs; ++o) {
-              if (!has(o)) continue;
-              uint32_t hi[kOut], lo[kOut];
-              const uint32_t at = lane_base + (uint32_t)o * G::kOCols + (uint32_t)(h * G::kN + c);
-              tmem_cols<kOut>(at, hi);
-              tmem_cols<kOut>(at + R, lo);
-              tmem_ready<kOut>(hi);
-              tmem_ready<kOut>(lo);
-#pragma unroll
-              for (int i = 0; i < kOut; ++i) {
-                const float y = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-                x[i] = G::kTurns ? fmaf(y, C.mix[o * kCols + c + i], x[i]) : y;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < kOut; ++i) {
-              const int64_t where = C.where[c + i];
-              if (where < 0) continue;
-              const float y = x[i] * C.inv[c + i];
-              if (whole) a.out[where + d] = (uint16_t)f32_to_bf16(y);
-              else part_o[where + d] = y;
-            }
-          }
-        }
-      }
-      if (fix) {  // rare: the rows of this thread's dims that see a cleared NaN
-        const int first = w * (R / 2);
-        for (int n = first; n < first + R / 2 && m0 + n < m_all; ++n) {
-          const int32_t j = fast_div(plan.group_div, m0 + n);
-          const uint32_t *mrow = chain ? nullptr : a.seqs.mask + (int64_t)(g.row0 + j) * a.seqs.mask_words;
-          const int32_t at = g.ctx + (chain ? j : C.depth[n]);
-#pragma unroll 1
-          for (int h = 0; h < G::kHalves; ++h) {
-            bool hit = false;
-            for (int i = 0; i < g.n; ++i) {
-              const int32_t t0 = g.tile(i) * kC8T;
-              if (!is_masked(t0)) continue;
-              for (int32_t t = t0; t < min(kv, t0 + kC8T); ++t) {
-                const bool drafted = t >= g.ctx;
-                if (drafted && !sees_draft(mrow, j, t - g.ctx)) continue;
-                if (a.window > 0 && t >= a.n_first && at - t >= a.window && (chain || !drafted)) continue;
-                const int64_t slot = token_slot(a.seqs, g.s, t);
-                hit = hit || (slot >= 0 && nan8(a.v_pool[(slot * a.nkv + g.kvh) * HD + h * 128 + tk]));
-              }
-            }
-            if (!hit) continue;
-            if (whole) a.out[C.where[n] + h * 128 + tk] = 0x7FC0u;
-            else part_o[C.where[n] + h * 128 + tk] = __int_as_float(0x7FC00000);
-          }
-        }
-        soft_sync();
-        if (load) load_q(next);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && g.n > 0) mbar_arrive(sm32(&C.o_free));
-      g = next;
+      more = advance(next);  // (its barrier: the part's references and sums are read)
     }
   }
 
