@@ -35,11 +35,12 @@ namespace qsa {
 namespace {
 
 constexpr int kC8Soft = 8, kC8Prod = 4, kC8MmaS = kC8Soft + kC8Prod, kC8MmaO = kC8MmaS + 1;
-constexpr int kC8Scale = kC8MmaO + 1;  // brings the scales
-constexpr int kC8Plan = kC8Scale + 1;  // walks the CTA's share
+constexpr int kC8Look = kC8MmaO + 1;   // looks pages up and brings the scales
+constexpr int kC8Plan = kC8Look + 1;   // walks the CTA's share
 constexpr int kC8Warps = kC8Plan + 1, kC8Threads = 32 * kC8Warps;
 constexpr int kC8Readers = kC8Plan;    // warps that take the walk's parts
 constexpr int kC8Segs = 4;             // parts it is ahead by
+constexpr int kC8Ahead = 8;            // tiles whose pages and scales are held
 constexpr int kC8T = 128;        // tokens of a tile: the MMAs' M
 constexpr int kC8MostRows = 64;  // rows of a unit at most
 constexpr int kC8MaxCtas = 160;
@@ -59,14 +60,13 @@ struct C8Geom {
   // O of its own, joined at the part's end; of 64 each takes half of every tile's rows.
   static constexpr bool kTurns = R < 64;
   static constexpr int kCols = kTurns ? R : R / 2;  // a group's rows of a tile
-  static constexpr int kOs = kTurns ? 2 : 1, kMix = kTurns ? 2 * R : 1;
+  static constexpr int kOs = kTurns ? 2 : 1, kMix = kTurns ? 3 * R : 1;
   static constexpr uint32_t kQBox = kN * 128, kBox = kC8T * 128, kSlot = kC8T * HD;
   static constexpr int kSlots = HD == 256 ? 5 : 10;
   static constexpr int kS = R < 64 ? 4 : HD == 256 ? 2 : 3;  // S buffers
   // Registers of the softmax's threads and of the others, of 128 a thread at the launch: 32
   // rows a thread do not fit those, and every spilled value would queue behind the copies.
   static constexpr int kSoftRegs = kCols < 32 ? 128 : 168, kOtherRegs = 256 - kSoftRegs;
-  static constexpr int kScales = 4;  // tiles whose scales are held
   static constexpr uint32_t kQBytes = (kHalves * kQBox + 1023) / 1024 * 1024;
   static constexpr uint32_t kPOff = kQBytes, kRingOff = kPOff + 2 * kBox, kCtrlOff = kRingOff + kSlots * kSlot;
   static constexpr uint32_t kOCols = kHalves * kN, kSCol = kOs * kOCols;  // TMEM: O's halves, then S
@@ -197,29 +197,33 @@ struct C8Walk {
   }
 };
 
-template <int kScales, int kMix>
+template <int kMix>
 struct C8Ctrl {
   float factor[kC8MostRows];    // log2 units a unit of S and ks
   float less_ref[kC8MostRows];  // [group][its rows]: the reference, negated
-  float alpha[kC8MostRows];     // [group][its rows]: what a move multiplies by
-  float mix[kMix], inv[kC8MostRows];  // ... and, at a part's end, the groups' join, and 1 / sum
+  // [group][its rows]: what a move multiplies by.  A part's output has 1 / sum there where
+  // a group writes out its own rows: its warps meet before the next move.
+  float alpha[kC8MostRows];
+  float mix[kMix];  // else, [2][row]: the groups' join at a part's end, and [2R + row]: 1 / sum
   int64_t where[kC8MostRows];   // a row's place in the output
   int32_t depth[kC8MostRows];
   C8Seg segs[kC8Segs];
-  float scales[kScales][2][8];  // [tile % kScales][K, V][16 tokens]
-  uint64_t full[10], empty[10], scaled[kScales];
+  // [tile % kC8Ahead][16 tokens]: the pool's row of the first that is read (-1: none), scales
+  int32_t slots[kC8Ahead][8];
+  float scales[kC8Ahead][2][8];
+  uint64_t full[10], empty[10], looked[kC8Ahead], scaled[kC8Ahead];
   uint64_t s_full[4], s_free[4], p_ready[2], pv_done[4];
   uint64_t q_full, o_free, drain[2], seg_full[kC8Segs], seg_free[kC8Segs];
   int32_t bad[2], abort;
   uint32_t tmem_base;
 };
-template <int kScales, int kMix>
+template <int kMix>
 union C8Scratch {  // the plan is made before anything else
-  C8Ctrl<kScales, kMix> c;
+  C8Ctrl<kMix> c;
   ShareScratch share;
 };
 template <int HD, int R>
-constexpr size_t c8_smem() { return C8Geom<HD, R>::kCtrlOff + sizeof(C8Scratch<C8Geom<HD, R>::kScales, C8Geom<HD, R>::kMix>); }
+constexpr size_t c8_smem() { return C8Geom<HD, R>::kCtrlOff + sizeof(C8Scratch<C8Geom<HD, R>::kMix>); }
 static_assert(c8_smem<256, 64>() <= 232448 && c8_smem<128, 64>() <= 232448, "227 KiB per CTA");
 
 // Ring position of tile j's V among a part's n tiles, counted from the part's first copy:
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
 cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml, float *__restrict__ part_o, int32_t *__restrict__ row_seq) {
   using G = C8Geom<HD, R>;
   extern __shared__ __align__(1024) uint8_t c8_shared[];
-  auto &both = *reinterpret_cast<C8Scratch<G::kScales, G::kMix> *>(c8_shared + G::kCtrlOff);
+  auto &both = *reinterpret_cast<C8Scratch<G::kMix> *>(c8_shared + G::kCtrlOff);
   auto &C = both.c;
   const uint32_t sQ = sm32(c8_shared), sP = sm32(c8_shared + G::kPOff), sRing = sm32(c8_shared + G::kRingOff);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -444,7 +448,10 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       mbar_init(sm32(&C.full[i]), 32 * kC8Prod);
       mbar_init(sm32(&C.empty[i]), 1);
     }
-    for (int i = 0; i < G::kScales; ++i) mbar_init(sm32(&C.scaled[i]), 32);
+    for (int i = 0; i < kC8Ahead; ++i) {
+      mbar_init(sm32(&C.looked[i]), 8);
+      mbar_init(sm32(&C.scaled[i]), 8);
+    }
     for (int b = 0; b < 4; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
       mbar_init(sm32(&C.s_free[b]), kC8Soft / G::kOs);
@@ -492,64 +499,50 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     C8Seg g;
     // ---- producers: warp p brings 32 of a tile's tokens, 512 bytes an instruction (kRows
     // rows).  A block's tokens, and so 16 of a tile's from a multiple of 16 on, lie in one
-    // page: two look-ups a tile, read two tiles ahead (under load a read takes several
-    // thousand cycles).  A slot's barrier takes each thread's arrival when its copies have
-    // landed, so the whole ring may be in flight.
+    // page: two places a tile.  A slot's barrier takes each thread's arrival when its copies
+    // have landed, so the whole ring may be in flight.
     constexpr int kCh = HD / 16, kRows = 32 / kCh, kN = 16 / kRows;  // chunks of a row, copies of 16 tokens
     const int p0 = (warp - kC8Soft) * 32, ch = lane % kCh, hl = lane / kCh;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * G::kBox + (uint32_t)(p0 + hl) * 128u;
     const int64_t pitch = (int64_t)a.nkv * HD;
     const int64_t step = kRows * pitch;
-    uint32_t slot = 0u, phase = 0u;
+    uint32_t slot = 0u, phase = 0u, jg = 0u;
     bool ok = true;
     while (ok && take_seg(g) && !(g.flags & C8Seg::kEnd)) {
       const int32_t kv = g.ctx + g.rows;
       const int64_t mine = (int64_t)g.kvh * HD + ch * 16 + hl * pitch;
-      struct Pages {
-        int32_t t0, page[2], at[2];  // of tile j: its first token here, its pages, the first token's place in them
-      };
-      auto fetch = [&](int j) -> Pages {
-        Pages y = {kv, {0, 0}, {0, 0}};
-        if (j >= g.n) return y;
-        y.t0 = g.tile(j) * kC8T + p0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int32_t t = y.t0 + 16 * i, pg = fast_div(a.seqs.page, t);
-          y.at[i] = t - pg * a.seqs.page.d;
-          if (t < kv) y.page[i] = a.seqs.table[(int64_t)g.s * a.seqs.table_cols + pg];
-        }
-        return y;
-      };
       // copies in the ring's order: K0, K1, V0, K2, V1, ..., V(n - 1)
-      Pages yv = fetch(0), yk = yv, later = fetch(1);
-      int j = 0;         // the tile of V's next copy; K's is one on
-      bool is_k = true;  // of this copy
+      int j = 0;         // the tile of this copy
+      bool is_k = true;
       for (int i = 0; i < 2 * g.n; ++i) {
-        const Pages y = is_k ? yk : yv;
-        const uint8_t *const pool = is_k ? a.k_pool : a.v_pool;
-        if (!warp_wait(sm32(&C.empty[slot]), phase ^ 1u, lim, abort_flag)) {
+        const uint32_t at = (jg + (uint32_t)j) % kC8Ahead;
+        if (!warp_wait(sm32(&C.looked[at]), ((jg + (uint32_t)j) / kC8Ahead) & 1u, lim, abort_flag) ||
+            !warp_wait(sm32(&C.empty[slot]), phase ^ 1u, lim, abort_flag)) {
           ok = false;
           break;
         }
+        const uint8_t *const pool = is_k ? a.k_pool : a.v_pool;
+        const int32_t t0 = g.tile(j) * kC8T + p0;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const bool there = (uint32_t)y.page[e] < (uint32_t)a.seqs.pool_pages;
-          const uint8_t *src = pool + (int64_t)(there ? y.page[e] * a.seqs.page.d + y.at[e] : 0) * pitch + mine;
+          const int32_t first = C.slots[at][p0 / 16 + e], t = t0 + 16 * e;
           const uint32_t dst = dst0 + slot * G::kSlot + (uint32_t)e * 16u * 128u;
-          const int32_t t = y.t0 + 16 * e;
           // row p0 + 16 e + kRows k + hl, its 16-byte chunks swizzled by row % 8
           auto to = [&](int k) { return dst + (uint32_t)(k * kRows) * 128u + (uint32_t)(((ch & 7) ^ ((kRows * k + hl) & 7)) << 4); };
-          if (there && t + 16 <= kv && (t + 16 <= a.n_first || t >= g.back)) {  // all of them
+          if (first >= 0 && t + 16 <= kv && (t + 16 <= a.n_first || t >= g.back)) {  // all of them
+            const uint8_t *src = pool + (int64_t)first * pitch + mine;
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
               cp_async16(to(k), src, 16u);
               src += step;
             }
           } else {
+            // `first` is that of token t, or of the first one that the window leaves
+            const int64_t skip = g.wants(a, t) ? 0 : g.back - t;
 #pragma unroll 1
             for (int k = 0; k < kN; ++k) {
-              const bool read = there && g.wants(a, t + kRows * k + hl);
-              cp_async16(to(k), read ? src + k * step : pool, read ? 16u : 0u);
+              const bool read = first >= 0 && g.wants(a, t + kRows * k + hl);
+              cp_async16(to(k), read ? pool + (first - skip) * pitch + mine + k * step : pool, read ? 16u : 0u);
             }
           }
         }
@@ -558,23 +551,23 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           slot = 0u;
           phase ^= 1u;
         }
-        // the next copy
-        if (i == 0 ? g.n > 1 : !is_k && j + 2 < g.n) {
-          if (i > 0) {
-            yv = yk;
-            ++j;
+        // K of tile j is followed by V of tile j - 1 (K0 by K1, where there is one), V of
+        // tile j by K of tile j + 2, and the last ones by V
+        if (is_k) {
+          if (j == 0 && g.n > 1) {
+            j = 1;
+          } else {
+            is_k = false;
+            j = max(0, j - 1);
           }
+        } else if (j + 2 < g.n) {
           is_k = true;
-          yk = later;
-          later = fetch(j + 2);
+          j += 2;
         } else {
-          if (i > 0 && !is_k) {
-            yv = yk;
-            ++j;
-          }
-          is_k = false;
+          ++j;
         }
       }
+      jg += (uint32_t)g.n;
       if (warp == kC8Soft && !(g.flags & (C8Seg::kWhole | C8Seg::kEmpty))) {  // the rows of a part, for the join
         const int32_t end = fast_div(plan.group_div, min(g.m0 + R, g.rows * a.group) - 1);
         for (int32_t j = fast_div(plan.group_div, g.m0) + lane; j <= end; j += 32) row_seq[g.row0 + j] = g.s;
@@ -596,47 +589,51 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
         if (g.flags & C8Seg::kEnd) break;
       }
-    } else if (warp == kC8Scale) {
-      // ---- the scales: lane i < 8 brings the K scale of a tile's tokens 16 i to 16 i + 15,
-      // lane i + 8 their V scale, once the tile four before it is weighed: P V of it is done.
+    } else if (warp == kC8Look) {
+      // ---- the look-ups: lane 8 i + e takes 16 tokens of the i-th of four tiles.  Under load
+      // a read takes several thousand cycles, so the pages of the next four tiles are read
+      // ahead.  Four tiles take the places of those eight before them once P V of the tile four
+      // before the first of them is done.
+      const int ti = lane >> 3, e = lane & 7;
       uint32_t jg = 0;
       bool ok = true;
       C8Seg g;
       while (ok && take_seg(g) && !(g.flags & C8Seg::kEnd)) {
         const int32_t kv = g.ctx + g.rows;
-        const float *scales = lane < 8 ? a.k_scale : a.v_scale;
-        auto fetch = [&](int j, int32_t &at) -> int32_t {  // the page of a token that is read, its place there (-1: none)
-          at = -1;
-          if (j >= g.n || lane >= 16) return -1;
-          int32_t t = g.tile(j) * kC8T + 16 * (lane & 7);
-          if (!g.wants(a, t)) {
-            if (t >= kv || t + 16 <= g.back || g.back >= kv) return -1;
-            t = g.back;  // the first of them that is
-          }
-          const int32_t pg = fast_div(a.seqs.page, t);
-          at = t - pg * a.seqs.page.d;
-          return a.seqs.table[(int64_t)g.s * a.seqs.table_cols + pg];
+        // the first token that is read of this lane's 16 of tile j, -1: none
+        auto token = [&](int j) -> int32_t {
+          if (j >= g.n) return -1;
+          const int32_t t = g.tile(j) * kC8T + 16 * e;
+          if (g.wants(a, t)) return t;
+          return t < kv && t + 16 > g.back && g.back < kv ? g.back : -1;
         };
-        int32_t at = 0, at1 = 0, at2 = 0;
-        int32_t page = fetch(0, at), page1 = fetch(1, at1);
-        for (int j = 0; j < g.n; ++j, ++jg) {
-          const int32_t page2 = fetch(j + 2, at2);
+        auto page_of = [&](int32_t t) -> int32_t {
+          return t < 0 ? 0 : a.seqs.table[(int64_t)g.s * a.seqs.table_cols + fast_div(a.seqs.page, t)];
+        };
+        int32_t t = token(ti), page = page_of(t);
+        for (int j = 0; j < g.n; j += 4) {
+          const int32_t t_next = token(j + 4 + ti), page_next = page_of(t_next);
+          const int count = min(4, g.n - j);
+          const uint32_t at = (jg + (uint32_t)ti) % kC8Ahead;
+          // (P V of tile jg cannot have been done, and that of tile jg - 8 has been waited for)
           if (jg >= 4 && !warp_wait(sm32(&C.pv_done[jg & 3u]), ((jg >> 2) & 1u) ^ 1u, lim, abort_flag)) {
             ok = false;
             break;
           }
-          __syncwarp();
-          if (lane < 16) {
-            const bool there = (uint32_t)page < (uint32_t)a.seqs.pool_pages;
-            if (!there && at >= 0) report_error(a.status, kErrTokenRange, g.s);
-            const int64_t block = there ? (int64_t)((page * a.seqs.page.d + at) >> a.unit_log) * a.nkv + g.kvh : 0;
-            cp_async4(sm32(&C.scales[jg % G::kScales][lane >> 3][lane & 7]), scales + block, there ? 4u : 0u);
+          if (ti < count) {
+            const bool there = t >= 0 && (uint32_t)page < (uint32_t)a.seqs.pool_pages;
+            if (t >= 0 && !there) report_error(a.status, kErrTokenRange, g.s);
+            const int32_t slot = there ? page * a.seqs.page.d + (t - fast_div(a.seqs.page, t) * a.seqs.page.d) : -1;
+            C.slots[at][e] = slot;
+            mbar_arrive(sm32(&C.looked[at]));
+            const int64_t block = there ? (int64_t)(slot >> a.unit_log) * a.nkv + g.kvh : 0;
+            cp_async4(sm32(&C.scales[at][0][e]), a.k_scale + block, there ? 4u : 0u);
+            cp_async4(sm32(&C.scales[at][1][e]), a.v_scale + block, there ? 4u : 0u);
+            cp_async_arrive(sm32(&C.scaled[at]));
           }
-          cp_async_arrive(sm32(&C.scaled[jg % G::kScales]));
-          page = page1;
-          at = at1;
-          page1 = page2;
-          at1 = at2;
+          jg += (uint32_t)count;
+          t = t_next;
+          page = page_next;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -751,6 +748,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     const int w = warp >> 2, wq = warp & 3, tk = wq * 32 + lane;
     const int n0 = G::kTurns ? 0 : w * kCols;  // this group's first row
     float *const less_ref = C.less_ref + w * kCols, *const alpha = C.alpha + w * kCols;
+    float *const inverse = G::kTurns ? C.mix + 2 * R : C.alpha;
     const uint32_t lane_base = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t my_o = lane_base + (G::kTurns ? w * G::kOCols : (uint32_t)n0);
     // P V of tile i.  A warp has waited for tile i - 4 (or a later one) by then, so of a
@@ -863,7 +861,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             for (int i = 0; i < kOut; ++i) {
               const int64_t where = C.where[c + i];
               if (where < 0) continue;
-              const float y = x[i] * C.inv[c + i];
+              const float y = x[i] * inverse[c + i];
               if (whole) a.out[where + d] = (uint16_t)f32_to_bf16(y);
               else part_o[where + d] = y;
             }
@@ -940,11 +938,11 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         const int32_t t0 = g.tile(j) * kC8T;
         const bool masked = is_masked(t0);
         const uint32_t see = masked ? sees(t0 + tk) : 0xFFFFFFFFu;
-        warp_wait(sm32(&C.scaled[jg % G::kScales]), (jg / (uint32_t)G::kScales) & 1u, lim, abort_flag);
+        warp_wait(sm32(&C.scaled[jg % kC8Ahead]), (jg / kC8Ahead) & 1u, lim, abort_flag);
         warp_wait(sm32(&C.s_full[b]), (jg / (uint32_t)G::kS) & 1u, lim, abort_flag);
         tc_fence_after();
         __syncwarp();
-        float ks = C.scales[jg % G::kScales][0][tk >> 4], vs = C.scales[jg % G::kScales][1][tk >> 4];
+        float ks = C.scales[jg % kC8Ahead][0][tk >> 4], vs = C.scales[jg % kC8Ahead][1][tk >> 4];
         if (!(ks >= 0.f && ks < INFINITY && vs >= 0.f && vs < INFINITY)) {
           if (see != 0u) report_error(a.status, kErrNonFinite, g.s);
           ks = vs = 0.f;
@@ -1155,7 +1153,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           ref = -C.less_ref[n];
           all = sum_of(n / kCols, n % kCols);
         }
-        C.inv[n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
+        inverse[n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
         int64_t where = -1;
         if (m0 + n < m_all) {
           const int32_t j = fast_div(plan.group_div, m0 + n), head = g.kvh * a.group + (m0 + n - j * a.group);
