@@ -40,7 +40,6 @@ constexpr int kC8Plan = kC8Look + 1;   // walks the CTA's share
 constexpr int kC8Warps = kC8Plan + 1, kC8Threads = 32 * kC8Warps;
 constexpr int kC8Readers = kC8Plan;    // warps that take the walk's parts
 constexpr int kC8Segs = 4;             // parts it is ahead by
-constexpr int kC8Ahead = 8;            // tiles whose pages and scales are held
 constexpr int kC8T = 128;        // tokens of a tile: the MMAs' M
 constexpr int kC8MostRows = 64;  // rows of a unit at most
 constexpr int kC8MaxCtas = 160;
@@ -67,6 +66,9 @@ struct C8Geom {
   // Registers of the softmax's threads and of the others, of 128 a thread at the launch: 32
   // rows a thread do not fit those, and every spilled value would queue behind the copies.
   static constexpr int kSoftRegs = kCols < 32 ? 128 : 168, kOtherRegs = 256 - kSoftRegs;
+  // P V's barriers: as many tiles as the look-ups may lead by.  The pages and scales of twice
+  // as many are held.
+  static constexpr uint32_t kPv = HD == 128 ? 8 : 4, kAhead = 2 * kPv;
   static constexpr uint32_t kQBytes = (kHalves * kQBox + 1023) / 1024 * 1024;
   static constexpr uint32_t kPOff = kQBytes, kRingOff = kPOff + 2 * kBox, kCtrlOff = kRingOff + kSlots * kSlot;
   static constexpr uint32_t kOCols = kHalves * kN, kSCol = kOs * kOCols;  // TMEM: O's halves, then S
@@ -85,7 +87,9 @@ struct C8Seq {
 // How the launch shares its work out.
 struct C8Plan {
   FastDiv group_div;
-  int32_t team_log;  // log2 of the CTAs that take units of rows side by side
+  // A team of CTAs takes the same tiles of as many units: log2 of the units of rows, and of
+  // the KV heads, side by side.
+  int32_t row_log, head_log;
   int32_t span;      // rows of a sequence that a unit holds of, at most
 };
 
@@ -106,8 +110,8 @@ __device__ __forceinline__ C8Seq c8_seq(const Cache8Args &a, const C8Plan &p, co
     const int64_t span = (int64_t)a.window + (a.seqs.mask ? q.v.rows : p.span);
     q.tiles = (int32_t)min((int64_t)q.tiles, first_tiles(a, q.v) + (span + kC8T - 1) / kC8T + 1);
   }
-  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + (R << p.team_log) - 1) >> (kLog + p.team_log));
-  q.count = q.tiles > 0 ? (int64_t)(q.tiles + kC8Start) * q.m_tiles * a.nkv : 0;
+  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + (R << p.row_log) - 1) >> (kLog + p.row_log));
+  q.count = q.tiles > 0 ? (int64_t)(q.tiles + kC8Start) * q.m_tiles * (a.nkv >> p.head_log) : 0;
   return q;
 }
 
@@ -159,7 +163,7 @@ struct C8Walk {
       ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
     }
     const int32_t length = q.tiles + kC8Start;
-    int32_t unit;  // (KV head, team of units of rows)
+    int32_t unit;  // (team of KV heads, team of units of rows)
     if ((off >> 31) == 0) unit = (int32_t)((uint32_t)off / (uint32_t)length);
     else unit = (int32_t)(off / length);
     const int32_t from = (int32_t)(off - (int64_t)unit * length);
@@ -168,8 +172,9 @@ struct C8Walk {
     left -= part;
     const int32_t i0 = max(0, from - kC8Start), take = max(0, from + part - kC8Start) - i0;
     g.s = s;
-    g.kvh = unit / q.m_tiles;
-    const int32_t mt = ((unit - g.kvh * q.m_tiles) << p.team_log) + (int32_t)(blockIdx.x & ((1u << p.team_log) - 1u));
+    const int32_t heads = unit / q.m_tiles, rank = (int32_t)blockIdx.x & ((1 << (p.row_log + p.head_log)) - 1);
+    g.kvh = (heads << p.head_log) + (rank >> p.row_log);
+    const int32_t mt = ((unit - heads * q.m_tiles) << p.row_log) + (rank & ((1 << p.row_log) - 1));
     g.row0 = q.v.row0;
     g.rows = q.v.rows;
     g.ctx = q.v.ctx;
@@ -197,7 +202,7 @@ struct C8Walk {
   }
 };
 
-template <int kMix>
+template <int kMix, int kAhead>
 struct C8Ctrl {
   float factor[kC8MostRows];    // log2 units a unit of S and ks
   float less_ref[kC8MostRows];  // [group][its rows]: the reference, negated
@@ -208,22 +213,22 @@ struct C8Ctrl {
   int64_t where[kC8MostRows];   // a row's place in the output
   int32_t depth[kC8MostRows];
   C8Seg segs[kC8Segs];
-  // [tile % kC8Ahead][16 tokens]: the pool's row of the first that is read (-1: none), scales
-  int32_t slots[kC8Ahead][8];
-  float scales[kC8Ahead][2][8];
-  uint64_t full[10], empty[10], looked[kC8Ahead], scaled[kC8Ahead];
-  uint64_t s_full[4], s_free[4], p_ready[2], pv_done[4];
+  // [tile % kAhead][16 tokens]: the pool's row of the first that is read (-1: none), scales
+  int32_t slots[kAhead][8];
+  float scales[kAhead][2][8];
+  uint64_t full[10], empty[10], looked[kAhead], scaled[kAhead];
+  uint64_t s_full[4], s_free[4], p_ready[2], pv_done[kAhead / 2];
   uint64_t q_full, o_free, drain[2], seg_full[kC8Segs], seg_free[kC8Segs];
   int32_t bad[2], abort;
   uint32_t tmem_base;
 };
-template <int kMix>
+template <int kMix, int kAhead>
 union C8Scratch {  // the plan is made before anything else
-  C8Ctrl<kMix> c;
+  C8Ctrl<kMix, kAhead> c;
   ShareScratch share;
 };
 template <int HD, int R>
-constexpr size_t c8_smem() { return C8Geom<HD, R>::kCtrlOff + sizeof(C8Scratch<C8Geom<HD, R>::kMix>); }
+constexpr size_t c8_smem() { return C8Geom<HD, R>::kCtrlOff + sizeof(C8Scratch<C8Geom<HD, R>::kMix, C8Geom<HD, R>::kAhead>); }
 static_assert(c8_smem<256, 64>() <= 232448 && c8_smem<128, 64>() <= 232448, "227 KiB per CTA");
 
 // Ring position of tile j's V among a part's n tiles, counted from the part's first copy:
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(kC8Threads, 1)
 cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml, float *__restrict__ part_o, int32_t *__restrict__ row_seq) {
   using G = C8Geom<HD, R>;
   extern __shared__ __align__(1024) uint8_t c8_shared[];
-  auto &both = *reinterpret_cast<C8Scratch<G::kMix> *>(c8_shared + G::kCtrlOff);
+  auto &both = *reinterpret_cast<C8Scratch<G::kMix, G::kAhead> *>(c8_shared + G::kCtrlOff);
   auto &C = both.c;
   const uint32_t sQ = sm32(c8_shared), sP = sm32(c8_shared + G::kPOff), sRing = sm32(c8_shared + G::kRingOff);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -421,7 +426,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
 
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
   // ---- the plan (CTA 0 also leaves the sums for the joining launch)
-  const uint32_t teams = gridDim.x >> plan.team_log, my_team = blockIdx.x >> plan.team_log;
+  const int team_log = plan.row_log + plan.head_log;
+  const uint32_t teams = gridDim.x >> team_log, my_team = blockIdx.x >> team_log;
   const FoundShare found = find_share(a.seqs.n_seqs, kC8Threads, teams, my_team, both.share, [&](int32_t s) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
     return c8_seq<R>(a, plan, read_seq(a.seqs, s)).count;
@@ -448,14 +454,14 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       mbar_init(sm32(&C.full[i]), 32 * kC8Prod);
       mbar_init(sm32(&C.empty[i]), 1);
     }
-    for (int i = 0; i < kC8Ahead; ++i) {
+    for (int i = 0; i < (int)G::kPv; ++i) mbar_init(sm32(&C.pv_done[i]), 1);
+    for (int i = 0; i < (int)G::kAhead; ++i) {
       mbar_init(sm32(&C.looked[i]), 8);
       mbar_init(sm32(&C.scaled[i]), 8);
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(sm32(&C.s_full[b]), 1);
       mbar_init(sm32(&C.s_free[b]), kC8Soft / G::kOs);
-      mbar_init(sm32(&C.pv_done[b]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sm32(&C.p_ready[b]), kC8Soft / G::kOs);
@@ -515,8 +521,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       int j = 0;         // the tile of this copy
       bool is_k = true;
       for (int i = 0; i < 2 * g.n; ++i) {
-        const uint32_t at = (jg + (uint32_t)j) % kC8Ahead;
-        if (!warp_wait(sm32(&C.looked[at]), ((jg + (uint32_t)j) / kC8Ahead) & 1u, lim, abort_flag) ||
+        const uint32_t at = (jg + (uint32_t)j) % G::kAhead;
+        if (!warp_wait(sm32(&C.looked[at]), ((jg + (uint32_t)j) / G::kAhead) & 1u, lim, abort_flag) ||
             !warp_wait(sm32(&C.empty[slot]), phase ^ 1u, lim, abort_flag)) {
           ok = false;
           break;
@@ -592,7 +598,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     } else if (warp == kC8Look) {
       // ---- the look-ups: lane 8 i + e takes 16 tokens of the i-th of four tiles.  Under load
       // a read takes several thousand cycles, so the pages of the next four tiles are read
-      // ahead.  Four tiles take the places of those eight before them once P V of the tile four
+      // ahead.  Four tiles take the places of those kAhead before them once P V of the tile kPv
       // before the first of them is done.
       const int ti = lane >> 3, e = lane & 7;
       uint32_t jg = 0;
@@ -614,9 +620,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         for (int j = 0; j < g.n; j += 4) {
           const int32_t t_next = token(j + 4 + ti), page_next = page_of(t_next);
           const int count = min(4, g.n - j);
-          const uint32_t at = (jg + (uint32_t)ti) % kC8Ahead;
-          // (P V of tile jg cannot have been done, and that of tile jg - 8 has been waited for)
-          if (jg >= 4 && !warp_wait(sm32(&C.pv_done[jg & 3u]), ((jg >> 2) & 1u) ^ 1u, lim, abort_flag)) {
+          const uint32_t at = (jg + (uint32_t)ti) % G::kAhead;
+          // (P V of tile jg cannot have been done, and that of tile jg - 2 kPv has been waited for)
+          if (jg >= G::kPv && !warp_wait(sm32(&C.pv_done[jg % G::kPv]), ((jg / G::kPv) & 1u) ^ 1u, lim, abort_flag)) {
             ok = false;
             break;
           }
@@ -684,7 +690,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           ++part;
           for (int j = 0; j < g.n; ++j, ++jg) {
             if (jg >= (uint32_t)G::kS && !wait(C.s_free[b], b_phase)) break;  // tile j - kS is read
-            if (jg >= 4 && !wait(C.pv_done[jg & 3u], ((jg >> 2) & 1u) ^ 1u)) break;
+            if (jg >= 4 && !wait(C.pv_done[(jg - 4u) % G::kPv], ((jg - 4u) / G::kPv) & 1u)) break;
             if (j > 0) step(j == 1 ? 1u : 2u);
             if (!landed()) break;
             const uint32_t d = tmem + G::kSCol + b * G::kN, k_lo = r_lo + slot * (G::kSlot >> 4);
@@ -726,7 +732,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
                 mma_e4m3(o + (uint32_t)h * G::kN, desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi),
                          desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
             mma_commit(sm32(&C.empty[slot]));
-            mma_commit(sm32(&C.pv_done[jg & 3u]));
+            mma_commit(sm32(&C.pv_done[jg % G::kPv]));
             }
             __syncwarp();
           }
@@ -753,7 +759,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     const uint32_t my_o = lane_base + (G::kTurns ? w * G::kOCols : (uint32_t)n0);
     // P V of tile i.  A warp has waited for tile i - 4 (or a later one) by then, so of a
     // barrier no phase but the last two is ever in question.
-    auto wait_pv = [&](uint32_t i) { warp_wait(sm32(&C.pv_done[i & 3u]), (i >> 2) & 1u, lim, abort_flag); };
+    auto wait_pv = [&](uint32_t i) { warp_wait(sm32(&C.pv_done[i % G::kPv]), (i / G::kPv) & 1u, lim, abort_flag); };
     // This warp's rows of a part's Q, split into two e4m3 terms, with what goes with a row.
     auto load_q = [&](const C8Seg &e) {
       const int32_t m_all = e.rows * a.group;
@@ -938,11 +944,11 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         const int32_t t0 = g.tile(j) * kC8T;
         const bool masked = is_masked(t0);
         const uint32_t see = masked ? sees(t0 + tk) : 0xFFFFFFFFu;
-        warp_wait(sm32(&C.scaled[jg % kC8Ahead]), (jg / kC8Ahead) & 1u, lim, abort_flag);
+        warp_wait(sm32(&C.scaled[jg % G::kAhead]), (jg / G::kAhead) & 1u, lim, abort_flag);
         warp_wait(sm32(&C.s_full[b]), (jg / (uint32_t)G::kS) & 1u, lim, abort_flag);
         tc_fence_after();
         __syncwarp();
-        float ks = C.scales[jg % kC8Ahead][0][tk >> 4], vs = C.scales[jg % kC8Ahead][1][tk >> 4];
+        float ks = C.scales[jg % G::kAhead][0][tk >> 4], vs = C.scales[jg % G::kAhead][1][tk >> 4];
         if (!(ks >= 0.f && ks < INFINITY && vs >= 0.f && vs < INFINITY)) {
           if (see != 0u) report_error(a.status, kErrNonFinite, g.s);
           ks = vs = 0.f;
@@ -1205,9 +1211,9 @@ cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t teams, const i
     const int32_t mt = (int32_t)(m / R);
     s = at;
     r = (int32_t)(m % R);
-    rank = mt & ((1 << plan.team_log) - 1);
+    rank = ((kvh & ((1 << plan.head_log) - 1)) << plan.row_log) + (mt & ((1 << plan.row_log) - 1));
     tiles = q.tiles;
-    u0 = ((int64_t)kvh * q.m_tiles + (mt >> plan.team_log)) * (tiles + kC8Start) + kC8Start;
+    u0 = ((int64_t)(kvh >> plan.head_log) * q.m_tiles + (mt >> plan.row_log)) * (tiles + kC8Start) + kC8Start;
   };
   if (row >= 0) place(seq_of_row(a.seqs, row));
   grid_dependency_sync();
@@ -1244,7 +1250,7 @@ cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t teams, const i
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         const int32_t at = c + e * kGroups;
-        const int64_t part = (((int64_t)min(at, c1) << plan.team_log) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
+        const int64_t part = (((int64_t)min(at, c1) << (plan.row_log + plan.head_log)) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
         ml[e] = part_ml[part * R + r];
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) x[e][i] = part_o[(part * R + r) * (HD / 4) + 32 * i + lane];
@@ -1319,9 +1325,14 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
   float *o = reinterpret_cast<float *>(ws + base_bytes(a.seqs.n_seqs) + ml_bytes(R));
   int32_t *row_seq = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(o) + o_bytes(R, HD));
   const int64_t mean_rows = (int64_t)a.seqs.n_rows * a.group / a.seqs.n_seqs;
-  const int team_log = R < 64 ? 0 : mean_rows >= 224 ? 2 : mean_rows >= 96 ? 1 : 0;
+  // Units of rows side by side read the same K and V at the same time, KV heads side by side
+  // neighbouring pieces of the same rows.
+  const int row_log = R < 64 ? 0 : mean_rows >= 224 ? 2 : mean_rows >= 96 ? 1 : 0;
+  int head_log = 0;
+  while (row_log == 0 && head_log < 3 && a.nkv % (2 << head_log) == 0) ++head_log;
+  const int team_log = row_log + head_log;
   const int ctas = ((device_sm_count() < kC8MaxCtas ? device_sm_count() : kC8MaxCtas) >> team_log) << team_log;
-  const C8Plan plan = {make_fast_div(a.group), team_log, R / a.group + 2};
+  const C8Plan plan = {make_fast_div(a.group), row_log, head_log, R / a.group + 2};
   cudaError_t r = launch_dependent(cache8_attn_kernel<HD, R>, dim3((unsigned)ctas), dim3(kC8Threads), c8_smem<HD, R>(), stream, 1u, a,
                                    plan, base, ml, o, row_seq);
   // a table of one tile leaves no unit to share
