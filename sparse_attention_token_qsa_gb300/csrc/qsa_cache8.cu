@@ -80,16 +80,14 @@ struct C8Geom {
 
 struct C8Seq {
   SeqView v;
-  int32_t tiles, m_tiles;  // in every unit's list; units of rows, a team's together
-  int64_t count;           // tiles of all its units, their starts included
+  int32_t tiles, m_tiles;  // in every unit's list; units of rows
+  int64_t count;           // tiles of all its units, their starts included, a team's counted once
 };
 
 // How the launch shares its work out.
 struct C8Plan {
   FastDiv group_div;
-  // A team of CTAs takes the same tiles of as many units: log2 of the units of rows, and of
-  // the KV heads, side by side.
-  int32_t row_log, head_log;
+  int32_t head_log;  // log2 of the CTAs of a team, which take the same tiles of as many KV heads
   int32_t span;      // rows of a sequence that a unit holds of, at most
 };
 
@@ -110,7 +108,7 @@ __device__ __forceinline__ C8Seq c8_seq(const Cache8Args &a, const C8Plan &p, co
     const int64_t span = (int64_t)a.window + (a.seqs.mask ? q.v.rows : p.span);
     q.tiles = (int32_t)min((int64_t)q.tiles, first_tiles(a, q.v) + (span + kC8T - 1) / kC8T + 1);
   }
-  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + (R << p.row_log) - 1) >> (kLog + p.row_log));
+  q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + R - 1) >> kLog);
   q.count = q.tiles > 0 ? (int64_t)(q.tiles + kC8Start) * q.m_tiles * (a.nkv >> p.head_log) : 0;
   return q;
 }
@@ -119,7 +117,7 @@ __device__ __forceinline__ C8Seq c8_seq(const Cache8Args &a, const C8Plan &p, co
 struct C8Seg {
   int32_t s, kvh, m0;         // sequence, KV head, this CTA's unit's first row
   int32_t n;                  // tiles to process
-  int32_t first, gap, near;   // tile i of the part is token tile first + i, gap more from `near` on
+  int32_t first, gap, near;   // tile i of the part is token tile first + i, gap less from `near` on
   int32_t back;               // no row sees the tokens from n_first to before `back`
   int32_t row0, rows, ctx;    // the sequence's
   int32_t flags;
@@ -129,7 +127,7 @@ struct C8Seg {
     kEmpty = 4,  // none of its tiles (a share that ends in a unit's start), or no rows
     kEnd = 8     // no part: the walk is over
   };
-  __device__ int32_t tile(int i) const { return first + i + (i >= near ? gap : 0); }
+  __device__ int32_t tile(int i) const { return first + i - (i >= near ? gap : 0); }
   // whether token t may be seen by a row (others are not read)
   __device__ bool wants(const Cache8Args &a, int32_t t) const { return t < ctx + rows && (t < a.n_first || t >= back); }
 };
@@ -163,7 +161,7 @@ struct C8Walk {
       ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
     }
     const int32_t length = q.tiles + kC8Start;
-    int32_t unit;  // (team of KV heads, team of units of rows)
+    int32_t unit;  // (team of KV heads, rows)
     if ((off >> 31) == 0) unit = (int32_t)((uint32_t)off / (uint32_t)length);
     else unit = (int32_t)(off / length);
     const int32_t from = (int32_t)(off - (int64_t)unit * length);
@@ -172,9 +170,8 @@ struct C8Walk {
     left -= part;
     const int32_t i0 = max(0, from - kC8Start), take = max(0, from + part - kC8Start) - i0;
     g.s = s;
-    const int32_t heads = unit / q.m_tiles, rank = (int32_t)blockIdx.x & ((1 << (p.row_log + p.head_log)) - 1);
-    g.kvh = (heads << p.head_log) + (rank >> p.row_log);
-    const int32_t mt = ((unit - heads * q.m_tiles) << p.row_log) + (rank & ((1 << p.row_log) - 1));
+    const int32_t heads = unit / q.m_tiles, mt = unit - heads * q.m_tiles;
+    g.kvh = (heads << p.head_log) + ((int32_t)blockIdx.x & ((1 << p.head_log) - 1));
     g.row0 = q.v.row0;
     g.rows = q.v.rows;
     g.ctx = q.v.ctx;
@@ -191,13 +188,21 @@ struct C8Walk {
     const bool chain = a.seqs.mask == nullptr;
     const int32_t j0 = fast_div(p.group_div, (int32_t)m0), j1 = fast_div(p.group_div, (int32_t)(min(m0 + R, m_all) - 1));
     const int32_t end = (q.v.ctx + (chain ? j1 + 1 : q.v.rows) + kC8T - 1) / kC8T;
+    int32_t count = end;
+    g.near = 0x7FFFFFFF;
     if (a.window > 0) {
-      g.near = min(end, first_tiles(a, q.v));
+      // Where they leave tiles out between them, the window's come first: a reference is to
+      // be taken from a tile that the rows see much of.
       g.back = max(0, q.v.ctx + (chain ? j0 : 0) - (a.window - 1));
-      g.gap = max(0, min(g.back / kC8T, end) - g.near);
+      const int32_t near = min(end, first_tiles(a, q.v)), from_back = min(g.back / kC8T, end);
+      if (from_back > near) {
+        count = end - from_back + near;
+        g.first = i0 + from_back;
+        g.near = max(0, end - from_back - i0);
+        g.gap = end;
+      }
     }
-    g.n = max(0, min(take, end - g.gap - i0));
-    g.near = max(0, g.near - i0);
+    g.n = max(0, min(take, count - i0));
     return g;
   }
 };
@@ -426,8 +431,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
 
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
   // ---- the plan (CTA 0 also leaves the sums for the joining launch)
-  const int team_log = plan.row_log + plan.head_log;
-  const uint32_t teams = gridDim.x >> team_log, my_team = blockIdx.x >> team_log;
+  const uint32_t teams = gridDim.x >> plan.head_log, my_team = blockIdx.x >> plan.head_log;
   const FoundShare found = find_share(a.seqs.n_seqs, kC8Threads, teams, my_team, both.share, [&](int32_t s) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
     return c8_seq<R>(a, plan, read_seq(a.seqs, s)).count;
@@ -460,7 +464,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       mbar_init(sm32(&C.scaled[i]), 8);
     }
     for (int b = 0; b < 4; ++b) {
-      mbar_init(sm32(&C.s_full[b]), 1);
+      mbar_init(sm32(&C.s_full[b]), 2);
       mbar_init(sm32(&C.s_free[b]), kC8Soft / G::kOs);
     }
     for (int b = 0; b < 2; ++b) {
@@ -692,7 +696,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             if (jg >= (uint32_t)G::kS && !wait(C.s_free[b], b_phase)) break;  // tile j - kS is read
             if (jg >= 4 && !wait(C.pv_done[(jg - 4u) % G::kPv], ((jg - 4u) / G::kPv) & 1u)) break;
             if (j > 0) step(j == 1 ? 1u : 2u);
-            if (!landed()) break;
+            // (the tile's scales: one wait less for the many)
+            if (!wait(C.scaled[jg % G::kAhead], (jg / G::kAhead) & 1u) || !landed()) break;
             const uint32_t d = tmem + G::kSCol + b * G::kN, k_lo = r_lo + slot * (G::kSlot >> 4);
             if (lead) {
 #pragma unroll
@@ -703,6 +708,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             }
             mma_commit(sm32(&C.empty[slot]));
             mma_commit(sm32(&C.s_full[b]));
+            mbar_arrive(sm32(&C.s_full[b]));
             }
             __syncwarp();
             if (++b == (uint32_t)G::kS) {
@@ -750,7 +756,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     // ---- softmax: thread tk has the tile's token tk (TMEM lane) and, at the end, dims tk
     // and tk + 128.  Group w takes every other tile, or its rows of each.  After an abort
     // every wait returns at once, and the loops and barriers run on to the end.
-    constexpr int kCols = G::kCols, kAtOnce = kCols < 16 ? kCols : 16;  // rows of a TMEM load
+    constexpr int kCols = G::kCols, kAtOnce = kCols;  // rows of a TMEM load
     const int w = warp >> 2, wq = warp & 3, tk = wq * 32 + lane;
     const int n0 = G::kTurns ? 0 : w * kCols;  // this group's first row
     float *const less_ref = C.less_ref + w * kCols, *const alpha = C.alpha + w * kCols;
@@ -761,26 +767,27 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     // barrier no phase but the last two is ever in question.
     auto wait_pv = [&](uint32_t i) { warp_wait(sm32(&C.pv_done[i % G::kPv]), (i / G::kPv) & 1u, lim, abort_flag); };
     // This warp's rows of a part's Q, split into two e4m3 terms, with what goes with a row.
-    auto load_q = [&](const C8Seg &e) {
+    constexpr int kLanes = HD / 8, kPer = 32 / kLanes;  // lanes a row, rows a warp takes at once
+    constexpr int kTimes = (R + kC8Soft * kPer - 1) / (kC8Soft * kPer);
+    const int ch = lane % kLanes, sub = lane / kLanes;
+    auto row_of = [&](int i) { return (i * kC8Soft + warp) * kPer + sub; };
+    uint4 raw[kTimes];
+    auto fetch_q = [&](const C8Seg &e) {
       const int32_t m_all = e.rows * a.group;
-      constexpr int kLanes = HD / 8, kPer = 32 / kLanes;  // lanes a row, rows a warp takes at once
-      constexpr int kTimes = (R + kC8Soft * kPer - 1) / (kC8Soft * kPer), kBatch = kTimes < 4 ? kTimes : 4;
-      const int ch = lane % kLanes, sub = lane / kLanes;
-      auto row_of = [&](int i) { return (i * kC8Soft + warp) * kPer + sub; };
-#pragma unroll 1
-      for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
-      uint4 raw[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int n = row_of(i0 + i);
+      for (int i = 0; i < kTimes; ++i) {
+        const int n = row_of(i);
         const bool valid = n < R && e.m0 + n < m_all;
         const int32_t m = valid ? e.m0 + n : 0, j = fast_div(plan.group_div, m);
         const int32_t head = e.kvh * a.group + (m - j * a.group);
         raw[i] = valid ? ldg_v4(a.q + (int64_t)(e.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch) : make_uint4(0, 0, 0, 0);
       }
+    };
+    auto store_q = [&](const C8Seg &e) {
+      const int32_t m_all = e.rows * a.group;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int n = row_of(i0 + i);
+      for (int i = 0; i < kTimes; ++i) {
+        const int n = row_of(i);
         const bool mine = n < R, valid = mine && e.m0 + n < m_all;
         float x[8], amax = 0.f;
         unpack8(raw[i], x);
@@ -823,7 +830,6 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
 #pragma unroll
           for (int o = 0; o < G::kOs; ++o) C.less_ref[o * kCols + n] = valid ? -kC8Unset : -kC8Nobody;
         }
-      }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -885,8 +891,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     };
     // Parts overlap: the next one's Q is fetched before this one's output is written.
     bool more = advance(next);
+    if (more && next.n > 0) fetch_q(next);
     while (true) {
-      if (more && next.n > 0) load_q(next);
+      if (more && next.n > 0) store_q(next);
       write_out();
       if (!more) break;
       g = next;
@@ -898,8 +905,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       const int32_t j0 = fast_div(plan.group_div, m0), j1 = fast_div(plan.group_div, max(0, min(m0 + R, m_all) - 1));
       // tokens below `clear` and, of a window, from `old` on or below n_first are seen by every row
       const int32_t clear = chain ? g.ctx + j0 + 1 : g.ctx;
-      const int32_t old = a.window > 0 ? g.ctx + (chain ? j1 : g.rows - 1) - (a.window - 1) : 0;
-      auto is_masked = [&](int32_t t0) { return t0 + kC8T > clear || (t0 < old && t0 + kC8T > a.n_first); };
+      const int32_t old = a.window > 0 ? max(0, g.ctx + (chain ? j1 : g.rows - 1) - (a.window - 1)) : 0;
+      const int32_t clear_tile = clear / kC8T, old_tile = (old + kC8T - 1) / kC8T, first_tile = a.n_first / kC8T;
+      auto is_masked = [&](int32_t tile) { return tile >= clear_tile || (tile < old_tile && tile >= first_tile); };
       // the columns of rows [from, to) of the sequence, among this group's
       auto columns = [&](int32_t from, int32_t to) -> uint32_t {
         const int lo = min(max(from * a.group - m0 - n0, 0), kCols), hi = min(max(to * a.group - m0 - n0, 0), kCols);
@@ -941,10 +949,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       for (int j = 0; j < g.n; ++j, ++jg) {
         if (G::kTurns && (int)(jg & 1u) != w) continue;
         const uint32_t b = jg % (uint32_t)G::kS, sc = lane_base + G::kSCol + b * G::kN + n0;
-        const int32_t t0 = g.tile(j) * kC8T;
-        const bool masked = is_masked(t0);
-        const uint32_t see = masked ? sees(t0 + tk) : 0xFFFFFFFFu;
-        warp_wait(sm32(&C.scaled[jg % G::kAhead]), (jg / G::kAhead) & 1u, lim, abort_flag);
+        const int32_t tile = g.tile(j);
+        const bool masked = is_masked(tile);
+        const uint32_t see = masked ? sees(tile * kC8T + tk) : 0xFFFFFFFFu;
         warp_wait(sm32(&C.s_full[b]), (jg / (uint32_t)G::kS) & 1u, lim, abort_flag);
         tc_fence_after();
         __syncwarp();
@@ -954,6 +961,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           ks = vs = 0.f;
         }
         const float vx = fmaxf(vs, kC8Least);
+        const bool p_free = jg < 2 || mbar_test(sm32(&C.pv_done[(jg - 2u) % G::kPv]), ((jg - 2u) / G::kPv) & 1u);
         uint8_t *const p_tile = c8_shared + G::kPOff + (jg & 1u) * G::kBox;
         float x[kCols];
         // Twice where references move: of the rows whose largest w of this tile is over 2^8,
@@ -984,7 +992,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             for (int i = 0; i < kCols; ++i) l[i] = ((see >> i) & 1u) ? x[i] + lv : -INFINITY;
             const float top = over_lanes<kCols>(l, lane, [](float p, float q) { return fmaxf(p, q); });
             // the warps' maxima meet in this group's bytes of the tile's P, which is written later
-            if (jg >= 2) wait_pv(jg - 2);
+            if (!__all_sync(0xffffffffu, p_free)) wait_pv(jg - 2);
             __syncwarp();
             auto spot = [&](int q, int i) {
               const int row = q * 32 + i;
@@ -1034,7 +1042,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sm32(&C.s_free[b]));
-        if (jg >= 2) wait_pv(jg - 2);  // P's buffer is free
+        if (!__all_sync(0xffffffffu, p_free)) wait_pv(jg - 2);  // P's buffer is free
         // The row of the P buffer that is this token's: the group's bytes of hi and of lo.
         // The sums keep 32 bits, as lse has to; the weights go to the two terms above.
         uint8_t *prow = p_tile + tk * 128;
@@ -1096,6 +1104,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         if (lane == 0) mbar_arrive(sm32(&C.p_ready[jg & 1u]));
       }
       ns += (uint32_t)(2 * g.n);
+      more = advance(next);
+      if (more && next.n > 0) fetch_q(next);
       bool fix = false;
       if (g.n > 0) {  // S and P V of every tile are done: Q may go, O may be read
         if (G::kTurns && g.n > 1) wait_pv(jg - 2);
@@ -1116,7 +1126,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             bool hit = false;
             for (int i = 0; i < g.n; ++i) {
               const int32_t t0 = g.tile(i) * kC8T;
-              if (!is_masked(t0)) continue;
+              if (!is_masked(g.tile(i))) continue;
               for (int32_t t = t0; t < min(kv, t0 + kC8T); ++t) {
                 const bool drafted = t >= g.ctx;
                 if (drafted && !sees_draft(mrow, j, t - g.ctx)) continue;
@@ -1170,7 +1180,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
         C.where[n] = where;
       }
-      more = advance(next);  // (its barrier: the part's references and sums are read)
+      soft_sync();  // the part's references and sums are read
     }
   }
 
@@ -1211,9 +1221,9 @@ cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t teams, const i
     const int32_t mt = (int32_t)(m / R);
     s = at;
     r = (int32_t)(m % R);
-    rank = ((kvh & ((1 << plan.head_log) - 1)) << plan.row_log) + (mt & ((1 << plan.row_log) - 1));
+    rank = kvh & ((1 << plan.head_log) - 1);
     tiles = q.tiles;
-    u0 = ((int64_t)(kvh >> plan.head_log) * q.m_tiles + (mt >> plan.row_log)) * (tiles + kC8Start) + kC8Start;
+    u0 = ((int64_t)(kvh >> plan.head_log) * q.m_tiles + mt) * (tiles + kC8Start) + kC8Start;
   };
   if (row >= 0) place(seq_of_row(a.seqs, row));
   grid_dependency_sync();
@@ -1250,7 +1260,7 @@ cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t teams, const i
 #pragma unroll
       for (int e = 0; e < kAhead; ++e) {
         const int32_t at = c + e * kGroups;
-        const int64_t part = (((int64_t)min(at, c1) << (plan.row_log + plan.head_log)) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
+        const int64_t part = (((int64_t)min(at, c1) << plan.head_log) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
         ml[e] = part_ml[part * R + r];
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) x[e][i] = part_o[(part * R + r) * (HD / 4) + 32 * i + lane];
@@ -1324,15 +1334,11 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
   float2 *ml = reinterpret_cast<float2 *>(ws + base_bytes(a.seqs.n_seqs));
   float *o = reinterpret_cast<float *>(ws + base_bytes(a.seqs.n_seqs) + ml_bytes(R));
   int32_t *row_seq = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(o) + o_bytes(R, HD));
-  const int64_t mean_rows = (int64_t)a.seqs.n_rows * a.group / a.seqs.n_seqs;
-  // Units of rows side by side read the same K and V at the same time, KV heads side by side
-  // neighbouring pieces of the same rows.
-  const int row_log = R < 64 ? 0 : mean_rows >= 224 ? 2 : mean_rows >= 96 ? 1 : 0;
+  // KV heads side by side read neighbouring pieces of the same rows.
   int head_log = 0;
-  while (row_log == 0 && head_log < 3 && a.nkv % (2 << head_log) == 0) ++head_log;
-  const int team_log = row_log + head_log;
-  const int ctas = ((device_sm_count() < kC8MaxCtas ? device_sm_count() : kC8MaxCtas) >> team_log) << team_log;
-  const C8Plan plan = {make_fast_div(a.group), row_log, head_log, R / a.group + 2};
+  while (head_log < 3 && a.nkv % (2 << head_log) == 0) ++head_log;
+  const int ctas = ((device_sm_count() < kC8MaxCtas ? device_sm_count() : kC8MaxCtas) >> head_log) << head_log;
+  const C8Plan plan = {make_fast_div(a.group), head_log, R / a.group + 2};
   cudaError_t r = launch_dependent(cache8_attn_kernel<HD, R>, dim3((unsigned)ctas), dim3(kC8Threads), c8_smem<HD, R>(), stream, 1u, a,
                                    plan, base, ml, o, row_seq);
   // a table of one tile leaves no unit to share
@@ -1343,7 +1349,7 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
   const bool many = ctas >= 8 * units;
   return launch_dependent(many ? cache8_join_kernel<HD, R, kC8JoinWarps> : cache8_join_kernel<HD, R, 1>,
                           dim3((unsigned)(many ? rows : (rows + kC8JoinWarps - 1) / kC8JoinWarps), (unsigned)a.nkv),
-                          dim3(32 * kC8JoinWarps), 0, stream, 1u, a, plan, (int32_t)(ctas >> team_log), base, ml,
+                          dim3(32 * kC8JoinWarps), 0, stream, 1u, a, plan, (int32_t)(ctas >> head_log), base, ml,
                           reinterpret_cast<const float4 *>(o), row_seq);
 }
 
