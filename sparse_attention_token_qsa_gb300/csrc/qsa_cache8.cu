@@ -767,17 +767,18 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     // barrier no phase but the last two is ever in question.
     auto wait_pv = [&](uint32_t i) { warp_wait(sm32(&C.pv_done[i % G::kPv]), (i / G::kPv) & 1u, lim, abort_flag); };
     // This warp's rows of a part's Q, split into two e4m3 terms, with what goes with a row.
+    // (In batches, the first of them fetched ahead: a part's code runs once or twice a
+    // launch, and its instructions cost as much to fetch as the rows.)
     constexpr int kLanes = HD / 8, kPer = 32 / kLanes;  // lanes a row, rows a warp takes at once
-    constexpr int kTimes = (R + kC8Soft * kPer - 1) / (kC8Soft * kPer);
+    constexpr int kTimes = (R + kC8Soft * kPer - 1) / (kC8Soft * kPer), kBatch = kTimes < 4 ? kTimes : 4;
     const int ch = lane % kLanes, sub = lane / kLanes;
     auto row_of = [&](int i) { return (i * kC8Soft + warp) * kPer + sub; };
-    uint4 raw[kTimes];
-    auto fetch_q = [&](const C8Seg &e) {
-      const int32_t m_all = e.rows * a.group;
+    uint4 raw[kBatch];
+    auto fetch_q = [&](const C8Seg &e, int i0) {
 #pragma unroll
-      for (int i = 0; i < kTimes; ++i) {
-        const int n = row_of(i);
-        const bool valid = n < R && e.m0 + n < m_all;
+      for (int i = 0; i < kBatch; ++i) {
+        const int n = row_of(i0 + i);
+        const bool valid = n < R && e.m0 + n < e.rows * a.group;
         const int32_t m = valid ? e.m0 + n : 0, j = fast_div(plan.group_div, m);
         const int32_t head = e.kvh * a.group + (m - j * a.group);
         raw[i] = valid ? ldg_v4(a.q + (int64_t)(e.row0 + j) * a.q_stride + (int64_t)head * HD + 8 * ch) : make_uint4(0, 0, 0, 0);
@@ -785,50 +786,55 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     };
     auto store_q = [&](const C8Seg &e) {
       const int32_t m_all = e.rows * a.group;
+#pragma unroll 1
+      for (int i0 = 0;;) {
 #pragma unroll
-      for (int i = 0; i < kTimes; ++i) {
-        const int n = row_of(i);
-        const bool mine = n < R, valid = mine && e.m0 + n < m_all;
-        float x[8], amax = 0.f;
-        unpack8(raw[i], x);
+        for (int i = 0; i < kBatch; ++i) {
+          const int n = row_of(i0 + i);
+          const bool mine = n < R, valid = mine && e.m0 + n < m_all;
+          // the largest magnitude; of a row with one that is not finite, that one, and NaN below
+          uint32_t top = __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu),
+                                  __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
+          top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(x[k]) < INFINITY ? fabsf(x[k]) : 0.f);
+          for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // the least power of two s with it <= 448 s = 1.75 * 2^8 s, and 1 / s
+          const int ex = max(-126, (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0));
+          const float s = __uint_as_float((uint32_t)(127 + ex) << 23), inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+          float x[8];
+          unpack8(raw[i], x);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // the least power of two s with amax <= 448 s = 1.75 * 2^8 s, and 1 / s
-        const uint32_t u = __float_as_uint(amax);
-        const int ex = max(-126, (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0));
-        const float s = __uint_as_float((uint32_t)(127 + ex) << 23), inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-        uint32_t hi[4], lo[4];
+          for (int k = 0; k < 4; ++k)  // (x + 0 x: an infinity becomes NaN, which the conversions keep)
+            split_e4m3(fmaf(x[2 * k], 0.f, x[2 * k]) * inv, fmaf(x[2 * k + 1], 0.f, x[2 * k + 1]) * inv, hi[k], lo[k]);
+          if (mine) {
+            auto at = [&](int row) {  // 8 bytes of a 128-byte row of a box, its 16-byte chunks swizzled
+              return c8_shared + (ch >> 4) * G::kQBox + row * 128 + (((ch >> 1) & 7) ^ (row & 7)) * 16 + (ch & 1) * 8;
+            };
+            *reinterpret_cast<uint2 *>(at(n)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2 *>(at(R + n)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if (ch == 0) {
+              C.factor[n] = a.scale_log2 * s;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // (x + 0 x: an infinity becomes NaN, which the conversions keep)
-          split_e4m3(fmaf(x[2 * k], 0.f, x[2 * k]) * inv, fmaf(x[2 * k + 1], 0.f, x[2 * k + 1]) * inv, hi[k], lo[k]);
-        if (mine) {
-          auto at = [&](int row) {  // 8 bytes of a 128-byte row of a box, its 16-byte chunks swizzled
-            const int byte = 8 * ch;
-            return c8_shared + (byte >> 7) * G::kQBox + row * 128 + (((byte >> 4) & 7) ^ (row & 7)) * 16 + (byte & 8);
-          };
-          *reinterpret_cast<uint2 *>(at(n)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-          *reinterpret_cast<uint2 *>(at(R + n)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+              for (int o = 0; o < G::kOs; ++o) C.less_ref[o * kCols + n] = valid ? -kC8Unset : -kC8Nobody;
+            }
+          }
         }
-        int32_t depth = 0;
-        if (a.window > 0 && a.seqs.mask != nullptr) {  // the row's drafted tokens, over its lanes
-          if (valid) {
-            const int32_t j = fast_div(plan.group_div, e.m0 + n);
-            const uint32_t *mrow = a.seqs.mask + (int64_t)(e.row0 + j) * a.seqs.mask_words;
-            for (int32_t k = ch; 32 * k < e.rows; k += kLanes) {
+        i0 += kBatch;
+        if (i0 >= kTimes) break;
+        fetch_q(e, i0);
+      }
+      if (a.window > 0 && a.seqs.mask != nullptr) {  // the rows' drafted tokens, a lane a row
+        for (int n = tid; n < R; n += 32 * kC8Soft) {
+          int32_t depth = 0;
+          if (e.m0 + n < m_all) {
+            const uint32_t *mrow = a.seqs.mask + (int64_t)(e.row0 + fast_div(plan.group_div, e.m0 + n)) * a.seqs.mask_words;
+            for (int32_t k = 0; 32 * k < e.rows; ++k) {
               const int32_t over = e.rows - 32 * k;
               depth += __popc(over >= 32 ? mrow[k] : mrow[k] & ((1u << over) - 1u));
             }
           }
-#pragma unroll
-          for (int o = kLanes / 2; o; o >>= 1) depth += __shfl_xor_sync(0xffffffffu, depth, o);
-        }
-        if (mine && ch == 0) {
-          C.factor[n] = a.scale_log2 * s;
           C.depth[n] = max(0, depth - 1);
-#pragma unroll
-          for (int o = 0; o < G::kOs; ++o) C.less_ref[o * kCols + n] = valid ? -kC8Unset : -kC8Nobody;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -844,7 +850,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     auto write_out = [&]() {
       if (!(g.flags & C8Seg::kEmpty)) {
         const bool whole = (g.flags & C8Seg::kWhole) != 0;
-        constexpr int kRows = R / 2, kOut = kRows < 16 ? kRows : 16;  // a group's rows of the output, at once
+        constexpr int kRows = R / 2, kOut = kRows < 8 ? kRows : 8;  // a group's rows of the output, at once
         const int first = w * kRows;
 #pragma unroll 1
         for (int h = 0; h < G::kHalves; ++h) {
@@ -891,7 +897,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     };
     // Parts overlap: the next one's Q is fetched before this one's output is written.
     bool more = advance(next);
-    if (more && next.n > 0) fetch_q(next);
+    if (more && next.n > 0) fetch_q(next, 0);
     while (true) {
       if (more && next.n > 0) store_q(next);
       write_out();
@@ -1105,7 +1111,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       }
       ns += (uint32_t)(2 * g.n);
       more = advance(next);
-      if (more && next.n > 0) fetch_q(next);
+      if (more && next.n > 0) fetch_q(next, 0);
       bool fix = false;
       if (g.n > 0) {  // S and P V of every tile are done: Q may go, O may be read
         if (G::kTurns && g.n > 1) wait_pv(jg - 2);
