@@ -43,7 +43,6 @@ constexpr int kC8Segs = 4;             // parts it is ahead by
 constexpr int kC8T = 128;        // tokens of a tile: the MMAs' M
 constexpr int kC8MostRows = 64;  // rows of a unit at most
 constexpr int kC8MaxCtas = 160;
-constexpr int kC8Start = 4;      // what beginning a unit costs, in tiles
 constexpr float kC8Unset = -1e30f;    // a row's reference before it has seen a token
 constexpr float kC8Nobody = 1e30f;    // ... of a column without a row: its weights are 0
 constexpr float kC8Head = 4.f;        // log2 of a largest w when the reference is set
@@ -78,6 +77,13 @@ struct C8Geom {
   static constexpr uint32_t kIdescO = kIdescS | (1u << 15) | (1u << 16);
 };
 
+// What beginning a unit costs, in tiles: its Q, its first references and its output.  At 3, 6, 9
+// and 13 tiles, single rows of 32 heads over 8 over 300 to 9001 tokens take 42.5, 44.3, 47.2 and
+// 46.4 us, and 64 single rows over 100 to 2000 tokens 24.8, 25.7, 27.3 and 27.9; trees of 5 to 37
+// rows of 16 heads over 2 (units of 64 rows) 109, 106, 99 and 108.
+template <int R>
+constexpr int c8_start() { return R < 64 ? 3 : 9; }
+
 struct C8Seq {
   SeqView v;
   int32_t tiles, m_tiles;  // in every unit's list; units of rows
@@ -109,7 +115,7 @@ __device__ __forceinline__ C8Seq c8_seq(const Cache8Args &a, const C8Plan &p, co
     q.tiles = (int32_t)min((int64_t)q.tiles, first_tiles(a, q.v) + (span + kC8T - 1) / kC8T + 1);
   }
   q.m_tiles = (int32_t)(((int64_t)q.v.rows * a.group + R - 1) >> kLog);
-  q.count = q.tiles > 0 ? (int64_t)(q.tiles + kC8Start) * q.m_tiles * (a.nkv >> p.head_log) : 0;
+  q.count = q.tiles > 0 ? (int64_t)(q.tiles + c8_start<R>()) * q.m_tiles * (a.nkv >> p.head_log) : 0;
   return q;
 }
 
@@ -160,7 +166,7 @@ struct C8Walk {
       q = c8_seq<R>(a, p, ahead);
       ahead = read_seq(a.seqs, min(s + 1, a.seqs.n_seqs - 1));
     }
-    const int32_t length = q.tiles + kC8Start;
+    const int32_t length = q.tiles + c8_start<R>();
     int32_t unit;  // (team of KV heads, rows)
     if ((off >> 31) == 0) unit = (int32_t)((uint32_t)off / (uint32_t)length);
     else unit = (int32_t)(off / length);
@@ -168,7 +174,7 @@ struct C8Walk {
     const int32_t part = (int32_t)min((int64_t)(length - from), left);
     off += part;
     left -= part;
-    const int32_t i0 = max(0, from - kC8Start), take = max(0, from + part - kC8Start) - i0;
+    const int32_t i0 = max(0, from - c8_start<R>()), take = max(0, from + part - c8_start<R>()) - i0;
     g.s = s;
     const int32_t heads = unit / q.m_tiles, mt = unit - heads * q.m_tiles;
     g.kvh = (heads << p.head_log) + ((int32_t)blockIdx.x & ((1 << p.head_log) - 1));
@@ -1229,7 +1235,7 @@ cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t teams, const i
     r = (int32_t)(m % R);
     rank = kvh & ((1 << plan.head_log) - 1);
     tiles = q.tiles;
-    u0 = ((int64_t)(kvh >> plan.head_log) * q.m_tiles + mt) * (tiles + kC8Start) + kC8Start;
+    u0 = ((int64_t)(kvh >> plan.head_log) * q.m_tiles + mt) * (tiles + c8_start<R>()) + c8_start<R>();
   };
   if (row >= 0) place(seq_of_row(a.seqs, row));
   grid_dependency_sync();
