@@ -10,9 +10,10 @@
 // 4g + 3 and those 32 on, the pairs that turn together, the others 8g to 8g + 7.
 //
 // Query heads (and those of K and V where they are held in bf16) are streamed: a warp has
-// a token and a run of its heads, whose loads it issues together.  K and V in 8 bits need a
-// block's maximum first: CTAs of their own take a block's K and V of one head (four warps
-// each, whose maxima meet) or, where blocks get a token or two, of four heads (a warp each).
+// a token and a run of its heads, whose loads it issues together.  K or V in 8 bits of a
+// block and a head is for as many warps as have four loads each, and up to eight: their
+// maxima meet, then they write from registers (or from what they read again).  Both kinds of
+// work are shared out over all CTAs alike.
 #include "qsa_launch.h"
 #include "qsa_share.cuh"
 #include "qsa_tc_cache.cuh"
@@ -132,18 +133,50 @@ __device__ __forceinline__ void prepare_head(uint64_t (&x)[4], bool norm, const 
   }
 }
 
-// How a launch shares its work out.
+// Runs of heads of a token, of q and, in bf16, of K and of V; a block's K and V in 8 bits of
+// every head, and log2 of the warps that take one.
 struct WriteCut {
-  int32_t kv_ctas;   // CTAs that take K and V in 8 bits, before those that stream
-  int32_t kv_parts;  // items of a block there
-  int32_t few;       // a warp takes K or V of a head alone, not four
-  FastDiv runs;      // runs of heads of a token
+  FastDiv runs;
+  int32_t q, k;
+  FastDiv streams;
+  int32_t warps_log;
 };
 
-constexpr int kRun = 8;  // loads of a run of heads
+constexpr int kRun = 4;  // loads of heads on their way
+
+// A warp's (or a few warps') walk through its CTA's share of a list: every step-th item from
+// the first-th on.
+template <typename Count>
+struct WarpWalk {
+  const CachedSeqs &seqs;
+  const Count &count_of;
+  int64_t left, off, count;
+  int32_t s, by;
+  SeqView v;
+  __device__ WarpWalk(const CachedSeqs &seqs_, const Count &count_of_, const FoundShare &f, int first, int by_)
+      : seqs(seqs_), count_of(count_of_), left(f.share.n - first), off(f.off + first), s(f.seq), by(by_) {
+    if (left <= 0) return;
+    v = view_seq(seqs, s);
+    count = count_of(v);
+  }
+  __device__ bool here() {  // to the sequence that has the item
+    if (left <= 0) return false;
+    while (off >= count) {
+      off -= count;
+      if (++s >= seqs.n_seqs) return false;
+      v = view_seq(seqs, s);
+      count = count_of(v);
+    }
+    return true;
+  }
+  __device__ void step() {
+    left -= by;
+    off += by;
+  }
+};
 
 template <int HD, bool EIGHT>
-__global__ void __launch_bounds__(kWrThreads, EIGHT ? 2 : 3) qkv_write_kernel(const WriteArgs a, const WriteCut cut) {
+__global__ void __launch_bounds__(kWrThreads, 3) qkv_write_kernel(const WriteArgs a, const WriteCut cut) {
   __shared__ ShareScratch scratch;
   __shared__ float most[kWrWarps];
   __shared__ int32_t some[kWrWarps];
@@ -152,39 +185,25 @@ __global__ void __launch_bounds__(kWrThreads, EIGHT ? 2 : 3) qkv_write_kernel(co
   grid_dependency_sync();
 
   const int ul = a.unit_log;
-  const bool kv = EIGHT && (int32_t)blockIdx.x < cut.kv_ctas;
-  // what a sequence has in the list of this CTA's kind: blocks' items, or tokens' runs
-  auto count_of = [&](const SeqView &v) -> int64_t {
-    if (v.rows == 0) return 0;
-    return kv ? (int64_t)(((v.ctx + v.rows - 1) >> ul) - (v.ctx >> ul) + 1) * cut.kv_parts : (int64_t)v.rows * cut.runs.d;
+  // a sequence's runs, and its blocks' K and V of every head
+  auto runs_of = [&](const SeqView &v) -> int64_t { return (int64_t)v.rows * cut.runs.d; };
+  auto blocks_of = [&](const SeqView &v) -> int64_t {
+    return v.rows == 0 ? 0 : (int64_t)(((v.ctx + v.rows - 1) >> ul) - (v.ctx >> ul) + 1) * cut.streams.d;
   };
-  FoundShare f = find_share(a.seqs.n_seqs, kWrThreads, kv ? cut.kv_ctas : gridDim.x - cut.kv_ctas,
-                            kv ? blockIdx.x : blockIdx.x - cut.kv_ctas, scratch, [&](int32_t s) -> int64_t {
-                              if (s >= a.seqs.n_seqs) return 0;
-                              const SeqView v = view_seq(a.seqs, s);
-                              if (!v.ok && blockIdx.x == 0) report_error(a.status, kErrRowRange, s);
-                              return count_of(v);
-                            });
-  SeqView v = {0, 0, 0, false};
-  int64_t count = 0;
-  if (f.share.n > 0) {
-    v = view_seq(a.seqs, f.seq);
-    count = count_of(v);
-  }
-  auto walk = [&](int64_t &off) -> bool {  // to the sequence that has item `off`
-    while (off >= count) {
-      off -= count;
-      if (++f.seq >= a.seqs.n_seqs) return false;
-      v = view_seq(a.seqs, f.seq);
-      count = count_of(v);
-    }
-    return true;
+  auto share_of = [&](auto &&count_of, bool report) {
+    return find_share(a.seqs.n_seqs, kWrThreads, gridDim.x, blockIdx.x, scratch, [&](int32_t s) -> int64_t {
+      if (s >= a.seqs.n_seqs) return 0;
+      const SeqView v = view_seq(a.seqs, s);
+      if (report && !v.ok && blockIdx.x == 0) report_error(a.status, kErrRowRange, s);
+      return count_of(v);
+    });
   };
+  const FoundShare by_runs = share_of(runs_of, true);
   // a token's position, or -1 where its row is left alone
-  auto position = [&](int32_t t) -> int32_t {
+  auto position = [&](const SeqView &v, int32_t s, int32_t t) -> int32_t {
     const int32_t at = a.pos ? a.pos[v.row0 + (t - v.ctx)] : t;
     const bool ok = at >= 0 && at < a.table_rows;
-    if (!ok) report_error(a.status, kErrRowRange, f.seq);
+    if (!ok) report_error(a.status, kErrRowRange, s);
     return ok ? at : -1;
   };
   auto angle = [&](int32_t at) -> HeadAngle {
@@ -197,122 +216,53 @@ __global__ void __launch_bounds__(kWrThreads, EIGHT ? 2 : 3) qkv_write_kernel(co
   };
   const uint4 none = make_uint4(0, 0, 0, 0);
 
-  const HeadWeights kw(a.k_norm_w, g);
-  if (!kv) {
-    // ---- heads streamed
-    const int32_t heads = a.nq + (EIGHT ? 0 : 2 * a.nkv);
-    const HeadWeights qw(a.q_norm_w, g);
-    int64_t off = f.off + warp;
-    for (int64_t left = f.share.n - warp; left > 0; left -= kWrWarps, off += kWrWarps) {
-      if (!walk(off)) return;
-      const int32_t j = fast_div(cut.runs, (int32_t)off), first = ((int32_t)off - j * cut.runs.d) * (kRun * kPer), h0 = first + sub;
-      const int32_t t = v.ctx + j;
-      const int64_t row = v.row0 + j;
-      uint4 x[kRun];
-#pragma unroll
-      for (int b = 0; b < kRun; ++b) {
-        const int32_t h = h0 + b * kPer;
-        const uint16_t *src = a.q + row * a.q_stride + (int64_t)h * HD;
-        if (!EIGHT && h >= a.nq)
-          src = h < a.nq + a.nkv ? a.k + row * a.k_stride + (int64_t)(h - a.nq) * HD
-                                 : a.v + row * a.v_stride + (int64_t)(h - a.nq - a.nkv) * HD;
-        x[b] = h < heads ? load_dims(src, g) : none;
-      }
-      const int32_t at = position(t);
-      const HeadAngle turn = angle(at);
-      int64_t slot = -1;
-      if (!EIGHT && first + kRun * kPer > a.nq) {
-        slot = token_slot(a.seqs, f.seq, t);
-        if (slot < 0) report_error(a.status, kErrTokenRange, f.seq);
-      }
-#pragma unroll
-      for (int b = 0; b < kRun; ++b) {
-        const int32_t h = h0 + b * kPer;
-        if (first + b * kPer >= heads) break;
-        const bool is_q = EIGHT || h < a.nq, is_v = !EIGHT && h >= a.nq + a.nkv;
-        uint64_t y[4] = {widen(x[b].x), widen(x[b].y), widen(x[b].z), widen(x[b].w)};
-        HeadAngle mine = turn;
-        bool norm = a.q_norm_w != nullptr;
-        if constexpr (!EIGHT) {
-          if (!is_q) norm = a.k_norm_w != nullptr && !is_v;
-          mine.on = turn.on && !is_v;
-          uint64_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = is_q ? qw.w[i] : kw.w[i];
-          prepare_head<HD>(y, norm, w, a.eps, mine);
-        } else {
-          prepare_head<HD>(y, norm, qw.w, a.eps, mine);
-        }
-        if (h >= heads || at < 0) continue;
-        uint2 lo = make_uint2(x[b].x, x[b].y), hi = make_uint2(x[b].z, x[b].w);  // V as it is
-        if (!is_v) {
-          lo = make_uint2(narrow(y[0]), narrow(y[1]));
-          hi = make_uint2(narrow(y[2]), narrow(y[3]));
-        }
-        uint16_t *dst = a.q_out + row * a.out_stride + (int64_t)h * HD;
-        if (!is_q) {
-          if (slot < 0) continue;
-          dst = static_cast<uint16_t *>(is_v ? a.v_pool : a.k_pool) + (slot * a.nkv + (h - a.nq - (is_v ? a.nkv : 0))) * HD;
-        }
-        *reinterpret_cast<uint2 *>(dst + dim_a(g)) = lo;
-        *reinterpret_cast<uint2 *>(dst + dim_b(g)) = hi;
-      }
-    }
-    return;
-  }
   if constexpr (EIGHT) {
-    // ---- K (warps 0 to 3) and V (4 to 7) of a block and a head: its scale, then its values
-    constexpr int kHeld = 4;  // loads of heads on their way
-    const bool is_k = warp < 4;
-    const int wi = cut.few ? 0 : warp & 3, ws = cut.few ? 1 : 4;  // this warp's place among those of its head
-    int64_t off = f.off;
-    for (int64_t left = f.share.n; left > 0; --left, ++off) {
-      if (!walk(off)) return;
-      const int32_t nth = (int32_t)(off / cut.kv_parts), part = (int32_t)(off - (int64_t)nth * cut.kv_parts);
-      const int32_t kvh = cut.few ? 4 * part + (warp & 3) : part;
-      if (kvh >= a.nkv) continue;  // (a warp alone: no barrier below)
+    if (a.seqs.n_seqs > 32) __syncthreads();  // the first share is read
+    const FoundShare by_blocks = share_of(blocks_of, false);
+    const int wl = cut.warps_log, ws = 1 << wl, group = warp >> wl, wi = warp & (ws - 1);
+    for (WarpWalk<decltype(blocks_of)> walk(a.seqs, blocks_of, by_blocks, group, kWrWarps >> wl); walk.here(); walk.step()) {
+      const SeqView v = walk.v;
+      const int32_t nth = fast_div(cut.streams, (int32_t)walk.off), part = (int32_t)walk.off - nth * cut.streams.d;
+      const bool is_k = part < a.nkv;
+      const int32_t kvh = is_k ? part : part - a.nkv;
       const int32_t begin = ((v.ctx >> ul) + nth) << ul;
       const int32_t t0 = max(v.ctx, begin), t1 = (int32_t)min((int64_t)v.ctx + v.rows, (int64_t)begin + (1 << ul));
-      const int32_t step = ws * kPer;
-      // kHeld of this warp's tokens from t on, ready to be held; which of them count
-      uint64_t y[kHeld][4];
+      const uint16_t *const src = (is_k ? a.k : a.v) + (int64_t)kvh * HD;
+      const int64_t src_stride = is_k ? a.k_stride : a.v_stride;
+      const bool norm = is_k && a.k_norm_w != nullptr;
+      const HeadWeights kw(norm ? a.k_norm_w : nullptr, g);
+      // kRun of the tokens from t on, ready to be held; which of them count
+      uint64_t y[kRun][4];
       uint32_t good = 0u;
       auto fetch = [&](int32_t t) {
-        uint4 x[kHeld];
-        int32_t at[kHeld];
+        uint4 x[kRun];
+        HeadAngle turn[kRun];
         good = 0u;
 #pragma unroll
-        for (int b = 0; b < kHeld; ++b) {
-          const int32_t tb = t + b * step + sub;
-          const int64_t row = v.row0 + (tb - v.ctx);
-          at[b] = -1;
+        for (int b = 0; b < kRun; ++b) {
+          const int32_t tb = t + (b * ws + wi) * kPer + sub;
+          int32_t at = -1;
           x[b] = none;
           if (tb < t1) {
-            x[b] = load_dims((is_k ? a.k + row * a.k_stride : a.v + row * a.v_stride) + (int64_t)kvh * HD, g);
-            at[b] = position(tb);
+            x[b] = load_dims(src + (int64_t)(v.row0 + (tb - v.ctx)) * src_stride, g);
+            at = position(v, walk.s, tb);
           }
-          good |= at[b] >= 0 ? 1u << b : 0u;
-        }
-        HeadAngle turn[kHeld];
-        if (is_k) {
-#pragma unroll
-          for (int b = 0; b < kHeld; ++b) turn[b] = angle(at[b]);
+          good |= at >= 0 ? 1u << b : 0u;
+          turn[b] = angle(is_k ? at : -1);
         }
 #pragma unroll
-        for (int b = 0; b < kHeld; ++b) {
+        for (int b = 0; b < kRun; ++b) {
           y[b][0] = widen(x[b].x);
           y[b][1] = widen(x[b].y);
           y[b][2] = widen(x[b].z);
           y[b][3] = widen(x[b].w);
-          if (is_k) prepare_head<HD>(y[b], a.k_norm_w != nullptr, kw.w, a.eps, turn[b]);
+          if (is_k) prepare_head<HD>(y[b], norm, kw.w, a.eps, turn[b]);
         }
       };
-      const int32_t first = t0 + wi * kPer, batch = kHeld * step;
-      const bool once = first + batch >= t1;  // what this warp has fits its registers
-      fetch(first);
-      const int64_t slot0 = token_slot(a.seqs, f.seq, begin);  // a block lies in one page
+      fetch(t0);
+      const int64_t slot0 = token_slot(a.seqs, walk.s, begin);  // a block lies in one page
       if (slot0 < 0) {
-        if (lane == 0) report_error(a.status, kErrTokenRange, f.seq);
+        if (lane == 0) report_error(a.status, kErrTokenRange, walk.s);
         continue;
       }
       float *scale = (is_k ? a.k_scale : a.v_scale) + (slot0 >> ul) * a.nkv + kvh;
@@ -321,9 +271,10 @@ __global__ void __launch_bounds__(kWrThreads, EIGHT ? 2 : 3) qkv_write_kernel(co
       const int64_t pitch = (int64_t)a.nkv * HD;
       float amax = 0.f;
       bool any = false;
-      for (int32_t t = first;;) {
+      const int32_t batch = (kRun * kPer) << wl;
+      for (int32_t t = t0;;) {
 #pragma unroll
-        for (int b = 0; b < kHeld; ++b) {
+        for (int b = 0; b < kRun; ++b) {
           if (!((good >> b) & 1u)) continue;
           any = true;
 #pragma unroll
@@ -342,22 +293,23 @@ __global__ void __launch_bounds__(kWrThreads, EIGHT ? 2 : 3) qkv_write_kernel(co
 #pragma unroll
       for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       any = __any_sync(0xffffffffu, any);
-      if (!cut.few) {
-        auto meet = [&]() { asm volatile("barrier.cta.sync %0, 128;" ::"r"(is_k ? 1 : 2) : "memory"); };
+      if (wl > 0) {
+        auto meet = [&]() { asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "r"(32 << wl) : "memory"); };
         if (lane == 0) {
           most[warp] = amax;
           some[warp] = any;
         }
         meet();
-        const int w0 = warp & 4;
-        amax = fmaxf(fmaxf(most[w0], most[w0 + 1]), fmaxf(most[w0 + 2], most[w0 + 3]));
-        any = some[w0] || some[w0 + 1] || some[w0 + 2] || some[w0 + 3];
+        for (int w = group << wl; w < (group + 1) << wl; ++w) {
+          amax = fmaxf(amax, most[w]);
+          any = any || some[w];
+        }
         meet();  // read before the next item's, and everyone has the old scale
       }
       if (!any) continue;
       const float now = fmaxf(old, scale_of(amax));
       if (now > old) {
-        for (int32_t t = begin + wi * kPer + sub; t < t0; t += step) {
+        for (int32_t t = begin + wi * kPer + sub; t < t0; t += kPer << wl) {
           uint2 *at = reinterpret_cast<uint2 *>(pool + (t - begin) * pitch + 8 * g);  // (in any order)
           float z[8];
           unpack_e4m3(*at, z);
@@ -367,17 +319,22 @@ __global__ void __launch_bounds__(kWrThreads, EIGHT ? 2 : 3) qkv_write_kernel(co
         }
       }
       const float inv = reciprocal(now);
-      if (!once) fetch(first);
-      for (int32_t t = first;;) {
+      if (t0 + batch < t1) fetch(t0);  // (else the registers have them)
+      for (int32_t t = t0;;) {
 #pragma unroll
-        for (int b = 0; b < kHeld; ++b) {
+        for (int b = 0; b < kRun; ++b) {
           if (!((good >> b) & 1u)) continue;
           float z[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) unpair_f32(y[b][i], z[2 * i], z[2 * i + 1]);
+          if (inv > 0.f) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = inv > 0.f ? z[i] * inv : over(z[i], now);
-          uint8_t *at = pool + (t + b * step + sub - begin) * pitch;
+            for (int i = 0; i < 8; ++i) z[i] *= inv;
+          } else {  // a begun block's scale that no power of two is
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = over(z[i], now);
+          }
+          uint8_t *at = pool + (t + (b * ws + wi) * kPer + sub - begin) * pitch;
           *reinterpret_cast<uint32_t *>(at + dim_a(g)) = pack_e4m3(z[0], z[1], z[2], z[3]);
           *reinterpret_cast<uint32_t *>(at + dim_b(g)) = pack_e4m3(z[4], z[5], z[6], z[7]);
         }
@@ -385,31 +342,70 @@ __global__ void __launch_bounds__(kWrThreads, EIGHT ? 2 : 3) qkv_write_kernel(co
         if (t >= t1) break;
         fetch(t);
       }
+      __syncwarp();
       if (wi == 0 && lane == 0) *scale = now;
+    }
+  }
+
+  // ---- heads streamed
+  const HeadWeights qw(a.q_norm_w, g), kw(EIGHT ? nullptr : a.k_norm_w, g);
+  for (WarpWalk<decltype(runs_of)> walk(a.seqs, runs_of, by_runs, warp, kWrWarps); walk.here(); walk.step()) {
+    const SeqView v = walk.v;
+    const int32_t j = fast_div(cut.runs, (int32_t)walk.off), run = (int32_t)walk.off - j * cut.runs.d, t = v.ctx + j;
+    const int64_t row = v.row0 + j;
+    // 0: q, 1: K, 2: V; the run's first head of its kind
+    const int kind = EIGHT || run < cut.q ? 0 : run < cut.q + cut.k ? 1 : 2;
+    const int32_t h0 = (run - (kind == 0 ? 0 : kind == 1 ? cut.q : cut.q + cut.k)) * (kRun * kPer) + sub;
+    const int32_t heads = kind == 0 ? a.nq : a.nkv;
+    const uint16_t *src = kind == 0 ? a.q + row * a.q_stride : kind == 1 ? a.k + row * a.k_stride : a.v + row * a.v_stride;
+    src += (int64_t)h0 * HD;
+    uint4 x[kRun];
+#pragma unroll
+    for (int b = 0; b < kRun; ++b) x[b] = h0 + b * kPer < heads ? load_dims(src + b * (kPer * HD), g) : none;
+    const int32_t at = position(v, walk.s, t);
+    const HeadAngle turn = angle(kind < 2 ? at : -1);
+    uint16_t *dst = a.q_out + row * a.out_stride;
+    if (!EIGHT && kind > 0) {
+      const int64_t slot = token_slot(a.seqs, walk.s, t);
+      if (slot < 0) {
+        report_error(a.status, kErrTokenRange, walk.s);
+        continue;
+      }
+      dst = static_cast<uint16_t *>(kind == 1 ? a.k_pool : a.v_pool) + slot * a.nkv * HD;
+    }
+    dst += (int64_t)h0 * HD;
+    if (at < 0) continue;
+    const bool norm = kind == 0 ? a.q_norm_w != nullptr : kind == 1 && a.k_norm_w != nullptr;
+#pragma unroll
+    for (int b = 0; b < kRun; ++b) {
+      uint2 lo = make_uint2(x[b].x, x[b].y), hi = make_uint2(x[b].z, x[b].w);
+      if (EIGHT || kind < 2) {  // (V as it is)
+        uint64_t y[4] = {widen(x[b].x), widen(x[b].y), widen(x[b].z), widen(x[b].w)};
+        if (EIGHT || kind == 0) prepare_head<HD>(y, norm, qw.w, a.eps, turn);
+        else prepare_head<HD>(y, norm, kw.w, a.eps, turn);
+        lo = make_uint2(narrow(y[0]), narrow(y[1]));
+        hi = make_uint2(narrow(y[2]), narrow(y[3]));
+      }
+      if (h0 + b * kPer >= heads) continue;
+      *reinterpret_cast<uint2 *>(dst + b * (kPer * HD) + dim_a(g)) = lo;
+      *reinterpret_cast<uint2 *>(dst + b * (kPer * HD) + dim_b(g)) = hi;
     }
   }
 }
 
 template <int HD>
 cudaError_t launch_hd(const WriteArgs &a, cudaStream_t stream) {
-  constexpr int kPer = 256 / HD;
+  constexpr int32_t kHeads = kRun * 256 / HD;  // of a run
   const bool eight = a.k_scale != nullptr;
-  const int64_t rows = a.seqs.n_rows, n = a.seqs.n_seqs;
-  const int32_t heads = a.nq + (eight ? 0 : 2 * a.nkv);
-  WriteCut cut = {0, 0, 0, make_fast_div((heads + kRun * kPer - 1) / (kRun * kPer))};
-  const int64_t room = (eight ? 2 : 3) * device_sm_count();
-  int64_t streams = (rows * cut.runs.d + kWrWarps - 1) / kWrWarps;  // CTAs with a run a warp
-  if (eight) {
-    cut.few = rows <= 4 * n;  // tokens a block gets, by the mean over the call
-    cut.kv_parts = cut.few ? (a.nkv + 3) / 4 : a.nkv;
-    const int64_t items = ((rows >> a.unit_log) + 2 * n) * cut.kv_parts;
-    // by the bytes that are read and written, 3 a value of K and V, 4 one of q, and as much
-    // again of K and V for their waits
-    const int64_t part = room * 12 * a.nkv / (12 * a.nkv + 4 * a.nq) + 1;
-    cut.kv_ctas = (int32_t)(items < part ? items : part);
-  }
-  if (streams > room - cut.kv_ctas) streams = room - cut.kv_ctas;
-  return launch_dependent(eight ? qkv_write_kernel<HD, true> : qkv_write_kernel<HD, false>, dim3((unsigned)(cut.kv_ctas + streams)),
+  const int32_t q = (a.nq + kHeads - 1) / kHeads, k = eight ? 0 : (a.nkv + kHeads - 1) / kHeads;
+  const int64_t rows = a.seqs.n_rows, n = a.seqs.n_seqs, unit = (int64_t)1 << a.unit_log;
+  // the loads of a block's tokens, by the mean over the call
+  const int64_t loads = ((rows / n < unit ? rows / n : unit) * HD + 255) / 256;
+  const int warps_log = loads <= kRun ? 0 : loads <= 2 * kRun ? 1 : loads <= 4 * kRun ? 2 : 3;
+  const WriteCut cut = {make_fast_div(q + 2 * k), q, k, make_fast_div(2 * a.nkv), warps_log};
+  const int64_t items = rows * cut.runs.d + (eight ? (((rows >> a.unit_log) + 2 * n) * 2 * a.nkv) << warps_log : 0);
+  const int64_t ctas = (items + kWrWarps - 1) / kWrWarps, room = 3 * device_sm_count();
+  return launch_dependent(eight ? qkv_write_kernel<HD, true> : qkv_write_kernel<HD, false>, dim3((unsigned)(ctas < room ? ctas : room)),
                           dim3(kWrThreads), 0, stream, 1u, a, cut);
 }
 
