@@ -7,18 +7,17 @@
 //
 // Whole numbers only, and little of them: three passes over the sequences' lengths and
 // one over the rows, 12 bytes each.  What costs is the chain: lengths, sums over the
-// sequences, the stack, the tables, the rows.  One CTA does a small step, a cluster of
-// eight a large one, whose CTAs all sum the lengths, move the pages of their own warps'
-// sequences and fill their own run of rows, with a cluster barrier where one reads what
-// another wrote; so the lengths, heights and tables may be updated in place, and a step
-// is one launch.
+// sequences, the stack, the tables, the rows.  One CTA does a small step; of many sequences
+// or rows a cluster of eight, whose CTAs all sum the lengths and share the pages to move, with a
+// cluster barrier where one reads what another wrote; so the lengths,
+// heights and tables may be updated in place.  Many rows are filled by a second launch.
 #include "qsa_launch.h"
 
 namespace qsa {
 
 namespace {
 
-constexpr int kPlThreads = 1024, kPlWarps = kPlThreads / 32, kPlCtas = 8;
+constexpr int kPlThreads = 1024, kPlWarps = kPlThreads / 32, kPlCtas = 8, kFillThreads = 256;
 
 struct PlanSeq {
   int32_t rows, back, take, held;
@@ -63,7 +62,51 @@ struct PlanSums {
   int64_t rows, back, take;
 };
 
-__global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a) {
+// Warp `at` of `warps` fills its run of the rows' places, 32 at a time; `base`: a sequence no
+// later than theirs.
+__device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t warps, int64_t rows, int lane) {
+  const int64_t per = (((int64_t)a.max_rows + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t r0 = at * per, r1 = min((int64_t)a.max_rows, r0 + per);
+  int32_t base = 0;
+  if (r0 < rows) {  // the last sequence that starts at or before r0
+    int32_t hi = a.n_seqs;
+    while (hi - base > 1) {
+      const int32_t step = (hi - base + 31) / 32, probe = base + lane * step;
+      const uint32_t hit = __ballot_sync(0xffffffffu, probe < hi && __ldcg(a.row_start + probe) <= r0);
+      base += (31 - __clz((int)hit)) * step;
+      hi = min(hi, base + step);
+    }
+  }
+  for (int64_t i0 = r0; i0 < r1; i0 += 32) {
+    const int64_t r = i0 + lane;
+    int32_t seq = -1;
+    bool open = r < rows;
+    while (__any_sync(0xffffffffu, open)) {
+      const int64_t end = __ldcg(a.row_start + min(base + 1 + lane, a.n_seqs));
+      const int n = lanes_upto(end, r);
+      if (open && n < 32) {
+        seq = base + n;
+        open = false;
+      }
+      if (__any_sync(0xffffffffu, open)) base += 32;
+    }
+    if (i0 < rows) base = max(base, __reduce_max_sync(0xffffffffu, seq));
+    if (r >= r1) continue;
+    int32_t slot = -1, t = 0;
+    if (seq >= 0) {
+      t = a.ctx_len[seq] + (int32_t)(r - __ldcg(a.row_start + seq));
+      const int32_t pg = fast_div(a.page, t), page = __ldcg(a.table + (int64_t)seq * a.table_cols + pg);
+      if (page >= 0 && page < a.pool_pages) slot = page * a.page.d + (t - pg * a.page.d);
+      else report_error(a.status, kErrTokenRange, seq);
+    }
+    a.slot[r] = slot;
+    if (a.pos) a.pos[r] = t;
+    if (a.row_seq) a.row_seq[r] = seq;
+  }
+}
+
+
+__global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a, bool fill) {
   __shared__ int64_t scan[3][kPlWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = blockIdx.x, ranks = gridDim.x;  // the grid is one cluster
@@ -107,32 +150,43 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a)
   const bool stack_ok = free0 >= 0 && height <= a.pool_pages, rows_ok = all.rows <= a.max_rows;
   const bool ok = stack_ok && rows_ok && all.take <= height;
 
-  // item(s, i, k): the i-th of sequence s's `count` items, the k-th of all
-  auto each = [&](int32_t s, int32_t count, int64_t first, auto &&item) {
+  // The items of this warp's sequences, shared with the same warp of the other CTAs, which has
+  // the same sequences: from(s, i, k) reads the i-th of sequence s's, the k-th of all, and
+  // to(s, i, k, page) puts it in its place.  Four at once: each is a trip to L2.
+  auto each = [&](int32_t s, int32_t count, int64_t first, auto &&from, auto &&to) {
     const int64_t incl = warp_scan(count, lane), total = __shfl_sync(0xffffffffu, incl, 31);
     const int64_t base = __shfl_sync(0xffffffffu, first, 0);
-    for (int64_t i0 = 0; i0 < total; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const int src = min(lanes_upto(incl, i), 31);
-      const int64_t begin = __shfl_sync(0xffffffffu, incl - count, src);
-      const int32_t seq = __shfl_sync(0xffffffffu, s, src);
-      if (i < total) item(seq, (int32_t)(i - begin), base + i);
+    constexpr int kAtOnce = 4;
+    for (int64_t i0 = 32 * (int64_t)rank; i0 < total; i0 += 32 * kAtOnce * (int64_t)ranks) {
+      int32_t seq[kAtOnce], at[kAtOnce], page[kAtOnce];
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int64_t i = i0 + 32 * (int64_t)ranks * e + lane;
+        const int src = min(lanes_upto(incl, i), 31);
+        at[e] = (int32_t)(i - __shfl_sync(0xffffffffu, incl - count, src));
+        seq[e] = __shfl_sync(0xffffffffu, s, src);
+        if (i < total) page[e] = from(seq[e], at[e], base + i);
+      }
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int64_t i = i0 + 32 * (int64_t)ranks * e + lane;
+        if (i >= total) continue;
+        if (page[e] < 0 || page[e] >= a.pool_pages) report_error(a.status, kErrTokenRange, seq[e]);
+        to(seq[e], at[e], base + i, page[e]);
+      }
     }
   };
-  auto mine = [&](int32_t s0) { return (uint32_t)(s0 / 32 + warp) % ranks == rank; };
 
   if (ok && all.back > 0) {
     PlanSums sums = {0, 0, 0};
     for (int32_t s0 = 0; s0 < a.n_seqs; s0 += kPlThreads) {
       if (!one_chunk) at = chunk(s0 + tid, p, sums);
-      if (!mine(s0)) continue;
-      each(s0 + tid, p.back, at.back, [&](int32_t s, int32_t i, int64_t k) {
-        const int32_t kv = a.ctx_len[s] + a.new_rows[s];
-        const int32_t entry = (kv > 0 ? fast_div(a.page, kv - 1) + 1 : 0) + i;
-        const int32_t page = a.table[(int64_t)s * a.table_cols + entry];
-        if (page < 0 || page >= a.pool_pages) report_error(a.status, kErrTokenRange, s);
-        a.free_pages[free0 + k] = page;
-      });
+      each(s0 + tid, p.back, at.back,
+           [&](int32_t s, int32_t i, int64_t) -> int32_t {
+             const int32_t kv = a.ctx_len[s] + a.new_rows[s];
+             return a.table[(int64_t)s * a.table_cols + (kv > 0 ? fast_div(a.page, kv - 1) + 1 : 0) + i];
+           },
+           [&](int32_t, int32_t, int64_t k, int32_t page) { a.free_pages[free0 + k] = page; });
     }
     plan_barrier();
   }
@@ -154,12 +208,9 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a)
           }
         }
       }
-      if (!ok || !mine(s0)) continue;
-      each(s, p.take, at.take, [&](int32_t seq, int32_t i, int64_t k) {
-        const int32_t page = __ldcg(a.free_pages + (height - 1 - k));
-        if (page < 0 || page >= a.pool_pages) report_error(a.status, kErrTokenRange, seq);
-        a.table[(int64_t)seq * a.table_cols + a.held[seq] + i] = page;
-      });
+      if (!ok) continue;
+      each(s, p.take, at.take, [&](int32_t, int32_t, int64_t k) -> int32_t { return __ldcg(a.free_pages + (height - 1 - k)); },
+           [&](int32_t seq, int32_t i, int64_t, int32_t page) { a.table[(int64_t)seq * a.table_cols + a.held[seq] + i] = page; });
     }
   }
   plan_barrier();
@@ -171,54 +222,26 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a)
   }
   if (rank == 0 && tid == 0) *a.n_free_out = ok ? (int32_t)(height - all.take) : (int32_t)free0;
 
-  // a run of rows per warp, 32 at a time; `base`: a sequence no later than theirs
-  const int64_t rows = ok ? all.rows : 0;
-  const int64_t warps = (int64_t)ranks * kPlWarps;
-  const int64_t per = (((int64_t)a.max_rows + warps - 1) / warps + 31) / 32 * 32;
-  const int64_t r0 = ((int64_t)rank * kPlWarps + warp) * per, r1 = min((int64_t)a.max_rows, r0 + per);
-  int32_t base = 0;
-  if (r0 < rows) {  // the last sequence that starts at or before r0
-    int32_t hi = a.n_seqs;
-    while (hi - base > 1) {
-      const int32_t step = (hi - base + 31) / 32, probe = base + lane * step;
-      const uint32_t hit = __ballot_sync(0xffffffffu, probe < hi && __ldcg(a.row_start + probe) <= r0);
-      base += (31 - __clz((int)hit)) * step;
-      hi = min(hi, base + step);
-    }
-  }
-  for (int64_t i0 = r0; i0 < r1; i0 += 32) {
-    const int64_t r = i0 + lane;
-    int32_t seq = -1;
-    bool open = r < rows;
-    while (__any_sync(0xffffffffu, open)) {
-      const int64_t end = __ldcg(a.row_start + min(base + 1 + lane, a.n_seqs));
-      const int n = lanes_upto(end, r);
-      if (open && n < 32) {
-        seq = base + n;
-        open = false;
-      }
-      if (__any_sync(0xffffffffu, open)) base += 32;
-    }
-    if (i0 < rows) base = max(base, __reduce_max_sync(0xffffffffu, seq));
-    if (r >= r1) continue;
-    int32_t slot = -1, t = 0;
-    if (seq >= 0) {
-      t = a.ctx_len[seq] + (int32_t)(r - __ldcg(a.row_start + seq));
-      const int32_t pg = fast_div(a.page, t), page = __ldcg(a.table + (int64_t)seq * a.table_cols + pg);
-      if (page >= 0 && page < a.pool_pages) slot = page * a.page.d + (t - pg * a.page.d);
-      else report_error(a.status, kErrTokenRange, seq);
-    }
-    a.slot[r] = slot;
-    if (a.pos) a.pos[r] = t;
-    if (a.row_seq) a.row_seq[r] = seq;
-  }
+  if (fill) fill_rows(a, (int64_t)rank * kPlWarps + warp, (int64_t)ranks * kPlWarps, ok ? all.rows : 0, lane);
+}
+
+// The rows of a large step, by all SMs.
+__global__ void __launch_bounds__(kFillThreads) plan_rows_kernel(const PlanArgs a) {
+  grid_dependency_sync();
+  const int64_t warps = (int64_t)gridDim.x * (kFillThreads / 32);
+  fill_rows(a, (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5), warps, a.row_start[a.n_seqs], threadIdx.x & 31);
 }
 
 }  // namespace
 
 cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t stream) {
-  const unsigned ctas = a.n_seqs > 256 || a.max_rows > 8192 ? kPlCtas : 1;
-  return launch_dependent(page_plan_kernel, dim3(ctas), dim3(kPlThreads), 0, stream, ctas, a);
+  const unsigned ctas = a.n_seqs > 256 || a.max_rows > 4096 ? kPlCtas : 1;
+  // Beyond the cluster's reach the rows are a launch of their own.
+  const bool fill = a.max_rows <= 8192;
+  const cudaError_t e = launch_dependent(page_plan_kernel, dim3(ctas), dim3(kPlThreads), 0, stream, ctas, a, fill);
+  if (e != cudaSuccess || fill) return e;
+  const int64_t blocks = ((int64_t)a.max_rows + 4 * kFillThreads - 1) / (4 * kFillThreads), most = 4 * device_sm_count();
+  return launch_dependent(plan_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kFillThreads), 0, stream, 1u, a);
 }
 
 }  // namespace qsa
