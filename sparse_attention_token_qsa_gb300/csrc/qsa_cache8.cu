@@ -23,8 +23,7 @@
 // A unit that lies in one CTA's share is written at once; the parts of any other go to
 // the workspace as (O, ref, sum) and a second launch joins them in a fixed order.
 //
-// The warps: two groups of four do the softmax of every tile, a token per thread and
-// half of the rows a group; four copy K and V rows into a ring of slots (16-byte
+// The warps: groups of four do the softmax, a token of a tile per thread; four copy K and V rows into a ring of slots (16-byte
 // cp.async, 128-byte swizzle); one issues S, one P V.
 #include "qsa_launch.h"
 #include "qsa_share.cuh"
@@ -34,12 +33,8 @@ namespace qsa {
 
 namespace {
 
-constexpr int kC8Soft = 8, kC8Prod = 4, kC8MmaS = kC8Soft + kC8Prod, kC8MmaO = kC8MmaS + 1;
-constexpr int kC8Look = kC8MmaO + 1;   // looks pages up and brings the scales
-constexpr int kC8Plan = kC8Look + 1;   // walks the CTA's share
-constexpr int kC8Warps = kC8Plan + 1, kC8Threads = 32 * kC8Warps;
-constexpr int kC8Readers = kC8Plan;    // warps that take the walk's parts
-constexpr int kC8Segs = 4;             // parts it is ahead by
+constexpr int kC8Prod = 4;  // warps that copy
+constexpr int kC8Segs = 4;  // parts that the walk is ahead by
 constexpr int kC8T = 128;        // tokens of a tile: the MMAs' M
 constexpr int kC8MostRows = 64;  // rows of a unit at most
 constexpr int kC8MaxCtas = 160;
@@ -54,17 +49,24 @@ template <int HD, int R>
 struct C8Geom {
   static constexpr int kN = 2 * R;               // columns: hi terms, lo terms
   static constexpr int kHalves = HD / 128;
-  // Up to 32 rows the softmax groups take tiles in turn, each with a sum, references and an
-  // O of its own, joined at the part's end; of 64 each takes half of every tile's rows.
+  // Up to 32 rows two softmax groups of four warps take tiles in turn, each with a sum,
+  // references and an O of its own, joined at the part's end; of 64, four groups take a
+  // quarter of every tile's rows each (two with a half of them: 120 us where four take N us).
   static constexpr bool kTurns = R < 64;
-  static constexpr int kCols = kTurns ? R : R / 2;  // a group's rows of a tile
+  static constexpr int kGroups = kTurns ? 2 : 4, kCols = kTurns ? R : R / kGroups;  // a group's rows of a tile
+  // the warps: softmax, copies, issuers of S and of P V, look-ups and scales, the walk
+  static constexpr int kSoft = 4 * kGroups, kMmaS = kSoft + kC8Prod, kMmaO = kMmaS + 1, kLook = kMmaO + 1, kWalk = kLook + 1;
+  static constexpr int kThreads = 32 * (kWalk + 1), kReaders = kWalk;  // (all but the walk take its parts)
   static constexpr int kOs = kTurns ? 2 : 1, kMix = kTurns ? 3 * R : 1;
   static constexpr uint32_t kQBox = kN * 128, kBox = kC8T * 128, kSlot = kC8T * HD;
   static constexpr int kSlots = HD == 256 ? 5 : 10;
   static constexpr int kS = R < 64 ? 4 : HD == 256 ? 2 : 3;  // S buffers
-  // Registers of the softmax's threads and of the others, of 128 a thread at the launch: 32
-  // rows a thread do not fit those, and every spilled value would queue behind the copies.
-  static constexpr int kSoftRegs = kCols < 32 ? 128 : 168, kOtherRegs = 256 - kSoftRegs;
+  // Registers of the softmax's threads and of the others, of kRegs a thread at the launch:
+  // 32 rows a thread do not fit 128, nor 16 of them 80, and every spilled value would queue
+  // behind the copies.
+  static constexpr int kRegs = kThreads == 512 ? 128 : 80;
+  static constexpr int kSoftRegs = R < 32 ? kRegs : R == 32 ? 168 : 96, kOtherRegs = R < 32 ? kRegs : R == 32 ? 88 : 48;
+  static_assert(32 * (kSoft * kSoftRegs + 8 * kOtherRegs) <= kThreads * kRegs, "registers of the launch");
   // P V's barriers: as many tiles as the look-ups may lead by.  The pages and scales of twice
   // as many are held.
   static constexpr uint32_t kPv = HD == 128 ? 8 : 4, kAhead = 2 * kPv;
@@ -405,17 +407,17 @@ __device__ __forceinline__ bool any_of_group(int g, bool x) {  // over a softmax
       : "memory");
   return r != 0;
 }
-// ... over both groups
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 3, 256;" ::: "memory"); }
-__device__ __forceinline__ bool soft_any(bool x) {
+// ... over all groups (`threads` of them)
+__device__ __forceinline__ void soft_sync(int threads) { asm volatile("barrier.cta.sync 5, %0;" ::"r"(threads) : "memory"); }
+__device__ __forceinline__ bool soft_any(int threads, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.or.pred p, 3, 256, q;\n\t"
+      "barrier.cta.red.or.pred p, 5, %2, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r)
-      : "r"(x ? 1u : 0u)
+      : "r"(x ? 1u : 0u), "r"(threads)
       : "memory");
   return r != 0;
 }
@@ -424,7 +426,7 @@ __device__ __forceinline__ void group_sync(int g) { asm volatile("barrier.cta.sy
 __device__ __forceinline__ bool nan8(uint32_t byte) { return (byte & 0x7Fu) == 0x7Fu; }
 
 template <int HD, int R>
-__global__ void __launch_bounds__(kC8Threads, 1)
+__global__ void __launch_bounds__(C8Geom<HD, R>::kThreads, 1)
 cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml, float *__restrict__ part_o, int32_t *__restrict__ row_seq) {
   using G = C8Geom<HD, R>;
   extern __shared__ __align__(1024) uint8_t c8_shared[];
@@ -438,7 +440,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
   // ---- the plan (CTA 0 also leaves the sums for the joining launch)
   const uint32_t teams = gridDim.x >> plan.head_log, my_team = blockIdx.x >> plan.head_log;
-  const FoundShare found = find_share(a.seqs.n_seqs, kC8Threads, teams, my_team, both.share, [&](int32_t s) -> int64_t {
+  const FoundShare found = find_share(a.seqs.n_seqs, G::kThreads, teams, my_team, both.share, [&](int32_t s) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
     return c8_seq<R>(a, plan, read_seq(a.seqs, s)).count;
   });
@@ -471,23 +473,23 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(sm32(&C.s_full[b]), 2);
-      mbar_init(sm32(&C.s_free[b]), kC8Soft / G::kOs);
+      mbar_init(sm32(&C.s_free[b]), G::kSoft / G::kOs);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(sm32(&C.p_ready[b]), kC8Soft / G::kOs);
+      mbar_init(sm32(&C.p_ready[b]), G::kSoft / G::kOs);
       mbar_init(sm32(&C.drain[b]), 1);
       C.bad[b] = 0;
     }
     for (int i = 0; i < kC8Segs; ++i) {
       mbar_init(sm32(&C.seg_full[i]), 1);
-      mbar_init(sm32(&C.seg_free[i]), kC8Readers);
+      mbar_init(sm32(&C.seg_free[i]), G::kReaders);
     }
-    mbar_init(sm32(&C.q_full), kC8Soft);
-    mbar_init(sm32(&C.o_free), kC8Soft);
+    mbar_init(sm32(&C.q_full), G::kSoft);
+    mbar_init(sm32(&C.o_free), G::kSoft);
     C.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kC8MmaS) {
+  if (warp == G::kMmaS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm32(&C.tmem_base)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -510,15 +512,15 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     return ok;
   };
 
-  if (warp >= kC8Soft && warp < kC8MmaS) {
-    if constexpr (G::kOtherRegs < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+  if (warp >= G::kSoft && warp < G::kMmaS) {
+    if constexpr (G::kOtherRegs < G::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
     C8Seg g;
     // ---- producers: warp p brings 32 of a tile's tokens, 512 bytes an instruction (kRows
     // rows).  A block's tokens, and so 16 of a tile's from a multiple of 16 on, lie in one
     // page: two places a tile.  A slot's barrier takes each thread's arrival when its copies
     // have landed, so the whole ring may be in flight.
     constexpr int kCh = HD / 16, kRows = 32 / kCh, kN = 16 / kRows;  // chunks of a row, copies of 16 tokens
-    const int p0 = (warp - kC8Soft) * 32, ch = lane % kCh, hl = lane / kCh;
+    const int p0 = (warp - G::kSoft) * 32, ch = lane % kCh, hl = lane / kCh;
     const uint32_t dst0 = sRing + (uint32_t)(ch >> 3) * G::kBox + (uint32_t)(p0 + hl) * 128u;
     const int64_t pitch = (int64_t)a.nkv * HD;
     const int64_t step = kRows * pitch;
@@ -584,15 +586,15 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
       }
       jg += (uint32_t)g.n;
-      if (warp == kC8Soft && !(g.flags & (C8Seg::kWhole | C8Seg::kEmpty))) {  // the rows of a part, for the join
+      if (warp == G::kSoft && !(g.flags & (C8Seg::kWhole | C8Seg::kEmpty))) {  // the rows of a part, for the join
         const int32_t end = fast_div(plan.group_div, min(g.m0 + R, g.rows * a.group) - 1);
         for (int32_t j = fast_div(plan.group_div, g.m0) + lane; j <= end; j += 32) row_seq[g.row0 + j] = g.s;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
-  } else if (warp >= kC8MmaS) {
-    if constexpr (G::kOtherRegs < 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
-    if (warp == kC8Plan) {
+  } else if (warp >= G::kMmaS) {
+    if constexpr (G::kOtherRegs < G::kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+    if (warp == G::kWalk) {
       // ---- the walk
       C8Walk<R> walk(a, plan, found.seq, found.off, laid_out ? found.share.n : 0);
       for (uint32_t k = 0;; ++k) {
@@ -605,7 +607,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
         if (g.flags & C8Seg::kEnd) break;
       }
-    } else if (warp == kC8Look) {
+    } else if (warp == G::kLook) {
       // ---- the look-ups: lane 8 i + e takes 16 tokens of the i-th of four tiles.  Under load
       // a read takes several thousand cycles, so the pages of the next four tiles are read
       // ahead.  Four tiles take the places of those kAhead before them once P V of the tile kPv
@@ -655,7 +657,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
     // ---- MMA issuers: the warp steps through its tiles, one elected lane issues
-    if (warp <= kC8MmaO) {
+    if (warp <= G::kMmaO) {
       C8Seg g;
       bool ok = true;
       auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -691,7 +693,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
       };
       const uint32_t desc_hi = (uint32_t)(sw128_desc(0) >> 32);
       uint32_t jg = 0, part = 0;  // tiles and parts before this one
-      if (warp == kC8MmaS) {
+      if (warp == G::kMmaS) {
         const uint32_t q_lo = (uint32_t)sw128_desc(sQ), r_lo = (uint32_t)sw128_desc(sRing);
         uint32_t b = 0, b_phase = 1;  // S buffer, parity of its s_free phase before this use
         while (ok && take_one()) {
@@ -752,13 +754,13 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
       }
       // every MMA this warp issued has finished before TMEM is freed
-      if (lead) mma_commit(sm32(&C.drain[warp - kC8MmaS]));
+      if (lead) mma_commit(sm32(&C.drain[warp - G::kMmaS]));
       __syncwarp();
-      if (lane == 0) tc_wait(sm32(&C.drain[warp - kC8MmaS]), 0u, kC8SpinLimit, nullptr);
+      if (lane == 0) tc_wait(sm32(&C.drain[warp - G::kMmaS]), 0u, kC8SpinLimit, nullptr);
     }
     __syncwarp();
   } else {
-    if constexpr (G::kSoftRegs > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftRegs));
+    if constexpr (G::kSoftRegs > G::kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftRegs));
     // ---- softmax: thread tk has the tile's token tk (TMEM lane) and, at the end, dims tk
     // and tk + 128.  Group w takes every other tile, or its rows of each.  After an abort
     // every wait returns at once, and the loops and barriers run on to the end.
@@ -776,9 +778,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     // (In batches, the first of them fetched ahead: a part's code runs once or twice a
     // launch, and its instructions cost as much to fetch as the rows.)
     constexpr int kLanes = HD / 8, kPer = 32 / kLanes;  // lanes a row, rows a warp takes at once
-    constexpr int kTimes = (R + kC8Soft * kPer - 1) / (kC8Soft * kPer), kBatch = kTimes < 4 ? kTimes : 4;
+    constexpr int kTimes = (R + G::kSoft * kPer - 1) / (G::kSoft * kPer), kBatch = kTimes < 4 ? kTimes : 4;
     const int ch = lane % kLanes, sub = lane / kLanes;
-    auto row_of = [&](int i) { return (i * kC8Soft + warp) * kPer + sub; };
+    auto row_of = [&](int i) { return (i * G::kSoft + warp) * kPer + sub; };
     uint4 raw[kBatch];
     auto fetch_q = [&](const C8Seg &e, int i0) {
 #pragma unroll
@@ -831,7 +833,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         fetch_q(e, i0);
       }
       if (a.window > 0 && a.seqs.mask != nullptr) {  // the rows' drafted tokens, a lane a row
-        for (int n = tid; n < R; n += 32 * kC8Soft) {
+        for (int n = tid; n < R; n += 32 * G::kSoft) {
           int32_t depth = 0;
           if (e.m0 + n < m_all) {
             const uint32_t *mrow = a.seqs.mask + (int64_t)(e.row0 + fast_div(plan.group_div, e.m0 + n)) * a.seqs.mask_words;
@@ -856,7 +858,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     auto write_out = [&]() {
       if (!(g.flags & C8Seg::kEmpty)) {
         const bool whole = (g.flags & C8Seg::kWhole) != 0;
-        constexpr int kRows = R / 2, kOut = kRows < 8 ? kRows : 8;  // a group's rows of the output, at once
+        constexpr int kRows = R / G::kGroups, kOut = kRows < 8 ? kRows : 8;  // a group's rows of the output, at once
         const int first = w * kRows;
 #pragma unroll 1
         for (int h = 0; h < G::kHalves; ++h) {
@@ -899,7 +901,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     // the next part, unless a wait of one of the softmax's warps gave up
     auto advance = [&](C8Seg &to) -> bool {
       const bool ok = take_seg(to);
-      return !soft_any(!ok) && !(to.flags & C8Seg::kEnd);
+      return !soft_any(32 * G::kSoft, !ok) && !(to.flags & C8Seg::kEnd);
     };
     // Parts overlap: the next one's Q is fetched before this one's output is written.
     bool more = advance(next);
@@ -1094,7 +1096,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           warp_wait(sm32(&C.full[slot]), (at / G::kSlots) & 1u, lim, abort_flag);
           __syncwarp();
           uint4 *vt = reinterpret_cast<uint4 *>(c8_shared + G::kRingOff + slot * G::kSlot);
-          for (int i = G::kTurns ? tk : tid; i < (int)(G::kSlot / 16); i += 32 * kC8Soft / G::kOs) {
+          for (int i = G::kTurns ? tk : tid; i < (int)(G::kSlot / 16); i += 32 * G::kSoft / G::kOs) {
             const uint4 y = vt[i];
             uint32_t e[4] = {y.x, y.y, y.z, y.w}, hit = 0u;
 #pragma unroll
@@ -1127,9 +1129,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         fix = *reinterpret_cast<volatile int32_t *>(&C.bad[seg & 1]) == seg;
       }
       if (fix) {  // rare: the rows of this thread's dims that see a cleared NaN
-        const int first = w * (R / 2);
+        const int first = w * (R / G::kGroups);
 #pragma unroll 1
-        for (int n = first; n < first + R / 2 && m0 + n < m_all; ++n) {
+        for (int n = first; n < first + R / G::kGroups && m0 + n < m_all; ++n) {
           const int32_t j = fast_div(plan.group_div, m0 + n);
           const uint32_t *mrow = chain ? nullptr : a.seqs.mask + (int64_t)(g.row0 + j) * a.seqs.mask_words;
           const int32_t at = g.ctx + (chain ? j : C.depth[n]);
@@ -1164,7 +1166,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         const float mine = over_lanes<kCols>(sum, lane, [](float p, float q) { return p + q; });
         if (lane % (32 / kCols) == 0) sums[warp][lane / (32 / kCols)] = mine;
       }
-      soft_sync();
+      soft_sync(32 * G::kSoft);
       if (!empty && tid < R) {
         const int n = tid;
         float ref = kC8Unset, all = 0.f;
@@ -1192,7 +1194,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
         C.where[n] = where;
       }
-      soft_sync();  // the part's references and sums are read
+      soft_sync(32 * G::kSoft);  // the part's references and sums are read
     }
   }
 
@@ -1200,7 +1202,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && found.share.n > 0 && (C.abort || !laid_out)) report_error(a.status, kErrTimeout, found.seq);
-  if (warp == kC8MmaS)
+  if (warp == G::kMmaS)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -1351,7 +1353,7 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
   while (head_log < 3 && a.nkv % (2 << head_log) == 0) ++head_log;
   const int ctas = ((device_sm_count() < kC8MaxCtas ? device_sm_count() : kC8MaxCtas) >> head_log) << head_log;
   const C8Plan plan = {make_fast_div(a.group), head_log, R / a.group + 2};
-  cudaError_t r = launch_dependent(cache8_attn_kernel<HD, R>, dim3((unsigned)ctas), dim3(kC8Threads), c8_smem<HD, R>(), stream, 1u, a,
+  cudaError_t r = launch_dependent(cache8_attn_kernel<HD, R>, dim3((unsigned)ctas), dim3(C8Geom<HD, R>::kThreads), c8_smem<HD, R>(), stream, 1u, a,
                                    plan, base, ml, o, row_seq);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kC8T) return r;
