@@ -255,8 +255,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Bounded wait on a phase.  Every role's loop has several and they share the instruction
-// cache, so it is short: one instruction that sleeps until the phase completes or some time
-// has passed, then a look at the abort flag and the clock.
+// cache, so it is short: after a test, a look at the abort flag and the clock and one
+// instruction that sleeps until the phase completes or some time has passed.
 __device__ __forceinline__ bool phase_done(uint32_t mb, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -269,15 +269,15 @@ __device__ __forceinline__ bool phase_done(uint32_t mb, uint32_t parity) {
   return ok != 0;
 }
 __device__ __forceinline__ bool one_wait(uint32_t mb, uint32_t parity, long long limit, volatile int32_t *abort_flag) {
-  if (phase_done(mb, parity)) return true;
+  if (mbar_test(mb, parity)) return true;
   const long long t0 = clock64();
-  while (!phase_done(mb, parity)) {
+  do {
     if (*abort_flag) return false;
     if (clock64() - t0 > limit) {
       *abort_flag = 1;
       return false;
     }
-  }
+  } while (!phase_done(mb, parity));
   return true;
 }
 // ... of a warp, each lane for itself, the verdict the warp's.
