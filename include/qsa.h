@@ -94,9 +94,10 @@ const char *qsa_status_string(int32_t status);
  * the block keys they copy into shared memory and for their MMAs
  * (qsa_score_rows on the SIMT and QSA_SCORE_STREAM paths), the fused
  * decode step's waits for its key copies, its MMAs and its barrier over a
- * row's CTAs (qsa_decode_index_select), and the waits of tree attention and
- * attention mass for their copies, their MMAs and the buffers that these pass
- * on (qsa_tree_attn, qsa_attn_mass: what they then leave is said there).  A wait
+ * row's CTAs (qsa_decode_index_select), and the waits of tree attention,
+ * attention over an 8-bit cache and attention mass for their copies, their MMAs and
+ * the buffers that these pass on (qsa_tree_attn, qsa_cache8_attn, qsa_attn_mass:
+ * what they then leave is said there).  A wait
  * that reaches the limit records QSA_ERR_TIMEOUT with its row in dev_status
  * and the row's output is left unspecified (a fused decode call may then
  * leave its workspace dirty: zero it before the next call); the CTA first
@@ -640,6 +641,7 @@ qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, 
  *  tables, pages and heights stay as they were.  A page outside the pool among those
  *  given back, taken or used by a row is QSA_ERR_TOKEN_RANGE with the sequence's index; a
  *  slot in it is -1.
+ *  n_seqs 0 does nothing: no output is written.
  *  Refused: n_seqs > 65535, pool_pages * page_size or table_len * page_size past 31
  *  bits, table_cols = 0 with several sequences.
  */
@@ -679,7 +681,8 @@ qsa_status qsa_page_plan(const int32_t *ctx_len, const int32_t *new_rows, int32_
  *           an infinity is held as NaN.
  *  q_out    DEVICE bf16, row i at q_out + i*out_stride (nq*head_dim values), 16-byte
  *           aligned, out_stride a multiple of 8; q itself with q_stride is allowed.
- *  Everything runs in f32 and is rounded once, to bf16 or e4m3.  head_dim is 128 or 256.
+ *  Everything runs in f32 and is rounded once, to bf16 or e4m3; bf16 V is copied.
+ *  head_dim is 128 or 256.
  *  Rows outside every sequence, and what the cache holds past its new tokens, are left
  *  alone.  Sequences must not share a page that new tokens go to.
  *  Device errors: a sequence whose rows or context contradict n_rows or the table is
@@ -715,9 +718,11 @@ qsa_status qsa_qkv_write(const uint16_t *q, int64_t q_stride, int32_t nq, const 
  *           is ctx_len + j for row j without a tree_mask (which then holds for drafted
  *           tokens t <= p too), and ctx_len + max(0, c - 1) for a row whose tree_mask
  *           names c drafted tokens of its sequence (those are seen whatever the window).
- *           Cached tokens that no row sees are not read.
+ *           Tokens from n_first on that lie window or more before ctx_len are not read:
+ *           pages, scales and table entries that hold only such tokens may be gone.
  *  A row that attends no token gets zeros, and lse -inf.  What a row does not see does
- *  not reach its output, NaN though it be.
+ *  not reach its output, NaN though it be.  A query head with a value that is not finite
+ *  gets NaN.
  *  Products, softmax and sums run in f32.  A row's weights times their block's V scale
  *  enter the weighted sum as two e4m3 terms, relative to the row's largest: off by at
  *  most 2^-8 of themselves, or 2^-18 of the largest; those of 2^-96 of it and less may
@@ -727,7 +732,7 @@ qsa_status qsa_qkv_write(const uint16_t *q, int64_t q_stride, int32_t nq, const 
  *           its contents on entry do not matter.  Calls that share one must be
  *           stream-ordered.
  *  Device errors and refusals as in qsa_tree_attn (its product bounds too), and: a scale
- *  that is negative or not finite among tokens that are read is QSA_ERR_NONFINITE with
+ *  of a token that a row sees which is negative or not finite is QSA_ERR_NONFINITE with
  *  the sequence's index, whose output is then unspecified.  Refused: another unit, a
  *  negative window or n_first.
  */

@@ -12,19 +12,37 @@
 //
 // What e4m3's four bits lose is kept in a second term, its own columns beside the first:
 // q 2^-e = hi + lo / 16 (a bf16 q has eight bits, so this is exact but for what lies
-// 2^-21 below the head's largest value), and the weight w = exp(s - ref) vs = hi + lo / 16
-// (off by 2^-9 of itself, or by 2^-15 where ref is such that the row's largest w is 32 or
-// more: 2^-20 of it).  ref is log2 of a maximum of exp(s) vs seen earlier, less 5; it
-// moves (the row's sum and its columns of O rescaled) when a w passes 448, e4m3's largest.
-// The sum is of the f32 weights without vs.
+// 2^-20 below the head's largest value), and the weight w = exp(s - ref) vs = hi + lo / 16,
+// off by 2^-9 of itself, or by 2^-14 where w is small: 2^-18 of the row's largest, which is
+// 16 or more.  ref is log2 of a maximum of exp(s) vs seen earlier, less 4; it moves (the
+// row's sum and its columns of O rescaled) when a w passes 448, e4m3's largest.  The sum is
+// of the f32 weights without vs.  Against 64 bits the outputs are off by 0.0018 of their
+// norm, by 0.0017 if q and the weights had 32 bits.
 //
 // A unit of work is (sequence, KV head, R such rows); its tiles are a run of the launch's
 // linear list of tiles, of which every CTA (one per SM) takes an equal, contiguous share.
 // A unit that lies in one CTA's share is written at once; the parts of any other go to
-// the workspace as (O, ref, sum) and a second launch joins them in a fixed order.
+// the workspace as (O, ref, sum) and a second launch joins them in a fixed order.  CTAs take
+// up to eight KV heads side by side: they read neighbouring pieces of the same rows at the
+// same time, which for 8 heads of 128 bytes brings HBM from 5.3 to 6.4 TB/s.  Units of
+// rows side by side gained nothing (64 rows of 65k tokens 126 us each way) and lost where
+// sequences have fewer units (24 of 5 to 37 rows 194 us alone, 227 in pairs).
 //
-// The warps: groups of four do the softmax, a token of a tile per thread; four copy K and V rows into a ring of slots (16-byte
-// cp.async, 128-byte swizzle); one issues S, one P V.
+// Roles by warp: groups of four do the softmax, a token of a tile per thread; four copy K
+// and V rows into a ring of slots (16-byte cp.async, 128-byte swizzle); one issues S, one
+// P V; one looks pages up, ahead, and brings the scales; one walks the CTA's share and hands
+// its parts to the others.  Their loops run side by side and share one instruction cache:
+// at about 40 KB of hot code a quarter of the fetches missed, and every instruction waited three
+// cycles for its fetch (decode 118 us, 64 rows of 65k 197 us); one copy loop, waits of a few
+// instructions and MMAs issued from a uniform loop took the misses to 5 % (106 and 127 us).
+// For the same reason a part's beginning and end are short: they run once or twice a launch.
+//
+// Decode is bound by HBM: 16 sequences of 16k to 64k tokens, 16 heads over 2 x 256, take
+// 106 us, 90 % of the copy bandwidth; 32 heads over 8 x 128 197 us, 97 %.  With more rows the
+// softmax bounds it: a tile of 64 rows is 8192 weights, each about 12 instructions (two
+// terms of S joined, two scales, the exponential, two terms of w), beside 150 a warp for
+// barriers and look-ups.  64 rows of 65471 tokens take 117 us (31 % of the bf16 rate), the
+// MMAs busy for 22 % of it.
 #include "qsa_launch.h"
 #include "qsa_share.cuh"
 #include "qsa_tc_cache.cuh"
@@ -51,7 +69,9 @@ struct C8Geom {
   static constexpr int kHalves = HD / 128;
   // Up to 32 rows two softmax groups of four warps take tiles in turn, each with a sum,
   // references and an O of its own, joined at the part's end; of 64, four groups take a
-  // quarter of every tile's rows each (two with a half of them: 120 us where four take N us).
+  // quarter of every tile's rows each.  (Two groups with a half of them: a chunk of 2048 rows
+  // in a window of 1024 229 us, four 209; trees of 5 to 37 rows 176 and 171; 64 rows of 65k
+  // tokens 117 each way.)
   static constexpr bool kTurns = R < 64;
   static constexpr int kGroups = kTurns ? 2 : 4, kCols = kTurns ? R : R / kGroups;  // a group's rows of a tile
   // the warps: softmax, copies, issuers of S and of P V, look-ups and scales, the walk
@@ -709,14 +729,14 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             const uint32_t d = tmem + G::kSCol + b * G::kN, k_lo = r_lo + slot * (G::kSlot >> 4);
             if (lead) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 32; ++kk) {
-              const uint32_t in = (uint32_t)(kk & 3) * 2u;  // 32 bytes
-              mma_e4m3(d, desc_of(k_lo + (uint32_t)(kk >> 2) * (G::kBox >> 4) + in, desc_hi),
-                       desc_of(q_lo + (uint32_t)(kk >> 2) * (G::kQBox >> 4) + in, desc_hi), G::kIdescS, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(sm32(&C.empty[slot]));
-            mma_commit(sm32(&C.s_full[b]));
-            mbar_arrive(sm32(&C.s_full[b]));
+              for (int kk = 0; kk < HD / 32; ++kk) {
+                const uint32_t in = (uint32_t)(kk & 3) * 2u;  // 32 bytes
+                mma_e4m3(d, desc_of(k_lo + (uint32_t)(kk >> 2) * (G::kBox >> 4) + in, desc_hi),
+                         desc_of(q_lo + (uint32_t)(kk >> 2) * (G::kQBox >> 4) + in, desc_hi), G::kIdescS, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(sm32(&C.empty[slot]));
+              mma_commit(sm32(&C.s_full[b]));
+              mbar_arrive(sm32(&C.s_full[b]));
             }
             __syncwarp();
             if (++b == (uint32_t)G::kS) {
@@ -740,13 +760,13 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             const uint32_t p = p_lo + (jg & 1u) * (G::kBox >> 4), v_lo = r_lo + slot * (G::kSlot >> 4);
             if (lead) {
 #pragma unroll
-            for (int h = 0; h < G::kHalves; ++h)
+              for (int h = 0; h < G::kHalves; ++h)
 #pragma unroll
-              for (int kk = 0; kk < kC8T / 32; ++kk)  // 32 tokens a step: 4 KiB of V's and of P's rows
-                mma_e4m3(o + (uint32_t)h * G::kN, desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi),
-                         desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
-            mma_commit(sm32(&C.empty[slot]));
-            mma_commit(sm32(&C.pv_done[jg % G::kPv]));
+                for (int kk = 0; kk < kC8T / 32; ++kk)  // 32 tokens a step: 4 KiB of V's and of P's rows
+                  mma_e4m3(o + (uint32_t)h * G::kN, desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi),
+                           desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
+              mma_commit(sm32(&C.empty[slot]));
+              mma_commit(sm32(&C.pv_done[jg % G::kPv]));
             }
             __syncwarp();
           }
