@@ -36,12 +36,14 @@
 // cycles for its fetch (decode 118 us, 64 rows of 65k 197 us); one copy loop, waits of a few
 // instructions and MMAs issued from a uniform loop took the misses to 5 % (106 and 127 us).
 // For the same reason a part's beginning and end are short: they run once or twice a launch.
+// (Where they run often, they bound it: 512 rows over 64 to 400 tokens of 8 KV heads, 27 parts
+// of one or two tiles a CTA, take 130 us, 4.4 us a part, of which the tiles are 40 %.)
 //
 // Decode is bound by HBM: 16 sequences of 16k to 64k tokens, 16 heads over 2 x 256, take
 // 106 us, 90 % of the copy bandwidth; 32 heads over 8 x 128 197 us, 97 %.  With more rows the
 // softmax bounds it: a tile of 64 rows is 8192 weights, each about 12 instructions (two
 // terms of S joined, two scales, the exponential, two terms of w), beside 150 a warp for
-// barriers and look-ups.  64 rows of 65471 tokens take 117 us (31 % of the bf16 rate), the
+// barriers and look-ups.  64 rows of 65471 tokens take 116 us (31 % of the bf16 rate), the
 // MMAs busy for 22 % of it.
 #include "qsa_launch.h"
 #include "qsa_share.cuh"
@@ -70,8 +72,8 @@ struct C8Geom {
   // Up to 32 rows two softmax groups of four warps take tiles in turn, each with a sum,
   // references and an O of its own, joined at the part's end; of 64, four groups take a
   // quarter of every tile's rows each.  (Two groups with a half of them: a chunk of 2048 rows
-  // in a window of 1024 229 us, four 209; trees of 5 to 37 rows 176 and 171; 64 rows of 65k
-  // tokens 117 each way.)
+  // in a window of 1024 229 us, four 207; trees of 5 to 37 rows 176 and 169; 64 rows of 65k
+  // tokens 116 each way.)
   static constexpr bool kTurns = R < 64;
   static constexpr int kGroups = kTurns ? 2 : 4, kCols = kTurns ? R : R / kGroups;  // a group's rows of a tile
   // the warps: softmax, copies, issuers of S and of P V, look-ups and scales, the walk
@@ -372,6 +374,18 @@ __device__ __forceinline__ void tmem_scale1(uint32_t taddr, float by) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x)::"memory");
   x = __float_as_uint(__uint_as_float(x) * by);
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(x) : "memory");
+}
+
+// Within 2^-23 of 1 / x, and within 2^-22 of log2 x: short, for code that runs once a part.
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -1020,7 +1034,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
             }
           }
           if (move) {
-            const float lv = log2f(vx);
+            const float lv = lg2(vx);
             float l[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) l[i] = ((see >> i) & 1u) ? x[i] + lv : -INFINITY;
@@ -1203,14 +1217,14 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           ref = -C.less_ref[n];
           all = sum_of(n / kCols, n % kCols);
         }
-        inverse[n] = !whole ? 1.f : all == 0.f ? 0.f : 1.f / all;
+        inverse[n] = !whole ? 1.f : all == 0.f ? 0.f : rcp(all);
         int64_t where = -1;
         if (m0 + n < m_all) {
           const int32_t j = fast_div(plan.group_div, m0 + n), head = g.kvh * a.group + (m0 + n - j * a.group);
           where = whole ? (int64_t)(g.row0 + j) * a.out_stride + (int64_t)head * HD : (part * R + n) * HD;
           if (!whole) part_ml[part * R + n] = make_float2(ref, all);
           else if (a.lse)
-            a.lse[(int64_t)(g.row0 + j) * a.nq + head] = all == 0.f ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
+            a.lse[(int64_t)(g.row0 + j) * a.nq + head] = all == 0.f ? -INFINITY : (ref + lg2(all)) * 0.6931471805599453f;
         }
         C.where[n] = where;
       }
