@@ -24,7 +24,7 @@
 // A unit that lies in one CTA's share is written at once; the parts of any other go to
 // the workspace as (O, ref, sum) and a second launch joins them in a fixed order.  CTAs take
 // up to eight KV heads side by side: they read neighbouring pieces of the same rows at the
-// same time, which for 8 heads of 128 bytes brings HBM from 5.3 to 6.4 TB/s.  Units of
+// same time, which for 8 heads of 128 bytes brought HBM from 5.3 to 6.4 TB/s.  Units of
 // rows side by side gained nothing (64 rows of 65k tokens 126 us each way) and lost where
 // sequences have fewer units (24 of 5 to 37 rows 194 us alone, 227 in pairs).
 //
@@ -37,14 +37,14 @@
 // instructions and MMAs issued from a uniform loop took the misses to 5 % (106 and 127 us).
 // For the same reason a part's beginning and end are short: they run once or twice a launch.
 // (Where they run often, they bound it: 512 rows over 64 to 400 tokens of 8 KV heads, 27 parts
-// of one or two tiles a CTA, take 130 us, 4.4 us a part, of which the tiles are 40 %.)
+// of one or two tiles a CTA, take 125 us, 4.4 us a part, of which the tiles are 40 %.)
 //
 // Decode is bound by HBM: 16 sequences of 16k to 64k tokens, 16 heads over 2 x 256, take
-// 106 us, 90 % of the copy bandwidth; 32 heads over 8 x 128 197 us, 97 %.  With more rows the
+// 104 us, 92 % of the copy bandwidth; 32 heads over 8 x 128 194 us, 98 %.  With more rows the
 // softmax bounds it: a tile of 64 rows is 8192 weights, each about 12 instructions (two
 // terms of S joined, two scales, the exponential, two terms of w), beside 150 a warp for
-// barriers and look-ups.  64 rows of 65471 tokens take 116 us (31 % of the bf16 rate), the
-// MMAs busy for 22 % of it.
+// barriers and look-ups.  64 rows of 65471 tokens take 114 us (32 % of the bf16 rate), the
+// MMAs busy for 28 % of it.
 #include "qsa_launch.h"
 #include "qsa_share.cuh"
 #include "qsa_tc_cache.cuh"
@@ -1244,7 +1244,10 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
 // 4 dims a lane and half, and every kGroups-th part; the groups' results are then added
 // in order.  The plan and the parts are written while this launch is already resident, so
 // they are no __restrict__ arguments: nothing may read them ahead of the wait.
-constexpr int kC8JoinWarps = 8;
+// Four warps of 64 registers are what the SM has left beside a CTA of 8 rows, so that they wait
+// there while it runs (of eight, which start when it ends: decode of 16 rows 106.6 us, 104.6
+// with four; in a window of 4096 24.6 and 23.4; one row of 65535 tokens 25.7 and 24.4).
+constexpr int kC8JoinWarps = 4;
 
 template <int HD, int R, int kGroups>
 __global__ void __launch_bounds__(32 * kC8JoinWarps)
@@ -1391,7 +1394,7 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
                                    plan, base, ml, o, row_seq);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kC8T) return r;
-  // One group of parts per warp where units outnumber the CTAs (few parts each), eight
+  // One group of parts per warp where units outnumber the CTAs (few parts each), a CTA's
   // where a unit spreads over many.
   const int64_t rows = (int64_t)a.seqs.n_rows * a.group, units = (int64_t)a.nkv * ((rows + R - 1) / R);
   const bool many = ctas >= 8 * units;

