@@ -376,7 +376,8 @@ __device__ __forceinline__ void tmem_scale1(uint32_t taddr, float by) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(x) : "memory");
 }
 
-// Within 2^-23 of 1 / x, and within 2^-22 of log2 x: short, for code that runs once a part.
+// 1 / x within 2^-23 of it, and log2 x (within 2^-22, or 2^-22 of it outside [1/2, 2]): short,
+// for code that runs once a part.
 __device__ __forceinline__ float rcp(float x) {
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -386,6 +387,14 @@ __device__ __forceinline__ float lg2(float x) {
   float r;
   asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// ref + log2 of a sum (a normal number), in units of e: x = 2^e m with m in [3/4, 3/2), whose
+// logarithm is within 2^-22.
+__device__ __forceinline__ float lse_of(float ref, float x) {
+  const int32_t e = ((int32_t)__float_as_uint(x) - 0x3F400000) >> 23;
+  const float m = __uint_as_float(__float_as_uint(x) - ((uint32_t)e << 23));
+  return (ref + (float)e + lg2(m)) * 0.6931471805599453f;
 }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -1224,7 +1233,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
           where = whole ? (int64_t)(g.row0 + j) * a.out_stride + (int64_t)head * HD : (part * R + n) * HD;
           if (!whole) part_ml[part * R + n] = make_float2(ref, all);
           else if (a.lse)
-            a.lse[(int64_t)(g.row0 + j) * a.nq + head] = all == 0.f ? -INFINITY : (ref + lg2(all)) * 0.6931471805599453f;
+            a.lse[(int64_t)(g.row0 + j) * a.nq + head] = all == 0.f ? -INFINITY : lse_of(ref, all);
         }
         C.where[n] = where;
       }

@@ -5,7 +5,7 @@ Tolerances, from the arithmetic (U = 2^-24, a rounding to f32; 2^-8 one to bf16,
 one to e4m3, whose steps below 2^-6 are 2^-9 each).
 
 Write: a head's sum of squares runs in f32 over 8 terms a lane and 5 sums of lanes, the
-root and its reciprocal round once each, x r (1 + w) three times: under 16 U of a value
+reciprocal root is off by 2^-22.9, x r (1 + w) rounds three times: under 16 U of a value
 together, and a turned value x c + y s adds 2 U (|x c| + |y s|).
 
 Attention: a logit is scale ks sum q_d k_d, accumulated in f32 whose adder may
