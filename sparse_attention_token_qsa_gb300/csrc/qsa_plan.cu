@@ -11,8 +11,9 @@
 // or rows a cluster of eight, whose CTAs all sum the lengths and share the pages to move, with a
 // cluster barrier where one reads what another wrote; so the lengths,
 // heights and tables may be updated in place.  Many rows are filled by a second launch: 1024
-// sequences of up to 256 rows, 131k in all, take 16.3 us (32.8 by one cluster alone, whose CTAs
-// each moved their own sequences' pages).  64 single rows take as long as a launch.
+// sequences of up to 256 rows, 131k in all, take 15.0 us (32.8 by one cluster alone, whose CTAs
+// each moved their own sequences' pages).  64 single rows take 6.5 us, a launch and the chain
+// (7.7 with the warps' sums added up one by one and the rows' places fetched from L2).
 #include "qsa_launch.h"
 
 namespace qsa {
@@ -65,8 +66,9 @@ struct PlanSums {
 };
 
 // Warp `at` of `warps` fills its run of the rows' places, 32 at a time; `base`: a sequence no
-// later than theirs.
-__device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t warps, int64_t rows, int lane) {
+// later than theirs.  start(s): sequence s's first row, ctx(s): its cached tokens.
+template <typename Start, typename Ctx>
+__device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t warps, int64_t rows, int lane, Start &&start, Ctx &&ctx) {
   const int64_t per = (((int64_t)a.max_rows + warps - 1) / warps + 31) / 32 * 32;
   const int64_t r0 = at * per, r1 = min((int64_t)a.max_rows, r0 + per);
   int32_t base = 0;
@@ -74,7 +76,7 @@ __device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t
     int32_t hi = a.n_seqs;
     while (hi - base > 1) {
       const int32_t step = (hi - base + 31) / 32, probe = base + lane * step;
-      const uint32_t hit = __ballot_sync(0xffffffffu, probe < hi && __ldcg(a.row_start + probe) <= r0);
+      const uint32_t hit = __ballot_sync(0xffffffffu, probe < hi && start(probe) <= r0);
       base += (31 - __clz((int)hit)) * step;
       hi = min(hi, base + step);
     }
@@ -84,7 +86,7 @@ __device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t
     int32_t seq = -1;
     bool open = r < rows;
     while (__any_sync(0xffffffffu, open)) {
-      const int64_t end = __ldcg(a.row_start + min(base + 1 + lane, a.n_seqs));
+      const int64_t end = start(min(base + 1 + lane, a.n_seqs));
       const int n = lanes_upto(end, r);
       if (open && n < 32) {
         seq = base + n;
@@ -96,7 +98,7 @@ __device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t
     if (r >= r1) continue;
     int32_t slot = -1, t = 0;
     if (seq >= 0) {
-      t = a.ctx_len[seq] + (int32_t)(r - __ldcg(a.row_start + seq));
+      t = ctx(seq) + (int32_t)(r - start(seq));
       const int32_t pg = fast_div(a.page, t), page = __ldcg(a.table + (int64_t)seq * a.table_cols + pg);
       if (page >= 0 && page < a.pool_pages) slot = page * a.page.d + (t - pg * a.page.d);
       else report_error(a.status, kErrTokenRange, seq);
@@ -109,6 +111,9 @@ __device__ __forceinline__ void fill_rows(const PlanArgs &a, int64_t at, int64_t
 
 __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a, bool fill) {
   __shared__ int64_t scan[3][kPlWarps];
+  // Up to as many sequences as threads: their first rows and contexts, which the rows
+  // would else fetch in three trips to L2, one after another.
+  __shared__ int32_t starts[kPlThreads + 1], contexts[kPlThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = blockIdx.x, ranks = gridDim.x;  // the grid is one cluster
   grid_dependency_sync();
@@ -124,21 +129,20 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a,
       scan[2][warp] = t;
     }
     __syncthreads();
-    PlanSums at = {before.rows + r - p.rows, before.back + b - p.back, before.take + t - p.take};
-    for (int i = 0; i < kPlWarps; ++i) {
-      const int64_t x = scan[0][i], y = scan[1][i], z = scan[2][i];
-      if (i < warp) {
-        at.rows += x;
-        at.back += y;
-        at.take += z;
-      }
-      before.rows += x;
-      before.back += y;
-      before.take += z;
-    }
+    // the warps' sums, a lane a warp
+    auto place = [&](const int64_t *sums, int64_t incl, int64_t &all) -> int64_t {
+      const int64_t own = sums[lane], upto = warp_scan(own, lane), first = all + __shfl_sync(0xffffffffu, upto - own, warp);
+      all += __shfl_sync(0xffffffffu, upto, 31);
+      return first + incl;
+    };
+    PlanSums at;
+    at.rows = place(scan[0], r - p.rows, before.rows);
+    at.back = place(scan[1], b - p.back, before.back);
+    at.take = place(scan[2], t - p.take, before.take);
     return at;
   };
 
+  const int64_t free0 = *a.n_free;  // (on its way beside the lengths)
   PlanSums all = {0, 0, 0};
   PlanSeq p;
   PlanSums at = {0, 0, 0};
@@ -147,9 +151,16 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a,
     if (rank == 0 && !p.ok) report_error(a.status, kErrRowRange, s0 + tid);
   }
   const bool one_chunk = a.n_seqs <= kPlThreads;  // p and at stay good
-  const int64_t free0 = *a.n_free, height = free0 + all.back;
+  const int64_t height = free0 + all.back;
   const bool stack_ok = free0 >= 0 && height <= a.pool_pages, rows_ok = all.rows <= a.max_rows;
   const bool ok = stack_ok && rows_ok && all.take <= height;
+  if (one_chunk && ok) {  // (met by the barriers before the rows)
+    if (tid < a.n_seqs) {
+      starts[tid] = (int32_t)at.rows;
+      contexts[tid] = a.ctx_len[tid];
+    }
+    if (tid == 0) starts[a.n_seqs] = (int32_t)all.rows;
+  }
 
   // The items of this warp's sequences, shared with the same warp of the other CTAs, which has
   // the same sequences: from(s, i, k) reads the i-th of sequence s's, the k-th of all, and
@@ -223,14 +234,18 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a,
   }
   if (rank == 0 && tid == 0) *a.n_free_out = ok ? (int32_t)(height - all.take) : (int32_t)free0;
 
-  if (fill) fill_rows(a, (int64_t)rank * kPlWarps + warp, (int64_t)ranks * kPlWarps, ok ? all.rows : 0, lane);
+  if (!fill) return;
+  const int64_t mine = (int64_t)rank * kPlWarps + warp, warps = (int64_t)ranks * kPlWarps, rows = ok ? all.rows : 0;
+  if (one_chunk) fill_rows(a, mine, warps, rows, lane, [&](int32_t s) { return starts[s]; }, [&](int32_t s) { return contexts[s]; });
+  else fill_rows(a, mine, warps, rows, lane, [&](int32_t s) { return __ldcg(a.row_start + s); }, [&](int32_t s) { return a.ctx_len[s]; });
 }
 
 // The rows of a large step, by all SMs.
 __global__ void __launch_bounds__(kFillThreads) plan_rows_kernel(const PlanArgs a) {
   grid_dependency_sync();
   const int64_t warps = (int64_t)gridDim.x * (kFillThreads / 32);
-  fill_rows(a, (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5), warps, a.row_start[a.n_seqs], threadIdx.x & 31);
+  fill_rows(a, (int64_t)blockIdx.x * (kFillThreads / 32) + (threadIdx.x >> 5), warps, a.row_start[a.n_seqs], threadIdx.x & 31,
+            [&](int32_t s) { return __ldcg(a.row_start + s); }, [&](int32_t s) { return a.ctx_len[s]; });
 }
 
 }  // namespace
