@@ -40,7 +40,7 @@
 // of one or two tiles a CTA, take 125 us, 4.4 us a part, of which the tiles are 40 %.)
 //
 // Decode is bound by HBM: 16 sequences of 16k to 64k tokens, 16 heads over 2 x 256, take
-// 104 us, 92 % of the copy bandwidth; 32 heads over 8 x 128 194 us, 98 %.  With more rows the
+// 102 us, 93 % of the copy bandwidth; 32 heads over 8 x 128 194 us, 98 %.  With more rows the
 // softmax bounds it: a tile of 64 rows is 8192 weights, each about 12 instructions (two
 // terms of S joined, two scales, the exponential, two terms of w), beside 150 a warp for
 // barriers and look-ups.  64 rows of 65471 tokens take 114 us (32 % of the bf16 rate), the
@@ -73,7 +73,8 @@ struct C8Geom {
   // references and an O of its own, joined at the part's end; of 64, four groups take a
   // quarter of every tile's rows each.  (Two groups with a half of them: a chunk of 2048 rows
   // in a window of 1024 229 us, four 207; trees of 5 to 37 rows 176 and 169; 64 rows of 65k
-  // tokens 116 each way.)
+  // tokens 116 each way.  Two that take tiles of 64 columns in turn, which heads of 128 leave
+  // room for: 267 us the chunk, 212 the trees.)
   static constexpr bool kTurns = R < 64;
   static constexpr int kGroups = kTurns ? 2 : 4, kCols = kTurns ? R : R / kGroups;  // a group's rows of a tile
   // the warps: softmax, copies, issuers of S and of P V, look-ups and scales, the walk
