@@ -1414,17 +1414,39 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
                           reinterpret_cast<const float4 *>(o), row_seq);
 }
 
+// The rows of a unit.  Enough for a sequence's rows by the call's mean, as a tile of 64 costs
+// 2.1 us of a CTA where one of 32 costs 1.2, of 16 0.86 and of 8 0.77.  Fewer where the GPU would
+// stand idle meanwhile: a unit of 64 takes 10 us besides its tiles, one of 8 a third of that.
+// So by how many tiles of such units, and 3 for what a unit costs besides, a CTA would get at
+// most.  8, 16, 32, 64 rows a unit (us, in a graph):
+//   0.4  2 sequences of 10 rows, 16 heads over 2, a window of 199     13.6  14.0  15.2  17.4
+//   0.9  4 of 24, 16 over 2, 300 tokens                               19.9  15.2  16.9  20.1
+//   1.0  1 of 64, 16 over 2, 600 tokens                               18.8  16.5  17.5  19.9
+//   1.4  1 of 24, 16 over 2, 4000 tokens                              20.3  20.3  18.9  20.9
+//   2.5  4 of 64, 16 over 2, 300 tokens                               31.2  25.4  18.7  21.3
+//   3.3  6 of 112, 16 over 2, 22 to 139 tokens                        58.1  40.2  35.1  34.7
+//   8.9  17 of 95, 12 over 4, 8 tokens                                80.6  55.7  43.0  35.8
+int32_t rows_of_unit(const Cache8Args &a, int64_t most) {
+  const int64_t n = a.seqs.n_seqs, mean = ((int64_t)a.seqs.n_rows * a.group + n - 1) / n;
+  const int64_t all = (most + kC8T - 1) / kC8T;
+  const int64_t near = a.window > 0 ? ((int64_t)a.n_first + kC8T - 1) / kC8T + ((int64_t)a.window + kC8T - 1) / kC8T + 1 : all;
+  const int64_t work = n * a.nkv * ((mean + 63) / 64) * ((all < near ? all : near) + 3), ctas = device_sm_count();
+  const int32_t by_work = 2 * work <= ctas ? 8 : 5 * work <= 6 * ctas ? 16 : work <= 3 * ctas ? 32 : 64;
+  const int32_t by_mean = mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+  return by_work < by_mean ? by_work : by_mean;
+}
+
 template <int HD>
 cudaError_t launch_hd(const Cache8Args &args, cudaStream_t stream) {
   Cache8Args a = args;
   const int64_t most = (int64_t)a.seqs.table_len * a.seqs.page.d;  // (below 2^31 - 256)
   if (a.window >= most) a.window = 0;  // no cached token is that far back
   a.n_first = a.window == 0 ? 0 : (int32_t)(a.n_first < most ? a.n_first : most);
-  const int64_t mean_rows = ((int64_t)a.seqs.n_rows * a.group + a.seqs.n_seqs - 1) / a.seqs.n_seqs;
-  return mean_rows <= 8    ? launch_rows<HD, 8>(a, stream)
-         : mean_rows <= 16 ? launch_rows<HD, 16>(a, stream)
-         : mean_rows <= 32 ? launch_rows<HD, 32>(a, stream)
-                           : launch_rows<HD, 64>(a, stream);
+  const int32_t rows = rows_of_unit(a, most);
+  return rows == 8    ? launch_rows<HD, 8>(a, stream)
+         : rows == 16 ? launch_rows<HD, 16>(a, stream)
+         : rows == 32 ? launch_rows<HD, 32>(a, stream)
+                      : launch_rows<HD, 64>(a, stream);
 }
 
 }  // namespace
