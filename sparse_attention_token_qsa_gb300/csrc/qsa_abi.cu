@@ -655,7 +655,7 @@ int64_t qsa_cache8_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t nq, i
   if (n_seqs < 0 || n_rows < 0 || nq <= 0 || nkv <= 0 || nq % nkv != 0 ||
       (head_dim != 128 && head_dim != 256))
     return -1;
-  return qsa::cache8_workspace_bytes(n_seqs, n_rows, nq / nkv, head_dim);
+  return qsa::cache8_workspace_bytes(n_rows, nq / nkv, head_dim);
 }
 
 qsa_status qsa_cache8_attn(const uint16_t *q, int64_t q_stride, int32_t nq, int32_t nkv,

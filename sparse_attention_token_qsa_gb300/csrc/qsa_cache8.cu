@@ -163,6 +163,11 @@ struct C8Seg {
   __device__ bool wants(const Cache8Args &a, int32_t t) const { return t < ctx + rows && (t < a.n_first || t >= back); }
 };
 
+// The unit whose first tiles a CTA ends with, and the team that has its last ones; -1: none.
+struct C8Open {
+  int32_t row0, rows, m0, kvh, last;
+};
+
 // Walks a team's share of the list, unit by unit, the sequences' lengths read one ahead.
 template <int R>
 struct C8Walk {
@@ -172,6 +177,7 @@ struct C8Walk {
   int32_t s;
   C8Seq q;
   SeqRaw ahead;
+  int32_t rest;  // of the unit whose part next() gave, the tiles behind it
   __device__ C8Walk(const Cache8Args &a_, const C8Plan &p_, int32_t s_, int64_t off_, int64_t left_)
       : a(a_), p(p_), left(left_), off(off_), s(s_) {
     if (left <= 0) return;
@@ -200,6 +206,7 @@ struct C8Walk {
     off += part;
     left -= part;
     const int32_t i0 = max(0, from - c8_start<R>()), take = max(0, from + part - c8_start<R>()) - i0;
+    rest = q.tiles - i0 - take;
     g.s = s;
     const int32_t heads = unit / q.m_tiles, mt = unit - heads * q.m_tiles;
     g.kvh = (heads << p.head_log) + ((int32_t)blockIdx.x & ((1 << p.head_log) - 1));
@@ -471,7 +478,7 @@ __device__ __forceinline__ bool nan8(uint32_t byte) { return (byte & 0x7Fu) == 0
 
 template <int HD, int R>
 __global__ void __launch_bounds__(C8Geom<HD, R>::kThreads, 1)
-cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ base_out, float2 *__restrict__ part_ml, float *__restrict__ part_o, int32_t *__restrict__ row_seq) {
+cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ open, float2 *__restrict__ part_ml, float *__restrict__ part_o) {
   using G = C8Geom<HD, R>;
   extern __shared__ __align__(1024) uint8_t c8_shared[];
   auto &both = *reinterpret_cast<C8Scratch<G::kMix, G::kAhead> *>(c8_shared + G::kCtrlOff);
@@ -482,28 +489,14 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
   volatile int32_t *abort_flag = &C.abort;
 
   grid_dependency_sync();  // before TMEM too: an earlier launch may hold it
-  // ---- the plan (CTA 0 also leaves the sums for the joining launch)
+  // ---- the plan
   const uint32_t teams = gridDim.x >> plan.head_log, my_team = blockIdx.x >> plan.head_log;
   const FoundShare found = find_share(a.seqs.n_seqs, G::kThreads, teams, my_team, both.share, [&](int32_t s) -> int64_t {
     if (s >= a.seqs.n_seqs) return 0;
-    return c8_seq<R>(a, plan, read_seq(a.seqs, s)).count;
+    const C8Seq q = c8_seq<R>(a, plan, read_seq(a.seqs, s));
+    if (!q.v.ok && blockIdx.x == 0) report_error(a.status, kErrRowRange, s);
+    return q.count;
   });
-  if (blockIdx.x == 0) {
-    int64_t before = 0;
-    for (int32_t s0 = 0; s0 < a.seqs.n_seqs && warp == 0; s0 += 32) {
-      const int32_t s = s0 + lane;
-      int64_t count = 0;
-      if (s < a.seqs.n_seqs) {
-        const C8Seq q = c8_seq<R>(a, plan, read_seq(a.seqs, s));
-        if (!q.v.ok) report_error(a.status, kErrRowRange, s);
-        count = q.count;
-      }
-      const int64_t incl = warp_scan(count, lane);
-      if (s < a.seqs.n_seqs) base_out[s] = before + incl - count;
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (tid == 0) base_out[a.seqs.n_seqs] = before;
-  }
   __syncthreads();  // the plan's scratch lies where the barriers do
   if (tid == 0) {
     for (int i = 0; i < G::kSlots; ++i) {
@@ -630,10 +623,6 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
       }
       jg += (uint32_t)g.n;
-      if (warp == G::kSoft && !(g.flags & (C8Seg::kWhole | C8Seg::kEmpty))) {  // the rows of a part, for the join
-        const int32_t end = fast_div(plan.group_div, min(g.m0 + R, g.rows * a.group) - 1);
-        for (int32_t j = fast_div(plan.group_div, g.m0) + lane; j <= end; j += 32) row_seq[g.row0 + j] = g.s;
-      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
   } else if (warp >= G::kMmaS) {
@@ -641,8 +630,11 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     if (warp == G::kWalk) {
       // ---- the walk
       C8Walk<R> walk(a, plan, found.seq, found.off, laid_out ? found.share.n : 0);
+      C8Open last = {0, 0, 0, 0, -1};
       for (uint32_t k = 0;; ++k) {
         const C8Seg g = walk.next();
+        if (!(g.flags & (C8Seg::kEnd | C8Seg::kEmpty | C8Seg::kHead | C8Seg::kWhole)))  // (then the share ends here)
+          last = {g.row0, g.rows, g.m0, g.kvh, (int32_t)(my_team + (walk.rest + found.share.per - 1) / found.share.per)};
         if (k >= kC8Segs && !warp_wait(sm32(&C.seg_free[k % kC8Segs]), ((k / kC8Segs) & 1u) ^ 1u, lim, abort_flag)) break;
         __syncwarp();
         if (lane == 0) {
@@ -651,6 +643,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
         }
         if (g.flags & C8Seg::kEnd) break;
       }
+      if (lane == 0) open[blockIdx.x] = last;
     } else if (warp == G::kLook) {
       // ---- the look-ups: lane 8 i + e takes 16 tokens of the i-th of four tiles.  Under load
       // a read takes several thousand cycles, so the pages of the next four tiles are read
@@ -1250,10 +1243,12 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, int64_t *__restrict__ 
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// Joins the parts of the units that several CTAs share.  A warp has a row of a KV head,
-// 4 dims a lane and half, and every kGroups-th part; the groups' results are then added
-// in order.  The plan and the parts are written while this launch is already resident, so
-// they are no __restrict__ arguments: nothing may read them ahead of the wait.
+// Joins the parts of the units that several CTAs share.  A block has the unit that one CTA
+// ended with, if it did; a warp a row of it, 4 dims a lane and half, and every kGroups-th part; the
+// groups' results are then added in order.  (A warp for every row of the call, which looked
+// its unit up, took 23 us of a chunk of 2048 rows' 210.)  Units and parts are written while this
+// launch is already resident, so they are no __restrict__ arguments: nothing may read them ahead
+// of the wait.
 // Four warps of 64 registers are what the SM has left beside a CTA of 8 rows, so that they wait
 // there while it runs (of eight, which start when it ends: decode of 16 rows 106.6 us, 104.6
 // with four; in a window of 4096 24.6 and 23.4; one row of 65535 tokens 25.7 and 24.4).
@@ -1261,127 +1256,119 @@ constexpr int kC8JoinWarps = 4;
 
 template <int HD, int R, int kGroups>
 __global__ void __launch_bounds__(32 * kC8JoinWarps)
-cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t teams, const int64_t *base,
-                   const float2 *part_ml, const float4 *part_o, const int32_t *row_seq) {
+cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t ctas, const C8Open *open, const float2 *part_ml, const float4 *part_o) {
   constexpr int kQuads = HD / 128;
   __shared__ float4 acc_s[kGroups > 1 ? kC8JoinWarps : 1][kQuads][32];
   __shared__ float2 ml_s[kGroups > 1 ? kC8JoinWarps : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp % kGroups;
-  const int64_t mg = (int64_t)blockIdx.x * (kC8JoinWarps / kGroups) + warp / kGroups;
-  const int32_t kvh = blockIdx.y;
-  const int32_t row = mg < (int64_t)a.seqs.n_rows * a.group ? fast_div(plan.group_div, (int32_t)mg) : -1;
-  const int32_t head = kvh * a.group + (int32_t)(mg - (int64_t)row * a.group);
-  // Where the row lies in the plan, while the launch before still runs: it wrote none of
-  // what this reads, and it began after everything before it was complete.
-  int32_t s = 0, r = 0, rank = 0, tiles = 0;
-  int64_t u0 = 0;  // the unit's first tile, from its sequence's first
-  auto place = [&](int32_t at) {  // where the row lies, if sequence `at` has it
-    const C8Seq q = c8_seq<R>(a, plan, read_seq(a.seqs, at));
-    if (row < q.v.row0 || row >= q.v.row0 + q.v.rows) return;
-    const int64_t m = (int64_t)(row - q.v.row0) * a.group + (head - kvh * a.group);
-    const int32_t mt = (int32_t)(m / R);
-    s = at;
-    r = (int32_t)(m % R);
-    rank = kvh & ((1 << plan.head_log) - 1);
-    tiles = q.tiles;
-    u0 = ((int64_t)(kvh >> plan.head_log) * q.m_tiles + mt) * (tiles + c8_start<R>()) + c8_start<R>();
-  };
-  if (row >= 0) place(seq_of_row(a.seqs, row));
   grid_dependency_sync();
-  // Where bad sequences' starts do not ascend, the search above may have missed a good
-  // one: who wrote a part of the row left its sequence.  (A row without parts has what an
-  // earlier call left there, which names its sequence or is no place for it.)
-  if (row >= 0 && tiles == 0) {
-    const int32_t at = row_seq[row];
-    if (at >= 0 && at < a.seqs.n_seqs) place(at);
-  }
-  int32_t c0 = 0, c1 = 0;  // teams of the first and last part
-  if (tiles > 0) {
-    const int64_t per = (base[a.seqs.n_seqs] + teams - 1) / teams;
-    u0 += base[s];
-    c0 = (int32_t)(u0 / per);
-    c1 = (int32_t)((u0 + tiles - 1) / per);
-  }
-  const bool mine = c0 != c1;
-  float top = -INFINITY, all = 0.f;
-  float4 acc[kQuads];
+  // The units are those that CTAs ended with, a block's own CTA's or, where there are fewer
+  // blocks, the nth that there is.  (As many as there can be, but for sequences that overlap.)
+  for (int32_t nth = blockIdx.x;; nth += (int32_t)gridDim.x) {
+    int32_t from = nth < ctas ? nth : -1;
+    if (gridDim.x < (uint32_t)ctas) {
+      int32_t last[kC8MaxCtas / 32], left = nth;
 #pragma unroll
-  for (int i = 0; i < kQuads; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [](float4 &t, const float4 &x, float by) {
-    t.x = fmaf(x.x, by, t.x);
-    t.y = fmaf(x.y, by, t.y);
-    t.z = fmaf(x.z, by, t.z);
-    t.w = fmaf(x.w, by, t.w);
-  };
-  if (mine) {
-    constexpr int kAhead = 4;  // parts on their way
-    for (int32_t c = c0 + grp; c <= c1; c += kAhead * kGroups) {
-      float2 ml[kAhead];
-      float4 x[kAhead][kQuads];
+      for (int i = 0; i < kC8MaxCtas / 32; ++i) last[i] = 32 * i + lane < ctas ? open[32 * i + lane].last : -1;
+      from = -1;
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        const int32_t at = c + e * kGroups;
-        const int64_t part = (((int64_t)min(at, c1) << plan.head_log) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
-        ml[e] = part_ml[part * R + r];
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) x[e][i] = part_o[(part * R + r) * (HD / 4) + 32 * i + lane];
-        if (at > c1) ml[e] = make_float2(-INFINITY, 0.f);
-      }
-      float now = top;
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e) now = fmaxf(now, ml[e].x);
-      const float keep = ex2(top - now);  // (a part's reference is finite)
-      top = now;
-      all *= keep;
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
-#pragma unroll
-      for (int e = 0; e < kAhead; ++e) {
-        if (ml[e].x == -INFINITY) continue;
-        const float by = ex2(ml[e].x - now);
-        all = fmaf(ml[e].y, by, all);
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) add(acc[i], x[e][i], by);
+      for (int i = 0; i < kC8MaxCtas / 32; ++i) {
+        const uint32_t has = __ballot_sync(0xffffffffu, last[i] >= 0);
+        const uint32_t it = __ballot_sync(0xffffffffu, last[i] >= 0 && __popc(has & ((1u << lane) - 1u)) == left);
+        if (it != 0u) from = 32 * i + __ffs(it) - 1;
+        left -= __popc(has);
       }
     }
-  }
-  if constexpr (kGroups > 1) {
-#pragma unroll
-    for (int i = 0; i < kQuads; ++i) acc_s[warp][i][lane] = acc[i];
-    if (lane == 0) ml_s[warp] = make_float2(top, all);
-    __syncthreads();
-    if (grp != 0) return;
-    for (int g = 1; g < kGroups; ++g) top = fmaxf(top, ml_s[warp + g].x);
-    const float use = top == -INFINITY ? 0.f : top;
-    all = 0.f;
+    if (from < 0) return;
+    const int32_t rank = from & ((1 << plan.head_log) - 1), c0 = from >> plan.head_log;
+    const C8Open unit = open[from];
+    const int32_t c1 = unit.last;  // the team of the last part
+    if (c1 < 0) continue;
+    const int32_t r = (int32_t)blockIdx.y * (kC8JoinWarps / kGroups) + warp / kGroups;
+    const bool mine = unit.m0 + r < unit.rows * a.group;
+    const int32_t j = mine ? fast_div(plan.group_div, unit.m0 + r) : 0, row = unit.row0 + j;
+    const int32_t head = unit.kvh * a.group + (unit.m0 + r - j * a.group);
+    float top = -INFINITY, all = 0.f;
+    float4 acc[kQuads];
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int g = 0; g < kGroups; ++g) {
-      if (ml_s[warp + g].x == -INFINITY) continue;
-      const float by = ex2(ml_s[warp + g].x - use);
-      all = fmaf(ml_s[warp + g].y, by, all);
+    auto add = [](float4 &t, const float4 &x, float by) {
+      t.x = fmaf(x.x, by, t.x);
+      t.y = fmaf(x.y, by, t.y);
+      t.z = fmaf(x.z, by, t.z);
+      t.w = fmaf(x.w, by, t.w);
+    };
+    if (mine) {
+      constexpr int kAhead = 4;  // parts on their way
+      for (int32_t c = c0 + grp; c <= c1; c += kAhead * kGroups) {
+        float2 ml[kAhead];
+        float4 x[kAhead][kQuads];
 #pragma unroll
-      for (int i = 0; i < kQuads; ++i) add(acc[i], acc_s[warp + g][i][lane], by);
+        for (int e = 0; e < kAhead; ++e) {
+          const int32_t at = c + e * kGroups;
+          const int64_t part = (((int64_t)min(at, c1) << plan.head_log) + rank) * 2 + (min(at, c1) == c0 ? 1 : 0);
+          ml[e] = part_ml[part * R + r];
+#pragma unroll
+          for (int i = 0; i < kQuads; ++i) x[e][i] = part_o[(part * R + r) * (HD / 4) + 32 * i + lane];
+          if (at > c1) ml[e] = make_float2(-INFINITY, 0.f);
+        }
+        float now = top;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) now = fmaxf(now, ml[e].x);
+        const float keep = ex2(top - now);  // (a part's reference is finite)
+        top = now;
+        all *= keep;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          if (ml[e].x == -INFINITY) continue;
+          const float by = ex2(ml[e].x - now);
+          all = fmaf(ml[e].y, by, all);
+#pragma unroll
+          for (int i = 0; i < kQuads; ++i) add(acc[i], x[e][i], by);
+        }
+      }
     }
-  }
-  if (!mine) return;
-  const float inv = all == 0.f ? 0.f : 1.f / all;
+    if constexpr (kGroups > 1) {
 #pragma unroll
-  for (int i = 0; i < kQuads; ++i)
-    *reinterpret_cast<uint2 *>(a.out + (int64_t)row * a.out_stride + (int64_t)head * HD + 128 * i + 4 * lane) =
-        make_uint2(pack_f32_bf16(acc[i].x * inv, acc[i].y * inv), pack_f32_bf16(acc[i].z * inv, acc[i].w * inv));
-  if (lane == 0 && a.lse)
-    a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+      for (int i = 0; i < kQuads; ++i) acc_s[warp][i][lane] = acc[i];
+      if (lane == 0) ml_s[warp] = make_float2(top, all);
+      __syncthreads();
+      const int first = warp - grp;
+      top = -INFINITY;
+      for (int g = 0; g < kGroups; ++g) top = fmaxf(top, ml_s[first + g].x);
+      const float use = top == -INFINITY ? 0.f : top;
+      all = 0.f;
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int g = 0; g < kGroups && grp == 0; ++g) {
+        if (ml_s[first + g].x == -INFINITY) continue;
+        const float by = ex2(ml_s[first + g].x - use);
+        all = fmaf(ml_s[first + g].y, by, all);
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) add(acc[i], acc_s[first + g][i][lane], by);
+      }
+    }
+    if constexpr (kGroups > 1) __syncthreads();  // read before the next unit's
+    if (!mine || grp != 0) continue;
+    const float inv = all == 0.f ? 0.f : 1.f / all;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+      *reinterpret_cast<uint2 *>(a.out + (int64_t)row * a.out_stride + (int64_t)head * HD + 128 * i + 4 * lane) =
+          make_uint2(pack_f32_bf16(acc[i].x * inv, acc[i].y * inv), pack_f32_bf16(acc[i].z * inv, acc[i].w * inv));
+    if (lane == 0 && a.lse)
+      a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+  }
 }
 
-// The workspace: the sequences' first tiles and their sum, the parts' (ref, sum) and O, the
-// sequence of each row that has parts.
+// The workspace: the units that CTAs end with, the parts' (ref, sum) and O.
 int64_t rows_of_part(int64_t n_rows, int32_t group) {
   int64_t r = 8;
   while (r < kC8MostRows && r < n_rows * group) r *= 2;
   return r;
 }
-int64_t base_bytes(int32_t n_seqs) { return ((int64_t)(n_seqs + 1) * 8 + 255) / 256 * 256; }
+constexpr int64_t kC8OpenBytes = (kC8MaxCtas * (int64_t)sizeof(C8Open) + 255) / 256 * 256;
 int64_t ml_bytes(int64_t rows) { return (int64_t)kC8MaxCtas * 2 * rows * 8; }
 int64_t o_bytes(int64_t rows, int32_t head_dim) { return (int64_t)kC8MaxCtas * 2 * rows * head_dim * 4; }
 
@@ -1391,27 +1378,28 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
   const cudaError_t e = set_smem_once(smem_attr, cache8_attn_kernel<HD, R>, c8_smem<HD, R>());
   if (e != cudaSuccess) return e;
   uint8_t *ws = static_cast<uint8_t *>(a.ws);
-  int64_t *base = reinterpret_cast<int64_t *>(ws);
-  float2 *ml = reinterpret_cast<float2 *>(ws + base_bytes(a.seqs.n_seqs));
-  float *o = reinterpret_cast<float *>(ws + base_bytes(a.seqs.n_seqs) + ml_bytes(R));
-  int32_t *row_seq = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(o) + o_bytes(R, HD));
+  C8Open *open = reinterpret_cast<C8Open *>(ws);
+  float2 *ml = reinterpret_cast<float2 *>(ws + kC8OpenBytes);
+  float *o = reinterpret_cast<float *>(ws + kC8OpenBytes + ml_bytes(R));
   // KV heads side by side read neighbouring pieces of the same rows.
   int head_log = 0;
   while (head_log < 3 && a.nkv % (2 << head_log) == 0) ++head_log;
   const int ctas = ((device_sm_count() < kC8MaxCtas ? device_sm_count() : kC8MaxCtas) >> head_log) << head_log;
   const C8Plan plan = {make_fast_div(a.group), head_log, R / a.group + 2};
   cudaError_t r = launch_dependent(cache8_attn_kernel<HD, R>, dim3((unsigned)ctas), dim3(C8Geom<HD, R>::kThreads), c8_smem<HD, R>(), stream, 1u, a,
-                                   plan, base, ml, o, row_seq);
+                                   plan, open, ml, o);
   // a table of one tile leaves no unit to share
   if (r != cudaSuccess || (int64_t)a.seqs.table_len * a.seqs.page.d <= kC8T) return r;
   // One group of parts per warp where units outnumber the CTAs (few parts each), a CTA's
-  // where a unit spreads over many.
+  // where a unit spreads over many.  A block for every CTA, or for as many units as there can
+  // be, where the rows of more would be thousands of blocks (64 rows over 65k tokens 118 us, 112;
+  // but one row over 515 9.7 us, 10.5 where it has to find its unit).
   const int64_t rows = (int64_t)a.seqs.n_rows * a.group, units = (int64_t)a.nkv * ((rows + R - 1) / R);
+  const int64_t open_most = (int64_t)a.nkv * (a.seqs.n_seqs + rows / R);
   const bool many = ctas >= 8 * units;
   return launch_dependent(many ? cache8_join_kernel<HD, R, kC8JoinWarps> : cache8_join_kernel<HD, R, 1>,
-                          dim3((unsigned)(many ? rows : (rows + kC8JoinWarps - 1) / kC8JoinWarps), (unsigned)a.nkv),
-                          dim3(32 * kC8JoinWarps), 0, stream, 1u, a, plan, (int32_t)(ctas >> head_log), base, ml,
-                          reinterpret_cast<const float4 *>(o), row_seq);
+                          dim3((unsigned)(R > 8 && open_most < ctas ? open_most : ctas), many ? R : R / kC8JoinWarps), dim3(32 * kC8JoinWarps), 0,
+                          stream, 1u, a, plan, ctas, open, ml, reinterpret_cast<const float4 *>(o));
 }
 
 // The rows of a unit.  Enough for a sequence's rows by the call's mean, as a tile of 64 costs
@@ -1451,9 +1439,9 @@ cudaError_t launch_hd(const Cache8Args &args, cudaStream_t stream) {
 
 }  // namespace
 
-int64_t cache8_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t group, int32_t head_dim) {
+int64_t cache8_workspace_bytes(int32_t n_rows, int32_t group, int32_t head_dim) {
   const int64_t rows = rows_of_part(n_rows, group);
-  return base_bytes(n_seqs) + ml_bytes(rows) + o_bytes(rows, head_dim) + (int64_t)n_rows * 4;
+  return kC8OpenBytes + ml_bytes(rows) + o_bytes(rows, head_dim);
 }
 
 cudaError_t launch_cache8_attn(const Cache8Args &a, int32_t head_dim, cudaStream_t stream) {

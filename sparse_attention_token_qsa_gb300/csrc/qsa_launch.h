@@ -262,7 +262,7 @@ struct Cache8Args {
   void *ws;
   long long wait_limit;
 };
-int64_t cache8_workspace_bytes(int32_t n_seqs, int32_t n_rows, int32_t group, int32_t head_dim);
+int64_t cache8_workspace_bytes(int32_t n_rows, int32_t group, int32_t head_dim);
 cudaError_t launch_cache8_attn(const Cache8Args &a, int32_t head_dim, cudaStream_t stream);
 
 }  // namespace qsa
