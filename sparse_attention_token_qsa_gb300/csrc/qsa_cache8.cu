@@ -37,7 +37,7 @@
 // instructions and MMAs issued from a uniform loop took the misses to 5 % (106 and 127 us).
 // For the same reason a part's beginning and end are short: they run once or twice a launch.
 // (Where they run often, they bound it: 512 rows over 64 to 400 tokens of 8 KV heads, 27 parts
-// of one or two tiles a CTA, take 125 us, 4.4 us a part, of which the tiles are 40 %.)
+// of one or two tiles a CTA, take 117 us, 4.3 us a part, of which the tiles are 40 %.)
 //
 // Decode is bound by HBM: 16 sequences of 16k to 64k tokens, 16 heads over 2 x 256, take
 // 102 us, 93 % of the copy bandwidth; 32 heads over 8 x 128 194 us, 98 %.  With more rows the
@@ -72,7 +72,7 @@ struct C8Geom {
   // Up to 32 rows two softmax groups of four warps take tiles in turn, each with a sum,
   // references and an O of its own, joined at the part's end; of 64, four groups take a
   // quarter of every tile's rows each.  (Two groups with a half of them: a chunk of 2048 rows
-  // in a window of 1024 229 us, four 207; trees of 5 to 37 rows 176 and 169; 64 rows of 65k
+  // in a window of 1024 229 us, four 207 then; trees of 5 to 37 rows 176 and 169; 64 rows of 65k
   // tokens 116 each way.  Two that take tiles of 64 columns in turn, which heads of 128 leave
   // room for: 267 us the chunk, 212 the trees.)
   static constexpr bool kTurns = R < 64;
