@@ -38,3 +38,14 @@ def test_windows_over_many_rows(qsa, nq, nkv, hd, rows, mask):  # noqa: F811
         out, lse, st = base.call(qsa, c)
         assert st == (0, 0)
         base.check(c, out, lse)
+
+
+def test_sequences_over_the_same_rows(qsa):  # noqa: F811
+    """Starts 0, 300, 0, 300, ...: every other sequence is bad, the good ones have the same rows and the same cache, and
+    more units are split between CTAs than as many rows of sequences apart would make."""
+    c = Cache8(base.qi.rng_for(131), [1000] * 5, [300, 0, 0, 0, 0], 8, 1, 128, 16, 16, "chain")
+    c.table[:] = c.table[0]
+    c.row_start = np.array([0, 300, 0, 300, 0, 300], np.int32)
+    out, lse, st = base.call(qsa, c)
+    assert st[0] == 3 and st[1] in (1, 3)
+    base.check(c, out, lse, seqs=[0])
