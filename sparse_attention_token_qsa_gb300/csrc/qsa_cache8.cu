@@ -397,9 +397,11 @@ __device__ __forceinline__ float lg2(float x) {
   return r;
 }
 
-// ref + log2 of a sum (a normal number), in units of e: x = 2^e m with m in [3/4, 3/2), whose
-// logarithm is within 2^-22.
+// ref + log2 of a sum, in units of e: x = 2^e m (a normal number) with m in [3/4, 3/2), whose
+// logarithm is within 2^-22.  A sum that is not finite is the result: taken apart, its bits
+// would give a number.
 __device__ __forceinline__ float lse_of(float ref, float x) {
+  if (!(x < INFINITY)) return x;
   const int32_t e = ((int32_t)__float_as_uint(x) - 0x3F400000) >> 23;
   const float m = __uint_as_float(__float_as_uint(x) - ((uint32_t)e << 23));
   return (ref + (float)e + lg2(m)) * 0.6931471805599453f;
