@@ -1360,7 +1360,7 @@ cache8_join_kernel(const Cache8Args a, const C8Plan plan, int32_t ctas, const C8
       *reinterpret_cast<uint2 *>(a.out + (int64_t)row * a.out_stride + (int64_t)head * HD + 128 * i + 4 * lane) =
           make_uint2(pack_f32_bf16(acc[i].x * inv, acc[i].y * inv), pack_f32_bf16(acc[i].z * inv, acc[i].w * inv));
     if (lane == 0 && a.lse)
-      a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : (top + log2f(all)) * 0.6931471805599453f;
+      a.lse[(int64_t)row * a.nq + head] = all == 0.f ? -INFINITY : lse_of(top, all);
   }
 }
 
