@@ -972,8 +972,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
         if (t >= kv) return 0u;
         const int32_t k = t - g.ctx;
         if (chain) {  // row j: k <= j, and j - k < window or t < n_first
-          const bool near = a.window > 0 && t >= a.n_first;
-          return columns(max(k, 0), near ? max(0, min(g.rows, k + a.window)) : g.rows);
+          // (k + window may pass 31 bits, where the table's end is near them; rows - k does not)
+          const bool near = a.window > 0 && t >= a.n_first && g.rows - k > a.window;
+          return columns(max(k, 0), near ? max(0, k + a.window) : g.rows);
         }
         uint32_t s = 0u;
         if (k >= 0) {
