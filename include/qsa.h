@@ -637,10 +637,11 @@ qsa_status qsa_cache_compact(uint16_t *k_pool, uint16_t *v_pool, int32_t width, 
  *  QSA_ERR_ROW_RANGE with its index, has no rows and keeps its pages.  More rows than
  *  max_rows (QSA_ERR_ROW_RANGE), more pages than are free (QSA_ERR_NO_PAGES), both with
  *  the first sequence that has no room, or a stack that would not fit pool_pages entries
- *  (QSA_ERR_TOKEN_RANGE, sequence 0): the call then plans nothing, row_start is zero, and
- *  tables, pages and heights stay as they were.  A page outside the pool among those
- *  given back, taken or used by a row is QSA_ERR_TOKEN_RANGE with the sequence's index; a
- *  slot in it is -1.
+ *  (QSA_ERR_TOKEN_RANGE, sequence 0), or a page outside the pool among those given back
+ *  (QSA_ERR_TOKEN_RANGE with the sequence's index: the stack would hand it on): the call then
+ *  plans nothing, row_start is zero, and tables, pages and heights stay as they were.  A
+ *  page outside the pool among those taken or used by a row is QSA_ERR_TOKEN_RANGE with the
+ *  sequence's index; a slot in it is -1, and it stays in that sequence's table.
  *  n_seqs 0 does nothing: no output is written.
  *  Refused: n_seqs > 65535, pool_pages * page_size or table_len * page_size past 31
  *  bits, table_cols = 0 with several sequences.

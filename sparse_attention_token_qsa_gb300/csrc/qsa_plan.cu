@@ -61,6 +61,18 @@ __device__ __forceinline__ void plan_barrier() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Sets a flag in the shared memory of every CTA of the cluster; plan_barrier shows it to them.
+__device__ __forceinline__ void flag_all(int32_t &flag) {
+  if (gridDim.x == 1) {
+    flag = 1;
+    return;
+  }
+  const uint32_t here = (uint32_t)__cvta_generic_to_shared(&flag);
+  for (uint32_t r = 0; r < gridDim.x; ++r)
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.u32 [a], %2;\n\t}" ::"r"(here), "r"(r), "r"(1)
+                 : "memory");
+}
+
 struct PlanSums {
   int64_t rows, back, take;
 };
@@ -114,8 +126,12 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a,
   // Up to as many sequences as threads: their first rows and contexts, which the rows
   // would else fetch in three trips to L2, one after another.
   __shared__ int32_t starts[kPlThreads + 1], contexts[kPlThreads];
+  __shared__ int32_t spoiled;  // a page that is given back is none of the pool's
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = blockIdx.x, ranks = gridDim.x;  // the grid is one cluster
+  if (tid == 0) spoiled = 0;
+  // (met before another CTA's flag may be set)
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   grid_dependency_sync();
 
   // this thread's sequence of a chunk, and the sums before it; adds the chunk to `before`
@@ -153,7 +169,7 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a,
   const bool one_chunk = a.n_seqs <= kPlThreads;  // p and at stay good
   const int64_t height = free0 + all.back;
   const bool stack_ok = free0 >= 0 && height <= a.pool_pages, rows_ok = all.rows <= a.max_rows;
-  const bool ok = stack_ok && rows_ok && all.take <= height;
+  bool ok = stack_ok && rows_ok && all.take <= height;
   if (one_chunk && ok) {  // (met by the barriers before the rows)
     if (tid < a.n_seqs) {
       starts[tid] = (int32_t)at.rows;
@@ -164,8 +180,10 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a,
 
   // The items of this warp's sequences, shared with the same warp of the other CTAs, which has
   // the same sequences: from(s, i, k) reads the i-th of sequence s's, the k-th of all, and
-  // to(s, i, k, page) puts it in its place.  Four at once: each is a trip to L2.
-  auto each = [&](int32_t s, int32_t count, int64_t first, auto &&from, auto &&to) {
+  // to(s, i, k, page) puts it in its place.  Four at once: each is a trip to L2.  True where a
+  // page of this thread's is none of the pool's.
+  auto each = [&](int32_t s, int32_t count, int64_t first, auto &&from, auto &&to) -> bool {
+    bool bad = false;
     const int64_t incl = warp_scan(count, lane), total = __shfl_sync(0xffffffffu, incl, 31);
     const int64_t base = __shfl_sync(0xffffffffu, first, 0);
     constexpr int kAtOnce = 4;
@@ -183,24 +201,34 @@ __global__ void __launch_bounds__(kPlThreads) page_plan_kernel(const PlanArgs a,
       for (int e = 0; e < kAtOnce; ++e) {
         const int64_t i = i0 + 32 * (int64_t)ranks * e + lane;
         if (i >= total) continue;
-        if (page[e] < 0 || page[e] >= a.pool_pages) report_error(a.status, kErrTokenRange, seq[e]);
+        if (page[e] < 0 || page[e] >= a.pool_pages) {
+          report_error(a.status, kErrTokenRange, seq[e]);
+          bad = true;
+        }
         to(seq[e], at[e], base + i, page[e]);
       }
     }
+    return bad;
   };
 
+  if (ranks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (ok && all.back > 0) {
     PlanSums sums = {0, 0, 0};
+    bool bad = false;
     for (int32_t s0 = 0; s0 < a.n_seqs; s0 += kPlThreads) {
       if (!one_chunk) at = chunk(s0 + tid, p, sums);
-      each(s0 + tid, p.back, at.back,
-           [&](int32_t s, int32_t i, int64_t) -> int32_t {
-             const int32_t kv = a.ctx_len[s] + a.new_rows[s];
-             return a.table[(int64_t)s * a.table_cols + (kv > 0 ? fast_div(a.page, kv - 1) + 1 : 0) + i];
-           },
-           [&](int32_t, int32_t, int64_t k, int32_t page) { a.free_pages[free0 + k] = page; });
+      bad |= each(s0 + tid, p.back, at.back,
+                  [&](int32_t s, int32_t i, int64_t) -> int32_t {
+                    const int32_t kv = a.ctx_len[s] + a.new_rows[s];
+                    return a.table[(int64_t)s * a.table_cols + (kv > 0 ? fast_div(a.page, kv - 1) + 1 : 0) + i];
+                  },
+                  [&](int32_t, int32_t, int64_t k, int32_t page) { a.free_pages[free0 + k] = page; });
     }
+    if (bad) flag_all(spoiled);
     plan_barrier();
+    // The stack would hand the page to another sequence: nothing is planned (what was put
+    // past the stack's height is not on it).
+    ok = *static_cast<volatile int32_t *>(&spoiled) == 0;
   }
   {
     PlanSums sums = {0, 0, 0};
