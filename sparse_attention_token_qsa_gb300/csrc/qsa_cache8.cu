@@ -803,7 +803,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
     // ---- softmax: thread tk has the tile's token tk (TMEM lane) and, at the end, dims tk
     // and tk + 128.  Group w takes every other tile, or its rows of each.  After an abort
     // every wait returns at once, and the loops and barriers run on to the end.
-    constexpr int kCols = G::kCols, kAtOnce = kCols;  // rows of a TMEM load
+    constexpr int kCols = G::kCols;
     const int w = warp >> 2, wq = warp & 3, tk = wq * 32 + lane;
     const int n0 = G::kTurns ? 0 : w * kCols;  // this group's first row
     float *const less_ref = C.less_ref + w * kCols, *const alpha = C.alpha + w * kCols;
@@ -814,17 +814,16 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
     // barrier no phase but the last two is ever in question.
     auto wait_pv = [&](uint32_t i) { warp_wait(sm32(&C.pv_done[i % G::kPv]), (i / G::kPv) & 1u, lim, abort_flag); };
     // This warp's rows of a part's Q, split into two e4m3 terms, with what goes with a row.
-    // (In batches, the first of them fetched ahead: a part's code runs once or twice a
-    // launch, and its instructions cost as much to fetch as the rows.)
     constexpr int kLanes = HD / 8, kPer = 32 / kLanes;  // lanes a row, rows a warp takes at once
-    constexpr int kTimes = (R + G::kSoft * kPer - 1) / (G::kSoft * kPer), kBatch = kTimes < 4 ? kTimes : 4;
+    constexpr int kTimes = (R + G::kSoft * kPer - 1) / (G::kSoft * kPer);
+    static_assert(kTimes <= 4, "rows of Q held in registers between their fetch and their split");
     const int ch = lane % kLanes, sub = lane / kLanes;
     auto row_of = [&](int i) { return (i * G::kSoft + warp) * kPer + sub; };
-    uint4 raw[kBatch];
-    auto fetch_q = [&](const C8Seg &e, int i0) {
+    uint4 raw[kTimes];
+    auto fetch_q = [&](const C8Seg &e) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int n = row_of(i0 + i);
+      for (int i = 0; i < kTimes; ++i) {
+        const int n = row_of(i);
         const bool valid = n < R && e.m0 + n < e.rows * a.group;
         const int32_t m = valid ? e.m0 + n : 0, j = fast_div(plan.group_div, m);
         const int32_t head = e.kvh * a.group + (m - j * a.group);
@@ -833,43 +832,37 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
     };
     auto store_q = [&](const C8Seg &e) {
       const int32_t m_all = e.rows * a.group;
-#pragma unroll 1
-      for (int i0 = 0;;) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int n = row_of(i0 + i);
-          const bool mine = n < R, valid = mine && e.m0 + n < m_all;
-          // the largest magnitude; of a row with one that is not finite, that one, and NaN below
-          uint32_t top = __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu),
-                                  __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
-          top = max(top & 0xFFFFu, top >> 16);
+      for (int i = 0; i < kTimes; ++i) {
+        const int n = row_of(i);
+        const bool mine = n < R, valid = mine && e.m0 + n < m_all;
+        // the largest magnitude; of a row with one that is not finite, that one, and NaN below
+        uint32_t top = __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu),
+                                __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
+        top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-          for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // the least power of two s with it <= 448 s = 1.75 * 2^8 s, and 1 / s
-          const int ex = max(-126, (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0));
-          const float s = __uint_as_float((uint32_t)(127 + ex) << 23), inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-          float x[8];
-          unpack8(raw[i], x);
-          uint32_t hi[4], lo[4];
+        for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // the least power of two s with it <= 448 s = 1.75 * 2^8 s, and 1 / s
+        const int ex = max(-126, (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0));
+        const float s = __uint_as_float((uint32_t)(127 + ex) << 23), inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+        float x[8];
+        unpack8(raw[i], x);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // (x + 0 x: an infinity becomes NaN, which the conversions keep)
-            split_e4m3(fmaf(x[2 * k], 0.f, x[2 * k]) * inv, fmaf(x[2 * k + 1], 0.f, x[2 * k + 1]) * inv, hi[k], lo[k]);
-          if (mine) {
-            auto at = [&](int row) {  // 8 bytes of a 128-byte row of a box, its 16-byte chunks swizzled
-              return c8_shared + (ch >> 4) * G::kQBox + row * 128 + (((ch >> 1) & 7) ^ (row & 7)) * 16 + (ch & 1) * 8;
-            };
-            *reinterpret_cast<uint2 *>(at(n)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2 *>(at(R + n)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            if (ch == 0) {
-              C.factor[n] = a.scale_log2 * s;
+        for (int k = 0; k < 4; ++k)  // (x + 0 x: an infinity becomes NaN, which the conversions keep)
+          split_e4m3(fmaf(x[2 * k], 0.f, x[2 * k]) * inv, fmaf(x[2 * k + 1], 0.f, x[2 * k + 1]) * inv, hi[k], lo[k]);
+        if (mine) {
+          auto at = [&](int row) {  // 8 bytes of a 128-byte row of a box, its 16-byte chunks swizzled
+            return c8_shared + (ch >> 4) * G::kQBox + row * 128 + (((ch >> 1) & 7) ^ (row & 7)) * 16 + (ch & 1) * 8;
+          };
+          *reinterpret_cast<uint2 *>(at(n)) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          *reinterpret_cast<uint2 *>(at(R + n)) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          if (ch == 0) {
+            C.factor[n] = a.scale_log2 * s;
 #pragma unroll
-              for (int o = 0; o < G::kOs; ++o) C.less_ref[o * kCols + n] = valid ? -kC8Unset : -kC8Nobody;
-            }
+            for (int o = 0; o < G::kOs; ++o) C.less_ref[o * kCols + n] = valid ? -kC8Unset : -kC8Nobody;
           }
         }
-        i0 += kBatch;
-        if (i0 >= kTimes) break;
-        fetch_q(e, i0);
       }
       if (a.window > 0 && a.seqs.mask != nullptr) {  // the rows' drafted tokens, a lane a row
         for (int n = tid; n < R; n += 32 * G::kSoft) {
@@ -944,7 +937,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
     };
     // Parts overlap: the next one's Q is fetched before this one's output is written.
     bool more = advance(next);
-    if (more && next.n > 0) fetch_q(next, 0);
+    if (more && next.n > 0) fetch_q(next);
     while (true) {
       if (more && next.n > 0) store_q(next);
       write_out();
@@ -1024,20 +1017,17 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
           // Logits in log2 units, rounded as they are: a reference taken from them is then met
           // exactly, however large they are.
           const uint64_t ks2 = pair_f32(ks, ks), sixteenth = pair_f32(0.0625f, 0.0625f);
+          uint32_t hi[kCols], lo[kCols];
+          tmem_cols<kCols>(sc, hi);
+          tmem_cols<kCols>(sc + R, lo);
+          tmem_ready<kCols>(hi);
+          tmem_ready<kCols>(lo);
 #pragma unroll
-          for (int c = 0; c < kCols; c += kAtOnce) {
-            uint32_t hi[kAtOnce], lo[kAtOnce];
-            tmem_cols<kAtOnce>(sc + c, hi);
-            tmem_cols<kAtOnce>(sc + R + c, lo);
-            tmem_ready<kAtOnce>(hi);
-            tmem_ready<kAtOnce>(lo);
-#pragma unroll
-            for (int i = 0; i < kAtOnce; i += 2) {
-              const uint64_t s2 = fma2(pair_f32(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])), sixteenth,
-                                       pair_f32(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])));
-              const uint64_t f2 = pair_f32(C.factor[n0 + c + i], C.factor[n0 + c + i + 1]);
-              unpair_f32(mul2(mul2(s2, ks2), f2), x[c + i], x[c + i + 1]);
-            }
+          for (int i = 0; i < kCols; i += 2) {
+            const uint64_t s2 = fma2(pair_f32(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])), sixteenth,
+                                     pair_f32(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])));
+            const uint64_t f2 = pair_f32(C.factor[n0 + i], C.factor[n0 + i + 1]);
+            unpair_f32(mul2(mul2(s2, ks2), f2), x[i], x[i + 1]);
           }
           if (move) {
             const float lv = lg2(vx);
@@ -1159,7 +1149,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
       }
       ns += (uint32_t)(2 * g.n);
       more = advance(next);
-      if (more && next.n > 0) fetch_q(next, 0);
+      if (more && next.n > 0) fetch_q(next);
       bool fix = false;
       if (g.n > 0) {  // S and P V of every tile are done: Q may go, O may be read
         if (G::kTurns && g.n > 1) wait_pv(jg - 2);
