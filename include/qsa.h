@@ -725,10 +725,12 @@ qsa_status qsa_qkv_write(const uint16_t *q, int64_t q_stride, int32_t nq, const 
  *  not reach its output, NaN though it be.  A query head with a value that is not finite
  *  gets NaN.
  *  Products, softmax and sums run in f32.  A row's weights times their block's V scale
- *  enter the weighted sum as two e4m3 terms, relative to the row's largest: off by at
- *  most 2^-8 of themselves, or 2^-18 of the largest; those of 2^-96 of it and less may
- *  count as nothing.  q is split likewise, exact but for what is below 2^-17 of its
- *  head's largest value.  The normaliser and lse use the f32 weights.
+ *  enter the weighted sum as three e5m2 terms, relative to the row's largest: off by at
+ *  most 2^-8 of themselves, or 2^-27 of the largest (2^-33 where that is far above the
+ *  other tokens near it).  q enters as two e4m3 terms, off by at most 2^-21 of its head's
+ *  largest value.  The normaliser and lse use the f32 weights.  V scales below 2^-80 count
+ *  with fewer bits, below 2^-100 perhaps as zeros; beside one above 2^38, tokens of 2^-96 of the
+ *  largest and less perhaps as nothing.
  *  workspace  DEVICE scratch of qsa_cache8_workspace_bytes(...) bytes, 16-byte aligned;
  *           its contents on entry do not matter.  Calls that share one must be
  *           stream-ordered.

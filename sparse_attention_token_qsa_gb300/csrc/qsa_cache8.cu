@@ -3,21 +3,27 @@
 //
 //   s_t = scale ks_t q . k8_t,  lse = ln sum_t exp(s_t),  out = sum_t exp(s_t - lse) vs_t v8_t
 //
-// over the tokens t that the row sees.  The products run on tcgen05 in e4m3, the type the
+// over the tokens t that the row sees.  The products run on tcgen05 in 8 bits, the type the
 // cache is held in, straight from the tiles that the copies leave in shared memory:
 // nothing is widened.  Tokens are the M dimension: a tile of 128 gives S^T = K Q^T (lanes
 // tokens, columns rows) and O^T += V^T P (lanes dims, columns rows, V and P read MN-major).
 // So a tile of 8 rows costs an MMA of N = 16, not one padded to 128 rows, a thread has one
 // token and with it one K and one V scale, and a row's reference moves with its columns.
 //
-// What e4m3's four bits lose is kept in a second term, its own columns beside the first:
-// q 2^-e = hi + lo / 16 (a bf16 q has eight bits, so this is exact but for what lies
-// 2^-20 below the head's largest value), and the weight w = exp(s - ref) vs = hi + lo / 16,
-// off by 2^-9 of itself, or by 2^-14 where w is small: 2^-18 of the row's largest, which is
-// 16 or more.  ref is log2 of a maximum of exp(s) vs seen earlier, less 4; it moves (the
-// row's sum and its columns of O rescaled) when a w passes 448, e4m3's largest.  The sum is
-// of the f32 weights without vs.  Against 64 bits the outputs are off by 0.0018 of their
-// norm, by 0.0017 if q and the weights had 32 bits.
+// What few bits lose is kept in further terms, their own columns beside the first.  q 2^-e = hi +
+// lo / 16, both e4m3: a bf16 q has eight bits, so this is off by 2^-21 of the head's largest
+// value and exact where q is 2^-13 of it or more.  The weight w = exp(s - ref) vs = hi + (mid +
+// lo) / 4, all e5m2 (P's type; V's stays e4m3): off by 2^-9 of itself and 2^-11 for its passage
+// through f16, or by 2^-19.  ref is log2 of a maximum of exp(s) vs seen earlier, less 8, so that
+// is 2^-27 of the row's largest.  Many small weights may still outweigh one that is larger, as
+// beside a first token whose V is small (with two e4m3 terms, 2^-18, the outputs of 65536 tokens
+// beside one of weight 0.9 were off by 14 to 27 % of their norm): a maximum that is far above the
+// others of its tile is put up to 6 binades higher.  ref moves (the row's sum and its columns of
+// O rescaled) when a w passes 57344, e5m2's largest: a move costs most of a tile's time, and the
+// 7.8 binades before it are why 8 and not more (8, 10, 11, 12, 14: 64 rows of 65k tokens 107,
+// 109, 116, 126, 138 us, a chunk of 2048 in a window 168, 185, 202, 213, 236).  The sum is of the
+// f32 weights without vs.  Against 64 bits the outputs are off by 0.0017 of their norm, as with q
+// and weights of 32 bits: bf16's rounding.
 //
 // A unit of work is (sequence, KV head, R such rows); its tiles are a run of the launch's
 // linear list of tiles, of which every CTA (one per SM) takes an equal, contiguous share.
@@ -60,8 +66,10 @@ constexpr int kC8MostRows = 64;  // rows of a unit at most
 constexpr int kC8MaxCtas = 160;
 constexpr float kC8Unset = -1e30f;    // a row's reference before it has seen a token
 constexpr float kC8Nobody = 1e30f;    // ... of a column without a row: its weights are 0
-constexpr float kC8Head = 4.f;        // log2 of a largest w when the reference is set
-constexpr float kC8Least = 0x1p-92f;  // a V scale below counts as this for the reference
+constexpr float kC8Head = 8.f;        // log2 of a largest w when the reference is set
+constexpr float kC8Gap = 6.f;         // ... and more by what it is above the others beyond this, up to twice
+constexpr float kC8Most = 57344.f;    // a w above moves the reference: e5m2's largest
+constexpr float kC8Least = 0x1p-80f;  // a V scale below counts as this for the reference
 constexpr uint32_t kC8SuspendNs = 2000;  // a wait's sleep at most (it ends early when its phase completes)
 constexpr long long kC8SpinLimit = 4000000000LL;
 
@@ -82,7 +90,7 @@ struct C8Geom {
   static constexpr int kThreads = 32 * (kWalk + 1), kReaders = kWalk;  // (all but the walk take its parts)
   static constexpr int kOs = kTurns ? 2 : 1, kMix = kTurns ? 3 * R : 1;
   static constexpr uint32_t kQBox = kN * 128, kBox = kC8T * 128, kSlot = kC8T * HD;
-  static constexpr int kSlots = HD == 256 ? 5 : 10;
+  static constexpr int kSlots = HD == 128 ? (R < 64 ? 10 : 9) : R < 64 ? 5 : 4;
   static constexpr int kS = R < 64 ? 4 : HD == 256 ? 2 : 3;  // S buffers
   // Registers of the softmax's threads and of the others, of kRegs a thread at the launch:
   // 32 rows a thread do not fit 128, nor 16 of them 80, and every spilled value would queue
@@ -94,12 +102,19 @@ struct C8Geom {
   // as many are held.
   static constexpr uint32_t kPv = HD == 128 ? 8 : 4, kAhead = 2 * kPv;
   static constexpr uint32_t kQBytes = (kHalves * kQBox + 1023) / 1024 * 1024;
-  static constexpr uint32_t kPOff = kQBytes, kRingOff = kPOff + 2 * kBox, kCtrlOff = kRingOff + kSlots * kSlot;
+  // P's two buffers are boxes of a token a row, with its hi and mid terms and, up to 32 rows, lo
+  // (of 8 rows: behind eight zeros, as an MMA has 16 columns at least); of 64 rows the lo terms
+  // of both buffers fill a third box.
+  static constexpr uint32_t kPOff = kQBytes, kLoBox = kPOff + 2 * kBox, kRingOff = kLoBox + (R < 64 ? 0 : kBox);
+  static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kSlot;
   static constexpr uint32_t kOCols = kHalves * kN, kSCol = kOs * kOCols;  // TMEM: O's halves, then S
   static_assert(kSCol + kS * kN <= 512, "TMEM has 512 columns");
-  // kind::f8f6f4, D f32, A and B e4m3, M = 128, N = kN; O: A and B MN-major
+  // kind::f8f6f4, D f32, A and B e4m3, M = 128, N = kN; O: A and B MN-major, B e5m2, and again
+  // with the lo terms, which are added to mid's columns
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kN >> 3) << 17) | ((128u >> 4) << 24);
-  static constexpr uint32_t kIdescO = kIdescS | (1u << 15) | (1u << 16);
+  static constexpr uint32_t kIdescO = kIdescS | (1u << 10) | (1u << 15) | (1u << 16);
+  static constexpr int kLoN = R < 16 ? 16 : R;
+  static constexpr uint32_t kIdescLo = kIdescO - ((uint32_t)((kN - kLoN) >> 3) << 17), kLoCol = R < 16 ? 0 : R;
 };
 
 // What beginning a unit costs, in tiles: its Q, its first references and its output.  At 3, 6, 9
@@ -320,7 +335,8 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-__device__ __forceinline__ void mma_e4m3(uint32_t dtmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// D += A B of 8-bit types.
+__device__ __forceinline__ void mma_8(uint32_t dtmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -432,8 +448,7 @@ __device__ __forceinline__ float over_lanes(float (&x)[K], int lane, Join &&join
   return x[0];
 }
 
-// Two values as e4m3 terms hi + lo / 16.  Through f16: its eleven bits hold hi's four and
-// the four that lo rounds to (2^-12 of the value is lost beside lo's 2^-9).
+// Two values as e4m3 terms hi + lo / 16: exact for eight bits, as bf16 has, of 2^-6 and more.
 __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint32_t &lo) {
   uint32_t w, h;
   uint16_t c, d;
@@ -446,6 +461,19 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t &hi, uint3
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(w));
   hi = c;
   lo = d;
+}
+
+// Two values of 0 to 57344 as e5m2 terms hi + (mid + lo) / 4, the upper bytes of f16 halves: an
+// e5m2 is an f16's upper byte, so hi and mid are cut off by a mask (a NaN's stays one) and lo is
+// rounded by adding half a step.  hi leaves eight of an f16's eleven bits, at most 8160, mid five,
+// of which lo has three: off by 2^-9 of a value, by 2^-11 for its f16, or by 2^-19.
+__device__ __forceinline__ void split_e5m2(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+  asm("{\n\t.reg .b32 t, s;\n\tsub.f16x2 t, %1, %2;\n\tmov.b32 s, 0x44004400;\n\tmul.f16x2 %0, t, s;\n\t}"  // 4
+      : "=r"(mid)
+      : "r"(hi), "r"(hi & 0xFF00FF00u));
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(mid), "r"(mid & 0xFF00FF00u));
+  lo += 0x00800080u;
 }
 
 __device__ __forceinline__ bool any_of_group(int g, bool x) {  // over a softmax group's four warps
@@ -750,7 +778,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
 #pragma unroll
               for (int kk = 0; kk < HD / 32; ++kk) {
                 const uint32_t in = (uint32_t)(kk & 3) * 2u;  // 32 bytes
-                mma_e4m3(d, desc_of(k_lo + (uint32_t)(kk >> 2) * (G::kBox >> 4) + in, desc_hi),
+                mma_8(d, desc_of(k_lo + (uint32_t)(kk >> 2) * (G::kBox >> 4) + in, desc_hi),
                          desc_of(q_lo + (uint32_t)(kk >> 2) * (G::kQBox >> 4) + in, desc_hi), G::kIdescS, kk > 0 ? 1u : 0u);
               }
               mma_commit(sm32(&C.empty[slot]));
@@ -767,6 +795,8 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
         }
       } else {
         const uint32_t r_lo = (uint32_t)sw128_mn_desc(sRing, 0), p_lo = (uint32_t)sw128_mn_desc(sP, 0);
+        // the lo terms' place beside p, and from one buffer to the next
+        constexpr uint32_t kLoAt = R < 64 ? 2 * R : 2 * G::kBox, kLoStep = R < 64 ? G::kBox : 64u;
         while (ok && take_one()) {
           if (g.n == 0) continue;
           if (part > 0 && !wait(C.o_free, (part - 1) & 1u)) break;  // the part before has left O
@@ -776,14 +806,18 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
             step(j + 1 < g.n ? 2u : 1u);
             if (!landed()) break;
             const uint32_t o = tmem + (G::kTurns ? (jg & 1u) * G::kOCols : 0u);
-            const uint32_t p = p_lo + (jg & 1u) * (G::kBox >> 4), v_lo = r_lo + slot * (G::kSlot >> 4);
+            const uint32_t p = p_lo + (jg & 1u) * (G::kBox >> 4), p3 = p_lo + (kLoAt >> 4) + (jg & 1u) * (kLoStep >> 4);
+            const uint32_t v_lo = r_lo + slot * (G::kSlot >> 4);
             if (lead) {
 #pragma unroll
               for (int h = 0; h < G::kHalves; ++h)
 #pragma unroll
-                for (int kk = 0; kk < kC8T / 32; ++kk)  // 32 tokens a step: 4 KiB of V's and of P's rows
-                  mma_e4m3(o + (uint32_t)h * G::kN, desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi),
-                           desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < kC8T / 32; ++kk) {  // 32 tokens a step: 4 KiB of V's and of P's rows
+                  const uint64_t v = desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi);
+                  const uint32_t d = o + (uint32_t)h * G::kN;
+                  mma_8(d, v, desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
+                  mma_8(d + G::kLoCol, v, desc_of(p3 + 256u * kk, desc_hi), G::kIdescLo, 1u);
+                }
               mma_commit(sm32(&C.empty[slot]));
               mma_commit(sm32(&C.pv_done[jg % G::kPv]));
             }
@@ -911,7 +945,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
               tmem_ready<kOut>(lo);
 #pragma unroll
               for (int i = 0; i < kOut; ++i) {
-                const float y = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                const float y = fmaf(__uint_as_float(lo[i]), 0.25f, __uint_as_float(hi[i]));
                 x[i] = G::kTurns ? fmaf(y, C.mix[o * kCols + c + i], x[i]) : y;
               }
             }
@@ -1011,7 +1045,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
         const bool p_free = jg < 2 || mbar_test(sm32(&C.pv_done[(jg - 2u) % G::kPv]), ((jg - 2u) / G::kPv) & 1u);
         uint8_t *const p_tile = c8_shared + G::kPOff + (jg & 1u) * G::kBox;
         float x[kCols];
-        // Twice where references move: of the rows whose largest w of this tile is over 2^8,
+        // Twice where references move: of the rows whose largest w of this tile is over 2^15,
         // or of all in a part's first tile.
         for (bool move = j < G::kOs;; move = true) {
           // Logits in log2 units, rounded as they are: a reference taken from them is then met
@@ -1045,9 +1079,16 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
             if (lane % (32 / kCols) == 0) *spot(wq, lane / (32 / kCols)) = top;
             group_sync(w);
             if (tk < kCols) {
-              const float most = fmaxf(fmaxf(*spot(0, tk), *spot(1, tk)), fmaxf(*spot(2, tk), *spot(3, tk)));
-              const float was = -less_ref[tk], now = most - kC8Head;
-              const bool moves = most > was + 8.f;
+              // the largest, and the least of the warps' largest (of those that see a token)
+              float most = -INFINITY, least = INFINITY;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float one = *spot(q, tk);
+                most = fmaxf(most, one);
+                least = fminf(least, one == -INFINITY ? INFINITY : one);
+              }
+              const float was = -less_ref[tk], now = most - kC8Head - fminf(fmaxf(most - least - kC8Gap, 0.f), kC8Gap);
+              const bool moves = most > was + 15.f;
               alpha[tk] = moves ? ex2(was - now) : 1.f;
               if (moves) less_ref[tk] = -now;
             }
@@ -1081,41 +1122,44 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
           float most = 0.f;
 #pragma unroll
           for (int i = 0; i < kCols; i += 2) most = max3(most, x[i], x[i + 1]);
-          if (move || !any_of_group(w, most * vx > 448.f)) break;
+          if (move || !any_of_group(w, most * vx > kC8Most)) break;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sm32(&C.s_free[b]));
         if (!__all_sync(0xffffffffu, p_free)) wait_pv(jg - 2);  // P's buffer is free
-        // The row of the P buffer that is this token's: the group's bytes of hi and of lo.
-        // The sums keep 32 bits, as lse has to; the weights go to the two terms above.
-        uint8_t *prow = p_tile + tk * 128;
-        constexpr int kPut = kCols < 16 ? kCols : 16;  // bytes at once
-        auto put = [&](int col, const uint32_t *v) {
-          uint8_t *at = prow + (((col >> 4) ^ (tk & 7)) << 4) + (col & 15);
-          if constexpr (kPut == 16) *reinterpret_cast<uint4 *>(at) = make_uint4(v[0], v[1], v[2], v[3]);
-          else *reinterpret_cast<uint2 *>(at) = make_uint2(v[0], v[1]);
-        };
+        // The rows of P that are this token's: the group's bytes of its terms.  The sums keep
+        // 32 bits, as lse has to; the weights go to the three terms above.
+        uint8_t *const prow = p_tile + tk * 128, *const third = R < 64 ? prow : c8_shared + G::kLoBox + tk * 128;
+        auto place = [&](uint8_t *row, int col) { return row + (((col >> 4) ^ (tk & 7)) << 4); };
+        constexpr int kPut = kCols < 16 ? kCols : 16;  // columns at once
         const uint64_t vs2 = pair_f32(vs, vs);
 #pragma unroll
         for (int c = 0; c < kCols; c += kPut) {
-          uint32_t ph[kPut / 4], pl[kPut / 4];
+          uint32_t ph[kPut / 4], pm[kPut / 4], pl[kPut / 4];
 #pragma unroll
           for (int i = 0; i < kPut; i += 4) {
-            uint32_t h[2], l[2];
+            uint32_t h[2], m[2], l[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint64_t p2 = pair_f32(x[c + i + 2 * k], x[c + i + 2 * k + 1]);
               float w0, w1;
               unpair_f32(mul2(p2, vs2), w0, w1);
-              split_e4m3(w0, w1, h[k], l[k]);
+              split_e5m2(w0, w1, h[k], m[k], l[k]);
               sum2[(c + i) / 2 + k] = add2(sum2[(c + i) / 2 + k], p2);
             }
-            ph[i / 4] = h[0] | h[1] << 16;
-            pl[i / 4] = l[0] | l[1] << 16;
+            ph[i / 4] = __byte_perm(h[0], h[1], 0x7531);
+            pm[i / 4] = __byte_perm(m[0], m[1], 0x7531);
+            pl[i / 4] = __byte_perm(l[0], l[1], 0x7531);
           }
-          put(n0 + c, ph);
-          put(R + n0 + c, pl);
+          if constexpr (kPut == 8) {
+            *reinterpret_cast<uint4 *>(place(prow, 0)) = make_uint4(ph[0], ph[1], pm[0], pm[1]);
+            *reinterpret_cast<uint4 *>(place(prow, 16)) = make_uint4(0u, 0u, pl[0], pl[1]);
+          } else {
+            *reinterpret_cast<uint4 *>(place(prow, n0 + c)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+            *reinterpret_cast<uint4 *>(place(prow, R + n0 + c)) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
+            *reinterpret_cast<uint4 *>(place(third, (R < 64 ? 2 * R : (int)(jg & 1u) * 64) + n0 + c)) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+          }
         }
         if (masked && veiled) {
           // A NaN of V would reach, as 0 x NaN, the rows that do not see its token: it is
