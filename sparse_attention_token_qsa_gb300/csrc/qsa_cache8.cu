@@ -17,8 +17,8 @@
 // through f16, or by 2^-19.  ref is log2 of a maximum of exp(s) vs seen earlier, less 8, so that
 // is 2^-27 of the row's largest.  Many small weights may still outweigh one that is larger, as
 // beside a first token whose V is small (with two e4m3 terms, 2^-18, the outputs of 65536 tokens
-// beside one of weight 0.9 were off by 14 to 27 % of their norm): a maximum that is far above the
-// others of its tile is put up to 6 binades higher.  ref moves (the row's sum and its columns of
+// beside one of weight 0.9 were off by 14 to 27 % of their norm): a maximum that is more than 10
+// binades above the others of its tile is put up to 6 higher.  ref moves (the row's sum and its columns of
 // O rescaled) when a w passes 57344, e5m2's largest: a move costs most of a tile's time, and the
 // 7.8 binades before it are why 8 and not more (8, 10, 11, 12, 14: 64 rows of 65k tokens 107,
 // 109, 116, 126, 138 us, a chunk of 2048 in a window 168, 185, 202, 213, 236).  The sum is of the
@@ -67,7 +67,8 @@ constexpr int kC8MaxCtas = 160;
 constexpr float kC8Unset = -1e30f;    // a row's reference before it has seen a token
 constexpr float kC8Nobody = 1e30f;    // ... of a column without a row: its weights are 0
 constexpr float kC8Head = 8.f;        // log2 of a largest w when the reference is set
-constexpr float kC8Gap = 6.f;         // ... and more by what it is above the others beyond this, up to twice
+constexpr float kC8Gap = 10.f;        // ... and more by what it is above the others beyond this,
+constexpr float kC8Lift = 6.f;        // up to this
 constexpr float kC8Most = 57344.f;    // a w above moves the reference: e5m2's largest
 constexpr float kC8Least = 0x1p-80f;  // a V scale below counts as this for the reference
 constexpr uint32_t kC8SuspendNs = 2000;  // a wait's sleep at most (it ends early when its phase completes)
@@ -1087,7 +1088,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
                 most = fmaxf(most, one);
                 least = fminf(least, one == -INFINITY ? INFINITY : one);
               }
-              const float was = -less_ref[tk], now = most - kC8Head - fminf(fmaxf(most - least - kC8Gap, 0.f), kC8Gap);
+              const float was = -less_ref[tk], now = most - kC8Head - fminf(fmaxf(most - least - kC8Gap, 0.f), kC8Lift);
               const bool moves = most > was + 15.f;
               alpha[tk] = moves ? ex2(was - now) : 1.f;
               if (moves) less_ref[tk] = -now;

@@ -4,9 +4,10 @@ small ones are the output.
 The tolerance is that of drafted-row attention over a bf16 cache (cache_cases.ref_tree) on the values that the cache
 stands for, beside which the logits' bound (step_cases) counts what q's two terms lose: 2^-8 of every weight, nothing of
 the largest one.  A weight's terms are off by 2^-9 of it and 2^-11 for its f16, or by 2^-19 where the row's largest is
-2^8, and 2^13 or more where that is 2^11 times the others of its tile, as here (14.7 binades above the others' mean and
-more, the least of four maxima of 32 normal logits being 3.7 below): over 65536 tokens of which one has 0.99 of the sum,
-2^16 * 2^-33 of it together (such a one is at 2^14), within the (2^-8 - 2^-9 - 2^-11) * 0.01 that is left.
+2^8, or up to 2^14: as much more as it is more than 2^10 above the others of its tile.  One that has 0.99 of the sum of
+65536 is 2^22.6 above the others' mean and 2^18 above theirs (of 32 normal logits the largest is some 2^3 above the mean,
+the least of four such less), so at 2^14: 2^16 * 2^-33 of it together, within the (2^-8 - 2^-9 - 2^-11) * 0.01 that is
+left.  One of 0.9 among 16384 is 2^17.9 above the mean, so at 2^12 or more: 2^14 * 2^-31 beside 0.1.
 """
 import numpy as np
 import pytest
