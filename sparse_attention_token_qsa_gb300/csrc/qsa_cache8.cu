@@ -103,19 +103,22 @@ struct C8Geom {
   // as many are held.
   static constexpr uint32_t kPv = HD == 128 ? 8 : 4, kAhead = 2 * kPv;
   static constexpr uint32_t kQBytes = (kHalves * kQBox + 1023) / 1024 * 1024;
-  // P's two buffers are boxes of a token a row, with its hi and mid terms and, up to 32 rows, lo
-  // (of 8 rows: behind eight zeros, as an MMA has 16 columns at least); of 64 rows the lo terms
-  // of both buffers fill a third box.
+  // P's two buffers are boxes of a token a row, with its hi and mid terms and, up to 32 rows, lo;
+  // of 64 rows the lo terms of both buffers fill a third box.
   static constexpr uint32_t kPOff = kQBytes, kLoBox = kPOff + 2 * kBox, kRingOff = kLoBox + (R < 64 ? 0 : kBox);
   static constexpr uint32_t kCtrlOff = kRingOff + kSlots * kSlot;
-  static constexpr uint32_t kOCols = kHalves * kN, kSCol = kOs * kOCols;  // TMEM: O's halves, then S
+  // O has columns for each of P's terms (and zeros, of 8 rows, to a multiple of 16) where TMEM has
+  // room for them; else a second MMA adds V lo to mid's.  (Two MMAs of 8 rows: decode of 16
+  // sequences 103.2 us for 102.9, 600 rows over 200 to 800 tokens 69.0 for 68.3.)
+  static constexpr bool kThree = R < 32;
+  static constexpr int kON = kThree ? (3 * R + 15) / 16 * 16 : kN;
+  static constexpr uint32_t kOCols = kHalves * kON, kSCol = kOs * kOCols;  // TMEM: O's halves, then S
   static_assert(kSCol + kS * kN <= 512, "TMEM has 512 columns");
-  // kind::f8f6f4, D f32, A and B e4m3, M = 128, N = kN; O: A and B MN-major, B e5m2, and again
-  // with the lo terms, which are added to mid's columns
+  // kind::f8f6f4, D f32, A and B e4m3, M = 128, N = kN; O: A and B MN-major, B e5m2
   static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kN >> 3) << 17) | ((128u >> 4) << 24);
-  static constexpr uint32_t kIdescO = kIdescS | (1u << 10) | (1u << 15) | (1u << 16);
-  static constexpr int kLoN = R < 16 ? 16 : R;
-  static constexpr uint32_t kIdescLo = kIdescO - ((uint32_t)((kN - kLoN) >> 3) << 17), kLoCol = R < 16 ? 0 : R;
+  static constexpr uint32_t kIdescO =
+      (1u << 4) | ((uint32_t)(kON >> 3) << 17) | ((128u >> 4) << 24) | (1u << 10) | (1u << 15) | (1u << 16);
+  static constexpr uint32_t kIdescLo = kIdescO - ((uint32_t)((kON - R) >> 3) << 17);
 };
 
 // What beginning a unit costs, in tiles: its Q, its first references and its output.  At 3, 6, 9
@@ -376,19 +379,19 @@ __device__ __forceinline__ void tmem_ready(uint32_t *v) {
   for (int i = 4; i < K; i += 4) asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3])::"memory");
 }
 
-// A column of O's halves (`half` columns apart) and its lo term (`lo` columns on), times `by`.
-template <int kHalves>
-__device__ __forceinline__ void tmem_scale(uint32_t taddr, uint32_t half, uint32_t lo, float by) {
-  uint32_t x[2 * kHalves];
+// A column of O's halves (`half` columns apart) and its other terms (`term` columns on), times `by`.
+template <int kHalves, int kTerms>
+__device__ __forceinline__ void tmem_scale(uint32_t taddr, uint32_t half, uint32_t term, float by) {
+  uint32_t x[kTerms * kHalves];
 #pragma unroll
-  for (int i = 0; i < 2 * kHalves; ++i)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x[i]) : "r"(taddr + (i >> 1) * half + (i & 1) * lo));
+  for (int i = 0; i < kTerms * kHalves; ++i)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x[i]) : "r"(taddr + (i / kTerms) * half + (i % kTerms) * term));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 2 * kHalves; ++i) {
+  for (int i = 0; i < kTerms * kHalves; ++i) {
     asm volatile("" : "+r"(x[i])::"memory");
     x[i] = __float_as_uint(__uint_as_float(x[i]) * by);
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr + (i >> 1) * half + (i & 1) * lo), "r"(x[i])
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr + (i / kTerms) * half + (i % kTerms) * term), "r"(x[i])
                  : "memory");
   }
 }
@@ -749,9 +752,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
       // The slot holds its copy.  A parity tells two phases apart, so the slot's copy
       // before this one has to be known to have landed.  S of tile j: that one is K, of a
       // tile whose S this warp issued, or V of tile j - 4 or an earlier one, whose P V
-      // was waited for, or, in a part's first tiles, V of a part before the last, whose
-      // output was written before this part's Q was fetched.  P V of tile j: it is V, or K
-      // of an earlier tile.
+      // was waited for, or, in a part's first tiles, of an earlier part, all of whose P V
+      // were done before this part's Q was stored.  P V of tile j: it is V, or K of an
+      // earlier tile.
       auto landed = [&]() {
         if (!wait(C.full[slot], phase)) return false;
         // the copies wrote through the generic proxy; the MMAs read through the async one
@@ -815,9 +818,9 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
 #pragma unroll
                 for (int kk = 0; kk < kC8T / 32; ++kk) {  // 32 tokens a step: 4 KiB of V's and of P's rows
                   const uint64_t v = desc_of(v_lo + (uint32_t)h * (G::kBox >> 4) + 256u * kk, desc_hi);
-                  const uint32_t d = o + (uint32_t)h * G::kN;
+                  const uint32_t d = o + (uint32_t)h * G::kON;
                   mma_8(d, v, desc_of(p + 256u * kk, desc_hi), G::kIdescO, (j >= G::kOs || kk > 0) ? 1u : 0u);
-                  mma_8(d + G::kLoCol, v, desc_of(p3 + 256u * kk, desc_hi), G::kIdescLo, 1u);
+                  if constexpr (!G::kThree) mma_8(d + R, v, desc_of(p3 + 256u * kk, desc_hi), G::kIdescLo, 1u);
                 }
               mma_commit(sm32(&C.empty[slot]));
               mma_commit(sm32(&C.pv_done[jg % G::kPv]));
@@ -938,15 +941,18 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
 #pragma unroll
             for (int o = 0; o < G::kOs; ++o) {
               if (!has(o)) continue;
-              uint32_t hi[kOut], lo[kOut];
-              const uint32_t at = lane_base + (uint32_t)o * G::kOCols + (uint32_t)(h * G::kN + c);
+              uint32_t hi[kOut], mid[kOut], lo[kOut];
+              const uint32_t at = lane_base + (uint32_t)o * G::kOCols + (uint32_t)(h * G::kON + c);
               tmem_cols<kOut>(at, hi);
-              tmem_cols<kOut>(at + R, lo);
+              tmem_cols<kOut>(at + R, mid);
+              if constexpr (G::kThree) tmem_cols<kOut>(at + 2 * R, lo);
               tmem_ready<kOut>(hi);
-              tmem_ready<kOut>(lo);
+              tmem_ready<kOut>(mid);
+              if constexpr (G::kThree) tmem_ready<kOut>(lo);
 #pragma unroll
               for (int i = 0; i < kOut; ++i) {
-                const float y = fmaf(__uint_as_float(lo[i]), 0.25f, __uint_as_float(hi[i]));
+                const float less = G::kThree ? __uint_as_float(mid[i]) + __uint_as_float(lo[i]) : __uint_as_float(mid[i]);
+                const float y = fmaf(less, 0.25f, __uint_as_float(hi[i]));
                 x[i] = G::kTurns ? fmaf(y, C.mix[o * kCols + c + i], x[i]) : y;
               }
             }
@@ -1102,7 +1108,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
 #pragma unroll 1
               for (int i = 0; i < kCols; ++i) {
                 const float by = alpha[i];
-                if (by != 1.f) tmem_scale<G::kHalves>(my_o + i, G::kN, R, by);
+                if (by != 1.f) tmem_scale<G::kHalves, G::kThree ? 3 : 2>(my_o + i, G::kON, R, by);
               }
               tmem_wait_st();
             }
@@ -1155,7 +1161,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
           }
           if constexpr (kPut == 8) {
             *reinterpret_cast<uint4 *>(place(prow, 0)) = make_uint4(ph[0], ph[1], pm[0], pm[1]);
-            *reinterpret_cast<uint4 *>(place(prow, 16)) = make_uint4(0u, 0u, pl[0], pl[1]);
+            *reinterpret_cast<uint4 *>(place(prow, 16)) = make_uint4(pl[0], pl[1], 0u, 0u);
           } else {
             *reinterpret_cast<uint4 *>(place(prow, n0 + c)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
             *reinterpret_cast<uint4 *>(place(prow, R + n0 + c)) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
@@ -1225,7 +1231,7 @@ cache8_attn_kernel(const Cache8Args a, const C8Plan plan, C8Open *__restrict__ o
               }
             }
             __syncwarp();
-            tmem_scale1(lane_base + (has(0) ? 0u : G::kOCols) + (uint32_t)(h * G::kN + n), hit ? NAN : 1.f);
+            tmem_scale1(lane_base + (has(0) ? 0u : G::kOCols) + (uint32_t)(h * G::kON + n), hit ? NAN : 1.f);
           }
         }
         tmem_wait_st();
