@@ -15,7 +15,8 @@ import torch
 
 import qsa_inputs as qi
 from cache_cases import BF, U, dev, f64
-from step_cases import E4M3, Cache8, ref_attend, to_e4m3
+from step_cases import Cache8, ref_attend, to_e4m3
+from test_gpu_cache8 import call, check
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +90,15 @@ def test_small_weights_beside_a_large_one(qsa, tokens, weight, rows, group):
         err = np.abs(got - want[None]) / tol[None]
         assert err.max() <= 1, (hd, large, err.max())
         assert np.all(np.abs(lse.cpu().numpy().reshape(n, rows, group) - wl[None]) <= ltol[None])
+
+
+@pytest.mark.parametrize("log2", [-80, -60, 38, 100])
+def test_v_scales_at_the_ends_of_their_range(qsa, log2):
+    """V's scales far below and above 1, all alike: the bound is of the outputs' own size."""
+    rng = qi.rng_for(119, salt=log2 + 200)
+    for hd, rows in ((128, 1), (256, 12)):
+        c = Cache8(rng, [900, 40], [rows, 1], 8, 2, hd, 16, 16, "tree")
+        c.vs = np.ldexp(c.vs, log2).astype(np.float32)
+        out, lse, st = call(qsa, c)
+        assert st == (0, 0)
+        check(c, out, lse)
