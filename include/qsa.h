@@ -656,7 +656,8 @@ qsa_status qsa_page_plan(const int32_t *ctx_len, const int32_t *new_rows, int32_
 /*
  * The query and key heads of new tokens normed and rotated, and their K and V written
  * into the paged cache, in bf16 or in 8 bits.  What qsa_tree_attn, qsa_sparse_attn
- * (bf16) and qsa_cache8_attn (8 bits) then read.
+ * (bf16) and qsa_cache8_attn (8 bits) then read; qsa_gather_kv, qsa_attn_mass and
+ * qsa_cache_compact take bf16 pools alone.
  *  q, k, v  DEVICE bf16, row i at q + i*q_stride (nq heads of head_dim values), k +
  *           i*k_stride and v + i*v_stride (nkv heads): one projection's row, or three.
  *           16-byte aligned, strides multiples of 8.
@@ -676,7 +677,8 @@ qsa_status qsa_page_plan(const int32_t *ctx_len, const int32_t *new_rows, int32_
  *           unit*b to unit*b + unit - 1, holds value * scale.  unit is 16, 32, 64 or 128
  *           and divides page_size (it is not looked at for bf16 pools).
  *           A block's scale is the smallest power of two s with |x| <= 448 s for
- *           every finite new value x of the head in the block (0 if they are all 0),
+ *           every finite new value x of the head in the block (2^-126 at least; 0 if they
+ *           are all 0),
  *           and no less than its earlier scale where tokens before the new ones are in
  *           the block: those are then divided by the new one and rounded again.  A NaN or
  *           an infinity is held as NaN.
@@ -723,7 +725,7 @@ qsa_status qsa_qkv_write(const uint16_t *q, int64_t q_stride, int32_t nq, const 
  *           pages, scales and table entries that hold only such tokens may be gone.
  *  A row that attends no token gets zeros, and lse -inf.  What a row does not see does
  *  not reach its output, NaN though it be.  A query head with a value that is not finite
- *  gets NaN.
+ *  gets NaN, and lse NaN, as does a row that sees a K that is not finite.
  *  Products, softmax and sums run in f32.  A row's weights times their block's V scale
  *  enter the weighted sum as three e5m2 terms, relative to the row's largest: off by at
  *  most 2^-8 of themselves, or 2^-27 of the largest (2^-33 where that is far above the

@@ -43,14 +43,15 @@
 // instructions and MMAs issued from a uniform loop took the misses to 5 % (106 and 127 us).
 // For the same reason a part's beginning and end are short: they run once or twice a launch.
 // (Where they run often, they bound it: 512 rows over 64 to 400 tokens of 8 KV heads, 27 parts
-// of one or two tiles a CTA, take 117 us, 4.3 us a part, of which the tiles are 40 %.)
+// of one to four tiles a CTA, take 118 us, 4.4 us a part.)
 //
 // Decode is bound by HBM: 16 sequences of 16k to 64k tokens, 16 heads over 2 x 256, take
-// 102 us, 93 % of the copy bandwidth; 32 heads over 8 x 128 194 us, 98 %.  With more rows the
-// softmax bounds it: a tile of 64 rows is 8192 weights, each about 12 instructions (two
-// terms of S joined, two scales, the exponential, two terms of w), beside 150 a warp for
-// barriers and look-ups.  64 rows of 65471 tokens take 114 us (32 % of the bf16 rate), the
-// MMAs busy for 28 % of it.
+// 102 us, 93 % of the copy bandwidth; 32 heads over 8 x 128 193 us, 99 %.  With more rows the
+// softmax bounds it: a tile of 64 rows is 8192 weights and 8300 warp instructions of all roles,
+// 32 for every 32 weights, most of them a softmax warp's: S's two terms joined, two scales, the
+// exponential, the sum, three terms of w, and beside its 16 columns what a tile costs each of
+// the 16 warps (barriers, votes, look-ups).  64 rows of 65471 tokens take 107 us (34 % of the
+// bf16 rate), the MMAs busy for 36 % of it and 59 % of the issue slots used.
 #include "qsa_launch.h"
 #include "qsa_share.cuh"
 #include "qsa_tc_cache.cuh"
@@ -122,9 +123,9 @@ struct C8Geom {
 };
 
 // What beginning a unit costs, in tiles: its Q, its first references and its output.  At 3, 6, 9
-// and 13 tiles, single rows of 32 heads over 8 over 300 to 9001 tokens take 42.5, 44.3, 47.2 and
-// 46.4 us, and 64 single rows over 100 to 2000 tokens 24.8, 25.7, 27.3 and 27.9; trees of 5 to 37
-// rows of 16 heads over 2 (units of 64 rows) 109, 106, 99 and 108.
+// and 13 tiles (with weights of two terms), single rows of 32 heads over 8 over 300 to 9001 tokens
+// took 42.5, 44.3, 47.2 and 46.4 us, and 64 single rows over 100 to 2000 tokens 24.8, 25.7, 27.3
+// and 27.9; trees of 5 to 37 rows of 16 heads over 2 (units of 64 rows) 109, 106, 99 and 108.
 template <int R>
 constexpr int c8_start() { return R < 64 ? 3 : 9; }
 
@@ -1447,17 +1448,20 @@ cudaError_t launch_rows(const Cache8Args &a, cudaStream_t stream) {
 }
 
 // The rows of a unit.  Enough for a sequence's rows by the call's mean, as a tile of 64 costs
-// 2.1 us of a CTA where one of 32 costs 1.2, of 16 0.86 and of 8 0.77.  Fewer where the GPU would
-// stand idle meanwhile: a unit of 64 takes 10 us besides its tiles, one of 8 a third of that.
-// So by how many tiles of such units, and 3 for what a unit costs besides, a CTA would get at
-// most.  8, 16, 32, 64 rows a unit (us, in a graph):
-//   0.4  2 sequences of 10 rows, 16 heads over 2, a window of 199     13.6  14.0  15.2  17.4
-//   0.9  4 of 24, 16 over 2, 300 tokens                               19.9  15.2  16.9  20.1
-//   1.0  1 of 64, 16 over 2, 600 tokens                               18.8  16.5  17.5  19.9
-//   1.4  1 of 24, 16 over 2, 4000 tokens                              20.3  20.3  18.9  20.9
-//   2.5  4 of 64, 16 over 2, 300 tokens                               31.2  25.4  18.7  21.3
-//   3.3  6 of 112, 16 over 2, 22 to 139 tokens                        58.1  40.2  35.1  34.7
-//   8.9  17 of 95, 12 over 4, 8 tokens                                80.6  55.7  43.0  35.8
+// 1.46 us of a CTA where one of 32 costs 0.89, of 16 0.79 and of 8 0.73 (heads of 256, from L2).
+// Fewer where the GPU would stand idle meanwhile: a unit of 64 takes some 10 us besides its
+// tiles, one of 8 2 us.  So by how many tiles of units of 64 a CTA would get at most, with 3
+// tiles for a unit's beginning: the bounds are fitted with that, c8_start() is what balances CTAs
+// that have many.  8, 16, 32, 64 rows a unit, and the rule's choice under a table of 65536 tokens
+// a sequence (us, in a graph): without a window the bound is the table's, which the host knows,
+// not the contexts', so that a long one gets the mean's units.
+//   0.4  2 sequences of 10 rows, 16 heads over 2, a window of 199     13.0  14.5  16.2  18.1  13
+//   0.9  4 of 24, 16 over 2, 300 tokens                               18.9  16.5  17.5  19.9  20
+//   1.0  1 of 64, 16 over 2, 600 tokens                               18.2  16.7  17.7  20.2  20
+//   1.4  1 of 24, 16 over 2, 4000 tokens                              20.6  20.8  18.6  20.6  21
+//   2.5  4 of 64, 16 over 2, 300 tokens                               29.8  24.4  16.5  19.5  20
+//   3.3  6 of 112, 16 over 2, 22 to 139 tokens                        51.0  38.1  32.8  31.4  31
+//   8.9  17 of 95, 12 over 4, 8 tokens                                84.6  57.5  44.2  36.5  40
 int32_t rows_of_unit(const Cache8Args &a, int64_t most) {
   const int64_t n = a.seqs.n_seqs, mean = ((int64_t)a.seqs.n_rows * a.group + n - 1) / n;
   const int64_t all = (most + kC8T - 1) / kC8T;

@@ -12,7 +12,7 @@
 // cluster barrier where one reads what another wrote; so the lengths,
 // heights and tables may be updated in place.  Many rows are filled by a second launch: 1024
 // sequences of up to 256 rows, 131k in all, take 15.0 us (32.8 by one cluster alone, whose CTAs
-// each moved their own sequences' pages).  64 single rows take 6.5 us, a launch and the chain
+// each moved their own sequences' pages).  64 single rows take 6.2 us, a launch and the chain
 // (7.7 with the warps' sums added up one by one and the rows' places fetched from L2).
 #include "qsa_launch.h"
 
